@@ -71,7 +71,9 @@ enum mla_status {
   MLA_ERR_DEVICE_TIMEOUT = -7,     /* (device status) an internal pipeline wait gave up */
   MLA_ERR_SEQLEN = -8,             /* (device status) some seq_lens[b] outside [q_len, Smax] */
   MLA_ERR_ARG = -9,                /* any other invalid argument (e.g. non-finite scale) */
-  MLA_ERR_PAGE = -10               /* (device status) a block-table entry outside the page pool */
+  MLA_ERR_PAGE = -10,              /* (device status) a block-table entry outside the page pool */
+  MLA_ERR_POOL = -11,              /* (device status) the free-page list is too short (extend) or its array too small (trim) */
+  MLA_ERR_SLOT = -12               /* (device status) a cache slot or draft index outside its range */
 };
 
 /*
@@ -167,7 +169,8 @@ int mla_verify_attn_paged(const void* q_nope_abs, const void* q_rope, const void
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status
- * word: MLA_OK, MLA_ERR_SEQLEN, MLA_ERR_DEVICE_TIMEOUT or MLA_ERR_PAGE (the first recorded),
+ * word: MLA_OK, or of the errors recorded the first in the order MLA_ERR_SEQLEN,
+ * MLA_ERR_DEVICE_TIMEOUT, MLA_ERR_PAGE, MLA_ERR_POOL, MLA_ERR_SLOT,
  * or MLA_ERR_LAUNCH if the synchronisation itself failed.  The word is shared
  * by all calls on the device since it was last read.
  * Every internal pipeline wait gives up after 2 s; the call's kernels then
@@ -273,6 +276,159 @@ int mla_verify_attn_noalloc(const void* q_nope_abs, const void* q_rope, const vo
                             const int32_t* seq_lens, const uint32_t* tree_mask, int B, int q_len,
                             int H, int Smax, float scale, float* out, float* lse,
                             cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The cache around a verify step.  The pages have no counterpart for these
+ * entry points: they name a paged cache and its defragmentation as parts of the
+ * serving system around the kernel.  One step over a paged cache is
+ *   mla_blocks_extend   rows for the drafts: block table, lengths, slot map
+ *   mla_cache_append    the drafts' rows into the pool, by slot
+ *   mla_verify_attn_paged or mla_gqa_verify_attn_paged
+ *   mla_cache_keep      the accepted path's rows move together
+ *   mla_blocks_trim     lengths back to what was accepted, pages given back
+ * All of them work in place on the caller's device arrays, in stream order,
+ * read nothing on the host and may be captured into a CUDA graph.  Problems
+ * only the GPU can see are recorded in the device status word.
+ */
+
+/*
+ * Room for new tokens: grows every stream b by new_lens[b] tokens.  With
+ *   have_b = ceil(seq_lens[b] / page_size), need_b = ceil((seq_lens[b] + new_lens[b]) / page_size) - have_b
+ * the k-th new block of the batch (streams in order, then blocks in order) is
+ * page free_pages[free_count - 1 - k]; it is written to its entry of
+ * block_table.  Then seq_lens[b] += new_lens[b] and free_count -= sum need_b.
+ * slots[t] is the pool row of the t-th new token (streams in order, positions
+ * in order); slots past the last new token become -1.
+ *
+ *   seq_lens     [B] int32, in and out.
+ *   new_lens     [B] int32, >= 0 (0 for streams that do not grow, unused ones too).
+ *   block_table  [B, max_blocks] int32, in and out; only entries of new blocks are written.
+ *   free_pages   [free_capacity] int32, a stack of distinct free pages; not written.
+ *   free_count   [1] int32, pages on the stack; in and out.
+ *   pool_pages   pages in the pool; an entry used outside [0, pool_pages) gives the
+ *                token slot -1 and MLA_ERR_PAGE.
+ *   slots        [max_tokens] int32 (may be NULL when max_tokens is 0).
+ *   0 <= B <= 16384, page_size >= 1, max_blocks >= 1, max_blocks * page_size < 2^31,
+ *   pool_pages * page_size < 2^31; all pointers 4-byte aligned (slots: 16).
+ *
+ * Either the whole batch grows or nothing does: with too few free pages
+ * (MLA_ERR_POOL), or a negative length, a stream that would outgrow its table
+ * row or more than max_tokens new tokens (MLA_ERR_SEQLEN), tables, lengths and
+ * the free list stay as they were and every slot is -1.
+ */
+int mla_blocks_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table, int B,
+                      int max_blocks, int page_size, const int32_t* free_pages, int free_capacity,
+                      int32_t* free_count, int pool_pages, int32_t* slots, int max_tokens,
+                      cudaStream_t stream);
+
+/*
+ * The inverse: shortens every stream b to keep_lens[b] <= seq_lens[b] tokens
+ * (0 gives all its pages back).  The R = sum_b ceil(seq_lens[b] / page_size) -
+ * ceil(keep_lens[b] / page_size) released blocks go back onto the stack, the
+ * k-th of the batch to free_pages[free_count + R - 1 - k], so that a trim back
+ * to the old lengths undoes an extend exactly.  Then seq_lens[b] = keep_lens[b]
+ * and free_count += R.  Released entries of block_table keep their values.
+ * A stream's length that would grow or be negative (MLA_ERR_SEQLEN), a stack
+ * that would outgrow free_capacity (MLA_ERR_POOL): nothing changes.  Pages
+ * shared between streams must not be trimmed twice; nothing checks that.
+ */
+int mla_blocks_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* block_table, int B,
+                    int max_blocks, int page_size, int32_t* free_pages, int free_capacity,
+                    int32_t* free_count, cudaStream_t stream);
+
+/*
+ * Writes T rows into cache pools by slot: for every t with slots[t] >= 0
+ *   pool_a[slots[t]] = a[t] (a_bytes bytes), pool_b[slots[t]] = b[t] (b_bytes bytes).
+ * For the latent cache a = kv_c (1024 bytes), b = k_pe (128 bytes), pool_a the pool
+ * and pool_b the pool's address + 1024, both with a row stride of 1152 bytes;
+ * for separate keys and values a = k, b = v.  A contiguous cache is a pool of
+ * B * Smax rows.
+ *   a, b          T rows at a_stride / b_stride bytes.
+ *   pool_rows     rows in the pool(s), < 2^31; row strides in bytes.
+ *   slots         [T] int32; a negative slot skips its token; one at or beyond
+ *                 pool_rows skips it too and records MLA_ERR_SLOT.
+ * Addresses, strides and widths are multiples of 16 bytes; b_bytes may be 0.
+ * Slots of one call must be distinct: of two tokens with one slot, each 16-byte
+ * piece of the row may come from either.
+ */
+int mla_cache_append(const void* a, long long a_stride, int a_bytes, void* pool_a, long long pool_a_stride,
+                     const void* b, long long b_stride, int b_bytes, void* pool_b, long long pool_b_stride,
+                     long long pool_rows, const int32_t* slots, int T, cudaStream_t stream);
+
+/*
+ * After a tree was verified: moves the rows of each stream's accepted drafts
+ * together.  With prefix_b = seq_lens[b] - q_len, row prefix_b + j of stream b
+ * takes the value row prefix_b + path[b][j] had before the call, for every
+ * j < keep[b]; the other rows stay (seq_lens too: mla_blocks_trim with
+ * prefix_b + keep[b] follows).  Any path is allowed, repeated drafts included.
+ *   pool_a, pool_b as for mla_cache_append (b_bytes may be 0).
+ *   block_table  [B, max_blocks] int32; row t of stream b is
+ *                block_table[b][t / page_size] * page_size + t % page_size.
+ *                A contiguous cache is one page of Smax rows per stream.
+ *   seq_lens     [B] int32, q_len <= seq_lens[b] <= max_blocks * page_size where
+ *                keep[b] > 0 (MLA_ERR_SEQLEN otherwise, and the stream is left as it was).
+ *   path         [B, q_len] int32 draft indices in [0, q_len); entries past keep[b] are not read.
+ *   keep         [B] int32 in [0, q_len].
+ * A draft index or count out of range (MLA_ERR_SLOT) or a page outside the pool
+ * (MLA_ERR_PAGE) leaves that stream as it was.  1 <= q_len <= 64.  No row may
+ * be a draft row of two streams.
+ */
+int mla_cache_keep(void* pool_a, long long pool_a_stride, int a_bytes, void* pool_b,
+                   long long pool_b_stride, int b_bytes, long long pool_rows,
+                   const int32_t* block_table, int max_blocks, int page_size, const int32_t* seq_lens,
+                   const int32_t* path, const int32_t* keep, int B, int q_len, cudaStream_t stream);
+
+/* Types of the grouped-head caches and queries. */
+enum mla_dtype { MLA_BF16 = 0, MLA_FP16 = 1 };
+
+/*
+ * Verify attention with grouped query heads: the counterpart of
+ * mla_verify_attn for models whose keys and values are separate and shared by
+ * G = H / Hkv query heads (drafters, and targets without a latent cache).  For
+ * stream b, draft i < q_len, head h < H and its key head g = h / G:
+ *   s_t        = scale * sum_d q[b,i,h,d] k[b,t,g,d]        for the t visible to (b, i) as in mla_verify_attn
+ *   out[b,i,h] = sum_{visible t} softmax(s)_t v[b,t,g,:]    (0 if nothing is visible)
+ *   lse[b,i,h] = ln sum_{visible t} exp(s_t)                (-inf if nothing is visible)
+ * q_len = 1 with mask bit 0 set is ordinary decoding.
+ *
+ *   q, out     [B, q_len, H, D], k and v [B, Smax, Hkv, D], all of type `dtype`, D = 64 or 128,
+ *              H a multiple of Hkv; 16-byte aligned; out and lse [B, q_len, H] fp32 contiguous.
+ *   strides    NULL for contiguous tensors, or a host array of nine element strides
+ *              {q: batch, draft, head; k: batch, row, head; v: batch, row, head}, multiples
+ *              of 8 in [8, 2^38); the innermost dimension is contiguous.  Strides of
+ *              dimensions of size 1 are not used.
+ *   seq_lens   as for mla_verify_attn, and 0 for an unused stream (out 0, lse -inf).  A
+ *              stream with any other value outside [q_len, Smax] records MLA_ERR_SEQLEN and
+ *              gets the same result.  Rows t < seq_lens[b] of k and v must be finite; the
+ *              others may hold anything.
+ *   tree_mask, scale, B, q_len, Smax and the errors as for mla_verify_attn; B < 2^20.
+ *   workspace  at least mla_gqa_workspace_size(B, q_len, H, Hkv, D) bytes, 256-byte aligned;
+ *              contents do not matter, not read after the call; calls that share it must not overlap.
+ * Scores, softmax statistics and sums are fp32; the weights enter the product
+ * with v in v's type and out is rounded once to `dtype`.  Deterministic for
+ * fixed inputs and device.
+ */
+size_t mla_gqa_workspace_size(int B, int q_len, int H, int Hkv, int D);
+
+int mla_gqa_verify_attn(const void* q, const void* k, const void* v, const int64_t* strides,
+                        const int32_t* seq_lens, const uint32_t* tree_mask, int B, int q_len, int H,
+                        int Hkv, int D, int Smax, int dtype, float scale, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The same over a paged cache: k and v are pools [pool_rows, Hkv, D] (their
+ * batch strides are not used), key t of stream b is pool row
+ * block_table[b][t / page_size] * page_size + t % page_size, Smax = max_blocks *
+ * page_size.  Any page_size >= 1 is read in place.  Entries past
+ * ceil(seq_lens[b] / page_size) are not read; an entry outside the pool is
+ * recorded as MLA_ERR_PAGE (that stream's results are then undefined).
+ */
+int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_pool,
+                              const int64_t* strides, long long pool_rows, const int32_t* block_table,
+                              int max_blocks, int page_size, const int32_t* seq_lens,
+                              const uint32_t* tree_mask, int B, int q_len, int H, int Hkv, int D,
+                              int dtype, float scale, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

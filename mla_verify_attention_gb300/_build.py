@@ -1,4 +1,4 @@
-"""Builds the CUDA library in-tree with nvcc for sm_103a (one translation unit)."""
+"""Builds the CUDA library in-tree with nvcc for sm_103a (the translation units in parallel)."""
 from __future__ import annotations
 
 import glob
@@ -8,13 +8,14 @@ import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-CSRC = os.path.join(PKG, "csrc")
+CSRC = os.path.join(PKG, "csrc")                  # the latent-cache verify call
+CSRC_SERVING = os.path.join(PKG, "csrc_serving")  # grouped heads and the cache operators
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmla_verify_attn.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC"]
 _lock = threading.Lock()
 
 
@@ -24,9 +25,13 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def units() -> list[str]:
+    return sorted(f for d in (CSRC, CSRC_SERVING) for f in glob.glob(os.path.join(d, "*.cu")))
+
+
 def sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(INCLUDE, "*.h")))
+    return units() + sorted(f for d in (CSRC, CSRC_SERVING, INCLUDE) for e in ("*.cuh", "*.h")
+                            for f in glob.glob(os.path.join(d, e)))
 
 
 def is_stale(path: str = LIB_PATH) -> bool:
@@ -37,21 +42,39 @@ def is_stale(path: str = LIB_PATH) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/mla_verify_attn.cu into _build/libmla_verify_attn.so."""
+    """Compile every csrc*/*.cu and link them into _build/libmla_verify_attn.so."""
     with _lock:
         if not force and not is_stale():
             return LIB_PATH
         os.makedirs(OUT_DIR, exist_ok=True)
-        tmp = LIB_PATH + ".%d.tmp" % os.getpid()
-        cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp,
-               os.path.join(CSRC, "mla_verify_attn.cu")]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("nvcc failed (%d):\n%s\n%s" % (r.returncode, " ".join(cmd),
-                                                              r.stderr[-4000:]))
-        os.replace(tmp, LIB_PATH)
-        if verbose:
-            print(r.stderr)
+        tag = ".%d.tmp" % os.getpid()
+        include = [f for d in (INCLUDE, CSRC, CSRC_SERVING) for f in ("-I", d)]
+        objs, jobs = [], []
+        for src in units():
+            obj = os.path.join(OUT_DIR, os.path.basename(src) + tag + ".o")
+            cmd = [nvcc(), *NVCC_FLAGS, *include, "-c", "-o", obj, src]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+            objs.append(obj)
+            jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True)))
+        try:
+            said = [(cmd, p.communicate()[1], p.returncode) for cmd, p in jobs]
+            for cmd, err, rc in said:
+                _check(cmd, rc, err)
+                if verbose:
+                    print(err)
+            tmp = LIB_PATH + tag
+            cmd = [nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            _check(cmd, r.returncode, r.stderr)
+            os.replace(tmp, LIB_PATH)
+        finally:
+            for obj in objs:
+                if os.path.exists(obj):
+                    os.remove(obj)
         return LIB_PATH
+
+
+def _check(cmd, rc, err) -> None:
+    if rc != 0:
+        raise RuntimeError("nvcc failed (%d):\n%s\n%s" % (rc, " ".join(cmd), err[-4000:]))

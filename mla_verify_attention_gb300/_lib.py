@@ -18,12 +18,15 @@ STATUS_NAMES = {
     0: "MLA_OK", -1: "MLA_ERR_NULLPTR", -2: "MLA_ERR_SHAPE", -3: "MLA_ERR_ALIGN",
     -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_UNSUPPORTED_DEVICE", -6: "MLA_ERR_LAUNCH",
     -7: "MLA_ERR_DEVICE_TIMEOUT", -8: "MLA_ERR_SEQLEN", -9: "MLA_ERR_ARG", -10: "MLA_ERR_PAGE",
+    -11: "MLA_ERR_POOL", -12: "MLA_ERR_SLOT",
 }
 EXPORTED = ("mla_verify_attn", "mla_verify_attn_workspace_size", "mla_verify_attn_last_device_error",
             "mla_verify_attn_strerror", "mla_verify_attn_plan", "mla_verify_attn_paged",
             "mla_verify_attn_paged_workspace_size", "mla_verify_attn_set_timing_events",
             "mla_verify_attn_set_test_controls", "mla_verify_attn_noalloc",
-            "mla_verify_attn_set_two_term_max_keys")
+            "mla_verify_attn_set_two_term_max_keys", "mla_blocks_extend", "mla_blocks_trim",
+            "mla_cache_append", "mla_cache_keep", "mla_gqa_workspace_size", "mla_gqa_verify_attn",
+            "mla_gqa_verify_attn_paged")
 
 _lock = threading.Lock()
 _lib = None
@@ -68,6 +71,21 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.mla_verify_attn_set_two_term_max_keys.restype = I
         lib.mla_verify_attn_noalloc.argtypes = [P, P, P, P, P, I, I, I, I, F, P, P, P]
         lib.mla_verify_attn_noalloc.restype = I
+        lib.mla_blocks_extend.argtypes = [P, P, P, I, I, I, P, I, P, I, P, I, P]
+        lib.mla_blocks_extend.restype = I
+        lib.mla_blocks_trim.argtypes = [P, P, P, I, I, I, P, I, P, P]
+        lib.mla_blocks_trim.restype = I
+        lib.mla_cache_append.argtypes = [P, L, I, P, L, P, L, I, P, L, L, P, I, P]
+        lib.mla_cache_append.restype = I
+        lib.mla_cache_keep.argtypes = [P, L, I, P, L, I, L, P, I, I, P, P, P, I, I, P]
+        lib.mla_cache_keep.restype = I
+        lib.mla_gqa_workspace_size.argtypes = [I, I, I, I, I]
+        lib.mla_gqa_workspace_size.restype = Z
+        lib.mla_gqa_verify_attn.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, P, P, Z, P]
+        lib.mla_gqa_verify_attn.restype = I
+        lib.mla_gqa_verify_attn_paged.argtypes = [P, P, P, P, L, P, I, I, P, P, I, I, I, I, I, I, F, P, P,
+                                                  P, Z, P]
+        lib.mla_gqa_verify_attn_paged.restype = I
         _lib = lib
         return lib
 

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "mla_verify_attn.h"
+#include "internal.h"
 #include "combine.cuh"
 #include "verify_split.cuh"
 #include "repack.cuh"
@@ -206,6 +207,24 @@ int encode(DeviceInfo* d, CUtensorMap* map, const void* base, int rank, const cu
 
 }  // namespace
 
+namespace mla {
+
+static_assert(kBitSeqLen == kStatusSeqLen && kBitTimeout == kStatusTimeout && kBitPage == kStatusPage,
+              "one status word serves every kernel of the library");
+
+int device_common(DeviceCommon* out) {
+  DeviceInfo* d = nullptr;
+  const int st = device_info(&d);
+  if (st != MLA_OK) return st;
+  out->sms = d->sms;
+  out->status_word = d->status_word;
+  out->encode = d->encode;
+  out->test_stall = g_test_stall.load(std::memory_order_relaxed);
+  return MLA_OK;
+}
+
+}  // namespace mla
+
 extern "C" {
 
 const char* mla_verify_attn_strerror(int status) {
@@ -218,6 +237,8 @@ const char* mla_verify_attn_strerror(int status) {
     case MLA_ERR_UNSUPPORTED_DEVICE: return "MLA_ERR_UNSUPPORTED_DEVICE: current device is not sm_103";
     case MLA_ERR_LAUNCH: return "MLA_ERR_LAUNCH: kernel launch or tensor-map creation failed";
     case MLA_ERR_PAGE: return "MLA_ERR_PAGE: a block-table entry outside the page pool";
+    case MLA_ERR_POOL: return "MLA_ERR_POOL: free-page list too short, or too small for the pages given back";
+    case MLA_ERR_SLOT: return "MLA_ERR_SLOT: a cache slot or draft index outside its range";
     case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT: a device pipeline wait gave up";
     case MLA_ERR_SEQLEN: return "MLA_ERR_SEQLEN: seq_lens[b] outside [q_len, Smax]";
     case MLA_ERR_ARG: return "MLA_ERR_ARG: invalid argument";
@@ -639,6 +660,8 @@ int mla_verify_attn_last_device_error(cudaStream_t stream) {
   if (v & mla::kStatusSeqLen) return MLA_ERR_SEQLEN;
   if (v & mla::kStatusTimeout) return MLA_ERR_DEVICE_TIMEOUT;
   if (v & mla::kStatusPage) return MLA_ERR_PAGE;
+  if (v & mla::kBitPool) return MLA_ERR_POOL;
+  if (v & mla::kBitSlot) return MLA_ERR_SLOT;
   return MLA_OK;
 }
 

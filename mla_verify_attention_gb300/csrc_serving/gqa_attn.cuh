@@ -1,0 +1,820 @@
+// Verify attention with grouped query heads on sm_103a: the kernels behind
+// mla_gqa_verify_attn and mla_gqa_verify_attn_paged (include/mla_verify_attn.h).
+//
+// Mathematics.  The G = H / Hkv query heads of a key head and the q_len drafts
+// of a stream are the rows of one dense product: S = Q K^T over the stream's
+// keys, tree mask on the last q_len of them, online softmax (running max m,
+// sum l, in log2 units), O = P V.  Keys and values are read once.
+//
+// What bounds it.  A key costs 4 D bytes and 4 D flops a row, so up to ~290
+// rows (measured bf16 rate over measured copy rate) the cache read is the
+// floor: the kernel is built to keep ~160 KB of loads in flight on every SM
+// and to let nothing else take longer than the tile's share of bandwidth
+// (32 KB at D = 128: ~1,500 cycles).
+//
+// Split.  The work is a sequence of 64-key tiles: streams, then key heads,
+// then row groups, then keys.  Every CTA of one persistent wave takes an equal
+// run of that sequence, computed on the device from seq_lens, so that ragged
+// batches balance to one tile and nothing is planned on the host.  A (stream,
+// head, row group) unit that lies within one run is written to `out`; one that
+// is cut leaves unnormalised partials (at most two a CTA, which bounds the
+// workspace by the grid) that gqa_combine_kernel merges in order.
+//
+// CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), one
+// issues tcgen05.mma, eight softmax warps in two groups own one accumulator O
+// each in tensor memory:
+//   up to 128 rows: both groups share the row tile and take the key tiles in
+//     turn; their two (m, l, O) are merged when the unit's run ends.
+//   more rows (kRows2): each group owns 128 of 256 rows, every tile feeds both.
+// S is double-buffered per group in tensor memory (2 x 64 columns); P replaces
+// S in place and is the A operand of O += P V.  O is only rescaled when a
+// row's max grows by more than 2^8.
+#pragma once
+#include <cuda.h>
+#include <math_constants.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mla {
+namespace gqa {
+
+constexpr int kKeys = 64;                  // keys a tile
+constexpr int kRows = 128;                 // rows a group's accumulator (MMA M)
+constexpr int kThreads = 384;              // 4 control warps + 2 x 4 softmax warps
+constexpr int kGatherThreads = 96;         // control warps 0, 2 and 3 load rows of odd pages
+constexpr int kGatherAhead = 3;            // stages in flight a gathering thread
+constexpr float kLazy = 8.0f;              // log2 units a row's max may grow before O is rescaled
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct Params {
+  const uint8_t* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  long long q_stride[3], k_stride[3], v_stride[3];   // bytes: batch, draft / row, head
+  const int32_t* seq_lens;
+  const uint32_t* mask;
+  const int32_t* block_table;      // null: contiguous caches
+  void* out;
+  float* lse;
+  int4* desc;                      // [grid] the cut unit each CTA starts: {stream, head | group, first slot, parts}
+  float2* part_ml;                 // [2 * grid][part_rows]
+  float4* part_o;                  // [2 * grid][D / 4][part_rows]
+  unsigned int* status;
+  int B, q_len, H, Hkv, G, Smax, groups, part_rows, min_tiles;
+  int max_blocks, page, pool_pages;
+  int box_rows;                    // rows a TMA box: 64 or a divisor that no page boundary cuts; 0: gather
+  int test_stall;
+  float scale_log2;
+};
+
+template <int D>
+struct Shape {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTile = kKeys * D * 2;          // bytes of a K or V tile
+  static constexpr int kQTile = kRows * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 10;    // 160 KB of K and V tiles
+  static constexpr int kRing = 2 * kStages * kTile;
+};
+
+template <int D, bool kRows2>
+struct __align__(1024) Smem {
+  uint8_t q[(kRows2 ? 2 : 1) * Shape<D>::kQTile];
+  uint8_t ring[Shape<D>::kRing];                       // stage s: K tile, V tile
+  float2 ml[2][kRows2 ? 1 : kRows];
+  uint64_t kfull[Shape<D>::kStages], kempty[Shape<D>::kStages];
+  uint64_t vfull[Shape<D>::kStages], vempty[Shape<D>::kStages];
+  uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];     // [group][buffer]
+  uint64_t qfull, qfree, ofull, ofree, mlx, drain;
+  long long total, start_pre;
+  long long warp_sum[kThreads / 32];
+  int start_b;
+  uint32_t tmem_base, abort_flag;
+};
+
+// ------------------------------------------------------------ instructions
+
+template <bool kBf16>
+__host__ __device__ constexpr uint32_t idesc(uint32_t N, uint32_t b_mn) {
+  return (1u << 4) | (kBf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Four K = 16 steps of one 64-wide chunk, A and B K-major in shared memory.
+__device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, p;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+
+// O (+)= P V over 64 keys: P in tensor memory (8 columns a K = 16 step), V
+// MN-major in shared memory (16 rows of 128 bytes a step).
+__device__ __forceinline__ void mma_ts_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, p;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int row, int chunk, int head,
+                                            int batch, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(chunk), "r"(head), "r"(batch), "r"(bar)
+      : "memory");
+}
+
+// 16 bytes to shared memory, or 16 zero bytes when !full.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool full) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (kBf16) return pack_bf16x2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------ waits
+
+// Bounded; gives up at once when another warp of the CTA has.
+template <class S>
+__device__ __noinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile uint32_t*>(&sm.abort_flag)) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      atomicOr(p.status, kBitTimeout);
+      *reinterpret_cast<volatile uint32_t*>(&sm.abort_flag) = 1u;
+      return false;
+    }
+  }
+}
+// By a whole converged warp; the result is warp-uniform.
+template <class S>
+__device__ __forceinline__ bool wait(S& sm, uint64_t& bar, uint32_t parity, const Params& p) {
+  bool ok = mbar_try_wait(smem_u32(&bar), parity);
+  if (!ok) ok = wait_slow(sm, smem_u32(&bar), parity, p);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// ------------------------------------------------------------ work
+
+// Key tiles of stream b; 0 for an unused stream and for one whose length is out of range.
+__device__ __forceinline__ int stream_tiles(const Params& p, int b, int& S) {
+  S = __ldg(p.seq_lens + b);
+  return S < p.q_len || S > p.Smax ? 0 : (S + kKeys - 1) / kKeys;
+}
+
+// A CTA's part of one unit.
+struct Segment {
+  int b, S, head, group, tile0, n, nt;   // tiles tile0 .. tile0 + n - 1 of the unit's nt
+};
+
+// Walks a CTA's run of tiles [t, t1); every role walks it on its own.
+struct Walk {
+  long long t, t1, pre;
+  int b, S, nt;
+  __device__ __forceinline__ Walk(const Params& p, long long t0, long long t1_, int b0, long long pre0)
+      : t(t0), t1(t1_), pre(pre0), b(b0), S(0), nt(0) {
+    if (t < t1) nt = stream_tiles(p, b, S);
+  }
+  __device__ __forceinline__ bool next(const Params& p, Segment& s) {
+    if (t >= t1) return false;
+    const int units = p.Hkv * p.groups;
+    while (t >= pre + static_cast<long long>(nt) * units) {
+      pre += static_cast<long long>(nt) * units;
+      nt = stream_tiles(p, ++b, S);
+    }
+    const int local = static_cast<int>(t - pre);
+    const int u = local / nt;
+    s.b = b;
+    s.S = S;
+    s.nt = nt;
+    s.tile0 = local - u * nt;
+    s.head = u / p.groups;
+    s.group = u - s.head * p.groups;
+    const long long left = t1 - t;
+    s.n = left < nt - s.tile0 ? static_cast<int>(left) : nt - s.tile0;
+    t += s.n;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int rows_of_group(const Params& p, int group, int span) {
+  return min(span, p.q_len * p.G - group * span);
+}
+
+// ------------------------------------------------------------ loads
+
+__device__ __forceinline__ int page_of(const Params& p, int b, int key) {
+  int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + key / p.page);
+  if (page < 0 || page >= p.pool_pages) {
+    atomicOr(p.status, kBitPage);
+    page = 0;
+  }
+  return page;
+}
+
+// Warp 0: K and V tiles by TMA.  A tile is one box of 64 rows, or boxes of
+// box_rows rows and 64 dims when pages are shorter than a tile, one a lane.
+template <int D, bool kRows2>
+__device__ __forceinline__ void load_tma(Smem<D, kRows2>& sm, const Params& p, const CUtensorMap* mk,
+                                         const CUtensorMap* mv, Walk w) {
+  using C = Shape<D>;
+  const int lane = threadIdx.x & 31;
+  const int R = p.box_rows, boxes = R == kKeys ? 1 : kKeys / R;   // boxes along the keys
+  const int my_box = lane % boxes, my_chunk = lane / boxes;
+  const bool mine = lane < boxes * (R == kKeys ? 1 : C::kChunks);
+  const uint32_t dst0 = my_chunk * (kKeys * 128) + my_box * R * 128;
+  int kt = 0, issued[2] = {0, 0};
+  bool ok = true;
+  Segment s;
+  while (ok && w.next(p, s)) {
+    auto row_of = [&](int j) {
+      const int key = (s.tile0 + j) * kKeys + my_box * R;
+      if (p.block_table == nullptr || !mine || j >= s.n || key >= s.S) return key;
+      const int page = page_of(p, s.b, key);
+      return page * p.page + key % p.page;
+    };
+    int row = row_of(0);
+    for (int j = 0; j < s.n; ++j, ++kt) {
+      const int stage = kt % C::kStages;
+      const uint32_t parity = ((kt / C::kStages) & 1) ^ 1;
+      const int left = s.S - (s.tile0 + j) * kKeys;              // keys of the stream from this tile on
+      const uint32_t bytes =
+          R == kKeys ? C::kTile : min(boxes, (left + R - 1) / R) * static_cast<uint32_t>(R) * D * 2;
+      const bool issue = mine && (R == kKeys || my_box * R < left);
+      const int row_next = row_of(j + 1);
+      const int batch = p.block_table == nullptr ? s.b : 0;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = wait(sm, kv ? sm.vempty[stage] : sm.kempty[stage], parity, p);
+        if (!ok) break;
+        if (p.test_stall && kv == 1 && kt == 0 && blockIdx.x == 0) continue;   // this load never comes
+        const uint32_t full = smem_u32(kv ? &sm.vfull[stage] : &sm.kfull[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        issued[kv] = kt + 1;
+        if (issue)
+          tma_load_5d(smem_u32(sm.ring) + stage * 2 * C::kTile + kv * C::kTile + dst0, kv ? mv : mk, 0, row, my_chunk,
+                      s.head, batch, full);
+      }
+      if (!ok) break;
+      row = row_next;
+    }
+  }
+  // The copies issued must have landed before the CTA may end.
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+    for (int n = issued[kv] - 1; n >= 0 && n >= issued[kv] - C::kStages; --n) {
+      if (p.test_stall && kv == 1 && n == 0 && blockIdx.x == 0) continue;
+      mbar_wait(smem_u32(kv ? &sm.vfull[n % C::kStages] : &sm.kfull[n % C::kStages]), (n / C::kStages) & 1, kWaitNs / 2);
+    }
+}
+
+// Control warps 0, 2 and 3 when no TMA box fits the pages (page_size not a
+// multiple of 8): rows copied 16 bytes a thread, into the layout the boxes
+// would leave; rows past the stream are zeros.
+template <int D, bool kRows2>
+__device__ __forceinline__ void load_gather(Smem<D, kRows2>& sm, const Params& p, Walk w, int tid) {
+  using C = Shape<D>;
+  constexpr int kUnits = kKeys * D / 8;        // 16-byte units of a tile
+  int kt = 0;
+  Segment s;
+  bool ok = true;
+  auto publish = [&](int n) {                  // tile n's copies of this thread have landed
+    fence_proxy_async_smem();
+    mbar_arrive(smem_u32(&sm.kfull[n % C::kStages]));
+    mbar_arrive(smem_u32(&sm.vfull[n % C::kStages]));
+  };
+  while (ok && w.next(p, s)) {
+    for (int j = 0; j < s.n; ++j, ++kt) {
+      const int stage = kt % C::kStages;
+      const uint32_t parity = ((kt / C::kStages) & 1) ^ 1;
+      ok = wait(sm, sm.kempty[stage], parity, p) && wait(sm, sm.vempty[stage], parity, p);
+      if (!ok) break;
+      const uint32_t dst = smem_u32(sm.ring) + stage * 2 * C::kTile;
+      const int k0 = (s.tile0 + j) * kKeys;
+      for (int i = tid; i < kUnits; i += kGatherThreads) {
+        const int r = i / (D / 8), u = i % (D / 8);
+        const int key = k0 + r;
+        const bool in = key < s.S;
+        long long row = 0;
+        if (in) row = static_cast<long long>(page_of(p, s.b, key)) * p.page + key % p.page;
+        const uint32_t off = (u >> 3) * (kKeys * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+        cp_async_16(dst + off, p.k + row * p.k_stride[1] + s.head * p.k_stride[2] + u * 16, in);
+        cp_async_16(dst + C::kTile + off, p.v + row * p.v_stride[1] + s.head * p.v_stride[2] + u * 16, in);
+      }
+      cp_async_commit();
+      if (kt >= kGatherAhead - 1) {
+        cp_async_wait<kGatherAhead - 1>();
+        if (!(p.test_stall && blockIdx.x == 0)) publish(kt - (kGatherAhead - 1));
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (ok && !(p.test_stall && blockIdx.x == 0))
+    for (int n = max(0, kt - (kGatherAhead - 1)); n < kt; ++n) publish(n);
+}
+
+// ------------------------------------------------------------ products
+
+// Warp 1.  A segment's tasks are its tiles (both groups in turn), or with
+// kRows2 each tile for each group.  S of a task is computed `ahead` tasks
+// before its P V, so that the softmax warps always have the next S waiting.
+template <int D, bool kBf16, bool kRows2>
+__device__ __forceinline__ void products(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
+  using C = Shape<D>;
+  constexpr uint32_t kIdQK = idesc<kBf16>(kKeys, 0), kIdPV = idesc<kBf16>(D, 1);
+  const uint32_t ring = smem_u32(sm.ring), qs = smem_u32(sm.q);
+  int kt = 0, seg = 0;                         // tiles and segments before this segment
+  int ns[2] = {0, 0}, np[2] = {0, 0};          // S and P V tasks of each group so far
+  Segment s;
+  while (w.next(p, s)) {
+    const bool two = kRows2 ? rows_of_group(p, s.group, 2 * kRows) > kRows : true;   // both groups take part
+    const int per_tile = kRows2 && two ? 2 : 1;
+    const int tasks = s.n * per_tile;
+    const int ahead = two ? 2 : 1;
+    if (!wait(sm, sm.qfull, seg & 1, p)) return;
+    tc_fence_after();
+    for (int x = 0; x < tasks + ahead; ++x) {
+      if (x < tasks) {
+        const int g = two ? x & 1 : 0;
+        const int tile = kt + (per_tile == 2 ? x >> 1 : x), stage = tile % C::kStages;
+        const int n = g ? ns[1]++ : ns[0]++;
+        if (!wait(sm, sm.pvdone[g][n & 1], ((n >> 1) & 1) ^ 1, p)) return;
+        if (!wait(sm, sm.kfull[stage], (tile / C::kStages) & 1, p)) return;
+        tc_fence_after();
+        const uint32_t d = tmem + 256 + (2 * g + (n & 1)) * kKeys;
+        const uint64_t a = sdesc_sw128(qs + (kRows2 ? g * C::kQTile : 0), 16, 1024);
+        const uint64_t b = sdesc_sw128(ring + stage * 2 * C::kTile, 16, 1024);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          mma_ss_chunk(d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), kIdQK, c != 0);
+        mma_commit_elect(smem_u32(&sm.sfull[g][n & 1]));
+        if (per_tile == 1 || g == 1) mma_commit_elect(smem_u32(&sm.kempty[stage]));
+        if (x == tasks - 1) mma_commit_elect(smem_u32(&sm.qfree));
+      }
+      if (x >= ahead) {
+        const int y = x - ahead;
+        const int g = two ? y & 1 : 0;
+        const int tile = kt + (per_tile == 2 ? y >> 1 : y), stage = tile % C::kStages;
+        const int n = g ? np[1]++ : np[0]++;
+        const bool first = two ? y < 2 : y == 0;         // this group's first of the segment: O starts at 0
+        if (first && seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
+        if (!wait(sm, sm.vfull[stage], (tile / C::kStages) & 1, p)) return;
+        if (!wait(sm, sm.pfull[g][n & 1], (n >> 1) & 1, p)) return;
+        tc_fence_after();
+        mma_ts_pv(tmem + g * D, tmem + 256 + (2 * g + (n & 1)) * kKeys,
+                  sdesc_sw128(ring + stage * 2 * C::kTile + C::kTile, kKeys * 128, 1024), kIdPV, first ? 0u : 1u);
+        mma_commit_elect(smem_u32(&sm.pvdone[g][n & 1]));
+        if (per_tile == 1 || g == 1) mma_commit_elect(smem_u32(&sm.vempty[stage]));
+      }
+    }
+    mma_commit_elect(smem_u32(&sm.ofull));
+    kt += s.n;
+    ++seg;
+  }
+}
+
+// ------------------------------------------------------------ softmax
+
+// One row's result, columns c .. c + 31: fp32 to the partials or rounded to `out`.
+template <int D, bool kBf16>
+__device__ __forceinline__ void store_block(const Params& p, const float* o, int c, bool direct, long long out_row,
+                                            int slot, int rr) {
+  if (direct) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + out_row * (D * 2) + c * 2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      dst[e] = make_uint4(pack2<kBf16>(o[8 * e], o[8 * e + 1]), pack2<kBf16>(o[8 * e + 2], o[8 * e + 3]),
+                          pack2<kBf16>(o[8 * e + 4], o[8 * e + 5]), pack2<kBf16>(o[8 * e + 6], o[8 * e + 7]));
+  } else {
+    float4* dst = p.part_o + (static_cast<size_t>(slot) * (D / 4) + c / 4) * p.part_rows + rr;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      dst[static_cast<size_t>(e) * p.part_rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  }
+}
+
+// Warps 4..11: group g = 0, 1, warp wq of the group, one row a thread.
+template <int D, bool kBf16, bool kRows2>
+__device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w, int g, int wq,
+                                        int lane) {
+  using C = Shape<D>;
+  constexpr int kSpan = kRows2 ? 2 * kRows : kRows;        // rows a unit
+  // fp16 weights are kept 2^7 larger: the largest, 2^(8 + 7), is in range and
+  // the smallest that is not rounded to a subnormal is 2^-14 / 2^7 of a row's
+  // largest weight or more.  bf16 has fp32's range.
+  constexpr float kShift = kBf16 ? 0.f : 7.f;
+  const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+  const int r = wq * 32 + lane;
+  const uint32_t o_t = tmem + lanes + g * D;
+  const float a = p.scale_log2;
+  const bool pos = a > 0.f;
+  const float a_eff = pos ? a : 1.f;
+  int kt = 0, seg = 0, n = 0;                              // n: tasks of this group so far
+  Segment s;
+  while (w.next(p, s)) {
+    const int rows = rows_of_group(p, s.group, kSpan);
+    const int row0 = s.group * kSpan + (kRows2 ? g * kRows : 0);
+    const int mine = kRows2 ? rows - g * kRows : rows;     // valid rows of this group's tile
+    const bool two = kRows2 ? rows > kRows : true;
+    const int R = row0 + r;                                // row of the stream and head: draft * G + head in group
+    const bool valid = r < mine;
+    const bool warp_valid = wq * 32 < mine;
+    const int i = R / p.G;
+    const int head = s.head * p.G + (R - i * p.G);
+    // ---- Q rows into the swizzled tile.  (All rows of a shared tile are
+    // loaded by both groups, half each.)
+    if (seg > 0 && !wait(sm, sm.qfree, (seg - 1) & 1, p)) return;
+    {
+      const long long base = valid ? s.b * p.q_stride[0] + i * p.q_stride[1] + head * p.q_stride[2] : 0;
+      constexpr int kPer = 32 / (D / 8);                   // rows a warp loads at once
+      constexpr int kLoads = (kRows2 ? 32 : 16) / kPer;
+      uint8_t* tile = sm.q + (kRows2 ? g * C::kQTile : 0);
+      uint4 x[kLoads];
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int rl = (kRows2 ? 0 : g * 16) + e * kPer + lane / (D / 8);   // row within the warp's 32
+        const long long off = __shfl_sync(0xFFFFFFFFu, base, rl);
+        if (wq * 32 + rl < mine) x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + off) + lane % (D / 8));
+      }
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int row = wq * 32 + (kRows2 ? 0 : g * 16) + e * kPer + lane / (D / 8);
+        const int u = lane % (D / 8);
+        if (row < mine)
+          *reinterpret_cast<uint4*>(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = x[e];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
+    }
+    uint64_t mask64 = 0;
+    if (valid) {
+      const int words = (p.q_len + 31) >> 5;
+      const uint32_t* mrow = p.mask + (static_cast<size_t>(s.b) * p.q_len + i) * words;
+      mask64 = mrow[0];
+      if (words > 1) mask64 |= static_cast<uint64_t>(mrow[1]) << 32;
+      if (p.q_len < 64) mask64 &= (1ull << p.q_len) - 1ull;
+    }
+    const int prefix = s.S - p.q_len;
+    float m = -CUDART_INF_F, l = 0.f;
+    const int j0 = kRows2 ? 0 : g, step = kRows2 ? 1 : 2;
+    for (int j = j0; j < s.n && (two || g == 0); j += step, ++n) {
+      const int buf = n & 1;
+      const uint32_t s_t = tmem + lanes + 256 + (2 * g + buf) * kKeys;
+      if (!wait(sm, sm.sfull[g][buf], (n >> 1) & 1, p)) return;
+      const int k0 = (s.tile0 + j) * kKeys;
+      if (warp_valid) {
+        tc_fence_after();
+        uint32_t sr[64];
+        MLA_TMEM_LD_32x32b_X32(s_t, sr);
+        MLA_TMEM_LD_32x32b_X32(s_t + 32, (sr + 32));
+        tmem_ld_wait();
+        if (!pos) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a);
+        }
+        if (k0 + kKeys > prefix) {
+          const int np = prefix - k0;                      // prefix keys of this tile (may be <= 0)
+          uint64_t vis = np > 0 ? (1ull << np) - 1ull : 0ull;      // (np < 64 here)
+          vis |= np > 0 ? mask64 << np : (-np < 64 ? mask64 >> (-np) : 0ull);
+          const uint32_t lo = static_cast<uint32_t>(vis), hi = static_cast<uint32_t>(vis >> 32);
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!(((c < 32 ? lo : hi) >> (c & 31)) & 1u)) sr[c] = __float_as_uint(-CUDART_INF_F);
+        }
+        float mx[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sr[e]);
+#pragma unroll
+        for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a_eff;
+        const bool grow = mt > m + kLazy;
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float alpha = grow ? ex2(m - mt) : 1.f;    // 0 when nothing was visible before
+          if (grow) m = mt;
+          l *= alpha;
+          if (j > j0) {
+            // O holds tiles up to the previous one of this group, once its product is done.
+            if (!wait(sm, sm.pvdone[g][(n - 1) & 1], ((n - 1) >> 1) & 1, p)) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              MLA_TMEM_LD_32x32b_X32(o_t + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              MLA_TMEM_ST_32x32b_X32(o_t + c, o);
+            }
+          }
+        }
+        const float msub = m == -CUDART_INF_F ? 0.f : m - kShift;
+        const uint64_t a2 = f2pack(a_eff, a_eff), m2 = f2pack(-msub, -msub);
+        uint64_t sum[2] = {0ull, 0ull};
+        uint32_t pw[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float x0, x1;
+          f2unpack(ffma2(f2pack(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), a2, m2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          sum[c & 1] = fadd2(sum[c & 1], f2pack(p0, p1));
+          pw[c] = pack2<kBf16>(p0, p1);
+        }
+        MLA_TMEM_ST_32x32b_X32(s_t, pw);
+        float s0, s1, s2, s3;
+        f2unpack(sum[0], s0, s1);
+        f2unpack(sum[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      if (k0 + kKeys > s.S && (!kRows2 || g == 0)) {
+        // Rows past the stream may hold anything: P is 0 there, but 0 * NaN is not.
+        const int stage = (kt + j) % C::kStages;
+        if (!wait(sm, sm.vfull[stage], ((kt + j) / C::kStages) & 1, p)) return;
+        const int z0 = s.S - k0, nz = kKeys - z0;
+        uint8_t* tile = sm.ring + stage * 2 * C::kTile + C::kTile;
+        for (int it = r; it < nz * (D / 8); it += kRows) {
+          const int rr = z0 + it / (D / 8), u = it % (D / 8);
+          *reinterpret_cast<uint4*>(tile + (u >> 3) * (kKeys * 128) + rr * 128 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[g][buf]));
+    }
+
+    // ---- end of the segment
+    const bool direct = s.n == s.nt;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
+    const int rr = (kRows2 ? g * kRows : 0) + r;
+    const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head;
+    float m_off = m == -CUDART_INF_F ? -CUDART_INF_F : m - kShift;
+    float w0 = 1.f, w1 = 0.f;                              // weights of the groups' accumulators
+    if (!kRows2) {
+      sm.ml[g][r] = make_float2(m_off, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.mlx));
+      if (!wait(sm, sm.mlx, seg & 1, p)) return;
+      const float2 x0 = sm.ml[0][r], x1 = sm.ml[1][r];
+      const float mt = fmaxf(x0.x, x1.x);
+      w0 = x0.x == -CUDART_INF_F ? 0.f : ex2(x0.x - mt);
+      w1 = x1.x == -CUDART_INF_F ? 0.f : ex2(x1.x - mt);
+      l = w0 * x0.y + w1 * x1.y;
+      m_off = mt;
+    }
+    if (!wait(sm, sm.ofull, seg & 1, p)) return;
+    if (warp_valid) {
+      tc_fence_after();
+      if (direct) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+      }
+      const int c0 = kRows2 ? 0 : g * (D / 2), c1 = kRows2 ? D : c0 + D / 2;
+      const uint32_t o0 = tmem + lanes + (kRows2 ? g * D : 0);
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 32) {
+        uint32_t x0[32];
+        float o[32];
+        MLA_TMEM_LD_32x32b_X32(o0 + c, x0);
+        if (!kRows2 && s.n > 1) {
+          uint32_t x1[32];
+          MLA_TMEM_LD_32x32b_X32(o0 + D + c, x1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = w0 * __uint_as_float(x0[e]) + w1 * __uint_as_float(x1[e]);
+        } else {
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = w0 * __uint_as_float(x0[e]);
+        }
+        if (valid) store_block<D, kBf16>(p, o, c, direct, out_row, slot, rr);
+      }
+      if (valid && (kRows2 || g == 0)) {
+        if (direct)
+          p.lse[out_row] = l > 0.f ? (m_off + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+        else
+          p.part_ml[static_cast<size_t>(slot) * p.part_rows + rr] = make_float2(m_off, l);
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.ofree));
+    kt += s.n;
+    ++seg;
+  }
+}
+
+// ------------------------------------------------------------ kernel
+
+// Tells the merge of the cut unit that starts in this CTA's run, if there is
+// one: it goes on in the CTAs after this one.  Written before the first wait,
+// so that the merge finds it whatever becomes of the loads.
+__device__ __forceinline__ void note_cut_unit(const Params& p, Walk w, long long t1, long long total, long long ctas) {
+  int4 d = make_int4(0, 0, 0, 0);
+  Segment s;
+  int segs = 0;
+  while (w.next(p, s)) ++segs;
+  if (segs > 0 && s.tile0 == 0 && s.n < s.nt) {
+    const long long end = t1 - s.n + s.nt;                 // past the unit's last tile
+    const long long last = (end * ctas - 1) / total;       // the CTA that has it
+    d = make_int4(s.b, s.head * p.groups + s.group, 2 * static_cast<int>(blockIdx.x) + (segs > 1 ? 1 : 0),
+                  static_cast<int>(last - blockIdx.x) + 1);
+  }
+  p.desc[blockIdx.x] = d;
+}
+
+template <int D, bool kBf16, bool kRows2>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
+  using S = Smem<D, kRows2>;
+  using C = Shape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  if (tid == 0) {
+    grid_launch_dependents();
+    if (p.box_rows) {
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+    }
+    const uint32_t loaders = p.box_rows ? 1 : kGatherThreads;
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(smem_u32(&sm.kfull[i]), loaders);
+      mbar_init(smem_u32(&sm.vfull[i]), loaders);
+      mbar_init(smem_u32(&sm.kempty[i]), 1);
+      mbar_init(smem_u32(&sm.vempty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sm.sfull[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&sm.pfull[i >> 1][i & 1]), 4);
+      mbar_init(smem_u32(&sm.pvdone[i >> 1][i & 1]), 1);
+    }
+    mbar_init(smem_u32(&sm.qfull), 8);
+    mbar_init(smem_u32(&sm.qfree), 1);
+    mbar_init(smem_u32(&sm.ofull), 1);
+    mbar_init(smem_u32(&sm.ofree), 8);
+    mbar_init(smem_u32(&sm.mlx), 8);
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort_flag = 0;
+    sm.start_b = 0;
+    sm.start_pre = 0;
+    fence_mbarrier_init_cluster();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+
+  // ---- this CTA's run of tiles: each thread sums a run of streams, then a
+  // scan over threads; the thread whose streams hold the first tile says which.
+  const int units = p.Hkv * p.groups;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long sum = 0;
+  int len;
+  for (int b = b0; b < b1; ++b) {
+    sum += static_cast<long long>(stream_tiles(p, b, len)) * units;
+    if (blockIdx.x == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) sm.warp_sum[warp] = inc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i == warp) before = total;
+    total += sm.warp_sum[i];
+  }
+  long long ctas = total / p.min_tiles;
+  ctas = ctas < 1 ? 1 : (ctas < gridDim.x ? ctas : gridDim.x);
+  const long long t0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+  const long long t1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+  before += inc - sum;
+  if (t0 >= before && t0 < before + sum) {
+    int b = b0;
+    while (true) {
+      const long long n = static_cast<long long>(stream_tiles(p, b, len)) * units;
+      if (t0 < before + n) break;
+      before += n;
+      ++b;
+    }
+    sm.start_b = b;
+    sm.start_pre = before;
+  }
+  __syncthreads();
+  const uint32_t tmem = sm.tmem_base;
+  const Walk walk(p, t0, t1, sm.start_b, sm.start_pre);
+
+  if (p.box_rows == 0 && (warp == 0 || warp == 2 || warp == 3)) {
+    load_gather<D, kRows2>(sm, p, walk, warp == 0 ? lane : (warp - 1) * 32 + lane);
+  } else if (warp == 0) {
+    load_tma<D, kRows2>(sm, p, &map_k, &map_v, walk);
+  } else if (warp == 1) {
+    if (lane == 0) note_cut_unit(p, walk, t1, total, ctas);
+    __syncwarp();
+    products<D, kBf16, kRows2>(sm, p, tmem, walk);
+    mma_commit_elect(smem_u32(&sm.drain));
+    mbar_wait(smem_u32(&sm.drain), 0, kWaitNs);
+    __syncwarp();
+  } else if (warp >= 4) {
+    softmax<D, kBf16, kRows2>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
+  }
+  // Streams without keys.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (stream_tiles(p, b, len) != 0) continue;
+    const long long rows = static_cast<long long>(p.q_len) * p.H;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + b * rows * (D * 2));
+    for (long long x = tid; x < rows * (D / 8); x += kThreads) o[x] = make_uint4(0, 0, 0, 0);
+    for (long long x = tid; x < rows; x += kThreads) p.lse[b * rows + x] = -CUDART_INF_F;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merges the partials of each cut unit: block (x, c) takes eight rows of the
+// unit that CTA c of the split kernel started.  Its parts are that CTA's slot
+// and the first slots of the CTAs after it, merged in that order.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(2 * D) combine_kernel(const Params p) {
+  grid_dependency_wait();
+  const int4 d = p.desc[blockIdx.y];
+  if (d.w == 0) return;
+  const int span = p.part_rows;
+  const int head = d.y / p.groups, group = d.y - head * p.groups;
+  const int full = p.q_len * p.G > kRows ? 2 * kRows : kRows;
+  const int rr = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x & 7);
+  const int c4 = threadIdx.x >> 3;
+  const int R = group * full + rr;
+  if (rr >= full || R >= p.q_len * p.G) return;
+  const int next = 2 * (static_cast<int>(blockIdx.y) + 1);
+  float m = -CUDART_INF_F;
+  for (int k = 0; k < d.w; ++k)
+    m = fmaxf(m, p.part_ml[static_cast<size_t>(k ? next + 2 * (k - 1) : d.z) * span + rr].x);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < d.w; ++k) {
+    const size_t slot = k ? next + 2 * (k - 1) : d.z;
+    const float2 ml = p.part_ml[slot * span + rr];
+    const float4 x = p.part_o[(slot * (D / 4) + c4) * span + rr];
+    const float w = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - m);
+    l += w * ml.y;
+    o.x += w * x.x;
+    o.y += w * x.y;
+    o.z += w * x.z;
+    o.w += w * x.w;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int i = R / p.G;
+  const long long row = (static_cast<long long>(d.x) * p.q_len + i) * p.H + head * p.G + (R - i * p.G);
+  reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (D * 2))[c4] =
+      make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
+  if (c4 == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+}
+
+}  // namespace gqa
+}  // namespace mla
