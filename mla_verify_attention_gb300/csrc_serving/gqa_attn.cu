@@ -19,6 +19,8 @@ namespace gqa {
 constexpr int kMaxDevices = 64;
 // Fewest tiles a CTA takes: below that, fewer CTAs share a short call's work.
 constexpr int kMinTiles = 2;
+// Parts a unit from which four part groups share the merge of a row.
+constexpr int kManyParts = 32;
 
 struct Plan {
   bool rows2;          // more than 128 rows a key head: two row tiles a CTA
@@ -41,6 +43,9 @@ Plan plan(int q, int H, int Hkv) {
   return p;
 }
 
+// One persistent CTA an SM.
+int cta_count(const DeviceCommon& d) { return d.sms < kMaxParts ? d.sms : kMaxParts; }
+
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
@@ -60,14 +65,14 @@ using CombineFn = void (*)(Params);
 
 struct Variant {
   AttnFn attn;
-  CombineFn combine;
+  CombineFn combine[2];   // one part group; four
   size_t smem;
 };
 template <int D, bool kBf16, bool kRows2>
 Variant variant() {
   constexpr size_t smem = sizeof(Smem<D, kRows2>) + 1024;   // + manual 1 KB alignment
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16, kRows2>, combine_kernel<D, kBf16>, smem};
+  return {attn_kernel<D, kBf16, kRows2>, {combine_kernel<D, kBf16, 1>, combine_kernel<D, kBf16, 4>}, smem};
 }
 
 std::mutex g_ready_mutex;
@@ -167,7 +172,7 @@ int run(const Call& c) {
   DeviceCommon d;
   st = device_common(&d);
   if (st != MLA_OK) return st;
-  const int grid = d.sms;
+  const int grid = cta_count(d);
   const Layout lay = layout(pl, grid, c.D);
   if (!c.workspace || c.workspace_bytes < lay.bytes) return MLA_ERR_WORKSPACE;
   Variant var;
@@ -230,10 +235,12 @@ int run(const Call& c) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }
+  // Few units: each is cut into many parts.
+  const bool many = static_cast<long long>(c.B) * c.Hkv * pl.groups * kManyParts <= grid;
   cfg.gridDim = dim3(pl.part_rows / 8, grid, 1);
-  cfg.blockDim = dim3(2 * c.D, 1, 1);
+  cfg.blockDim = dim3(2 * c.D * (many ? 4 : 1), 1, 1);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, var.combine, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, var.combine[many ? 1 : 0], p) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }
@@ -250,7 +257,7 @@ size_t mla_gqa_workspace_size(int B, int q_len, int H, int Hkv, int D) {
   if (!gqa::shape_ok(B, q_len, H, Hkv, D)) return 0;
   DeviceCommon d;
   if (device_common(&d) != MLA_OK) return 0;
-  return gqa::layout(gqa::plan(q_len, H, Hkv), d.sms, D).bytes;
+  return gqa::layout(gqa::plan(q_len, H, Hkv), gqa::cta_count(d), D).bytes;
 }
 
 int mla_gqa_verify_attn(const void* q, const void* k, const void* v, const int64_t* strides,

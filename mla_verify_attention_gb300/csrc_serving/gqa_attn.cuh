@@ -20,8 +20,8 @@
 // is cut leaves unnormalised partials (at most two a CTA, which bounds the
 // workspace by the grid) that gqa_combine_kernel merges in order.
 //
-// CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), one
-// issues tcgen05.mma, eight softmax warps in two groups own one accumulator O
+// CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), two
+// issue tcgen05.mma, eight softmax warps in two groups own one accumulator O
 // each in tensor memory:
 //   up to 128 rows: both groups share the row tile and take the key tiles in
 //     turn; their two (m, l, O) are merged when the unit's run ends.
@@ -44,7 +44,7 @@ namespace gqa {
 constexpr int kKeys = 64;                  // keys a tile
 constexpr int kRows = 128;                 // rows a group's accumulator (MMA M)
 constexpr int kThreads = 384;              // 4 control warps + 2 x 4 softmax warps
-constexpr int kGatherThreads = 96;         // control warps 0, 2 and 3 load rows of odd pages
+constexpr int kGatherThreads = 64;         // control warps 0 and 2 load rows of odd pages
 constexpr int kGatherAhead = 3;            // stages in flight a gathering thread
 constexpr float kLazy = 8.0f;              // log2 units a row's max may grow before O is rescaled
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -87,7 +87,7 @@ struct __align__(1024) Smem {
   uint64_t kfull[Shape<D>::kStages], kempty[Shape<D>::kStages];
   uint64_t vfull[Shape<D>::kStages], vempty[Shape<D>::kStages];
   uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];     // [group][buffer]
-  uint64_t qfull, qfree, ofull, ofree, mlx, drain;
+  uint64_t qfull, qfree, ofull, ofree, mlx, drain[2];
   long long total, start_pre;
   long long warp_sum[kThreads / 32];
   int start_b;
@@ -296,7 +296,7 @@ __device__ __forceinline__ void load_tma(Smem<D, kRows2>& sm, const Params& p, c
     }
 }
 
-// Control warps 0, 2 and 3 when no TMA box fits the pages (page_size not a
+// Control warps 0 and 2 when no TMA box fits the pages (page_size not a
 // multiple of 8): rows copied 16 bytes a thread, into the layout the boxes
 // would leave; rows past the stream are zeros.
 template <int D, bool kRows2>
@@ -343,57 +343,81 @@ __device__ __forceinline__ void load_gather(Smem<D, kRows2>& sm, const Params& p
 
 // ------------------------------------------------------------ products
 
-// Warp 1.  A segment's tasks are its tiles (both groups in turn), or with
-// kRows2 each tile for each group.  S of a task is computed `ahead` tasks
-// before its P V, so that the softmax warps always have the next S waiting.
+// A segment's tasks are its tiles (the groups in turn), or with kRows2 each
+// tile for each group.  Issuing one task's products takes a warp 400 to 600
+// cycles (waits, descriptors, commits), as long as the tensor pipe needs for
+// them; S = Q K^T and O += P V are therefore issued by a warp each, and run
+// apart by as many tasks as there are S buffers.
+struct Task {
+  int g, tile;       // group, tile within the segment
+  bool last_use;     // the tile's last task
+};
+template <bool kRows2>
+__device__ __forceinline__ Task task_of(int x, bool two) {
+  if (!kRows2) return {x & 1, x, true};
+  return two ? Task{x & 1, x >> 1, (x & 1) != 0} : Task{0, x, true};
+}
+
+// Warp 1: S of every task.
 template <int D, bool kBf16, bool kRows2>
-__device__ __forceinline__ void products(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
+__device__ __forceinline__ void products_qk(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
   using C = Shape<D>;
-  constexpr uint32_t kIdQK = idesc<kBf16>(kKeys, 0), kIdPV = idesc<kBf16>(D, 1);
-  const uint32_t ring = smem_u32(sm.ring), qs = smem_u32(sm.q);
+  constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
+  const uint64_t q0 = sdesc_sw128(smem_u32(sm.q), 16, 1024), k0 = sdesc_sw128(smem_u32(sm.ring), 16, 1024);
   int kt = 0, seg = 0;                         // tiles and segments before this segment
-  int ns[2] = {0, 0}, np[2] = {0, 0};          // S and P V tasks of each group so far
+  int done[2] = {0, 0};                        // tasks of each group so far
   Segment s;
   while (w.next(p, s)) {
-    const bool two = kRows2 ? rows_of_group(p, s.group, 2 * kRows) > kRows : true;   // both groups take part
-    const int per_tile = kRows2 && two ? 2 : 1;
-    const int tasks = s.n * per_tile;
-    const int ahead = two ? 2 : 1;
+    const bool two = kRows2 && rows_of_group(p, s.group, 2 * kRows) > kRows;
+    const int tasks = two ? 2 * s.n : s.n;
     if (!wait(sm, sm.qfull, seg & 1, p)) return;
-    tc_fence_after();
-    for (int x = 0; x < tasks + ahead; ++x) {
-      if (x < tasks) {
-        const int g = two ? x & 1 : 0;
-        const int tile = kt + (per_tile == 2 ? x >> 1 : x), stage = tile % C::kStages;
-        const int n = g ? ns[1]++ : ns[0]++;
-        if (!wait(sm, sm.pvdone[g][n & 1], ((n >> 1) & 1) ^ 1, p)) return;
-        if (!wait(sm, sm.kfull[stage], (tile / C::kStages) & 1, p)) return;
-        tc_fence_after();
-        const uint32_t d = tmem + 256 + (2 * g + (n & 1)) * kKeys;
-        const uint64_t a = sdesc_sw128(qs + (kRows2 ? g * C::kQTile : 0), 16, 1024);
-        const uint64_t b = sdesc_sw128(ring + stage * 2 * C::kTile, 16, 1024);
+    for (int x = 0; x < tasks; ++x) {
+      const Task t = task_of<kRows2>(x, two);
+      const int stage = (kt + t.tile) % C::kStages;
+      const int n = t.g ? done[1]++ : done[0]++;
+      if (!wait(sm, sm.pvdone[t.g][n & 1], ((n >> 1) & 1) ^ 1, p)) return;
+      if (!wait(sm, sm.kfull[stage], ((kt + t.tile) / C::kStages) & 1, p)) return;
+      tc_fence_after();
+      const uint32_t d = tmem + 256 + (2 * t.g + (n & 1)) * kKeys;
+      const uint64_t a = q0 + (kRows2 ? t.g * (C::kQTile >> 4) : 0), b = k0 + stage * (2 * C::kTile >> 4);
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
-          mma_ss_chunk(d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), kIdQK, c != 0);
-        mma_commit_elect(smem_u32(&sm.sfull[g][n & 1]));
-        if (per_tile == 1 || g == 1) mma_commit_elect(smem_u32(&sm.kempty[stage]));
-        if (x == tasks - 1) mma_commit_elect(smem_u32(&sm.qfree));
-      }
-      if (x >= ahead) {
-        const int y = x - ahead;
-        const int g = two ? y & 1 : 0;
-        const int tile = kt + (per_tile == 2 ? y >> 1 : y), stage = tile % C::kStages;
-        const int n = g ? np[1]++ : np[0]++;
-        const bool first = two ? y < 2 : y == 0;         // this group's first of the segment: O starts at 0
-        if (first && seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
-        if (!wait(sm, sm.vfull[stage], (tile / C::kStages) & 1, p)) return;
-        if (!wait(sm, sm.pfull[g][n & 1], (n >> 1) & 1, p)) return;
-        tc_fence_after();
-        mma_ts_pv(tmem + g * D, tmem + 256 + (2 * g + (n & 1)) * kKeys,
-                  sdesc_sw128(ring + stage * 2 * C::kTile + C::kTile, kKeys * 128, 1024), kIdPV, first ? 0u : 1u);
-        mma_commit_elect(smem_u32(&sm.pvdone[g][n & 1]));
-        if (per_tile == 1 || g == 1) mma_commit_elect(smem_u32(&sm.vempty[stage]));
-      }
+      for (int c = 0; c < C::kChunks; ++c)
+        mma_ss_chunk(d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), kId, c != 0);
+      mma_commit_elect(smem_u32(&sm.sfull[t.g][n & 1]));
+      if (t.last_use) mma_commit_elect(smem_u32(&sm.kempty[stage]));
+      if (x == tasks - 1) mma_commit_elect(smem_u32(&sm.qfree));
+    }
+    kt += s.n;
+    ++seg;
+  }
+}
+
+// Warp 3: O += P V of every task.
+template <int D, bool kBf16, bool kRows2>
+__device__ __forceinline__ void products_pv(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
+  using C = Shape<D>;
+  constexpr uint32_t kId = idesc<kBf16>(D, 1);
+  const uint64_t v0 = sdesc_sw128(smem_u32(sm.ring) + C::kTile, kKeys * 128, 1024);
+  int kt = 0, seg = 0;
+  int done[2] = {0, 0};
+  Segment s;
+  while (w.next(p, s)) {
+    const bool two = kRows2 && rows_of_group(p, s.group, 2 * kRows) > kRows;
+    const int tasks = two ? 2 * s.n : s.n;
+    // The last segment's results have been read out of both accumulators.
+    if (seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
+    for (int x = 0; x < tasks; ++x) {
+      const Task t = task_of<kRows2>(x, two);
+      const int stage = (kt + t.tile) % C::kStages;
+      const int n = t.g ? done[1]++ : done[0]++;
+      const bool first = kRows2 ? t.tile == 0 : x < 2;     // the group's first of the segment: O starts at 0
+      if (!wait(sm, sm.vfull[stage], ((kt + t.tile) / C::kStages) & 1, p)) return;
+      if (!wait(sm, sm.pfull[t.g][n & 1], (n >> 1) & 1, p)) return;
+      tc_fence_after();
+      mma_ts_pv(tmem + t.g * D, tmem + 256 + (2 * t.g + (n & 1)) * kKeys, v0 + stage * (2 * C::kTile >> 4), kId,
+                first ? 0u : 1u);
+      mma_commit_elect(smem_u32(&sm.pvdone[t.g][n & 1]));
+      if (t.last_use) mma_commit_elect(smem_u32(&sm.vempty[stage]));
     }
     mma_commit_elect(smem_u32(&sm.ofull));
     kt += s.n;
@@ -421,6 +445,41 @@ __device__ __forceinline__ void store_block(const Params& p, const float* o, int
   }
 }
 
+// A segment's Q rows into the swizzled tile, by all softmax warps: each group
+// its own tile, or half the rows of each warp's 32 when the groups share one.
+template <int D, bool kRows2>
+__device__ __forceinline__ void load_q(Smem<D, kRows2>& sm, const Params& p, const Segment& s, int g, int wq, int lane) {
+  using C = Shape<D>;
+  constexpr int kSpan = kRows2 ? 2 * kRows : kRows;
+  constexpr int kUnits = D / 8;                            // 16-byte units a row
+  constexpr int kPer = 32 / kUnits;                        // rows a warp loads at once
+  constexpr int kLoads = (kRows2 ? 32 : 16) / kPer;
+  const int mine = rows_of_group(p, s.group, kSpan) - (kRows2 ? g * kRows : 0);
+  const int R = s.group * kSpan + (kRows2 ? g * kRows : 0) + wq * 32 + lane;
+  const int i = R / p.G;
+  // Each lane knows its row's address; the lanes that load a row ask for it.
+  const long long base = wq * 32 + lane < mine ? s.b * p.q_stride[0] + i * p.q_stride[1] +
+                                                     (s.head * p.G + (R - i * p.G)) * p.q_stride[2]
+                                               : 0;
+  uint8_t* const tile = sm.q + (kRows2 ? g * C::kQTile : 0);
+  const int r0 = (kRows2 ? 0 : g * 16) + lane / kUnits, u = lane % kUnits;
+  uint4 x[kLoads];
+#pragma unroll
+  for (int e = 0; e < kLoads; ++e) {
+    const long long off = __shfl_sync(0xFFFFFFFFu, base, r0 + e * kPer);
+    if (wq * 32 + r0 + e * kPer < mine) x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + off) + u);
+  }
+#pragma unroll
+  for (int e = 0; e < kLoads; ++e) {
+    const int row = wq * 32 + r0 + e * kPer;
+    if (row < mine)
+      *reinterpret_cast<uint4*>(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = x[e];
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
+}
+
 // Warps 4..11: group g = 0, 1, warp wq of the group, one row a thread.
 template <int D, bool kBf16, bool kRows2>
 __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w, int g, int wq,
@@ -438,8 +497,10 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
   const bool pos = a > 0.f;
   const float a_eff = pos ? a : 1.f;
   int kt = 0, seg = 0, n = 0;                              // n: tasks of this group so far
-  Segment s;
-  while (w.next(p, s)) {
+  Segment s, next;
+  bool more = w.next(p, s);
+  if (more) load_q<D, kRows2>(sm, p, s, g, wq, lane);
+  for (; more; s = next) {
     const int rows = rows_of_group(p, s.group, kSpan);
     const int row0 = s.group * kSpan + (kRows2 ? g * kRows : 0);
     const int mine = kRows2 ? rows - g * kRows : rows;     // valid rows of this group's tile
@@ -449,32 +510,6 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
     const bool warp_valid = wq * 32 < mine;
     const int i = R / p.G;
     const int head = s.head * p.G + (R - i * p.G);
-    // ---- Q rows into the swizzled tile.  (All rows of a shared tile are
-    // loaded by both groups, half each.)
-    if (seg > 0 && !wait(sm, sm.qfree, (seg - 1) & 1, p)) return;
-    {
-      const long long base = valid ? s.b * p.q_stride[0] + i * p.q_stride[1] + head * p.q_stride[2] : 0;
-      constexpr int kPer = 32 / (D / 8);                   // rows a warp loads at once
-      constexpr int kLoads = (kRows2 ? 32 : 16) / kPer;
-      uint8_t* tile = sm.q + (kRows2 ? g * C::kQTile : 0);
-      uint4 x[kLoads];
-#pragma unroll
-      for (int e = 0; e < kLoads; ++e) {
-        const int rl = (kRows2 ? 0 : g * 16) + e * kPer + lane / (D / 8);   // row within the warp's 32
-        const long long off = __shfl_sync(0xFFFFFFFFu, base, rl);
-        if (wq * 32 + rl < mine) x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + off) + lane % (D / 8));
-      }
-#pragma unroll
-      for (int e = 0; e < kLoads; ++e) {
-        const int row = wq * 32 + (kRows2 ? 0 : g * 16) + e * kPer + lane / (D / 8);
-        const int u = lane % (D / 8);
-        if (row < mine)
-          *reinterpret_cast<uint4*>(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = x[e];
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
-    }
     uint64_t mask64 = 0;
     if (valid) {
       const int words = (p.q_len + 31) >> 5;
@@ -572,7 +607,13 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[g][buf]));
     }
 
-    // ---- end of the segment
+    // ---- end of the segment.  The next one's Q first: its products then
+    // start while this one's results are written.
+    more = w.next(p, next);
+    if (more) {
+      if (!wait(sm, sm.qfree, seg & 1, p)) return;
+      load_q<D, kRows2>(sm, p, next, g, wq, lane);
+    }
     const bool direct = s.n == s.nt;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
     const int rr = (kRows2 ? g * kRows : 0) + r;
@@ -636,6 +677,13 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
 
 // ------------------------------------------------------------ kernel
 
+// This warp's products are done (or its CTA may not end).
+__device__ __forceinline__ void drain_products(uint64_t& bar) {
+  mma_commit_elect(smem_u32(&bar));
+  mbar_wait(smem_u32(&bar), 0, kWaitNs);
+  __syncwarp();
+}
+
 // Tells the merge of the cut unit that starts in this CTA's run, if there is
 // one: it goes on in the CTAs after this one.  Written before the first wait,
 // so that the merge finds it whatever becomes of the loads.
@@ -685,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sm.ofull), 1);
     mbar_init(smem_u32(&sm.ofree), 8);
     mbar_init(smem_u32(&sm.mlx), 8);
-    mbar_init(smem_u32(&sm.drain), 1);
+    mbar_init(smem_u32(&sm.drain[0]), 1);
+    mbar_init(smem_u32(&sm.drain[1]), 1);
     sm.abort_flag = 0;
     sm.start_b = 0;
     sm.start_pre = 0;
@@ -744,17 +793,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   const Walk walk(p, t0, t1, sm.start_b, sm.start_pre);
 
-  if (p.box_rows == 0 && (warp == 0 || warp == 2 || warp == 3)) {
-    load_gather<D, kRows2>(sm, p, walk, warp == 0 ? lane : (warp - 1) * 32 + lane);
+  if (p.box_rows == 0 && (warp == 0 || warp == 2)) {
+    load_gather<D, kRows2>(sm, p, walk, warp * 16 + lane);
   } else if (warp == 0) {
     load_tma<D, kRows2>(sm, p, &map_k, &map_v, walk);
   } else if (warp == 1) {
+    products_qk<D, kBf16, kRows2>(sm, p, tmem, walk);
+    drain_products(sm.drain[0]);
+  } else if (warp == 3) {
     if (lane == 0) note_cut_unit(p, walk, t1, total, ctas);
     __syncwarp();
-    products<D, kBf16, kRows2>(sm, p, tmem, walk);
-    mma_commit_elect(smem_u32(&sm.drain));
-    mbar_wait(smem_u32(&sm.drain), 0, kWaitNs);
-    __syncwarp();
+    products_pv<D, kBf16, kRows2>(sm, p, tmem, walk);
+    drain_products(sm.drain[1]);
   } else if (warp >= 4) {
     softmax<D, kBf16, kRows2>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
   }
@@ -777,37 +827,85 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merges the partials of each cut unit: block (x, c) takes eight rows of the
 // unit that CTA c of the split kernel started.  Its parts are that CTA's slot
-// and the first slots of the CTAs after it, merged in that order.
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(2 * D) combine_kernel(const Params p) {
+// and the first slots of the CTAs after it.  The parts' weights are worked out
+// once for the block; a thread then sums one row's four columns over its part
+// group's parts (kGroups of them take the parts in turn when parts are many),
+// eight loads in flight, and the groups' sums are added in order.
+constexpr int kMaxParts = 320;               // CTAs of the split kernel at most
+template <int D, bool kBf16, int kGroups>
+__global__ void __launch_bounds__(2 * D * kGroups) combine_kernel(const Params p) {
+  constexpr int kThreadsG = 2 * D;           // 8 rows x D / 4 column quads
+  constexpr int kWarps = kThreadsG * kGroups / 32;
+  __shared__ float weight[kMaxParts][8];
+  __shared__ float top[kWarps][8], mass[kWarps][8];
+  __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][kThreadsG];
   grid_dependency_wait();
   const int4 d = p.desc[blockIdx.y];
   if (d.w == 0) return;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int span = p.part_rows;
-  const int head = d.y / p.groups, group = d.y - head * p.groups;
-  const int full = p.q_len * p.G > kRows ? 2 * kRows : kRows;
-  const int rr = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x & 7);
-  const int c4 = threadIdx.x >> 3;
-  const int R = group * full + rr;
-  if (rr >= full || R >= p.q_len * p.G) return;
+  const int first_row = static_cast<int>(blockIdx.x) * 8;
+  const int r = tid & 7, rr = first_row + r;               // (part_rows is a multiple of 8)
   const int next = 2 * (static_cast<int>(blockIdx.y) + 1);
+  auto slot_of = [&](int k) { return static_cast<size_t>(k ? next + 2 * (k - 1) : d.z); };
+
+  // Parts k = tid / 8, ... of row r: the row's max, then weights and mass.
   float m = -CUDART_INF_F;
-  for (int k = 0; k < d.w; ++k)
-    m = fmaxf(m, p.part_ml[static_cast<size_t>(k ? next + 2 * (k - 1) : d.z) * span + rr].x);
+  for (int k = tid >> 3; k < d.w; k += kThreadsG * kGroups / 8) m = fmaxf(m, p.part_ml[slot_of(k) * span + rr].x);
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+  if ((tid & 31) < 8) top[warp][r] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, top[w][r]);
   float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < d.w; ++k) {
-    const size_t slot = k ? next + 2 * (k - 1) : d.z;
-    const float2 ml = p.part_ml[slot * span + rr];
-    const float4 x = p.part_o[(slot * (D / 4) + c4) * span + rr];
+  for (int k = tid >> 3; k < d.w; k += kThreadsG * kGroups / 8) {
+    const float2 ml = p.part_ml[slot_of(k) * span + rr];
     const float w = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - m);
+    weight[k][r] = w;
     l += w * ml.y;
-    o.x += w * x.x;
-    o.y += w * x.y;
-    o.z += w * x.z;
-    o.w += w * x.w;
   }
+  l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+  l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+  if ((tid & 31) < 8) mass[warp][r] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) l += mass[w][r];
+
+  const int group = tid / kThreadsG, t = tid % kThreadsG, c4 = t >> 3;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = group; k < d.w; k += 8 * kGroups) {
+    float4 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e * kGroups < d.w) x[e] = __ldcg(p.part_o + (slot_of(k + e * kGroups) * (D / 4) + c4) * span + rr);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e * kGroups < d.w) {
+        const float w = weight[k + e * kGroups][r];
+        o.x += w * x[e].x;
+        o.y += w * x[e].y;
+        o.z += w * x[e].z;
+        o.w += w * x[e].w;
+      }
+  }
+  if (kGroups > 1) {
+    if (group) sums[group - 1][t] = o;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int g = 0; g < kGroups - 1; ++g) {
+      const float4 x = sums[g][t];
+      o.x += x.x;
+      o.y += x.y;
+      o.z += x.z;
+      o.w += x.w;
+    }
+  }
+  const int full = p.q_len * p.G > kRows ? 2 * kRows : kRows;
+  const int head = d.y / p.groups, R = (d.y - head * p.groups) * full + rr;
+  if (R >= p.q_len * p.G) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int i = R / p.G;
   const long long row = (static_cast<long long>(d.x) * p.q_len + i) * p.H + head * p.G + (R - i * p.G);
