@@ -44,8 +44,6 @@ namespace gqa {
 constexpr int kKeys = 64;                  // keys a tile
 constexpr int kRows = 128;                 // rows a group's accumulator (MMA M)
 constexpr int kThreads = 384;              // 4 control warps + 2 x 4 softmax warps
-constexpr int kGatherThreads = 64;         // control warps 0 and 2 load rows of odd pages
-constexpr int kGatherAhead = 3;            // stages in flight a gathering thread
 constexpr float kLazy = 8.0f;              // log2 units a row's max may grow before O is rescaled
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -101,41 +99,65 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t N, uint32_t b_mn) {
   return (1u << 4) | (kBf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// Shared-memory matrix descriptors (128-byte swizzle, 1 KB between groups of
+// eight rows) have a constant upper half; the lower half holds the address and,
+// for V, the distance between 64-wide chunks.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+// The products are issued by one elected lane of a converged warp: the operands
+// then move to uniform registers once, not lane by lane (a single-lane loop
+// took 1.5 times as long).
+
 // Four K = 16 steps of one 64-wide chunk, A and B K-major in shared memory.
-__device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
   asm volatile(
-      "{\n .reg .pred e, p;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      "{\n .reg .pred e, p;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
       " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
-      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+      " add.u32 x, %1, 2;\n add.u32 y, %2, 2;\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
+      " add.u32 x, %1, 4;\n add.u32 y, %2, 4;\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
+      " add.u32 x, %1, 6;\n add.u32 y, %2, 6;\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id),
+      "n"(kAcc ? 1 : 0), "n"(kDescHi)
       : "memory");
 }
 
 // O (+)= P V over 64 keys: P in tensor memory (8 columns a K = 16 step), V
 // MN-major in shared memory (16 rows of 128 bytes a step).
-__device__ __forceinline__ void mma_ts_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred e, p;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
-      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
-      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred e, p;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 b, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 b, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n"
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 b, {y, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc),
+      "n"(kDescHi)
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int row, int chunk, int head,
-                                            int batch, uint32_t bar) {
+// One box of a cache by the elected lane of a converged warp.
+__device__ __forceinline__ void tma_box_elect(uint32_t dst, const CUtensorMap* map, int row, int chunk, int head, int batch,
+                                              uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(chunk), "r"(head), "r"(batch), "r"(bar)
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(batch), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_expect_elect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar), "r"(bytes)
       : "memory");
 }
 
@@ -162,6 +184,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Bounded; gives up at once when another warp of the CTA has.
 template <class S>
 __device__ __noinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
+  for (int i = 0; i < 64; ++i)       // (reading the timer takes longer than most waits)
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -239,106 +263,131 @@ __device__ __forceinline__ int page_of(const Params& p, int b, int key) {
   return page;
 }
 
-// Warp 0: K and V tiles by TMA.  A tile is one box of 64 rows, or boxes of
-// box_rows rows and 64 dims when pages are shorter than a tile, one a lane.
+// Position in a ring of stages.
+template <int kStages>
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Warps 0 (K) and 2 (V): tiles by TMA.  A tile is one box of 64 rows, or boxes
+// of box_rows rows and 64 dims when pages are shorter than a tile.  (One warp
+// for both took longer to issue a tile's copies than the memory to deliver them.)
 template <int D, bool kRows2>
-__device__ __forceinline__ void load_tma(Smem<D, kRows2>& sm, const Params& p, const CUtensorMap* mk,
-                                         const CUtensorMap* mv, Walk w) {
+__device__ __forceinline__ void load_tma(Smem<D, kRows2>& sm, const Params& p, const CUtensorMap* map, Walk w, bool is_v) {
   using C = Shape<D>;
   const int lane = threadIdx.x & 31;
-  const int R = p.box_rows, boxes = R == kKeys ? 1 : kKeys / R;   // boxes along the keys
-  const int my_box = lane % boxes, my_chunk = lane / boxes;
-  const bool mine = lane < boxes * (R == kKeys ? 1 : C::kChunks);
-  const uint32_t dst0 = my_chunk * (kKeys * 128) + my_box * R * 128;
-  int kt = 0, issued[2] = {0, 0};
-  bool ok = true;
+  uint64_t* const full = is_v ? sm.vfull : sm.kfull;
+  uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
+  const uint32_t ring = smem_u32(sm.ring) + (is_v ? C::kTile : 0);
+  const int R = p.box_rows, boxes = kKeys / R;             // boxes along the keys; lane i looks up box i's row
+  const bool paged = p.block_table != nullptr;
+  Ring<C::kStages> at;
+  int issued = 0;
   Segment s;
-  while (ok && w.next(p, s)) {
+  while (w.next(p, s)) {
     auto row_of = [&](int j) {
-      const int key = (s.tile0 + j) * kKeys + my_box * R;
-      if (p.block_table == nullptr || !mine || j >= s.n || key >= s.S) return key;
+      const int key = (s.tile0 + j) * kKeys + lane * R;
+      if (!paged) return key;
+      if (lane >= boxes || j >= s.n || key >= s.S) return 0;
       const int page = page_of(p, s.b, key);
       return page * p.page + key % p.page;
     };
+    const int batch = paged ? 0 : s.b;
     int row = row_of(0);
-    for (int j = 0; j < s.n; ++j, ++kt) {
-      const int stage = kt % C::kStages;
-      const uint32_t parity = ((kt / C::kStages) & 1) ^ 1;
-      const int left = s.S - (s.tile0 + j) * kKeys;              // keys of the stream from this tile on
-      const uint32_t bytes =
-          R == kKeys ? C::kTile : min(boxes, (left + R - 1) / R) * static_cast<uint32_t>(R) * D * 2;
-      const bool issue = mine && (R == kKeys || my_box * R < left);
+    for (int j = 0; j < s.n; ++j, at.advance()) {
       const int row_next = row_of(j + 1);
-      const int batch = p.block_table == nullptr ? s.b : 0;
+      if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
+      const uint32_t bar = smem_u32(&full[at.stage]), dst = ring + at.stage * 2 * C::kTile;
+      if (p.test_stall && is_v && issued == 0 && blockIdx.x == 0) goto out;       // this load never comes
+      if (R == kKeys) {
+        arrive_expect_elect(bar, C::kTile);
+        tma_box_elect(dst, map, __shfl_sync(0xFFFFFFFFu, row, 0), 0, s.head, batch, bar);
+      } else {
+        const int n = min(boxes, (s.S - (s.tile0 + j) * kKeys + R - 1) / R);       // boxes with keys of the stream
+        arrive_expect_elect(bar, n * R * D * 2);
+        for (int i = 0; i < n; ++i) {
+          const int r = __shfl_sync(0xFFFFFFFFu, row, i);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        ok = wait(sm, kv ? sm.vempty[stage] : sm.kempty[stage], parity, p);
-        if (!ok) break;
-        if (p.test_stall && kv == 1 && kt == 0 && blockIdx.x == 0) continue;   // this load never comes
-        const uint32_t full = smem_u32(kv ? &sm.vfull[stage] : &sm.kfull[stage]);
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-        issued[kv] = kt + 1;
-        if (issue)
-          tma_load_5d(smem_u32(sm.ring) + stage * 2 * C::kTile + kv * C::kTile + dst0, kv ? mv : mk, 0, row, my_chunk,
-                      s.head, batch, full);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_box_elect(dst + c * (kKeys * 128) + i * R * 128, map, r, c, s.head, batch, bar);
+        }
       }
-      if (!ok) break;
+      ++issued;
       row = row_next;
     }
   }
+out:
   // The copies issued must have landed before the CTA may end.
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
-    for (int n = issued[kv] - 1; n >= 0 && n >= issued[kv] - C::kStages; --n) {
-      if (p.test_stall && kv == 1 && n == 0 && blockIdx.x == 0) continue;
-      mbar_wait(smem_u32(kv ? &sm.vfull[n % C::kStages] : &sm.kfull[n % C::kStages]), (n / C::kStages) & 1, kWaitNs / 2);
-    }
+  for (int n = issued - 1; n >= 0 && n >= issued - C::kStages; --n)
+    mbar_wait(smem_u32(&full[n % C::kStages]), (n / C::kStages) & 1, kWaitNs / 2);
 }
 
-// Control warps 0 and 2 when no TMA box fits the pages (page_size not a
-// multiple of 8): rows copied 16 bytes a thread, into the layout the boxes
-// would leave; rows past the stream are zeros.
+// Warps 0 (K) and 2 (V) when no TMA box fits the pages (page_size not a
+// multiple of 8): rows copied 16 bytes a lane, into the layout the boxes would
+// leave; rows past the stream are zeros.  A lane looks up the pages of two rows
+// of the next tile while it copies this one.
 template <int D, bool kRows2>
-__device__ __forceinline__ void load_gather(Smem<D, kRows2>& sm, const Params& p, Walk w, int tid) {
+__device__ __forceinline__ void load_gather(Smem<D, kRows2>& sm, const Params& p, Walk w, bool is_v) {
   using C = Shape<D>;
-  constexpr int kUnits = kKeys * D / 8;        // 16-byte units of a tile
-  int kt = 0;
-  Segment s;
-  bool ok = true;
-  auto publish = [&](int n) {                  // tile n's copies of this thread have landed
+  constexpr int kUnits = D / 8;                // 16-byte units a row
+  constexpr int kPer = 32 / kUnits;            // rows a warp copies at once
+  constexpr int kAhead = C::kStages - 1 < 8 ? C::kStages - 1 : 8;   // stages in flight
+  const int lane = threadIdx.x & 31;
+  uint64_t* const full = is_v ? sm.vfull : sm.kfull;
+  uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
+  const uint32_t ring = smem_u32(sm.ring) + (is_v ? C::kTile : 0);
+  const uint8_t* const pool = is_v ? p.v : p.k;
+  const long long row_stride = is_v ? p.v_stride[1] : p.k_stride[1];
+  const long long head_stride = is_v ? p.v_stride[2] : p.k_stride[2];
+  const bool withheld = p.test_stall && is_v && blockIdx.x == 0;
+  Ring<C::kStages> at, landed;
+  int started = 0;
+  auto publish = [&]() {                       // the oldest tile's copies of this lane have landed
     fence_proxy_async_smem();
-    mbar_arrive(smem_u32(&sm.kfull[n % C::kStages]));
-    mbar_arrive(smem_u32(&sm.vfull[n % C::kStages]));
+    if (!withheld) mbar_arrive(smem_u32(&full[landed.stage]));
+    landed.advance();
   };
-  while (ok && w.next(p, s)) {
-    for (int j = 0; j < s.n; ++j, ++kt) {
-      const int stage = kt % C::kStages;
-      const uint32_t parity = ((kt / C::kStages) & 1) ^ 1;
-      ok = wait(sm, sm.kempty[stage], parity, p) && wait(sm, sm.vempty[stage], parity, p);
-      if (!ok) break;
-      const uint32_t dst = smem_u32(sm.ring) + stage * 2 * C::kTile;
-      const int k0 = (s.tile0 + j) * kKeys;
-      for (int i = tid; i < kUnits; i += kGatherThreads) {
-        const int r = i / (D / 8), u = i % (D / 8);
-        const int key = k0 + r;
-        const bool in = key < s.S;
-        long long row = 0;
-        if (in) row = static_cast<long long>(page_of(p, s.b, key)) * p.page + key % p.page;
-        const uint32_t off = (u >> 3) * (kKeys * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-        cp_async_16(dst + off, p.k + row * p.k_stride[1] + s.head * p.k_stride[2] + u * 16, in);
-        cp_async_16(dst + C::kTile + off, p.v + row * p.v_stride[1] + s.head * p.v_stride[2] + u * 16, in);
+  Segment s;
+  while (w.next(p, s)) {
+    auto row_of = [&](int j, int half) {       // -1 past the stream
+      const int key = (s.tile0 + j) * kKeys + half * 32 + lane;
+      if (j >= s.n || key >= s.S) return -1;
+      const int page = page_of(p, s.b, key);
+      return page * p.page + key % p.page;
+    };
+    const uint8_t* const head = pool + s.head * head_stride + (lane % kUnits) * 16;
+    int lo = row_of(0, 0), hi = row_of(0, 1);
+    for (int j = 0; j < s.n; ++j, at.advance()) {
+      const int lo_next = row_of(j + 1, 0), hi_next = row_of(j + 1, 1);
+      if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
+      const uint32_t dst = ring + at.stage * 2 * C::kTile + (lane % kUnits >> 3) * (kKeys * 128);
+#pragma unroll
+      for (int e = 0; e < kKeys / kPer; ++e) {
+        const int r = e * kPer + lane / kUnits;                     // row of the tile
+        const int row = __shfl_sync(0xFFFFFFFFu, e * kPer < 32 ? lo : hi, r & 31);
+        cp_async_16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4), head + (row < 0 ? 0 : row) * row_stride, row >= 0);
       }
       cp_async_commit();
-      if (kt >= kGatherAhead - 1) {
-        cp_async_wait<kGatherAhead - 1>();
-        if (!(p.test_stall && blockIdx.x == 0)) publish(kt - (kGatherAhead - 1));
+      if (++started >= kAhead) {
+        cp_async_wait<kAhead - 1>();
+        publish();
       }
+      lo = lo_next;
+      hi = hi_next;
     }
   }
   cp_async_wait<0>();
-  if (ok && !(p.test_stall && blockIdx.x == 0))
-    for (int n = max(0, kt - (kGatherAhead - 1)); n < kt; ++n) publish(n);
+  for (int n = min(started, kAhead - 1); n > 0; --n) publish();
+  return;
+out:
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------ products
@@ -363,9 +412,10 @@ template <int D, bool kBf16, bool kRows2>
 __device__ __forceinline__ void products_qk(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
   using C = Shape<D>;
   constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
-  const uint64_t q0 = sdesc_sw128(smem_u32(sm.q), 16, 1024), k0 = sdesc_sw128(smem_u32(sm.ring), 16, 1024);
-  int kt = 0, seg = 0;                         // tiles and segments before this segment
-  int done[2] = {0, 0};                        // tasks of each group so far
+  const uint32_t q0 = desc_lo(smem_u32(sm.q), 16), k0 = desc_lo(smem_u32(sm.ring), 16);
+  Ring<C::kStages> at;
+  Ring<2> buf[2];                              // the groups' S buffers
+  int seg = 0;
   Segment s;
   while (w.next(p, s)) {
     const bool two = kRows2 && rows_of_group(p, s.group, 2 * kRows) > kRows;
@@ -373,21 +423,24 @@ __device__ __forceinline__ void products_qk(Smem<D, kRows2>& sm, const Params& p
     if (!wait(sm, sm.qfull, seg & 1, p)) return;
     for (int x = 0; x < tasks; ++x) {
       const Task t = task_of<kRows2>(x, two);
-      const int stage = (kt + t.tile) % C::kStages;
-      const int n = t.g ? done[1]++ : done[0]++;
-      if (!wait(sm, sm.pvdone[t.g][n & 1], ((n >> 1) & 1) ^ 1, p)) return;
-      if (!wait(sm, sm.kfull[stage], ((kt + t.tile) / C::kStages) & 1, p)) return;
+      const Ring<2> b = t.g ? buf[1] : buf[0];
+      if (!wait(sm, sm.pvdone[t.g][b.stage], b.phase ^ 1, p)) return;
+      if (!wait(sm, sm.kfull[at.stage], at.phase, p)) return;
       tc_fence_after();
-      const uint32_t d = tmem + 256 + (2 * t.g + (n & 1)) * kKeys;
-      const uint64_t a = q0 + (kRows2 ? t.g * (C::kQTile >> 4) : 0), b = k0 + stage * (2 * C::kTile >> 4);
+      const uint32_t d = tmem + 256 + (2 * t.g + b.stage) * kKeys;
+      const uint32_t q = q0 + (kRows2 ? t.g * (C::kQTile >> 4) : 0), k = k0 + at.stage * (2 * C::kTile >> 4);
+      mma_ss_chunk<false>(d, q, k, kId);
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c)
-        mma_ss_chunk(d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), kId, c != 0);
-      mma_commit_elect(smem_u32(&sm.sfull[t.g][n & 1]));
-      if (t.last_use) mma_commit_elect(smem_u32(&sm.kempty[stage]));
+      for (int c = 1; c < C::kChunks; ++c)
+        mma_ss_chunk<true>(d, q + c * (kRows * 128 >> 4), k + c * (kKeys * 128 >> 4), kId);
+      mma_commit_elect(smem_u32(&sm.sfull[t.g][b.stage]));
       if (x == tasks - 1) mma_commit_elect(smem_u32(&sm.qfree));
+      if (t.last_use) {
+        mma_commit_elect(smem_u32(&sm.kempty[at.stage]));
+        at.advance();
+      }
+      if (t.g) buf[1].advance(); else buf[0].advance();
     }
-    kt += s.n;
     ++seg;
   }
 }
@@ -397,9 +450,10 @@ template <int D, bool kBf16, bool kRows2>
 __device__ __forceinline__ void products_pv(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
   using C = Shape<D>;
   constexpr uint32_t kId = idesc<kBf16>(D, 1);
-  const uint64_t v0 = sdesc_sw128(smem_u32(sm.ring) + C::kTile, kKeys * 128, 1024);
-  int kt = 0, seg = 0;
-  int done[2] = {0, 0};
+  const uint32_t v0 = desc_lo(smem_u32(sm.ring) + C::kTile, kKeys * 128);
+  Ring<C::kStages> at;
+  Ring<2> buf[2];
+  int seg = 0;
   Segment s;
   while (w.next(p, s)) {
     const bool two = kRows2 && rows_of_group(p, s.group, 2 * kRows) > kRows;
@@ -408,19 +462,21 @@ __device__ __forceinline__ void products_pv(Smem<D, kRows2>& sm, const Params& p
     if (seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
     for (int x = 0; x < tasks; ++x) {
       const Task t = task_of<kRows2>(x, two);
-      const int stage = (kt + t.tile) % C::kStages;
-      const int n = t.g ? done[1]++ : done[0]++;
+      const Ring<2> b = t.g ? buf[1] : buf[0];
       const bool first = kRows2 ? t.tile == 0 : x < 2;     // the group's first of the segment: O starts at 0
-      if (!wait(sm, sm.vfull[stage], ((kt + t.tile) / C::kStages) & 1, p)) return;
-      if (!wait(sm, sm.pfull[t.g][n & 1], (n >> 1) & 1, p)) return;
+      if (!wait(sm, sm.vfull[at.stage], at.phase, p)) return;
+      if (!wait(sm, sm.pfull[t.g][b.stage], b.phase, p)) return;
       tc_fence_after();
-      mma_ts_pv(tmem + t.g * D, tmem + 256 + (2 * t.g + (n & 1)) * kKeys, v0 + stage * (2 * C::kTile >> 4), kId,
+      mma_ts_pv(tmem + t.g * D, tmem + 256 + (2 * t.g + b.stage) * kKeys, v0 + at.stage * (2 * C::kTile >> 4), kId,
                 first ? 0u : 1u);
-      mma_commit_elect(smem_u32(&sm.pvdone[t.g][n & 1]));
-      if (t.last_use) mma_commit_elect(smem_u32(&sm.vempty[stage]));
+      mma_commit_elect(smem_u32(&sm.pvdone[t.g][b.stage]));
+      if (t.last_use) {
+        mma_commit_elect(smem_u32(&sm.vempty[at.stage]));
+        at.advance();
+      }
+      if (t.g) buf[1].advance(); else buf[0].advance();
     }
     mma_commit_elect(smem_u32(&sm.ofull));
-    kt += s.n;
     ++seg;
   }
 }
@@ -716,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_k);
       tma_prefetch_desc(&map_v);
     }
-    const uint32_t loaders = p.box_rows ? 1 : kGatherThreads;
+    const uint32_t loaders = p.box_rows ? 1 : 32;
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&sm.kfull[i]), loaders);
       mbar_init(smem_u32(&sm.vfull[i]), loaders);
@@ -793,10 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   const Walk walk(p, t0, t1, sm.start_b, sm.start_pre);
 
-  if (p.box_rows == 0 && (warp == 0 || warp == 2)) {
-    load_gather<D, kRows2>(sm, p, walk, warp * 16 + lane);
-  } else if (warp == 0) {
-    load_tma<D, kRows2>(sm, p, &map_k, &map_v, walk);
+  if (warp == 0 || warp == 2) {
+    if (p.box_rows == 0) load_gather<D, kRows2>(sm, p, walk, warp == 2);
+    else load_tma<D, kRows2>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
   } else if (warp == 1) {
     products_qk<D, kBf16, kRows2>(sm, p, tmem, walk);
     drain_products(sm.drain[0]);
