@@ -107,40 +107,54 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { retu
 
 // The products are issued by one elected lane of a converged warp: the operands
 // then move to uniform registers once, not lane by lane (a single-lane loop
-// took 1.5 times as long).
+// took 1.5 times as long).  A task's products and the commits that follow them
+// are one block, with one election.
 
-// Four K = 16 steps of one 64-wide chunk, A and B K-major in shared memory.
-template <bool kAcc>
-__device__ __forceinline__ void mma_ss_chunk(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
-  asm volatile(
-      "{\n .reg .pred e, p;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
-      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
-      " add.u32 x, %1, 2;\n add.u32 y, %2, 2;\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
-      " add.u32 x, %1, 4;\n add.u32 y, %2, 4;\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
-      " add.u32 x, %1, 6;\n add.u32 y, %2, 6;\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id),
-      "n"(kAcc ? 1 : 0), "n"(kDescHi)
-      : "memory");
+// S = Q K^T of one task, A and B K-major in shared memory: D / 64 chunks of four
+// K = 16 steps; then the commits to `bar0`, and to `bar1` and `bar2` where c1 and c2 say so.
+#define MLA_QK_CHUNK(ao, bo, first)                                                                   \
+  " add.u32 x, %1, " #ao ";\n add.u32 y, %2, " #bo ";\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " #first ";\n"                              \
+  " add.u32 x, %1, " #ao " + 2;\n add.u32 y, %2, " #bo " + 2;\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"                                       \
+  " add.u32 x, %1, " #ao " + 4;\n add.u32 y, %2, " #bo " + 4;\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"                                       \
+  " add.u32 x, %1, " #ao " + 6;\n add.u32 y, %2, " #bo " + 6;\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
+#define MLA_COMMIT(pred, bar) \
+  " @" #pred " tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [" #bar "];\n"
+#define MLA_QK_BODY(chunks)                                                                                        \
+  asm volatile("{\n .reg .pred e, z, c1, c2;\n .reg .b32 x, y;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n" \
+               " setp.ne.and.b32 c1, %7, 0, e;\n setp.ne.and.b32 c2, %8, 0, e;\n setp.ne.b32 z, 0, 0;\n" chunks     \
+               MLA_COMMIT(e, %4) MLA_COMMIT(c1, %5) MLA_COMMIT(c2, %6) "}" ::"r"(d),                                \
+               "r"(a), "r"(b), "r"(id), "r"(bar0), "r"(bar1), "r"(bar2), "r"(static_cast<uint32_t>(c1)),            \
+               "r"(static_cast<uint32_t>(c2)), "n"(kDescHi)                                                         \
+               : "memory")
+template <int kChunks>
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t bar0, uint32_t bar1,
+                                         bool c1, uint32_t bar2, bool c2) {
+  // Chunks lie 16 KB (Q, 128 rows) and 8 KB (K, 64 keys) apart: 1024 and 512 descriptor units.
+  static_assert(kRows * 128 >> 4 == 1024 && kKeys * 128 >> 4 == 512, "chunk distances");
+  if (kChunks == 1) MLA_QK_BODY(MLA_QK_CHUNK(0, 0, z));
+  else MLA_QK_BODY(MLA_QK_CHUNK(0, 0, z) MLA_QK_CHUNK(1024, 512, 1));
 }
 
 // O (+)= P V over 64 keys: P in tensor memory (8 columns a K = 16 step), V
-// MN-major in shared memory (16 rows of 128 bytes a step).
-__device__ __forceinline__ void mma_ts_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+// MN-major in shared memory (16 rows of 128 bytes a step); then the commits.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t bar0,
+                                         uint32_t bar1, bool c1, uint32_t bar2, bool c2) {
   asm volatile(
-      "{\n .reg .pred e, p;\n .reg .b32 x, y;\n .reg .b64 b;\n"
-      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      "{\n .reg .pred e, p, c1, c2;\n .reg .b32 x, y;\n .reg .b64 b;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.and.b32 c1, %8, 0, e;\n setp.ne.and.b32 c2, %9, 0, e;\n mov.b64 b, {%2, %10};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n"
-      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 b, {y, %5};\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 b, {y, %10};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n"
-      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 b, {y, %5};\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 b, {y, %10};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n"
-      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 b, {y, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc),
-      "n"(kDescHi)
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 b, {y, %10};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n" MLA_COMMIT(e, %5) MLA_COMMIT(c1, %6)
+      MLA_COMMIT(c2, %7) "}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(bar0), "r"(bar1), "r"(bar2),
+      "r"(static_cast<uint32_t>(c1)), "r"(static_cast<uint32_t>(c2)), "n"(kDescHi)
       : "memory");
 }
 
@@ -202,6 +216,17 @@ template <class S>
 __device__ __forceinline__ bool wait(S& sm, uint64_t& bar, uint32_t parity, const Params& p) {
   bool ok = mbar_try_wait(smem_u32(&bar), parity);
   if (!ok) ok = wait_slow(sm, smem_u32(&bar), parity, p);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// For two barriers at once: half the lanes ask for each.
+template <class S>
+__device__ __forceinline__ bool wait2(S& sm, uint64_t& bar0, uint32_t parity0, uint64_t& bar1, uint32_t parity1,
+                                      const Params& p) {
+  const bool odd = (threadIdx.x & 1) != 0;
+  const uint32_t bar = odd ? smem_u32(&bar1) : smem_u32(&bar0), parity = odd ? parity1 : parity0;
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = wait_slow(sm, bar, parity, p);
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
@@ -424,21 +449,12 @@ __device__ __forceinline__ void products_qk(Smem<D, kRows2>& sm, const Params& p
     for (int x = 0; x < tasks; ++x) {
       const Task t = task_of<kRows2>(x, two);
       const Ring<2> b = t.g ? buf[1] : buf[0];
-      if (!wait(sm, sm.pvdone[t.g][b.stage], b.phase ^ 1, p)) return;
-      if (!wait(sm, sm.kfull[at.stage], at.phase, p)) return;
+      if (!wait2(sm, sm.pvdone[t.g][b.stage], b.phase ^ 1, sm.kfull[at.stage], at.phase, p)) return;
       tc_fence_after();
-      const uint32_t d = tmem + 256 + (2 * t.g + b.stage) * kKeys;
-      const uint32_t q = q0 + (kRows2 ? t.g * (C::kQTile >> 4) : 0), k = k0 + at.stage * (2 * C::kTile >> 4);
-      mma_ss_chunk<false>(d, q, k, kId);
-#pragma unroll
-      for (int c = 1; c < C::kChunks; ++c)
-        mma_ss_chunk<true>(d, q + c * (kRows * 128 >> 4), k + c * (kKeys * 128 >> 4), kId);
-      mma_commit_elect(smem_u32(&sm.sfull[t.g][b.stage]));
-      if (x == tasks - 1) mma_commit_elect(smem_u32(&sm.qfree));
-      if (t.last_use) {
-        mma_commit_elect(smem_u32(&sm.kempty[at.stage]));
-        at.advance();
-      }
+      issue_qk<C::kChunks>(tmem + 256 + (2 * t.g + b.stage) * kKeys, q0 + (kRows2 ? t.g * (C::kQTile >> 4) : 0),
+                           k0 + at.stage * (2 * C::kTile >> 4), kId, smem_u32(&sm.sfull[t.g][b.stage]),
+                           smem_u32(&sm.kempty[at.stage]), t.last_use, smem_u32(&sm.qfree), x == tasks - 1);
+      if (t.last_use) at.advance();
       if (t.g) buf[1].advance(); else buf[0].advance();
     }
     ++seg;
@@ -464,19 +480,14 @@ __device__ __forceinline__ void products_pv(Smem<D, kRows2>& sm, const Params& p
       const Task t = task_of<kRows2>(x, two);
       const Ring<2> b = t.g ? buf[1] : buf[0];
       const bool first = kRows2 ? t.tile == 0 : x < 2;     // the group's first of the segment: O starts at 0
-      if (!wait(sm, sm.vfull[at.stage], at.phase, p)) return;
-      if (!wait(sm, sm.pfull[t.g][b.stage], b.phase, p)) return;
+      if (!wait2(sm, sm.pfull[t.g][b.stage], b.phase, sm.vfull[at.stage], at.phase, p)) return;
       tc_fence_after();
-      mma_ts_pv(tmem + t.g * D, tmem + 256 + (2 * t.g + b.stage) * kKeys, v0 + at.stage * (2 * C::kTile >> 4), kId,
-                first ? 0u : 1u);
-      mma_commit_elect(smem_u32(&sm.pvdone[t.g][b.stage]));
-      if (t.last_use) {
-        mma_commit_elect(smem_u32(&sm.vempty[at.stage]));
-        at.advance();
-      }
+      issue_pv(tmem + t.g * D, tmem + 256 + (2 * t.g + b.stage) * kKeys, v0 + at.stage * (2 * C::kTile >> 4), kId,
+               first ? 0u : 1u, smem_u32(&sm.pvdone[t.g][b.stage]), smem_u32(&sm.vempty[at.stage]), t.last_use,
+               smem_u32(&sm.ofull), x == tasks - 1);
+      if (t.last_use) at.advance();
       if (t.g) buf[1].advance(); else buf[0].advance();
     }
-    mma_commit_elect(smem_u32(&sm.ofull));
     ++seg;
   }
 }
