@@ -19,6 +19,11 @@ namespace gqa {
 constexpr int kMaxDevices = 64;
 // Fewest tiles a CTA takes: below that, fewer CTAs share a short call's work.
 constexpr int kMinTiles = 2;
+// Caches of at most so many keys are not cut: a CTA then takes whole units, and
+// there is nothing to merge.
+constexpr int kWholeKeys = 512;
+// Row groups of a head that CTAs take side by side, at most.
+constexpr int kMaxMembers = 16;
 // Parts a unit from which four part groups share the merge of a row.
 constexpr int kManyParts = 32;
 
@@ -70,7 +75,7 @@ struct Variant {
 };
 template <int D, bool kBf16, bool kRows2>
 Variant variant() {
-  constexpr size_t smem = sizeof(Smem<D, kRows2>) + 1024;   // + manual 1 KB alignment
+  constexpr size_t smem = sizeof(Smem<D, kRows2>);
   static_assert(smem <= 232448, "one CTA's shared memory");
   return {attn_kernel<D, kBf16, kRows2>, {combine_kernel<D, kBf16, 1>, combine_kernel<D, kBf16, 4>}, smem};
 }
@@ -214,7 +219,10 @@ int run(const Call& c) {
   p.Smax = c.Smax;
   p.groups = pl.groups;
   p.part_rows = pl.part_rows;
-  p.min_tiles = kMinTiles;
+  p.whole = c.Smax <= kWholeKeys;
+  p.min_tiles = p.whole ? 1 : kMinTiles;
+  p.sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
+  p.members = (pl.groups + p.sets - 1) / p.sets;
   p.max_blocks = c.max_blocks;
   p.page = c.page;
   p.pool_pages = paged ? static_cast<int>(c.pool_rows / c.page) : 0;
@@ -236,6 +244,7 @@ int run(const Call& c) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }
+  if (p.whole) return MLA_OK;
   // Few units: each is cut into many parts.
   const bool many = static_cast<long long>(c.B) * c.Hkv * pl.groups * kManyParts <= grid;
   cfg.gridDim = dim3(pl.part_rows / 8, grid, 1);

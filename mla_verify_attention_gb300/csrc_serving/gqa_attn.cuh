@@ -13,12 +13,12 @@
 // (32 KB at D = 128: ~1,500 cycles).
 //
 // Split.  The work is a sequence of 64-key tiles: streams, then key heads,
-// then row groups, then keys.  Every CTA of one persistent wave takes an equal
+// then keys.  Every CTA (or team of CTAs, one a row group) of one persistent wave takes an equal
 // run of that sequence, computed on the device from seq_lens, so that ragged
 // batches balance to one tile and nothing is planned on the host.  A (stream,
 // head, row group) unit that lies within one run is written to `out`; one that
 // is cut leaves unnormalised partials (at most two a CTA, which bounds the
-// workspace by the grid) that gqa_combine_kernel merges in order.
+// workspace by the grid) that combine_kernel merges in order.
 //
 // CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), two
 // issue tcgen05.mma, eight softmax warps in two groups own one accumulator O
@@ -57,11 +57,13 @@ struct Params {
   const int32_t* block_table;      // null: contiguous caches
   void* out;
   float* lse;
-  int4* desc;                      // [grid] the cut unit each CTA starts: {stream, head | group, first slot, parts}
+  int4* desc;                      // [grid] the cut unit each CTA starts: {stream, head * groups + group, first slot, parts}
   float2* part_ml;                 // [2 * grid][part_rows]
   float4* part_o;                  // [2 * grid][D / 4][part_rows]
   unsigned int* status;
   int B, q_len, H, Hkv, G, Smax, groups, part_rows, min_tiles;
+  int members, sets;               // row groups side by side, and one after the other
+  int whole;                       // units are not cut (short caches): the work is counted in units
   int max_blocks, page, pool_pages;
   int box_rows;                    // rows a TMA box: 64 or a divisor that no page boundary cuts; 0: gather
   int test_stall;
@@ -79,13 +81,15 @@ struct Shape {
 
 template <int D, bool kRows2>
 struct __align__(1024) Smem {
-  uint8_t q[(kRows2 ? 2 : 1) * Shape<D>::kQTile];
+  uint8_t q[2 * Shape<D>::kQTile];                     // both row tiles, or this segment's and the next one's
   uint8_t ring[Shape<D>::kRing];                       // stage s: K tile, V tile
   float2 ml[2][kRows2 ? 1 : kRows];
   uint64_t kfull[Shape<D>::kStages], kempty[Shape<D>::kStages];
   uint64_t vfull[Shape<D>::kStages], vempty[Shape<D>::kStages];
   uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];     // [group][buffer]
-  uint64_t qfull, qfree, ofull, ofree, mlx, drain[2];
+  // (qfree: one a segment parity.  The products can be through with a short
+  // segment before a softmax warp asks for the one before it.)
+  uint64_t qfull, qfree[2], ofull, ofree, mlx, drain[2];
   long long total, start_pre;
   long long warp_sum[kThreads / 32];
   int start_b;
@@ -238,12 +242,19 @@ __device__ __forceinline__ int stream_tiles(const Params& p, int b, int& S) {
   return S < p.q_len || S > p.Smax ? 0 : (S + kKeys - 1) / kKeys;
 }
 
+// Its work a unit: tiles, or with p.whole the unit itself.
+__device__ __forceinline__ int stream_work(const Params& p, int nt) { return p.whole ? (nt > 0 ? 1 : 0) : nt; }
+
 // A CTA's part of one unit.
 struct Segment {
   int b, S, head, group, tile0, n, nt;   // tiles tile0 .. tile0 + n - 1 of the unit's nt
 };
 
-// Walks a CTA's run of tiles [t, t1); every role walks it on its own.
+// Walks a CTA's run of work [t, t1); every role walks it on its own.  The row
+// groups of a key head are taken side by side by `members` CTAs with the same
+// run, so that they read the same tiles at the same time and the caches come
+// from HBM once (one after the other, 1,024 rows a head over 8k keys read them
+// four times at 5.2 TB/s); a group that does not exist is skipped.
 struct Walk {
   long long t, t1, pre;
   int b, S, nt;
@@ -252,24 +263,28 @@ struct Walk {
     if (t < t1) nt = stream_tiles(p, b, S);
   }
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
-    if (t >= t1) return false;
-    const int units = p.Hkv * p.groups;
-    while (t >= pre + static_cast<long long>(nt) * units) {
-      pre += static_cast<long long>(nt) * units;
-      nt = stream_tiles(p, ++b, S);
+    const int units = p.Hkv * p.sets, member = static_cast<int>(blockIdx.x) % p.members;
+    while (t < t1) {
+      while (t >= pre + static_cast<long long>(stream_work(p, nt)) * units) {
+        pre += static_cast<long long>(stream_work(p, nt)) * units;
+        nt = stream_tiles(p, ++b, S);
+      }
+      const int local = static_cast<int>(t - pre);
+      const int work = stream_work(p, nt);
+      const int u = local / work;
+      s.b = b;
+      s.S = S;
+      s.nt = nt;
+      s.tile0 = local - u * work;
+      s.head = u / p.sets;
+      s.group = (u - s.head * p.sets) * p.members + member;
+      const long long left = t1 - t;
+      const int n = left < work - s.tile0 ? static_cast<int>(left) : work - s.tile0;
+      s.n = p.whole ? nt : n;
+      t += n;
+      if (s.group < p.groups) return true;
     }
-    const int local = static_cast<int>(t - pre);
-    const int u = local / nt;
-    s.b = b;
-    s.S = S;
-    s.nt = nt;
-    s.tile0 = local - u * nt;
-    s.head = u / p.groups;
-    s.group = u - s.head * p.groups;
-    const long long left = t1 - t;
-    s.n = left < nt - s.tile0 ? static_cast<int>(left) : nt - s.tile0;
-    t += s.n;
-    return true;
+    return false;
   }
 };
 
@@ -418,79 +433,108 @@ out:
 // ------------------------------------------------------------ products
 
 // A segment's tasks are its tiles (the groups in turn), or with kRows2 each
-// tile for each group.  Issuing one task's products takes a warp 400 to 600
-// cycles (waits, descriptors, commits), as long as the tensor pipe needs for
-// them; S = Q K^T and O += P V are therefore issued by a warp each, and run
-// apart by as many tasks as there are S buffers.
-struct Task {
-  int g, tile;       // group, tile within the segment
-  bool last_use;     // the tile's last task
-};
-template <bool kRows2>
-__device__ __forceinline__ Task task_of(int x, bool two) {
-  if (!kRows2) return {x & 1, x, true};
-  return two ? Task{x & 1, x >> 1, (x & 1) != 0} : Task{0, x, true};
-}
+// tile for each group.  Issuing one task's products takes a warp several
+// hundred cycles (waits, descriptors, commits), as long as the tensor pipe
+// needs for them; S = Q K^T and O += P V are therefore issued by a warp each,
+// and run apart by as many tasks as there are S buffers.
 
 // Warp 1: S of every task.
 template <int D, bool kBf16, bool kRows2>
-__device__ __forceinline__ void products_qk(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
+struct ProductsQk {
   using C = Shape<D>;
-  constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
-  const uint32_t q0 = desc_lo(smem_u32(sm.q), 16), k0 = desc_lo(smem_u32(sm.ring), 16);
+  static constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
+  Smem<D, kRows2>& sm;
+  const Params& p;
+  uint32_t tmem, q0, k0;
   Ring<C::kStages> at;
-  Ring<2> buf[2];                              // the groups' S buffers
-  int seg = 0;
-  Segment s;
-  while (w.next(p, s)) {
-    const bool two = kRows2 && rows_of_group(p, s.group, 2 * kRows) > kRows;
-    const int tasks = two ? 2 * s.n : s.n;
-    if (!wait(sm, sm.qfull, seg & 1, p)) return;
-    for (int x = 0; x < tasks; ++x) {
-      const Task t = task_of<kRows2>(x, two);
-      const Ring<2> b = t.g ? buf[1] : buf[0];
-      if (!wait2(sm, sm.pvdone[t.g][b.stage], b.phase ^ 1, sm.kfull[at.stage], at.phase, p)) return;
-      tc_fence_after();
-      issue_qk<C::kChunks>(tmem + 256 + (2 * t.g + b.stage) * kKeys, q0 + (kRows2 ? t.g * (C::kQTile >> 4) : 0),
-                           k0 + at.stage * (2 * C::kTile >> 4), kId, smem_u32(&sm.sfull[t.g][b.stage]),
-                           smem_u32(&sm.kempty[at.stage]), t.last_use, smem_u32(&sm.qfree), x == tasks - 1);
-      if (t.last_use) at.advance();
-      if (t.g) buf[1].advance(); else buf[0].advance();
-    }
-    ++seg;
+  int done[2] = {0, 0};                        // tasks of each group so far
+  __device__ __forceinline__ ProductsQk(Smem<D, kRows2>& sm_, const Params& p_, uint32_t tmem_)
+      : sm(sm_), p(p_), tmem(tmem_), q0(desc_lo(smem_u32(sm_.q), 16)), k0(desc_lo(smem_u32(sm_.ring), 16)) {}
+
+  template <int g>
+  __device__ __forceinline__ bool task(uint32_t q, bool last_use, bool last, int seg) {
+    const int b = done[g] & 1;
+    if (!wait2(sm, sm.pvdone[g][b], ((done[g] >> 1) & 1) ^ 1, sm.kfull[at.stage], at.phase, p)) return false;
+    tc_fence_after();
+    issue_qk<C::kChunks>(tmem + 256 + (2 * g + b) * kKeys, q + (kRows2 ? g * (C::kQTile >> 4) : 0),
+                         k0 + at.stage * (2 * C::kTile >> 4), kId, smem_u32(&sm.sfull[g][b]),
+                         smem_u32(&sm.kempty[at.stage]), last_use, smem_u32(&sm.qfree[seg & 1]), last);
+    ++done[g];
+    if (last_use) at.advance();
+    return true;
   }
-}
+
+  __device__ __forceinline__ void run(Walk w) {
+    int seg = 0;
+    Segment s;
+    while (w.next(p, s)) {
+      if (!wait(sm, sm.qfull, seg & 1, p)) return;
+      const uint32_t q = q0 + (!kRows2 && (seg & 1) ? (C::kQTile >> 4) : 0);
+      if (kRows2 && rows_of_group(p, s.group, 2 * kRows) <= kRows) {
+        for (int j = 0; j < s.n; ++j)
+          if (!task<0>(q, true, j == s.n - 1, seg)) return;
+      } else if (kRows2) {
+        for (int j = 0; j < s.n; ++j)
+          if (!task<0>(q, false, false, seg) || !task<1>(q, true, j == s.n - 1, seg)) return;
+      } else {
+        for (int j = 0; j < s.n; j += 2) {
+          if (!task<0>(q, true, j == s.n - 1, seg)) return;
+          if (j + 1 < s.n && !task<1>(q, true, j == s.n - 2, seg)) return;
+        }
+      }
+      ++seg;
+    }
+  }
+};
 
 // Warp 3: O += P V of every task.
 template <int D, bool kBf16, bool kRows2>
-__device__ __forceinline__ void products_pv(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w) {
+struct ProductsPv {
   using C = Shape<D>;
-  constexpr uint32_t kId = idesc<kBf16>(D, 1);
-  const uint32_t v0 = desc_lo(smem_u32(sm.ring) + C::kTile, kKeys * 128);
+  static constexpr uint32_t kId = idesc<kBf16>(D, 1);
+  Smem<D, kRows2>& sm;
+  const Params& p;
+  uint32_t tmem, v0;
   Ring<C::kStages> at;
-  Ring<2> buf[2];
-  int seg = 0;
-  Segment s;
-  while (w.next(p, s)) {
-    const bool two = kRows2 && rows_of_group(p, s.group, 2 * kRows) > kRows;
-    const int tasks = two ? 2 * s.n : s.n;
-    // The last segment's results have been read out of both accumulators.
-    if (seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
-    for (int x = 0; x < tasks; ++x) {
-      const Task t = task_of<kRows2>(x, two);
-      const Ring<2> b = t.g ? buf[1] : buf[0];
-      const bool first = kRows2 ? t.tile == 0 : x < 2;     // the group's first of the segment: O starts at 0
-      if (!wait2(sm, sm.pfull[t.g][b.stage], b.phase, sm.vfull[at.stage], at.phase, p)) return;
-      tc_fence_after();
-      issue_pv(tmem + t.g * D, tmem + 256 + (2 * t.g + b.stage) * kKeys, v0 + at.stage * (2 * C::kTile >> 4), kId,
-               first ? 0u : 1u, smem_u32(&sm.pvdone[t.g][b.stage]), smem_u32(&sm.vempty[at.stage]), t.last_use,
-               smem_u32(&sm.ofull), x == tasks - 1);
-      if (t.last_use) at.advance();
-      if (t.g) buf[1].advance(); else buf[0].advance();
-    }
-    ++seg;
+  int done[2] = {0, 0};
+  __device__ __forceinline__ ProductsPv(Smem<D, kRows2>& sm_, const Params& p_, uint32_t tmem_)
+      : sm(sm_), p(p_), tmem(tmem_), v0(desc_lo(smem_u32(sm_.ring) + C::kTile, kKeys * 128)) {}
+
+  // `first`: the group's first task of the segment, O starts at 0.
+  template <int g>
+  __device__ __forceinline__ bool task(bool first, bool last_use, bool last) {
+    const int b = done[g] & 1;
+    if (!wait2(sm, sm.pfull[g][b], (done[g] >> 1) & 1, sm.vfull[at.stage], at.phase, p)) return false;
+    tc_fence_after();
+    issue_pv(tmem + g * D, tmem + 256 + (2 * g + b) * kKeys, v0 + at.stage * (2 * C::kTile >> 4), kId, first ? 0u : 1u,
+             smem_u32(&sm.pvdone[g][b]), smem_u32(&sm.vempty[at.stage]), last_use, smem_u32(&sm.ofull), last);
+    ++done[g];
+    if (last_use) at.advance();
+    return true;
   }
-}
+
+  __device__ __forceinline__ void run(Walk w) {
+    int seg = 0;
+    Segment s;
+    while (w.next(p, s)) {
+      // The last segment's results have been read out of both accumulators.
+      if (seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
+      if (kRows2 && rows_of_group(p, s.group, 2 * kRows) <= kRows) {
+        for (int j = 0; j < s.n; ++j)
+          if (!task<0>(j == 0, true, j == s.n - 1)) return;
+      } else if (kRows2) {
+        for (int j = 0; j < s.n; ++j)
+          if (!task<0>(j == 0, false, false) || !task<1>(j == 0, true, j == s.n - 1)) return;
+      } else {
+        for (int j = 0; j < s.n; j += 2) {
+          if (!task<0>(j == 0, true, j == s.n - 1)) return;
+          if (j + 1 < s.n && !task<1>(j == 0, true, j == s.n - 2)) return;
+        }
+      }
+      ++seg;
+    }
+  }
+};
 
 // ------------------------------------------------------------ softmax
 
@@ -512,36 +556,38 @@ __device__ __forceinline__ void store_block(const Params& p, const float* o, int
   }
 }
 
-// A segment's Q rows into the swizzled tile, by all softmax warps: each group
-// its own tile, or half the rows of each warp's 32 when the groups share one.
+// Starts the copies of a segment's Q rows into a swizzled tile, by all softmax
+// warps: each group its own tile, or half the rows of each warp's 32 when the
+// groups share one.
 template <int D, bool kRows2>
-__device__ __forceinline__ void load_q(Smem<D, kRows2>& sm, const Params& p, const Segment& s, int g, int wq, int lane) {
+__device__ __forceinline__ void start_q(Smem<D, kRows2>& sm, const Params& p, const Segment& s, int seg, int g, int wq,
+                                        int lane) {
   using C = Shape<D>;
   constexpr int kSpan = kRows2 ? 2 * kRows : kRows;
   constexpr int kUnits = D / 8;                            // 16-byte units a row
-  constexpr int kPer = 32 / kUnits;                        // rows a warp loads at once
-  constexpr int kLoads = (kRows2 ? 32 : 16) / kPer;
+  constexpr int kPer = 32 / kUnits;                        // rows a warp copies at once
   const int mine = rows_of_group(p, s.group, kSpan) - (kRows2 ? g * kRows : 0);
   const int R = s.group * kSpan + (kRows2 ? g * kRows : 0) + wq * 32 + lane;
   const int i = R / p.G;
-  // Each lane knows its row's address; the lanes that load a row ask for it.
+  // Each lane knows its row's address; the lanes that copy a row ask for it.
   const long long base = wq * 32 + lane < mine ? s.b * p.q_stride[0] + i * p.q_stride[1] +
                                                      (s.head * p.G + (R - i * p.G)) * p.q_stride[2]
                                                : 0;
-  uint8_t* const tile = sm.q + (kRows2 ? g * C::kQTile : 0);
+  const uint32_t tile = smem_u32(sm.q) + (kRows2 ? g : seg & 1) * C::kQTile;
   const int r0 = (kRows2 ? 0 : g * 16) + lane / kUnits, u = lane % kUnits;
-  uint4 x[kLoads];
 #pragma unroll
-  for (int e = 0; e < kLoads; ++e) {
+  for (int e = 0; e < (kRows2 ? 32 : 16) / kPer; ++e) {
     const long long off = __shfl_sync(0xFFFFFFFFu, base, r0 + e * kPer);
-    if (wq * 32 + r0 + e * kPer < mine) x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + off) + u);
-  }
-#pragma unroll
-  for (int e = 0; e < kLoads; ++e) {
     const int row = wq * 32 + r0 + e * kPer;
     if (row < mine)
-      *reinterpret_cast<uint4*>(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = x[e];
+      cp_async_16(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), p.q + off + u * 16, true);
   }
+  cp_async_commit();
+}
+// The copies have landed: hands the tile to the products.
+template <int D, bool kRows2>
+__device__ __forceinline__ void finish_q(Smem<D, kRows2>& sm, int lane) {
+  cp_async_wait<0>();
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&sm.qfull));
@@ -566,8 +612,17 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
   int kt = 0, seg = 0, n = 0;                              // n: tasks of this group so far
   Segment s, next;
   bool more = w.next(p, s);
-  if (more) load_q<D, kRows2>(sm, p, s, g, wq, lane);
+  if (more) {
+    start_q<D, kRows2>(sm, p, s, 0, g, wq, lane);
+    finish_q<D, kRows2>(sm, lane);
+  }
   for (; more; s = next) {
+    more = w.next(p, next);
+    if (!kRows2 && more) {
+      // The next segment's Q lands while this one's tiles are worked on.
+      if (seg > 0 && !wait(sm, sm.qfree[(seg - 1) & 1], ((seg - 1) >> 1) & 1, p)) return;
+      start_q<D, kRows2>(sm, p, next, seg + 1, g, wq, lane);
+    }
     const int rows = rows_of_group(p, s.group, kSpan);
     const int row0 = s.group * kSpan + (kRows2 ? g * kRows : 0);
     const int mine = kRows2 ? rows - g * kRows : rows;     // valid rows of this group's tile
@@ -676,10 +731,14 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
 
     // ---- end of the segment.  The next one's Q first: its products then
     // start while this one's results are written.
-    more = w.next(p, next);
     if (more) {
-      if (!wait(sm, sm.qfree, seg & 1, p)) return;
-      load_q<D, kRows2>(sm, p, next, g, wq, lane);
+      if (kRows2) {
+        if (!wait(sm, sm.qfree[seg & 1], (seg >> 1) & 1, p)) return;
+        start_q<D, kRows2>(sm, p, next, seg + 1, g, wq, lane);
+      } else if (!wait(sm, sm.qfull, seg & 1, p)) {        // (a group without a task has not seen it)
+        return;
+      }
+      finish_q<D, kRows2>(sm, lane);
     }
     const bool direct = s.n == s.nt;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
@@ -754,16 +813,20 @@ __device__ __forceinline__ void drain_products(uint64_t& bar) {
 // Tells the merge of the cut unit that starts in this CTA's run, if there is
 // one: it goes on in the CTAs after this one.  Written before the first wait,
 // so that the merge finds it whatever becomes of the loads.
-__device__ __forceinline__ void note_cut_unit(const Params& p, Walk w, long long t1, long long total, long long ctas) {
+__device__ __forceinline__ void note_cut_unit(const Params& p, Walk w, long long t1, long long total, long long teams) {
   int4 d = make_int4(0, 0, 0, 0);
   Segment s;
   int segs = 0;
-  while (w.next(p, s)) ++segs;
-  if (segs > 0 && s.tile0 == 0 && s.n < s.nt) {
+  bool at_end = false;
+  while (w.next(p, s)) {
+    ++segs;
+    at_end = w.t == t1;
+  }
+  if (at_end && s.tile0 == 0 && s.n < s.nt) {
     const long long end = t1 - s.n + s.nt;                 // past the unit's last tile
-    const long long last = (end * ctas - 1) / total;       // the CTA that has it
+    const long long last = (end * teams - 1) / total;      // the team that has it
     d = make_int4(s.b, s.head * p.groups + s.group, 2 * static_cast<int>(blockIdx.x) + (segs > 1 ? 1 : 0),
-                  static_cast<int>(last - blockIdx.x) + 1);
+                  static_cast<int>(last - blockIdx.x / p.members) + 1);
   }
   p.desc[blockIdx.x] = d;
 }
@@ -773,8 +836,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
   using S = Smem<D, kRows2>;
   using C = Shape<D>;
-  extern __shared__ uint8_t smem_raw[];
-  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // Shared memory is full to the last KB: the tiles' alignment is asked for, and
+  // checked, instead of made with a spare KB.
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  if (smem_u32(smem_raw) & 1023) {
+    if (threadIdx.x == 0) {
+      atomicOr(p.status, kBitTimeout);
+      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   if (tid == 0) {
@@ -796,7 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.pvdone[i >> 1][i & 1]), 1);
     }
     mbar_init(smem_u32(&sm.qfull), 8);
-    mbar_init(smem_u32(&sm.qfree), 1);
+    mbar_init(smem_u32(&sm.qfree[0]), 1);
+    mbar_init(smem_u32(&sm.qfree[1]), 1);
     mbar_init(smem_u32(&sm.ofull), 1);
     mbar_init(smem_u32(&sm.ofree), 8);
     mbar_init(smem_u32(&sm.mlx), 8);
@@ -815,13 +888,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's run of tiles: each thread sums a run of streams, then a
   // scan over threads; the thread whose streams hold the first tile says which.
-  const int units = p.Hkv * p.groups;
+  const int units = p.Hkv * p.sets;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long sum = 0;
   int len;
   for (int b = b0; b < b1; ++b) {
-    sum += static_cast<long long>(stream_tiles(p, b, len)) * units;
+    sum += static_cast<long long>(stream_work(p, stream_tiles(p, b, len))) * units;
     if (blockIdx.x == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
   }
   long long inc = sum;
@@ -840,15 +913,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i == warp) before = total;
     total += sm.warp_sum[i];
   }
-  long long ctas = total / p.min_tiles;
-  ctas = ctas < 1 ? 1 : (ctas < gridDim.x ? ctas : gridDim.x);
-  const long long t0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-  const long long t1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+  // Teams of `members` CTAs share a run.
+  const int all = static_cast<int>(gridDim.x) / p.members, team = static_cast<int>(blockIdx.x) / p.members;
+  long long teams = total / p.min_tiles;
+  teams = teams < 1 ? 1 : (teams < all ? teams : all);
+  const long long t0 = team < teams ? total * team / teams : total;
+  const long long t1 = team < teams ? total * (team + 1) / teams : total;
   before += inc - sum;
   if (t0 >= before && t0 < before + sum) {
     int b = b0;
     while (true) {
-      const long long n = static_cast<long long>(stream_tiles(p, b, len)) * units;
+      const long long n = static_cast<long long>(stream_work(p, stream_tiles(p, b, len))) * units;
       if (t0 < before + n) break;
       before += n;
       ++b;
@@ -864,12 +939,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.box_rows == 0) load_gather<D, kRows2>(sm, p, walk, warp == 2);
     else load_tma<D, kRows2>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
   } else if (warp == 1) {
-    products_qk<D, kBf16, kRows2>(sm, p, tmem, walk);
+    ProductsQk<D, kBf16, kRows2>(sm, p, tmem).run(walk);
     drain_products(sm.drain[0]);
   } else if (warp == 3) {
-    if (lane == 0) note_cut_unit(p, walk, t1, total, ctas);
+    if (lane == 0 && !p.whole) note_cut_unit(p, walk, t1, total, teams);
     __syncwarp();
-    products_pv<D, kBf16, kRows2>(sm, p, tmem, walk);
+    ProductsPv<D, kBf16, kRows2>(sm, p, tmem).run(walk);
     drain_products(sm.drain[1]);
   } else if (warp >= 4) {
     softmax<D, kBf16, kRows2>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
@@ -893,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merges the partials of each cut unit: block (x, c) takes eight rows of the
 // unit that CTA c of the split kernel started.  Its parts are that CTA's slot
-// and the first slots of the CTAs after it.  The parts' weights are worked out
+// and the first slots of the same member of the teams after it.  The parts' weights are worked out
 // once for the block; a thread then sums one row's four columns over its part
 // group's parts (kGroups of them take the parts in turn when parts are many),
 // eight loads in flight, and the groups' sums are added in order.
@@ -912,8 +987,9 @@ __global__ void __launch_bounds__(2 * D * kGroups) combine_kernel(const Params p
   const int span = p.part_rows;
   const int first_row = static_cast<int>(blockIdx.x) * 8;
   const int r = tid & 7, rr = first_row + r;               // (part_rows is a multiple of 8)
-  const int next = 2 * (static_cast<int>(blockIdx.y) + 1);
-  auto slot_of = [&](int k) { return static_cast<size_t>(k ? next + 2 * (k - 1) : d.z); };
+  auto slot_of = [&](int k) {
+    return static_cast<size_t>(k ? 2 * (static_cast<int>(blockIdx.y) + k * p.members) : d.z);
+  };
 
   // Parts k = tid / 8, ... of row r: the row's max, then weights and mass.
   float m = -CUDART_INF_F;
