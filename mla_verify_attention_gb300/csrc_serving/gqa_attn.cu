@@ -24,13 +24,14 @@ constexpr int kMinTiles = 2;
 constexpr int kWholeKeys = 512;
 // Row groups of a head that CTAs take side by side, at most.
 constexpr int kMaxMembers = 16;
+
 // Parts a unit from which four part groups share the merge of a row.
-constexpr int kManyParts = 32;
+constexpr int kManyParts = 8;
 
 struct Plan {
   bool rows2;          // more than 128 rows a key head: two row tiles a CTA
   int groups;          // row groups a key head
-  int part_rows;       // rows of a partial, a multiple of 8
+  int part_rows;       // rows of a partial, a multiple of 16
 };
 
 bool shape_ok(int B, int q, int H, int Hkv, int D) {
@@ -44,7 +45,7 @@ Plan plan(int q, int H, int Hkv) {
   p.rows2 = rows > kRows;
   const int span = p.rows2 ? 2 * kRows : kRows;
   p.groups = (rows + span - 1) / span;
-  p.part_rows = rows < span ? (rows + 7) / 8 * 8 : span;
+  p.part_rows = rows < span ? (rows + 15) / 16 * 16 : span;
   return p;
 }
 
@@ -66,18 +67,18 @@ Layout layout(const Plan& pl, int grid, int D) {
 }
 
 using AttnFn = void (*)(CUtensorMap, CUtensorMap, Params);
-using CombineFn = void (*)(Params);
+using CombineFn = void (*)(Params, int);
 
 struct Variant {
   AttnFn attn;
-  CombineFn combine[2];   // one part group; four
+  CombineFn combine[2];   // many units; many parts
   size_t smem;
 };
 template <int D, bool kBf16, bool kRows2>
 Variant variant() {
   constexpr size_t smem = sizeof(Smem<D, kRows2>);
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16, kRows2>, {combine_kernel<D, kBf16, 1>, combine_kernel<D, kBf16, 4>}, smem};
+  return {attn_kernel<D, kBf16, kRows2>, {combine_many_units<D, kBf16>, combine_many_parts<D, kBf16>}, smem};
 }
 
 std::mutex g_ready_mutex;
@@ -219,6 +220,9 @@ int run(const Call& c) {
   p.Smax = c.Smax;
   p.groups = pl.groups;
   p.part_rows = pl.part_rows;
+  const int rows_a_head = c.q_len * (c.H / c.Hkv);
+  const long long units = static_cast<long long>(c.B) * c.Hkv * pl.groups;
+  p.desc_units = units <= grid;
   p.whole = c.Smax <= kWholeKeys;
   p.min_tiles = p.whole ? 1 : kMinTiles;
   p.sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
@@ -245,12 +249,21 @@ int run(const Call& c) {
     return MLA_ERR_LAUNCH;
   }
   if (p.whole) return MLA_OK;
-  // Few units: each is cut into many parts.
-  const bool many = static_cast<long long>(c.B) * c.Hkv * pl.groups * kManyParts <= grid;
-  cfg.gridDim = dim3(pl.part_rows / 8, grid, 1);
-  cfg.blockDim = dim3(2 * c.D * (many ? 4 : 1), 1, 1);
+  // The merge's shape: by the parts a cut unit has, about, if the blocks that
+  // gives are not more than fit the device at once (three an SM).
+  const int entries = p.desc_units ? static_cast<int>(units) : grid;
+  const int pairs = ((rows_a_head < pl.part_rows ? rows_a_head : pl.part_rows) + 1) / 2;
+  const bool many = p.desc_units && static_cast<long long>(entries) * pairs <= 3 * grid &&
+                    (grid / p.members) / (static_cast<long long>(c.B) * c.Hkv * p.sets) >= kManyParts;
+  if (many) {
+    cfg.gridDim = dim3(pairs, entries, 1);
+  } else {
+    const long long chunks = static_cast<long long>(entries) * (pl.part_rows / kMergeUnits);
+    cfg.gridDim = dim3(static_cast<unsigned>(chunks < 3 * grid ? chunks : 3 * grid), 1, 1);
+  }
+  cfg.blockDim = dim3(c.D / 4 * kMergeUnits, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, var.combine[many ? 1 : 0], p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, var.combine[many ? 1 : 0], p, entries) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }

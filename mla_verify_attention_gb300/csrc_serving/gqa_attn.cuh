@@ -18,7 +18,7 @@
 // batches balance to one tile and nothing is planned on the host.  A (stream,
 // head, row group) unit that lies within one run is written to `out`; one that
 // is cut leaves unnormalised partials (at most two a CTA, which bounds the
-// workspace by the grid) that combine_kernel merges in order.
+// workspace by the grid) that the combine kernels merge in order.
 //
 // CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), two
 // issue tcgen05.mma, eight softmax warps in two groups own one accumulator O
@@ -57,12 +57,13 @@ struct Params {
   const int32_t* block_table;      // null: contiguous caches
   void* out;
   float* lse;
-  int4* desc;                      // [grid] the cut unit each CTA starts: {stream, head * groups + group, first slot, parts}
+  int4* desc;                      // [grid] cut units: {stream, head * groups + group, first slot, parts}
   float2* part_ml;                 // [2 * grid][part_rows]
-  float4* part_o;                  // [2 * grid][D / 4][part_rows]
+  float4* part_o;                  // [2 * grid][part_rows][D / 4]
   unsigned int* status;
   int B, q_len, H, Hkv, G, Smax, groups, part_rows, min_tiles;
   int members, sets;               // row groups side by side, and one after the other
+  int desc_units;                  // entries of `desc`: one a unit, or one a CTA
   int whole;                       // units are not cut (short caches): the work is counted in units
   int max_blocks, page, pool_pages;
   int box_rows;                    // rows a TMA box: 64 or a divisor that no page boundary cuts; 0: gather
@@ -538,21 +539,21 @@ struct ProductsPv {
 
 // ------------------------------------------------------------ softmax
 
-// One row's result, columns c .. c + 31: fp32 to the partials or rounded to `out`.
-template <int D, bool kBf16>
-__device__ __forceinline__ void store_block(const Params& p, const float* o, int c, bool direct, long long out_row,
-                                            int slot, int rr) {
-  if (direct) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + out_row * (D * 2) + c * 2);
+// A warp's 32 rows of 64 bytes, one a lane, turned in `buf` (2 KB, 16-byte
+// units XOR-swizzled by row pair) so that four lanes then write one row's 64
+// bytes: row 8 i + lane / 4 to dst[i] (null: nothing), in units of 16 bytes.
+// (Stored straight from the lanes' rows, every store touched 32 lines.)
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint4* v, uint8_t* const* dst, int lane) {
+  __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      dst[e] = make_uint4(pack2<kBf16>(o[8 * e], o[8 * e + 1]), pack2<kBf16>(o[8 * e + 2], o[8 * e + 3]),
-                          pack2<kBf16>(o[8 * e + 4], o[8 * e + 5]), pack2<kBf16>(o[8 * e + 6], o[8 * e + 7]));
-  } else {
-    float4* dst = p.part_o + (static_cast<size_t>(slot) * (D / 4) + c / 4) * p.part_rows + rr;
+  for (int e = 0; e < 4; ++e)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = v[e];
+  __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      dst[static_cast<size_t>(e) * p.part_rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * i + (lane >> 2);
+    const uint4 x = *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+    if (dst[i] != nullptr) *reinterpret_cast<uint4*>(dst[i]) = x;
   }
 }
 
@@ -729,15 +730,10 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[g][buf]));
     }
 
-    // ---- end of the segment.  The next one's Q first: its products then
-    // start while this one's results are written.
-    if (more) {
-      if (kRows2) {
-        if (!wait(sm, sm.qfree[seg & 1], (seg >> 1) & 1, p)) return;
-        start_q<D, kRows2>(sm, p, next, seg + 1, g, wq, lane);
-      } else if (!wait(sm, sm.qfull, seg & 1, p)) {        // (a group without a task has not seen it)
-        return;
-      }
+    // ---- end of the segment.  When Q has two tiles the next one's is handed
+    // over first: its products then start while this one's results are written.
+    if (!kRows2 && more) {
+      if (!wait(sm, sm.qfull, seg & 1, p)) return;         // (a group without a task has not seen it)
       finish_q<D, kRows2>(sm, lane);
     }
     const bool direct = s.n == s.nt;
@@ -768,6 +764,20 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
       }
       const int c0 = kRows2 ? 0 : g * (D / 2), c1 = kRows2 ? D : c0 + D / 2;
       const uint32_t o0 = tmem + lanes + (kRows2 ? g * D : 0);
+      // The products are through with this segment's Q: the first 2 KB of the
+      // rows that this warp itself copies are free to turn the results in.
+      uint8_t* const buf = sm.q + (kRows2 ? g : seg & 1) * C::kQTile + (wq * 32 + (kRows2 ? 0 : g * 16)) * 128;
+      uint8_t* dst[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 8 * e + (lane >> 2);
+        const long long orow = __shfl_sync(0xFFFFFFFFu, out_row, row);
+        uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) + (orow * D + c0) * 2
+                                   : reinterpret_cast<uint8_t*>(
+                                         p.part_o + (static_cast<size_t>(slot) * p.part_rows + rr - lane + row) * (D / 4) +
+                                         c0 / 4);
+        dst[e] = wq * 32 + row < mine ? to + (lane & 3) * 16 : nullptr;
+      }
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
         uint32_t x0[32];
@@ -784,7 +794,29 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = w0 * __uint_as_float(x0[e]);
         }
-        if (valid) store_block<D, kBf16>(p, o, c, direct, out_row, slot, rr);
+        uint4 v[4];
+        if (direct) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = make_uint4(pack2<kBf16>(o[8 * e], o[8 * e + 1]), pack2<kBf16>(o[8 * e + 2], o[8 * e + 3]),
+                              pack2<kBf16>(o[8 * e + 4], o[8 * e + 5]), pack2<kBf16>(o[8 * e + 6], o[8 * e + 7]));
+          store_rows(buf, v, dst, lane);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = make_uint4(__float_as_uint(o[16 * h + 4 * e]), __float_as_uint(o[16 * h + 4 * e + 1]),
+                                __float_as_uint(o[16 * h + 4 * e + 2]), __float_as_uint(o[16 * h + 4 * e + 3]));
+            store_rows(buf, v, dst, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (h == 0 && dst[e] != nullptr) dst[e] += 64;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (dst[e] != nullptr) dst[e] += 64;
       }
       if (valid && (kRows2 || g == 0)) {
         if (direct)
@@ -796,6 +828,10 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.ofree));
+    if (kRows2 && more) {
+      start_q<D, kRows2>(sm, p, next, seg + 1, g, wq, lane);
+      finish_q<D, kRows2>(sm, lane);
+    }
     kt += s.n;
     ++seg;
   }
@@ -810,25 +846,26 @@ __device__ __forceinline__ void drain_products(uint64_t& bar) {
   __syncwarp();
 }
 
-// Tells the merge of the cut unit that starts in this CTA's run, if there is
-// one: it goes on in the CTAs after this one.  Written before the first wait,
-// so that the merge finds it whatever becomes of the loads.
-__device__ __forceinline__ void note_cut_unit(const Params& p, Walk w, long long t1, long long total, long long teams) {
+// Tells the merge about the units that start in this CTA's run: a cut one goes
+// on in the teams after this one (parts > 0), a whole one is none of its
+// business (0).  With p.desc_units there is an entry a unit, else one a CTA, for
+// the only unit that can be cut, its last.  Written before the first wait, so
+// that the merge finds it whatever becomes of the loads.
+__device__ __forceinline__ void note_cut_units(const Params& p, Walk w, long long t1, long long total, long long teams) {
+  const int cta = static_cast<int>(blockIdx.x);
   int4 d = make_int4(0, 0, 0, 0);
   Segment s;
-  int segs = 0;
-  bool at_end = false;
-  while (w.next(p, s)) {
-    ++segs;
-    at_end = w.t == t1;
+  for (int seg = 0; w.next(p, s); ++seg) {
+    if (s.tile0 != 0) continue;
+    const int hg = s.head * p.groups + s.group;
+    if (s.n < s.nt) {
+      const long long end = t1 - s.n + s.nt;               // past the unit's last tile
+      const long long last = (end * teams - 1) / total;    // the team that has it
+      d = make_int4(s.b, hg, 2 * cta + (seg > 0 ? 1 : 0), static_cast<int>(last - cta / p.members) + 1);
+    }
+    if (p.desc_units) p.desc[s.b * p.Hkv * p.groups + hg] = d;
   }
-  if (at_end && s.tile0 == 0 && s.n < s.nt) {
-    const long long end = t1 - s.n + s.nt;                 // past the unit's last tile
-    const long long last = (end * teams - 1) / total;      // the team that has it
-    d = make_int4(s.b, s.head * p.groups + s.group, 2 * static_cast<int>(blockIdx.x) + (segs > 1 ? 1 : 0),
-                  static_cast<int>(last - blockIdx.x / p.members) + 1);
-  }
-  p.desc[blockIdx.x] = d;
+  if (!p.desc_units) p.desc[cta] = d;
 }
 
 template <int D, bool kBf16, bool kRows2>
@@ -841,16 +878,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   if (smem_u32(smem_raw) & 1023) {
+    grid_dependency_wait();
     if (threadIdx.x == 0) {
       atomicOr(p.status, kBitTimeout);
-      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);          // (an entry a unit: there are no more than CTAs)
     }
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  grid_dependency_wait();
   if (tid == 0) {
-    grid_launch_dependents();
     if (p.box_rows) {
       tma_prefetch_desc(&map_k);
       tma_prefetch_desc(&map_v);
@@ -885,6 +921,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
     tmem_relinquish();
   }
+  grid_dependency_wait();                                  // nothing of the caller's was touched so far
+  if (tid == 0) grid_launch_dependents();
 
   // ---- this CTA's run of tiles: each thread sums a run of streams, then a
   // scan over threads; the thread whose streams hold the first tile says which.
@@ -942,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ProductsQk<D, kBf16, kRows2>(sm, p, tmem).run(walk);
     drain_products(sm.drain[0]);
   } else if (warp == 3) {
-    if (lane == 0 && !p.whole) note_cut_unit(p, walk, t1, total, teams);
+    if (lane == 0 && !p.whole) note_cut_units(p, walk, t1, total, teams);
     __syncwarp();
     ProductsPv<D, kBf16, kRows2>(sm, p, tmem).run(walk);
     drain_products(sm.drain[1]);
@@ -952,6 +990,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Streams without keys.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (stream_tiles(p, b, len) != 0) continue;
+    if (p.desc_units && !p.whole)
+      for (int u = tid; u < p.Hkv * p.groups; u += kThreads) p.desc[b * p.Hkv * p.groups + u] = make_int4(0, 0, 0, 0);
     const long long rows = static_cast<long long>(p.q_len) * p.H;
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + b * rows * (D * 2));
     for (long long x = tid; x < rows * (D / 8); x += kThreads) o[x] = make_uint4(0, 0, 0, 0);
@@ -966,94 +1006,138 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merges the partials of each cut unit: block (x, c) takes eight rows of the
-// unit that CTA c of the split kernel started.  Its parts are that CTA's slot
-// and the first slots of the same member of the teams after it.  The parts' weights are worked out
-// once for the block; a thread then sums one row's four columns over its part
-// group's parts (kGroups of them take the parts in turn when parts are many),
-// eight loads in flight, and the groups' sums are added in order.
+// Merges the partials of the cut units.  A unit's parts are the first one's slot
+// and the first slots of the same member of the teams after it.  A block takes
+// kR rows of a unit; kP part groups of threads share the parts, a thread one
+// row's four columns of eight parts at a time (weights, sums and values loaded
+// together), and the groups' results are put together through shared memory.
+// Everything is added in a fixed order.  The call is a chain of a few reads
+// that depend on each other (~1.5 us after the split kernel has ended), so there
+// is as little else in it as there can be.  Two shapes:
+//   few units, many parts: two rows and four part groups; block (x, y) takes
+//     chunk x of the unit of entry y;
+//   many units, few parts: eight rows and one part group; every block first lists
+//     the cut units (all entries read at once) and takes chunks of them in turn
+//     (a block a chunk and entry were 9,728 that mostly found nothing to do).
 constexpr int kMaxParts = 320;               // CTAs of the split kernel at most
-template <int D, bool kBf16, int kGroups>
-__global__ void __launch_bounds__(2 * D * kGroups) combine_kernel(const Params p) {
-  constexpr int kThreadsG = 2 * D;           // 8 rows x D / 4 column quads
-  constexpr int kWarps = kThreadsG * kGroups / 32;
-  __shared__ float weight[kMaxParts][8];
-  __shared__ float top[kWarps][8], mass[kWarps][8];
-  __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][kThreadsG];
-  grid_dependency_wait();
-  const int4 d = p.desc[blockIdx.y];
-  if (d.w == 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int span = p.part_rows;
-  const int first_row = static_cast<int>(blockIdx.x) * 8;
-  const int r = tid & 7, rr = first_row + r;               // (part_rows is a multiple of 8)
-  auto slot_of = [&](int k) {
-    return static_cast<size_t>(k ? 2 * (static_cast<int>(blockIdx.y) + k * p.members) : d.z);
-  };
-
-  // Parts k = tid / 8, ... of row r: the row's max, then weights and mass.
-  float m = -CUDART_INF_F;
-  for (int k = tid >> 3; k < d.w; k += kThreadsG * kGroups / 8) m = fmaxf(m, p.part_ml[slot_of(k) * span + rr].x);
-  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-  if ((tid & 31) < 8) top[warp][r] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, top[w][r]);
-  float l = 0.f;
-  for (int k = tid >> 3; k < d.w; k += kThreadsG * kGroups / 8) {
-    const float2 ml = p.part_ml[slot_of(k) * span + rr];
-    const float w = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - m);
-    weight[k][r] = w;
-    l += w * ml.y;
-  }
-  l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-  l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-  if ((tid & 31) < 8) mass[warp][r] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) l += mass[w][r];
-
-  const int group = tid / kThreadsG, t = tid % kThreadsG, c4 = t >> 3;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = group; k < d.w; k += 8 * kGroups) {
-    float4 x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k + e * kGroups < d.w) x[e] = __ldcg(p.part_o + (slot_of(k + e * kGroups) * (D / 4) + c4) * span + rr);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k + e * kGroups < d.w) {
-        const float w = weight[k + e * kGroups][r];
-        o.x += w * x[e].x;
-        o.y += w * x[e].y;
-        o.z += w * x[e].z;
-        o.w += w * x[e].w;
-      }
-  }
-  if (kGroups > 1) {
-    if (group) sums[group - 1][t] = o;
-    __syncthreads();
-    if (group) return;
-#pragma unroll
-    for (int g = 0; g < kGroups - 1; ++g) {
-      const float4 x = sums[g][t];
-      o.x += x.x;
-      o.y += x.y;
-      o.z += x.z;
-      o.w += x.w;
-    }
-  }
+constexpr int kMergeUnits = 8;               // rows x part groups of a block
+constexpr int kMergeParts = 4;               // part groups when there are many parts
+template <int D, bool kBf16, int kP>
+__device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int chunk) {
+  constexpr int kR = kMergeUnits / kP;
+  constexpr int kGroup = D / 4 * kR;                       // threads a part group
+  __shared__ float4 sums[kP > 1 ? kP - 1 : 1][kGroup];
+  __shared__ float2 stats[kP > 1 ? kP - 1 : 1][kR];
+  const int tid = threadIdx.x, c4 = tid % (D / 4), r = tid / (D / 4) % kR, group = tid / kGroup, t = tid % kGroup;
+  const int parts = d.w, rr = chunk * kR + r;
   const int full = p.q_len * p.G > kRows ? 2 * kRows : kRows;
   const int head = d.y / p.groups, R = (d.y - head * p.groups) * full + rr;
-  if (R >= p.q_len * p.G) return;
+  const bool valid = rr < full && R < p.q_len * p.G;
+  // Row rr of part k >= 1 lies in slot 2 * (CTA of part 0 + k * members).
+  const size_t row_k = static_cast<size_t>(2 * (d.z >> 1)) * p.part_rows + rr, row_0 = static_cast<size_t>(d.z) * p.part_rows + rr;
+  const size_t step = static_cast<size_t>(2 * p.members) * p.part_rows;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -CUDART_INF_F, l = 0.f;
+  for (int k0 = group; valid && k0 < parts; k0 += 8 * kP) {
+    float4 x[8];
+    float2 y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = k0 + e * kP;
+      y[e] = make_float2(-CUDART_INF_F, 0.f);
+      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < parts) {
+        const size_t row = k ? row_k + k * step : row_0;
+        y[e] = __ldcg(p.part_ml + row);
+        x[e] = __ldcg(p.part_o + row * (D / 4) + c4);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, y[e].x);
+    const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    m = top;
+    l *= keep;
+    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float w = y[e].x == -CUDART_INF_F ? 0.f : ex2(y[e].x - m);
+      l += w * y[e].y;
+      o.x += w * x[e].x;
+      o.y += w * x[e].y;
+      o.z += w * x[e].z;
+      o.w += w * x[e].w;
+    }
+  }
+  if (kP > 1) {
+    if (group) {
+      sums[group - 1][t] = o;
+      if (c4 == 0) stats[group - 1][r] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (group) return;
+    float top = m;
+#pragma unroll
+    for (int g = 0; g < kP - 1; ++g) top = fmaxf(top, stats[g][r].x);
+    const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    m = top;
+    l *= keep;
+    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+    for (int g = 0; g < kP - 1; ++g) {
+      const float2 y = stats[g][r];
+      const float4 x = sums[g][t];
+      const float w = y.x == -CUDART_INF_F ? 0.f : ex2(y.x - m);
+      l += w * y.y;
+      o.x += w * x.x;
+      o.y += w * x.y;
+      o.z += w * x.z;
+      o.w += w * x.w;
+    }
+  }
+  if (!valid) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int i = R / p.G;
   const long long row = (static_cast<long long>(d.x) * p.q_len + i) * p.H + head * p.G + (R - i * p.G);
   reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (D * 2))[c4] =
       make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
   if (c4 == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_parts(const Params p, int) {
+  grid_dependency_wait();
+  const int4 d = __ldcg(p.desc + blockIdx.y);
+  if (d.w != 0) merge_rows<D, kBf16, kMergeParts>(p, d, blockIdx.x);
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_units(const Params p, int entries) {
+  constexpr int kThreadsM = D / 4 * kMergeUnits, kWarps = kThreadsM / 32;
+  __shared__ int4 cut[kMaxParts];
+  __shared__ int warp_cut[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  grid_dependency_wait();
+  int n_cut = 0;
+  for (int base = 0; base < entries; base += kThreadsM) {
+    const int4 d = base + tid < entries ? __ldcg(p.desc + base + tid) : make_int4(0, 0, 0, 0);
+    const unsigned ballot = __ballot_sync(0xFFFFFFFFu, d.w != 0);
+    if ((tid & 31) == 0) warp_cut[warp] = __popc(ballot);
+    __syncthreads();
+    int at = n_cut;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp && d.w != 0) cut[at + __popc(ballot & ((1u << (tid & 31)) - 1u))] = d;
+      at += warp_cut[w];
+    }
+    n_cut = at;
+    __syncthreads();
+  }
+  const int chunks = p.part_rows / kMergeUnits;
+  for (int item = blockIdx.x; item < n_cut * chunks; item += gridDim.x) {
+    const int u = item / chunks;
+    merge_rows<D, kBf16, 1>(p, cut[u], item - u * chunks);
+  }
 }
 
 }  // namespace gqa
