@@ -29,8 +29,7 @@ constexpr int kMaxMembers = 16;
 constexpr int kManyParts = 8;
 
 struct Plan {
-  bool rows2;          // more than 128 rows a key head: two row tiles a CTA
-  int groups;          // row groups a key head
+  int groups;          // groups of 128 rows a key head
   int part_rows;       // rows of a partial, a multiple of 16
 };
 
@@ -42,10 +41,8 @@ bool shape_ok(int B, int q, int H, int Hkv, int D) {
 Plan plan(int q, int H, int Hkv) {
   const int rows = q * (H / Hkv);
   Plan p;
-  p.rows2 = rows > kRows;
-  const int span = p.rows2 ? 2 * kRows : kRows;
-  p.groups = (rows + span - 1) / span;
-  p.part_rows = rows < span ? (rows + 15) / 16 * 16 : span;
+  p.groups = (rows + kRows - 1) / kRows;
+  p.part_rows = rows < kRows ? (rows + 15) / 16 * 16 : kRows;
   return p;
 }
 
@@ -74,22 +71,20 @@ struct Variant {
   CombineFn combine[2];   // many units; many parts
   size_t smem;
 };
-template <int D, bool kBf16, bool kRows2>
+template <int D, bool kBf16>
 Variant variant() {
-  constexpr size_t smem = sizeof(Smem<D, kRows2>);
+  constexpr size_t smem = sizeof(Smem<D>);
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16, kRows2>, {combine_many_units<D, kBf16>, combine_many_parts<D, kBf16>}, smem};
+  return {attn_kernel<D, kBf16>, {combine_many_units<D, kBf16>, combine_many_parts<D, kBf16>}, smem};
 }
 
 std::mutex g_ready_mutex;
-bool g_ready[kMaxDevices][8];
+bool g_ready[kMaxDevices][4];
 
 // The kernels for these sizes, ready on the current device.
-int pick(int D, int dtype, bool rows2, Variant* out) {
-  static const Variant all[8] = {variant<64, true, false>(),  variant<64, true, true>(),  variant<64, false, false>(),
-                                 variant<64, false, true>(),  variant<128, true, false>(), variant<128, true, true>(),
-                                 variant<128, false, false>(), variant<128, false, true>()};
-  const int n = (D == 128 ? 4 : 0) + (dtype == MLA_FP16 ? 2 : 0) + (rows2 ? 1 : 0);
+int pick(int D, int dtype, Variant* out) {
+  static const Variant all[4] = {variant<64, true>(), variant<64, false>(), variant<128, true>(), variant<128, false>()};
+  const int n = (D == 128 ? 2 : 0) + (dtype == MLA_FP16 ? 1 : 0);
   *out = all[n];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED_DEVICE;
@@ -183,7 +178,7 @@ int run(const Call& c) {
   const Layout lay = layout(pl, grid, c.D);
   if (!c.workspace || c.workspace_bytes < lay.bytes) return MLA_ERR_WORKSPACE;
   Variant var;
-  st = pick(c.D, c.dtype, pl.rows2, &var);
+  st = pick(c.D, c.dtype, &var);
   if (st != MLA_OK) return st;
 
   // Rows a TMA box: whole 64-key tiles, or the largest power of two that no

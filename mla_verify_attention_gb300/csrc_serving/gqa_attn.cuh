@@ -13,19 +13,20 @@
 // (32 KB at D = 128: ~1,500 cycles).
 //
 // Split.  The work is a sequence of 64-key tiles: streams, then key heads,
-// then keys.  Every CTA (or team of CTAs, one a row group) of one persistent wave takes an equal
-// run of that sequence, computed on the device from seq_lens, so that ragged
+// then keys.  Every CTA (or team of CTAs, one a group of 128 rows) of one
+// persistent wave takes an equal run of that sequence, computed on the device from seq_lens, so that ragged
 // batches balance to one tile and nothing is planned on the host.  A (stream,
 // head, row group) unit that lies within one run is written to `out`; one that
 // is cut leaves unnormalised partials (at most two a CTA, which bounds the
 // workspace by the grid) that the combine kernels merge in order.
 //
 // CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), two
-// issue tcgen05.mma, eight softmax warps in two groups own one accumulator O
-// each in tensor memory:
-//   up to 128 rows: both groups share the row tile and take the key tiles in
-//     turn; their two (m, l, O) are merged when the unit's run ends.
-//   more rows (kRows2): each group owns 128 of 256 rows, every tile feeds both.
+// issue tcgen05.mma, eight softmax warps in two groups take the key tiles in
+// turn, each with an accumulator O (128 rows) of its own in tensor memory; their
+// (m, l, O) are merged when the unit's run ends.  More rows than 128 are taken
+// by as many CTAs side by side, which share the cache reads through L2.  (Two
+// row tiles a CTA, one a group, read the cache half as often but were slower:
+// 264 rows over 16k keys 44 us against 32, 1,024 rows 45 against 39.)
 // S is double-buffered per group in tensor memory (2 x 64 columns); P replaces
 // S in place and is the A operand of O += P V.  O is only rescaled when a
 // row's max grows by more than 2^8.
@@ -80,11 +81,11 @@ struct Shape {
   static constexpr int kRing = 2 * kStages * kTile;
 };
 
-template <int D, bool kRows2>
+template <int D>
 struct __align__(1024) Smem {
-  uint8_t q[2 * Shape<D>::kQTile];                     // both row tiles, or this segment's and the next one's
+  uint8_t q[2 * Shape<D>::kQTile];                     // this segment's rows and the next one's
   uint8_t ring[Shape<D>::kRing];                       // stage s: K tile, V tile
-  float2 ml[2][kRows2 ? 1 : kRows];
+  float2 ml[2][kRows];
   uint64_t kfull[Shape<D>::kStages], kempty[Shape<D>::kStages];
   uint64_t vfull[Shape<D>::kStages], vempty[Shape<D>::kStages];
   uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];     // [group][buffer]
@@ -112,32 +113,32 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { retu
 
 // The products are issued by one elected lane of a converged warp: the operands
 // then move to uniform registers once, not lane by lane (a single-lane loop
-// took 1.5 times as long).  A task's products and the commits that follow them
+// took 1.5 times as long).  A tile's products and the commits that follow them
 // are one block, with one election.
 
-// S = Q K^T of one task, A and B K-major in shared memory: D / 64 chunks of four
-// K = 16 steps; then the commits to `bar0`, and to `bar1` and `bar2` where c1 and c2 say so.
+// S = Q K^T of one tile, A and B K-major in shared memory: D / 64 chunks of four
+// K = 16 steps; then the commits to `bar0`, `bar1` and, at the end, `bar2`.
 #define MLA_QK_CHUNK(ao, bo, first)                                                                   \
-  " add.u32 x, %1, " #ao ";\n add.u32 y, %2, " #bo ";\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " add.u32 x, %1, " #ao ";\n add.u32 y, %2, " #bo ";\n mov.b64 a, {x, %8};\n mov.b64 b, {y, %8};\n" \
   " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " #first ";\n"                              \
-  " add.u32 x, %1, " #ao " + 2;\n add.u32 y, %2, " #bo " + 2;\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " add.u32 x, %1, " #ao " + 2;\n add.u32 y, %2, " #bo " + 2;\n mov.b64 a, {x, %8};\n mov.b64 b, {y, %8};\n" \
   " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"                                       \
-  " add.u32 x, %1, " #ao " + 4;\n add.u32 y, %2, " #bo " + 4;\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " add.u32 x, %1, " #ao " + 4;\n add.u32 y, %2, " #bo " + 4;\n mov.b64 a, {x, %8};\n mov.b64 b, {y, %8};\n" \
   " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"                                       \
-  " add.u32 x, %1, " #ao " + 6;\n add.u32 y, %2, " #bo " + 6;\n mov.b64 a, {x, %9};\n mov.b64 b, {y, %9};\n" \
+  " add.u32 x, %1, " #ao " + 6;\n add.u32 y, %2, " #bo " + 6;\n mov.b64 a, {x, %8};\n mov.b64 b, {y, %8};\n" \
   " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
 #define MLA_COMMIT(pred, bar) \
   " @" #pred " tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [" #bar "];\n"
 #define MLA_QK_BODY(chunks)                                                                                        \
-  asm volatile("{\n .reg .pred e, z, c1, c2;\n .reg .b32 x, y;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n" \
-               " setp.ne.and.b32 c1, %7, 0, e;\n setp.ne.and.b32 c2, %8, 0, e;\n setp.ne.b32 z, 0, 0;\n" chunks     \
-               MLA_COMMIT(e, %4) MLA_COMMIT(c1, %5) MLA_COMMIT(c2, %6) "}" ::"r"(d),                                \
-               "r"(a), "r"(b), "r"(id), "r"(bar0), "r"(bar1), "r"(bar2), "r"(static_cast<uint32_t>(c1)),            \
-               "r"(static_cast<uint32_t>(c2)), "n"(kDescHi)                                                         \
+  asm volatile("{\n .reg .pred e, z, c;\n .reg .b32 x, y;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n" \
+               " setp.ne.and.b32 c, %7, 0, e;\n setp.ne.b32 z, 0, 0;\n" chunks                                                \
+               MLA_COMMIT(e, %4) MLA_COMMIT(e, %5) MLA_COMMIT(c, %6) "}" ::"r"(d),                                  \
+               "r"(a), "r"(b), "r"(id), "r"(bar0), "r"(bar1), "r"(bar2), "r"(static_cast<uint32_t>(end)),           \
+               "n"(kDescHi)                                                                                         \
                : "memory")
 template <int kChunks>
 __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t bar0, uint32_t bar1,
-                                         bool c1, uint32_t bar2, bool c2) {
+                                         uint32_t bar2, bool end) {
   // Chunks lie 16 KB (Q, 128 rows) and 8 KB (K, 64 keys) apart: 1024 and 512 descriptor units.
   static_assert(kRows * 128 >> 4 == 1024 && kKeys * 128 >> 4 == 512, "chunk distances");
   if (kChunks == 1) MLA_QK_BODY(MLA_QK_CHUNK(0, 0, z));
@@ -147,19 +148,19 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uin
 // O (+)= P V over 64 keys: P in tensor memory (8 columns a K = 16 step), V
 // MN-major in shared memory (16 rows of 128 bytes a step); then the commits.
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t bar0,
-                                         uint32_t bar1, bool c1, uint32_t bar2, bool c2) {
+                                         uint32_t bar1, uint32_t bar2, bool end) {
   asm volatile(
-      "{\n .reg .pred e, p, c1, c2;\n .reg .b32 x, y;\n .reg .b64 b;\n elect.sync _|e, 0xffffffff;\n"
-      " setp.ne.b32 p, %4, 0;\n setp.ne.and.b32 c1, %8, 0, e;\n setp.ne.and.b32 c2, %9, 0, e;\n mov.b64 b, {%2, %10};\n"
+      "{\n .reg .pred e, p, c;\n .reg .b32 x, y;\n .reg .b64 b;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.and.b32 c, %8, 0, e;\n mov.b64 b, {%2, %9};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n"
-      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 b, {y, %10};\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 b, {y, %9};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n"
-      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 b, {y, %10};\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 b, {y, %9};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n"
-      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 b, {y, %10};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n" MLA_COMMIT(e, %5) MLA_COMMIT(c1, %6)
-      MLA_COMMIT(c2, %7) "}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(bar0), "r"(bar1), "r"(bar2),
-      "r"(static_cast<uint32_t>(c1)), "r"(static_cast<uint32_t>(c2)), "n"(kDescHi)
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 b, {y, %9};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n" MLA_COMMIT(e, %5) MLA_COMMIT(e, %6)
+      MLA_COMMIT(c, %7) "}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(bar0), "r"(bar1), "r"(bar2),
+      "r"(static_cast<uint32_t>(end)), "n"(kDescHi)
       : "memory");
 }
 
@@ -289,8 +290,8 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int rows_of_group(const Params& p, int group, int span) {
-  return min(span, p.q_len * p.G - group * span);
+__device__ __forceinline__ int rows_of_group(const Params& p, int group) {
+  return min(kRows, p.q_len * p.G - group * kRows);
 }
 
 // ------------------------------------------------------------ loads
@@ -320,8 +321,8 @@ struct Ring {
 // Warps 0 (K) and 2 (V): tiles by TMA.  A tile is one box of 64 rows, or boxes
 // of box_rows rows and 64 dims when pages are shorter than a tile.  (One warp
 // for both took longer to issue a tile's copies than the memory to deliver them.)
-template <int D, bool kRows2>
-__device__ __forceinline__ void load_tma(Smem<D, kRows2>& sm, const Params& p, const CUtensorMap* map, Walk w, bool is_v) {
+template <int D>
+__device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUtensorMap* map, Walk w, bool is_v) {
   using C = Shape<D>;
   const int lane = threadIdx.x & 31;
   uint64_t* const full = is_v ? sm.vfull : sm.kfull;
@@ -374,8 +375,8 @@ out:
 // multiple of 8): rows copied 16 bytes a lane, into the layout the boxes would
 // leave; rows past the stream are zeros.  A lane looks up the pages of two rows
 // of the next tile while it copies this one.
-template <int D, bool kRows2>
-__device__ __forceinline__ void load_gather(Smem<D, kRows2>& sm, const Params& p, Walk w, bool is_v) {
+template <int D>
+__device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk w, bool is_v) {
   using C = Shape<D>;
   constexpr int kUnits = D / 8;                // 16-byte units a row
   constexpr int kPer = 32 / kUnits;            // rows a warp copies at once
@@ -433,35 +434,34 @@ out:
 
 // ------------------------------------------------------------ products
 
-// A segment's tasks are its tiles (the groups in turn), or with kRows2 each
-// tile for each group.  Issuing one task's products takes a warp several
+// A segment's tiles are taken by the two softmax groups in turn.  Issuing one tile's products takes a warp several
 // hundred cycles (waits, descriptors, commits), as long as the tensor pipe
 // needs for them; S = Q K^T and O += P V are therefore issued by a warp each,
 // and run apart by as many tasks as there are S buffers.
 
-// Warp 1: S of every task.
-template <int D, bool kBf16, bool kRows2>
+// Warp 1: S of every tile.
+template <int D, bool kBf16>
 struct ProductsQk {
   using C = Shape<D>;
   static constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
-  Smem<D, kRows2>& sm;
+  Smem<D>& sm;
   const Params& p;
   uint32_t tmem, q0, k0;
   Ring<C::kStages> at;
-  int done[2] = {0, 0};                        // tasks of each group so far
-  __device__ __forceinline__ ProductsQk(Smem<D, kRows2>& sm_, const Params& p_, uint32_t tmem_)
+  int done[2] = {0, 0};                        // tiles of each group so far
+  __device__ __forceinline__ ProductsQk(Smem<D>& sm_, const Params& p_, uint32_t tmem_)
       : sm(sm_), p(p_), tmem(tmem_), q0(desc_lo(smem_u32(sm_.q), 16)), k0(desc_lo(smem_u32(sm_.ring), 16)) {}
 
   template <int g>
-  __device__ __forceinline__ bool task(uint32_t q, bool last_use, bool last, int seg) {
+  __device__ __forceinline__ bool tile(int seg, bool last) {
     const int b = done[g] & 1;
     if (!wait2(sm, sm.pvdone[g][b], ((done[g] >> 1) & 1) ^ 1, sm.kfull[at.stage], at.phase, p)) return false;
     tc_fence_after();
-    issue_qk<C::kChunks>(tmem + 256 + (2 * g + b) * kKeys, q + (kRows2 ? g * (C::kQTile >> 4) : 0),
+    issue_qk<C::kChunks>(tmem + 256 + (2 * g + b) * kKeys, q0 + (seg & 1) * (C::kQTile >> 4),
                          k0 + at.stage * (2 * C::kTile >> 4), kId, smem_u32(&sm.sfull[g][b]),
-                         smem_u32(&sm.kempty[at.stage]), last_use, smem_u32(&sm.qfree[seg & 1]), last);
+                         smem_u32(&sm.kempty[at.stage]), smem_u32(&sm.qfree[seg & 1]), last);
     ++done[g];
-    if (last_use) at.advance();
+    at.advance();
     return true;
   }
 
@@ -470,47 +470,38 @@ struct ProductsQk {
     Segment s;
     while (w.next(p, s)) {
       if (!wait(sm, sm.qfull, seg & 1, p)) return;
-      const uint32_t q = q0 + (!kRows2 && (seg & 1) ? (C::kQTile >> 4) : 0);
-      if (kRows2 && rows_of_group(p, s.group, 2 * kRows) <= kRows) {
-        for (int j = 0; j < s.n; ++j)
-          if (!task<0>(q, true, j == s.n - 1, seg)) return;
-      } else if (kRows2) {
-        for (int j = 0; j < s.n; ++j)
-          if (!task<0>(q, false, false, seg) || !task<1>(q, true, j == s.n - 1, seg)) return;
-      } else {
-        for (int j = 0; j < s.n; j += 2) {
-          if (!task<0>(q, true, j == s.n - 1, seg)) return;
-          if (j + 1 < s.n && !task<1>(q, true, j == s.n - 2, seg)) return;
-        }
+      for (int j = 0; j < s.n; j += 2) {
+        if (!tile<0>(seg, j == s.n - 1)) return;
+        if (j + 1 < s.n && !tile<1>(seg, j == s.n - 2)) return;
       }
       ++seg;
     }
   }
 };
 
-// Warp 3: O += P V of every task.
-template <int D, bool kBf16, bool kRows2>
+// Warp 3: O += P V of every tile.
+template <int D, bool kBf16>
 struct ProductsPv {
   using C = Shape<D>;
   static constexpr uint32_t kId = idesc<kBf16>(D, 1);
-  Smem<D, kRows2>& sm;
+  Smem<D>& sm;
   const Params& p;
   uint32_t tmem, v0;
   Ring<C::kStages> at;
   int done[2] = {0, 0};
-  __device__ __forceinline__ ProductsPv(Smem<D, kRows2>& sm_, const Params& p_, uint32_t tmem_)
+  __device__ __forceinline__ ProductsPv(Smem<D>& sm_, const Params& p_, uint32_t tmem_)
       : sm(sm_), p(p_), tmem(tmem_), v0(desc_lo(smem_u32(sm_.ring) + C::kTile, kKeys * 128)) {}
 
-  // `first`: the group's first task of the segment, O starts at 0.
+  // `first`: the group's first of the segment, O starts at 0.
   template <int g>
-  __device__ __forceinline__ bool task(bool first, bool last_use, bool last) {
+  __device__ __forceinline__ bool tile(bool first, bool last) {
     const int b = done[g] & 1;
     if (!wait2(sm, sm.pfull[g][b], (done[g] >> 1) & 1, sm.vfull[at.stage], at.phase, p)) return false;
     tc_fence_after();
     issue_pv(tmem + g * D, tmem + 256 + (2 * g + b) * kKeys, v0 + at.stage * (2 * C::kTile >> 4), kId, first ? 0u : 1u,
-             smem_u32(&sm.pvdone[g][b]), smem_u32(&sm.vempty[at.stage]), last_use, smem_u32(&sm.ofull), last);
+             smem_u32(&sm.pvdone[g][b]), smem_u32(&sm.vempty[at.stage]), smem_u32(&sm.ofull), last);
     ++done[g];
-    if (last_use) at.advance();
+    at.advance();
     return true;
   }
 
@@ -520,17 +511,9 @@ struct ProductsPv {
     while (w.next(p, s)) {
       // The last segment's results have been read out of both accumulators.
       if (seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
-      if (kRows2 && rows_of_group(p, s.group, 2 * kRows) <= kRows) {
-        for (int j = 0; j < s.n; ++j)
-          if (!task<0>(j == 0, true, j == s.n - 1)) return;
-      } else if (kRows2) {
-        for (int j = 0; j < s.n; ++j)
-          if (!task<0>(j == 0, false, false) || !task<1>(j == 0, true, j == s.n - 1)) return;
-      } else {
-        for (int j = 0; j < s.n; j += 2) {
-          if (!task<0>(j == 0, true, j == s.n - 1)) return;
-          if (j + 1 < s.n && !task<1>(j == 0, true, j == s.n - 2)) return;
-        }
+      for (int j = 0; j < s.n; j += 2) {
+        if (!tile<0>(j == 0, j == s.n - 1)) return;
+        if (j + 1 < s.n && !tile<1>(j == 0, j == s.n - 2)) return;
       }
       ++seg;
     }
@@ -558,36 +541,33 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, const uint4* v, uint8_t
 }
 
 // Starts the copies of a segment's Q rows into a swizzled tile, by all softmax
-// warps: each group its own tile, or half the rows of each warp's 32 when the
-// groups share one.
-template <int D, bool kRows2>
-__device__ __forceinline__ void start_q(Smem<D, kRows2>& sm, const Params& p, const Segment& s, int seg, int g, int wq,
-                                        int lane) {
+// warps: each group half the rows of each warp's 32.
+template <int D>
+__device__ __forceinline__ void start_q(Smem<D>& sm, const Params& p, const Segment& s, int seg, int g, int wq, int lane) {
   using C = Shape<D>;
-  constexpr int kSpan = kRows2 ? 2 * kRows : kRows;
   constexpr int kUnits = D / 8;                            // 16-byte units a row
   constexpr int kPer = 32 / kUnits;                        // rows a warp copies at once
-  const int mine = rows_of_group(p, s.group, kSpan) - (kRows2 ? g * kRows : 0);
-  const int R = s.group * kSpan + (kRows2 ? g * kRows : 0) + wq * 32 + lane;
+  const int rows = rows_of_group(p, s.group);
+  const int R = s.group * kRows + wq * 32 + lane;
   const int i = R / p.G;
   // Each lane knows its row's address; the lanes that copy a row ask for it.
-  const long long base = wq * 32 + lane < mine ? s.b * p.q_stride[0] + i * p.q_stride[1] +
+  const long long base = wq * 32 + lane < rows ? s.b * p.q_stride[0] + i * p.q_stride[1] +
                                                      (s.head * p.G + (R - i * p.G)) * p.q_stride[2]
                                                : 0;
-  const uint32_t tile = smem_u32(sm.q) + (kRows2 ? g : seg & 1) * C::kQTile;
-  const int r0 = (kRows2 ? 0 : g * 16) + lane / kUnits, u = lane % kUnits;
+  const uint32_t tile = smem_u32(sm.q) + (seg & 1) * C::kQTile;
+  const int r0 = g * 16 + lane / kUnits, u = lane % kUnits;
 #pragma unroll
-  for (int e = 0; e < (kRows2 ? 32 : 16) / kPer; ++e) {
+  for (int e = 0; e < 16 / kPer; ++e) {
     const long long off = __shfl_sync(0xFFFFFFFFu, base, r0 + e * kPer);
     const int row = wq * 32 + r0 + e * kPer;
-    if (row < mine)
+    if (row < rows)
       cp_async_16(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), p.q + off + u * 16, true);
   }
   cp_async_commit();
 }
 // The copies have landed: hands the tile to the products.
-template <int D, bool kRows2>
-__device__ __forceinline__ void finish_q(Smem<D, kRows2>& sm, int lane) {
+template <int D>
+__device__ __forceinline__ void finish_q(Smem<D>& sm, int lane) {
   cp_async_wait<0>();
   fence_proxy_async_smem();
   __syncwarp();
@@ -595,11 +575,10 @@ __device__ __forceinline__ void finish_q(Smem<D, kRows2>& sm, int lane) {
 }
 
 // Warps 4..11: group g = 0, 1, warp wq of the group, one row a thread.
-template <int D, bool kBf16, bool kRows2>
-__device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, uint32_t tmem, Walk w, int g, int wq,
+template <int D, bool kBf16>
+__device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t tmem, Walk w, int g, int wq,
                                         int lane) {
   using C = Shape<D>;
-  constexpr int kSpan = kRows2 ? 2 * kRows : kRows;        // rows a unit
   // fp16 weights are kept 2^7 larger: the largest, 2^(8 + 7), is in range and
   // the smallest that is not rounded to a subnormal is 2^-14 / 2^7 of a row's
   // largest weight or more.  bf16 has fp32's range.
@@ -614,23 +593,20 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
   Segment s, next;
   bool more = w.next(p, s);
   if (more) {
-    start_q<D, kRows2>(sm, p, s, 0, g, wq, lane);
-    finish_q<D, kRows2>(sm, lane);
+    start_q<D>(sm, p, s, 0, g, wq, lane);
+    finish_q<D>(sm, lane);
   }
   for (; more; s = next) {
     more = w.next(p, next);
-    if (!kRows2 && more) {
+    if (more) {
       // The next segment's Q lands while this one's tiles are worked on.
       if (seg > 0 && !wait(sm, sm.qfree[(seg - 1) & 1], ((seg - 1) >> 1) & 1, p)) return;
-      start_q<D, kRows2>(sm, p, next, seg + 1, g, wq, lane);
+      start_q<D>(sm, p, next, seg + 1, g, wq, lane);
     }
-    const int rows = rows_of_group(p, s.group, kSpan);
-    const int row0 = s.group * kSpan + (kRows2 ? g * kRows : 0);
-    const int mine = kRows2 ? rows - g * kRows : rows;     // valid rows of this group's tile
-    const bool two = kRows2 ? rows > kRows : true;
-    const int R = row0 + r;                                // row of the stream and head: draft * G + head in group
-    const bool valid = r < mine;
-    const bool warp_valid = wq * 32 < mine;
+    const int rows = rows_of_group(p, s.group);
+    const int R = s.group * kRows + r;                     // row of the stream and head: draft * G + head in group
+    const bool valid = r < rows;
+    const bool warp_valid = wq * 32 < rows;
     const int i = R / p.G;
     const int head = s.head * p.G + (R - i * p.G);
     uint64_t mask64 = 0;
@@ -643,8 +619,7 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
     }
     const int prefix = s.S - p.q_len;
     float m = -CUDART_INF_F, l = 0.f;
-    const int j0 = kRows2 ? 0 : g, step = kRows2 ? 1 : 2;
-    for (int j = j0; j < s.n && (two || g == 0); j += step, ++n) {
+    for (int j = g; j < s.n; j += 2, ++n) {
       const int buf = n & 1;
       const uint32_t s_t = tmem + lanes + 256 + (2 * g + buf) * kKeys;
       if (!wait(sm, sm.sfull[g][buf], (n >> 1) & 1, p)) return;
@@ -679,7 +654,7 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
           const float alpha = grow ? ex2(m - mt) : 1.f;    // 0 when nothing was visible before
           if (grow) m = mt;
           l *= alpha;
-          if (j > j0) {
+          if (j > g) {
             // O holds tiles up to the previous one of this group, once its product is done.
             if (!wait(sm, sm.pvdone[g][(n - 1) & 1], ((n - 1) >> 1) & 1, p)) return;
             tc_fence_after();
@@ -714,7 +689,7 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
         tmem_st_wait();
         tc_fence_before();
       }
-      if (k0 + kKeys > s.S && (!kRows2 || g == 0)) {
+      if (k0 + kKeys > s.S) {
         // Rows past the stream may hold anything: P is 0 there, but 0 * NaN is not.
         const int stage = (kt + j) % C::kStages;
         if (!wait(sm, sm.vfull[stage], ((kt + j) / C::kStages) & 1, p)) return;
@@ -730,30 +705,26 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[g][buf]));
     }
 
-    // ---- end of the segment.  When Q has two tiles the next one's is handed
-    // over first: its products then start while this one's results are written.
-    if (!kRows2 && more) {
-      if (!wait(sm, sm.qfull, seg & 1, p)) return;         // (a group without a task has not seen it)
-      finish_q<D, kRows2>(sm, lane);
+    // ---- end of the segment.  The next one's Q is handed over first: its
+    // products then start while this one's results are written.
+    if (more) {
+      if (!wait(sm, sm.qfull, seg & 1, p)) return;         // (a group without a tile has not seen it)
+      finish_q<D>(sm, lane);
     }
     const bool direct = s.n == s.nt;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
-    const int rr = (kRows2 ? g * kRows : 0) + r;
     const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head;
     float m_off = m == -CUDART_INF_F ? -CUDART_INF_F : m - kShift;
-    float w0 = 1.f, w1 = 0.f;                              // weights of the groups' accumulators
-    if (!kRows2) {
-      sm.ml[g][r] = make_float2(m_off, l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.mlx));
-      if (!wait(sm, sm.mlx, seg & 1, p)) return;
-      const float2 x0 = sm.ml[0][r], x1 = sm.ml[1][r];
-      const float mt = fmaxf(x0.x, x1.x);
-      w0 = x0.x == -CUDART_INF_F ? 0.f : ex2(x0.x - mt);
-      w1 = x1.x == -CUDART_INF_F ? 0.f : ex2(x1.x - mt);
-      l = w0 * x0.y + w1 * x1.y;
-      m_off = mt;
-    }
+    // The groups' accumulators: their weights, from both maxima and sums.
+    sm.ml[g][r] = make_float2(m_off, l);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.mlx));
+    if (!wait(sm, sm.mlx, seg & 1, p)) return;
+    const float2 ml0 = sm.ml[0][r], ml1 = sm.ml[1][r];
+    m_off = fmaxf(ml0.x, ml1.x);
+    float w0 = ml0.x == -CUDART_INF_F ? 0.f : ex2(ml0.x - m_off);
+    float w1 = ml1.x == -CUDART_INF_F ? 0.f : ex2(ml1.x - m_off);
+    l = w0 * ml0.y + w1 * ml1.y;
     if (!wait(sm, sm.ofull, seg & 1, p)) return;
     if (warp_valid) {
       tc_fence_after();
@@ -762,11 +733,10 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
         w0 *= inv;
         w1 *= inv;
       }
-      const int c0 = kRows2 ? 0 : g * (D / 2), c1 = kRows2 ? D : c0 + D / 2;
-      const uint32_t o0 = tmem + lanes + (kRows2 ? g * D : 0);
+      const int c0 = g * (D / 2), c1 = c0 + D / 2;         // each group writes half the columns
       // The products are through with this segment's Q: the first 2 KB of the
       // rows that this warp itself copies are free to turn the results in.
-      uint8_t* const buf = sm.q + (kRows2 ? g : seg & 1) * C::kQTile + (wq * 32 + (kRows2 ? 0 : g * 16)) * 128;
+      uint8_t* const buf = sm.q + (seg & 1) * C::kQTile + (wq * 32 + g * 16) * 128;
       uint8_t* dst[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -774,18 +744,18 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
         const long long orow = __shfl_sync(0xFFFFFFFFu, out_row, row);
         uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) + (orow * D + c0) * 2
                                    : reinterpret_cast<uint8_t*>(
-                                         p.part_o + (static_cast<size_t>(slot) * p.part_rows + rr - lane + row) * (D / 4) +
+                                         p.part_o + (static_cast<size_t>(slot) * p.part_rows + wq * 32 + row) * (D / 4) +
                                          c0 / 4);
-        dst[e] = wq * 32 + row < mine ? to + (lane & 3) * 16 : nullptr;
+        dst[e] = wq * 32 + row < rows ? to + (lane & 3) * 16 : nullptr;
       }
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
         uint32_t x0[32];
         float o[32];
-        MLA_TMEM_LD_32x32b_X32(o0 + c, x0);
-        if (!kRows2 && s.n > 1) {
+        MLA_TMEM_LD_32x32b_X32(tmem + lanes + c, x0);
+        if (s.n > 1) {
           uint32_t x1[32];
-          MLA_TMEM_LD_32x32b_X32(o0 + D + c, x1);
+          MLA_TMEM_LD_32x32b_X32(tmem + lanes + D + c, x1);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = w0 * __uint_as_float(x0[e]) + w1 * __uint_as_float(x1[e]);
@@ -818,20 +788,16 @@ __device__ __forceinline__ void softmax(Smem<D, kRows2>& sm, const Params& p, ui
         for (int e = 0; e < 4; ++e)
           if (dst[e] != nullptr) dst[e] += 64;
       }
-      if (valid && (kRows2 || g == 0)) {
+      if (valid && g == 0) {
         if (direct)
           p.lse[out_row] = l > 0.f ? (m_off + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
         else
-          p.part_ml[static_cast<size_t>(slot) * p.part_rows + rr] = make_float2(m_off, l);
+          p.part_ml[static_cast<size_t>(slot) * p.part_rows + r] = make_float2(m_off, l);
       }
       tc_fence_before();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.ofree));
-    if (kRows2 && more) {
-      start_q<D, kRows2>(sm, p, next, seg + 1, g, wq, lane);
-      finish_q<D, kRows2>(sm, lane);
-    }
     kt += s.n;
     ++seg;
   }
@@ -868,10 +834,10 @@ __device__ __forceinline__ void note_cut_units(const Params& p, Walk w, long lon
   if (!p.desc_units) p.desc[cta] = d;
 }
 
-template <int D, bool kBf16, bool kRows2>
+template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
-  using S = Smem<D, kRows2>;
+  using S = Smem<D>;
   using C = Shape<D>;
   // Shared memory is full to the last KB: the tiles' alignment is asked for, and
   // checked, instead of made with a spare KB.
@@ -974,18 +940,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Walk walk(p, t0, t1, sm.start_b, sm.start_pre);
 
   if (warp == 0 || warp == 2) {
-    if (p.box_rows == 0) load_gather<D, kRows2>(sm, p, walk, warp == 2);
-    else load_tma<D, kRows2>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
+    if (p.box_rows == 0) load_gather<D>(sm, p, walk, warp == 2);
+    else load_tma<D>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
   } else if (warp == 1) {
-    ProductsQk<D, kBf16, kRows2>(sm, p, tmem).run(walk);
+    ProductsQk<D, kBf16>(sm, p, tmem).run(walk);
     drain_products(sm.drain[0]);
   } else if (warp == 3) {
     if (lane == 0 && !p.whole) note_cut_units(p, walk, t1, total, teams);
     __syncwarp();
-    ProductsPv<D, kBf16, kRows2>(sm, p, tmem).run(walk);
+    ProductsPv<D, kBf16>(sm, p, tmem).run(walk);
     drain_products(sm.drain[1]);
   } else if (warp >= 4) {
-    softmax<D, kBf16, kRows2>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
+    softmax<D, kBf16>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
   }
   // Streams without keys.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -1030,9 +996,8 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
   __shared__ float2 stats[kP > 1 ? kP - 1 : 1][kR];
   const int tid = threadIdx.x, c4 = tid % (D / 4), r = tid / (D / 4) % kR, group = tid / kGroup, t = tid % kGroup;
   const int parts = d.w, rr = chunk * kR + r;
-  const int full = p.q_len * p.G > kRows ? 2 * kRows : kRows;
-  const int head = d.y / p.groups, R = (d.y - head * p.groups) * full + rr;
-  const bool valid = rr < full && R < p.q_len * p.G;
+  const int head = d.y / p.groups, R = (d.y - head * p.groups) * kRows + rr;
+  const bool valid = rr < kRows && R < p.q_len * p.G;
   // Row rr of part k >= 1 lies in slot 2 * (CTA of part 0 + k * members).
   const size_t row_k = static_cast<size_t>(2 * (d.z >> 1)) * p.part_rows + rr, row_0 = static_cast<size_t>(d.z) * p.part_rows + rr;
   const size_t step = static_cast<size_t>(2 * p.members) * p.part_rows;
