@@ -254,7 +254,7 @@ int run(const Call& c) {
     cfg.gridDim = dim3(pairs, entries, 1);
   } else {
     const long long chunks = static_cast<long long>(entries) * (pl.part_rows / kMergeUnits);
-    cfg.gridDim = dim3(static_cast<unsigned>(chunks < 3 * grid ? chunks : 3 * grid), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(chunks < 5 * grid ? chunks : 5 * grid), 1, 1);
   }
   cfg.blockDim = dim3(c.D / 4 * kMergeUnits, 1, 1);
   cfg.dynamicSmemBytes = 0;

@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merges the partials of the cut units.  A unit's parts are the first one's slot
 // and the first slots of the same member of the teams after it.  A block takes
 // kR rows of a unit; kP part groups of threads share the parts, a thread one
-// row's four columns of eight parts at a time (weights, sums and values loaded
+// row's four columns of several parts at a time (weights, sums and values loaded
 // together), and the groups' results are put together through shared memory.
 // Everything is added in a fixed order.  The call is a chain of a few reads
 // that depend on each other (~1.5 us after the split kernel has ended), so there
@@ -991,6 +991,7 @@ constexpr int kMergeParts = 4;               // part groups when there are many 
 template <int D, bool kBf16, int kP>
 __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int chunk) {
   constexpr int kR = kMergeUnits / kP;
+  constexpr int kAtOnce = kP > 1 ? 8 : 4;                  // parts a thread loads at once
   constexpr int kGroup = D / 4 * kR;                       // threads a part group
   __shared__ float4 sums[kP > 1 ? kP - 1 : 1][kGroup];
   __shared__ float2 stats[kP > 1 ? kP - 1 : 1][kR];
@@ -1003,11 +1004,11 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
   const size_t step = static_cast<size_t>(2 * p.members) * p.part_rows;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -CUDART_INF_F, l = 0.f;
-  for (int k0 = group; valid && k0 < parts; k0 += 8 * kP) {
-    float4 x[8];
-    float2 y[8];
+  for (int k0 = group; valid && k0 < parts; k0 += kAtOnce * kP) {
+    float4 x[kAtOnce];
+    float2 y[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kAtOnce; ++e) {
       const int k = k0 + e * kP;
       y[e] = make_float2(-CUDART_INF_F, 0.f);
       x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1019,13 +1020,13 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
     }
     float top = m;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, y[e].x);
+    for (int e = 0; e < kAtOnce; ++e) top = fmaxf(top, y[e].x);
     const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - top);
     m = top;
     l *= keep;
     o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kAtOnce; ++e) {
       const float w = y[e].x == -CUDART_INF_F ? 0.f : ex2(y[e].x - m);
       l += w * y[e].y;
       o.x += w * x[e].x;
