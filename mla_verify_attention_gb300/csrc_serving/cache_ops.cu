@@ -12,19 +12,62 @@
 
 namespace mla {
 
+// A programmatic dependent of the grid before it (every kernel here waits for
+// that grid before it reads anything): its launch overlaps that grid's end.
+template <class P>
+int launch_dependent(void (*fn)(P), const P& p, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_LAUNCH;
+  }
+  return MLA_OK;
+}
+
+// Quotients by a number fixed for the call: exact for 0 <= n < 2^31, as one
+// 64-bit product.  With 2^s >= d and m = floor(2^(31 + s) / d) + 1, m d exceeds
+// 2^(31 + s) by at most 2^s, which moves n m / 2^(31 + s) by less than 1 / d.
+struct Divisor {
+  unsigned d, m;
+  int shift;
+  Divisor() = default;
+  explicit Divisor(int by) : d(static_cast<unsigned>(by)), shift(31) {
+    while ((1ull << (shift - 31)) < d) ++shift;
+    m = static_cast<unsigned>((1ull << shift) / d + 1);
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return d == 1 ? n : static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(n)) * m >> shift);
+  }
+  __device__ __forceinline__ int up(int n) const { return n > 0 ? of(n - 1) + 1 : 0; }   // rounded up
+};
+
 // ------------------------------------------------------------ block tables
 //
 // need_b and the new tokens of each stream are summed up by a scan over the
 // batch; every new token and every new block then finds its stream by a binary
 // search in those sums, so that the work is even however ragged the batch is
-// (one long prompt among single tokens).  The call is latency bound (a few
-// dependent global reads and the scan), so it is one launch: one block, or for
-// many tokens one cluster of eight blocks that each repeat the scan and share
-// the tokens.  The in-place results (lengths, free count) are written by one
-// block after a cluster barrier, when every block has read the old ones.
-constexpr int kBlockThreads = 1024;
+// (one long prompt among single tokens).
+//
+// A call for a verify step is a chain of a few dependent reads, so it is one
+// block of as many threads as there are streams or token quads, and launched as
+// a dependent of the grid before it: 8 streams x 9 tokens.  Many tokens (an
+// extend of prompts) are shared by as many blocks as they fill, each with a
+// scan of its own, and a second grid then writes the lengths and the free
+// count, which every block of the first has to have read.
+constexpr int kMaxThreads = 1024;
 constexpr int kMaxStreams = 16384;     // three int32 a stream in shared memory
-constexpr int kClusterBlocks = 8;
+constexpr int kOneBlockTokens = 8192;  // up to here one block does it all
+constexpr int kMostBlocks = 128;
+constexpr unsigned kFull = 1u << 31;   // sums stay there: more than any limit they are held to
 
 struct BlocksParams {
   int32_t* seq_lens;
@@ -34,10 +77,11 @@ struct BlocksParams {
   int32_t* free_count;
   int32_t* slots;
   unsigned int* status;
-  int B, max_blocks, page, free_capacity, pool_pages, max_tokens;
+  int B, max_blocks, free_capacity, pool_pages, max_tokens;
+  Divisor page;
 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+__device__ __forceinline__ unsigned add_full(unsigned a, unsigned b) { return min(a + b, kFull); }
 
 // Largest i in [0, n) with pre[i] <= x, for pre[0] = 0 <= x < pre[n].
 __device__ __forceinline__ int find_stream(const int* pre, int n, int x) {
@@ -49,155 +93,187 @@ __device__ __forceinline__ int find_stream(const int* pre, int n, int x) {
   return lo;
 }
 
-template <bool kExtend>
-__global__ void __launch_bounds__(kBlockThreads, 1) blocks_kernel(const BlocksParams p) {
+enum { kAll = 0, kItems = 1, kCommit = 2 };   // what a grid does: everything, or one of the two parts
+
+template <bool kExtend, int kPart>
+__global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksParams p) {
   extern __shared__ int shared[];
   int* const base_len = shared;                   // [B] extend: old lengths; trim: kept lengths
   int* const blk_pre = base_len + p.B;            // [B + 1] blocks before stream b
   int* const tok_pre = blk_pre + p.B + 1;         // [B + 1] new tokens before stream b (extend)
-  __shared__ long long warp_sum[2][32];
+  __shared__ unsigned warp_sum[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int nthreads = static_cast<int>(gridDim.x) * kBlockThreads;
+  const int threads = blockDim.x, first = blockIdx.x * threads + tid, all_threads = gridDim.x * threads;
+  grid_dependency_wait();
+  if (tid == 0) grid_launch_dependents();
   const int fc = *p.free_count;
 
   // Each thread sums a run of consecutive streams; then a scan over threads.
-  const int per = (p.B + kBlockThreads - 1) / kBlockThreads;
+  const int per = (p.B + threads - 1) / threads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  const long long room = static_cast<long long>(p.max_blocks) * p.page;
-  long long blocks = 0, tokens = 0;
+  const long long room = static_cast<long long>(p.max_blocks) * p.page.d;
+  unsigned blocks = 0, tokens = 0;
   bool bad = false;
+  int len = 0, x = 0;                             // of the last stream: the only one of most calls' threads
   for (int b = b0; b < b1; ++b) {
-    const int len = p.seq_lens[b], x = p.target[b];
+    len = p.seq_lens[b];
+    x = p.target[b];
     const bool wrong = len < 0 || x < 0 || (kExtend ? len + static_cast<long long>(x) > room : x > len || len > room);
     bad |= wrong;
     if (wrong) continue;
-    blocks += kExtend ? ceil_div(len + x, p.page) - ceil_div(len, p.page)
-                      : ceil_div(len, p.page) - ceil_div(x, p.page);
-    if (kExtend) tokens += x;
+    blocks = add_full(blocks, kExtend ? p.page.up(len + x) - p.page.up(len) : p.page.up(len) - p.page.up(x));
+    if (kExtend) tokens = add_full(tokens, x);
   }
-  long long ib = blocks, it = tokens;             // inclusive sums over the warp's threads
+  unsigned ib = blocks, it = tokens;              // inclusive sums over the warp's threads
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long ob = __shfl_up_sync(0xFFFFFFFFu, ib, d), ot = __shfl_up_sync(0xFFFFFFFFu, it, d);
-    if (lane >= d) { ib += ob; it += ot; }
+    const unsigned ob = __shfl_up_sync(0xFFFFFFFFu, ib, d), ot = __shfl_up_sync(0xFFFFFFFFu, it, d);
+    if (lane >= d) {
+      ib = add_full(ib, ob);
+      it = add_full(it, ot);
+    }
   }
-  if (lane == 31) { warp_sum[0][warp] = ib; warp_sum[1][warp] = it; }
+  if (lane == 31) {
+    warp_sum[0][warp] = ib;
+    warp_sum[1][warp] = it;
+  }
   bad = __syncthreads_or(bad) != 0;
-  long long before_b = 0, before_t = 0, all_b = 0, all_t = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w == warp) { before_b = all_b; before_t = all_t; }
-    all_b += warp_sum[0][w];
-    all_t += warp_sum[1][w];
+  // Every warp scans the warps' sums.
+  unsigned wb = lane < threads / 32 ? warp_sum[0][lane] : 0, wt = lane < threads / 32 ? warp_sum[1][lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned ob = __shfl_up_sync(0xFFFFFFFFu, wb, d), ot = __shfl_up_sync(0xFFFFFFFFu, wt, d);
+    if (lane >= d) {
+      wb = add_full(wb, ob);
+      wt = add_full(wt, ot);
+    }
   }
+  const unsigned all_b = __shfl_sync(0xFFFFFFFFu, wb, 31), all_t = __shfl_sync(0xFFFFFFFFu, wt, 31);
+  const unsigned before_b = warp ? __shfl_sync(0xFFFFFFFFu, wb, warp - 1) : 0, before_t = warp ? __shfl_sync(0xFFFFFFFFu, wt, warp - 1) : 0;
 
   // Anything wrong: the batch stays as it was (the same verdict in every block).
-  const bool no_pages = fc < 0 || fc > p.free_capacity || (kExtend ? all_b > fc : all_b > p.free_capacity - fc);
-  bad |= kExtend && all_t > p.max_tokens;
+  const bool no_pages = fc < 0 || fc > p.free_capacity ||
+                        all_b > static_cast<unsigned>(kExtend ? fc : p.free_capacity - fc);
+  bad |= kExtend && all_t > static_cast<unsigned>(p.max_tokens);
   if (bad || no_pages) {
-    if (kExtend)
-      for (int t = rank * kBlockThreads + tid; t < p.max_tokens; t += nthreads) p.slots[t] = -1;
-    if (rank == 0 && tid == 0) atomicOr(p.status, bad ? kBitSeqLen : kBitPool);
+    if (kExtend && kPart != kCommit)
+      for (int t = first; t < p.max_tokens; t += all_threads) p.slots[t] = -1;
+    if (kPart != kItems && first == 0) atomicOr(p.status, bad ? kBitSeqLen : kBitPool);
     return;
   }
   const int n_blocks = static_cast<int>(all_b), n_tokens = static_cast<int>(all_t);
 
-  int eb = static_cast<int>(before_b + ib - blocks), et = static_cast<int>(before_t + it - tokens);
-  for (int b = b0; b < b1; ++b) {
-    const int len = p.seq_lens[b], x = p.target[b];
-    base_len[b] = kExtend ? len : x;
-    blk_pre[b] = eb;
-    eb += kExtend ? ceil_div(len + x, p.page) - ceil_div(len, p.page) : ceil_div(len, p.page) - ceil_div(x, p.page);
-    if (kExtend) {
-      tok_pre[b] = et;
-      et += x;
+  if (kPart != kCommit) {
+    int eb = static_cast<int>(before_b + ib - blocks), et = static_cast<int>(before_t + it - tokens);
+    for (int b = b0; b < b1; ++b) {
+      if (per > 1) {
+        len = p.seq_lens[b];
+        x = p.target[b];
+      }
+      base_len[b] = kExtend ? len : x;
+      blk_pre[b] = eb;
+      eb += kExtend ? p.page.up(len + x) - p.page.up(len) : p.page.up(len) - p.page.up(x);
+      if (kExtend) {
+        tok_pre[b] = et;
+        et += x;
+      }
     }
-  }
-  if (tid == 0) {
-    blk_pre[p.B] = n_blocks;
-    if (kExtend) tok_pre[p.B] = n_tokens;
-  }
-  __syncthreads();
+    if (tid == 0) {
+      blk_pre[p.B] = n_blocks;
+      if (kExtend) tok_pre[p.B] = n_tokens;
+    }
+    __syncthreads();
 
-  for (int k = rank * kBlockThreads + tid; k < n_blocks; k += nthreads) {
-    const int b = find_stream(blk_pre, p.B, k);
-    int32_t* const entry = p.table + static_cast<size_t>(b) * p.max_blocks + ceil_div(base_len[b], p.page) + (k - blk_pre[b]);
-    if (kExtend) *entry = p.free_pages[fc - 1 - k];
-    else p.free_pages[fc + n_blocks - 1 - k] = *entry;
-  }
-  if (kExtend) {
-    // Four consecutive tokens a thread: one search, one 16-byte store.  The
-    // page of a token's new block is read from the free list, not the table.
-    bool off = false;
-    for (long long t4 = 4ll * (rank * kBlockThreads + tid); t4 < p.max_tokens; t4 += 4ll * nthreads) {
-      const int t0 = static_cast<int>(t4);
-      int s[4] = {-1, -1, -1, -1};
-      if (t0 < n_tokens) {
-        int b = find_stream(tok_pre, p.B, t0);
-        int held = -1, row0 = 0;                 // the block that `row0` belongs to, of stream b
+    // Four blocks a thread at a time: their reads are under way together.
+    for (int k0 = first; k0 < n_blocks; k0 += 4 * all_threads) {
+      int32_t* to[4];
+      int page[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = t0 + e;
-          if (t >= n_tokens) break;
-          while (t >= tok_pre[b + 1]) { ++b; held = -1; }
-          const int len = base_len[b], pos = len + (t - tok_pre[b]), blk = pos / p.page;
-          if (blk != held) {
-            const int have = ceil_div(len, p.page);
-            const int page = blk < have ? p.table[static_cast<size_t>(b) * p.max_blocks + blk]
-                                        : p.free_pages[fc - 1 - (blk_pre[b] + blk - have)];
-            const bool ok = page >= 0 && page < p.pool_pages;
-            off |= !ok;
-            row0 = ok ? page * p.page : -1;
-            held = blk;
-          }
-          s[e] = row0 < 0 ? -1 : row0 + (pos - blk * p.page);
+      for (int e = 0; e < 4; ++e) {
+        const int k = k0 + e * all_threads;
+        to[e] = nullptr;
+        if (k < n_blocks) {
+          const int b = find_stream(blk_pre, p.B, k);
+          int32_t* const entry =
+              p.table + static_cast<size_t>(b) * p.max_blocks + p.page.up(base_len[b]) + (k - blk_pre[b]);
+          to[e] = kExtend ? entry : p.free_pages + fc + n_blocks - 1 - k;
+          page[e] = kExtend ? p.free_pages[fc - 1 - k] : *entry;
         }
       }
-      if (t0 + 4 <= p.max_tokens) {
-        *reinterpret_cast<int4*>(p.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
-      } else {
-        for (int e = 0; t0 + e < p.max_tokens; ++e) p.slots[t0 + e] = s[e];
-      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (to[e] != nullptr) *to[e] = page[e];
     }
-    if (off) atomicOr(p.status, kBitPage);
+    if (kExtend) {
+      // Four consecutive tokens a thread: one search, one 16-byte store.  The
+      // page of a token's new block is read from the free list, not the table.
+      bool off = false;
+      for (long long t4 = 4ll * first; t4 < p.max_tokens; t4 += 4ll * all_threads) {
+        const int t0 = static_cast<int>(t4);
+        int s[4] = {-1, -1, -1, -1};
+        if (t0 < n_tokens) {
+          int b = find_stream(tok_pre, p.B, t0);
+          int held = -1, row0 = 0;                 // the block that `row0` belongs to, of stream b
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = t0 + e;
+            if (t >= n_tokens) break;
+            while (t >= tok_pre[b + 1]) {
+              ++b;
+              held = -1;
+            }
+            const int old = base_len[b], pos = old + (t - tok_pre[b]), blk = p.page.of(pos);
+            if (blk != held) {
+              const int have = p.page.up(old);
+              const int page = blk < have ? p.table[static_cast<size_t>(b) * p.max_blocks + blk]
+                                          : p.free_pages[fc - 1 - (blk_pre[b] + blk - have)];
+              const bool ok = page >= 0 && page < p.pool_pages;
+              off |= !ok;
+              row0 = ok ? page * static_cast<int>(p.page.d) : -1;
+              held = blk;
+            }
+            s[e] = row0 < 0 ? -1 : row0 + (pos - blk * static_cast<int>(p.page.d));
+          }
+        }
+        if (t0 + 4 <= p.max_tokens) {
+          *reinterpret_cast<int4*>(p.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
+        } else {
+          for (int e = 0; t0 + e < p.max_tokens; ++e) p.slots[t0 + e] = s[e];
+        }
+      }
+      if (off) atomicOr(p.status, kBitPage);
+    }
   }
 
-  cluster_sync_all();   // every block has read the lengths and the free count
-  if (rank == 0) {
-    for (int b = tid; b < p.B; b += kBlockThreads)
-      p.seq_lens[b] = kExtend ? base_len[b] + (tok_pre[b + 1] - tok_pre[b]) : base_len[b];
+  if (kPart != kItems) {
+    // Every thread reads and writes its own streams; the lengths that the
+    // searches above used are in shared memory.
+    for (int b = b0; b < b1; ++b) {
+      if (per > 1) {
+        len = p.seq_lens[b];
+        x = p.target[b];
+      }
+      p.seq_lens[b] = kExtend ? len + x : x;
+    }
+    __syncthreads();                               // every thread has used the free count it read
     if (tid == 0) *p.free_count = kExtend ? fc - n_blocks : fc + n_blocks;
   }
 }
 
-template <bool kExtend>
-int launch_blocks(const BlocksParams& p, long long items, cudaStream_t stream) {
+using BlocksFn = void (*)(BlocksParams);
+
+int launch_blocks(BlocksFn fn, const BlocksParams& p, unsigned blocks, unsigned threads, cudaStream_t stream) {
   const size_t smem = (3 * static_cast<size_t>(p.B) + 2) * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(blocks_kernel<kExtend>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>((3 * kMaxStreams + 2) * sizeof(int))) != cudaSuccess) {
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>((3 * kMaxStreams + 2) * sizeof(int))) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }
-  const unsigned blocks = items > 4 * kBlockThreads ? kClusterBlocks : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(kBlockThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, blocks_kernel<kExtend>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_LAUNCH;
-  }
-  return MLA_OK;
+  return launch_dependent(fn, p, dim3(blocks), threads, smem, stream);
 }
+
+// Threads of a block that has this many streams and items to see to.
+unsigned threads_for(long long n) { return n <= 128 ? 128 : (n >= kMaxThreads ? kMaxThreads : static_cast<unsigned>((n + 31) / 32 * 32)); }
 
 bool blocks_shape_ok(int B, int max_blocks, int page, int free_capacity) {
   return B >= 0 && B <= kMaxStreams && max_blocks >= 1 && page >= 1 && free_capacity >= 0 &&
@@ -229,6 +305,8 @@ constexpr int kAppendWarps = 8;
 __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendParams p) {
   const int lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
   if (t >= p.T) return;
   const int slot = p.slots[t];
   if (slot < 0) return;
@@ -259,57 +337,67 @@ struct KeepParams {
   const int32_t* seq_lens;
   const int32_t* path;
   const int32_t* keep;
-  int max_blocks, page, pool_pages, B, q;
+  int max_blocks, pool_pages, B, q;
+  Divisor page;
 };
 
-// One block a stream and 512-byte column of the pool rows: eight warps read
-// the path's rows (eight rows a warp at most) into registers, and after a
-// barrier write them to their new places, so that any path is safe in place.
+// One block a stream and kKeepColumns 512-byte columns of the pool rows: eight
+// warps read the path's rows (eight rows a warp at most) into registers, and
+// after a barrier write them to their new places, so that any path is safe in
+// place.  Before that the block works out the rows (a thread a row; count,
+// length and path are read together, then the pages): two dependent reads that
+// the columns share.
 constexpr int kKeepWarps = 8;
 constexpr int kKeepRows = 64 / kKeepWarps;
+constexpr int kKeepColumns = 2;
 
 __global__ void __launch_bounds__(32 * kKeepWarps) keep_kernel(const KeepParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ int rows[2][64];                      // pool rows the j-th kept draft moves from / to
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
   const int units = p.r.units[0] + p.r.units[1];
-  const int c = static_cast<int>(blockIdx.x) * 32 + lane;
-  const int which = c < p.r.units[0] ? 0 : 1;
-  uint8_t* const pool = p.r.pool[which] + 16ll * (which ? c - p.r.units[0] : c);
-  const long long stride = p.r.pool_stride[which];
+  const int to = threadIdx.x & 1, j_mine = threadIdx.x >> 1;
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    const int n = p.keep[b];
+    const int n = p.keep[b], len = p.seq_lens[b];
+    int i = j_mine;
+    if (to == 0 && j_mine < p.q) i = p.path[static_cast<size_t>(b) * p.q + j_mine];   // (used below keep[b] only)
     if (n == 0) continue;
-    const int len = p.seq_lens[b];
     uint32_t wrong = 0;
     if (n < 0 || n > p.q) wrong = kBitSlot;
-    else if (len < p.q || len > static_cast<long long>(p.max_blocks) * p.page) wrong = kBitSeqLen;
-    else if (threadIdx.x < 2 * n) {
-      const int to = threadIdx.x & 1, j = threadIdx.x >> 1;
-      int i = j;
-      if (!to) {
-        i = p.path[static_cast<size_t>(b) * p.q + j];
-        if (i < 0 || i >= p.q) { wrong = kBitSlot; i = 0; }
+    else if (len < p.q || len > static_cast<long long>(p.max_blocks) * p.page.d) wrong = kBitSeqLen;
+    else if (j_mine < n) {
+      if (i < 0 || i >= p.q) {
+        wrong = kBitSlot;
+        i = 0;
       }
-      const int pos = len - p.q + i, blk = pos / p.page;
+      const int pos = len - p.q + i, blk = p.page.of(pos);
       const int page = p.table[static_cast<size_t>(b) * p.max_blocks + blk];
       if (page < 0 || page >= p.pool_pages) wrong |= kBitPage;
-      rows[to][j] = page * p.page + (pos - blk * p.page);
+      else rows[to][j_mine] = page * static_cast<int>(p.page.d) + (pos - blk * static_cast<int>(p.page.d));
     }
     if (wrong) atomicOr(p.r.status, wrong);
     if (__syncthreads_or(static_cast<int>(wrong))) continue;   // this stream stays as it was
-    uint4 v[kKeepRows];
+#pragma unroll 1
+    for (int col = 0; col < kKeepColumns; ++col) {
+      const int c = (static_cast<int>(blockIdx.x) * kKeepColumns + col) * 32 + lane;
+      const int which = c < p.r.units[0] ? 0 : 1;
+      uint8_t* const pool = p.r.pool[which] + 16ll * (which ? c - p.r.units[0] : c);
+      const long long stride = p.r.pool_stride[which];
+      uint4 v[kKeepRows];
 #pragma unroll
-    for (int e = 0; e < kKeepRows; ++e) {
-      const int j = warp + kKeepWarps * e;
-      if (j < n && c < units && rows[0][j] != rows[1][j])
-        v[e] = *reinterpret_cast<const uint4*>(pool + rows[0][j] * stride);
-    }
-    __syncthreads();
+      for (int e = 0; e < kKeepRows; ++e) {
+        const int j = warp + kKeepWarps * e;
+        if (j < n && c < units && rows[0][j] != rows[1][j])
+          v[e] = *reinterpret_cast<const uint4*>(pool + rows[0][j] * stride);
+      }
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kKeepRows; ++e) {
-      const int j = warp + kKeepWarps * e;
-      if (j < n && c < units && rows[0][j] != rows[1][j])
-        *reinterpret_cast<uint4*>(pool + rows[1][j] * stride) = v[e];
+      for (int e = 0; e < kKeepRows; ++e) {
+        const int j = warp + kKeepWarps * e;
+        if (j < n && c < units && rows[0][j] != rows[1][j])
+          *reinterpret_cast<uint4*>(pool + rows[1][j] * stride) = v[e];
+      }
     }
     __syncthreads();                                            // `rows` is rewritten for the next stream
   }
@@ -336,11 +424,6 @@ int rows_params(void* pool_a, long long stride_a, int bytes_a, void* pool_b, lon
   return MLA_OK;
 }
 
-int launched() {
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_LAUNCH;
-  return MLA_OK;
-}
-
 }  // namespace mla
 
 extern "C" {
@@ -364,8 +447,14 @@ int mla_blocks_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block
   const int st = device_common(&d);
   if (st != MLA_OK) return st;
   BlocksParams p = {seq_lens, new_lens, block_table, const_cast<int32_t*>(free_pages), free_count, slots,
-                    d.status_word, B, max_blocks, page_size, free_capacity, pool_pages, max_tokens};
-  return launch_blocks<true>(p, max_tokens, stream);
+                    d.status_word, B, max_blocks, free_capacity, pool_pages, max_tokens, Divisor(page_size)};
+  const long long quads = (static_cast<long long>(max_tokens) + 3) / 4;
+  if (max_tokens <= kOneBlockTokens)
+    return launch_blocks(blocks_kernel<true, kAll>, p, 1, threads_for(quads > B ? quads : B), stream);
+  const long long blocks = (quads + kMaxThreads - 1) / kMaxThreads;
+  const int first = launch_blocks(blocks_kernel<true, kItems>, p,
+                                  static_cast<unsigned>(blocks < kMostBlocks ? blocks : kMostBlocks), kMaxThreads, stream);
+  return first != MLA_OK ? first : launch_blocks(blocks_kernel<true, kCommit>, p, 1, threads_for(B), stream);
 }
 
 int mla_blocks_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* block_table, int B,
@@ -383,10 +472,8 @@ int mla_blocks_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* 
   const int st = device_common(&d);
   if (st != MLA_OK) return st;
   BlocksParams p = {seq_lens, keep_lens, const_cast<int32_t*>(block_table), free_pages, free_count, nullptr,
-                    d.status_word, B, max_blocks, page_size, free_capacity, 0, 0};
-  // At most this many pages come back.
-  const long long table = static_cast<long long>(B) * max_blocks;
-  return launch_blocks<false>(p, table < free_capacity ? table : free_capacity, stream);
+                    d.status_word, B, max_blocks, free_capacity, 0, 0, Divisor(page_size)};
+  return launch_blocks(blocks_kernel<false, kAll>, p, 1, threads_for(B > 16 ? kMaxThreads : B), stream);
 }
 
 int mla_cache_append(const void* a, long long a_stride, int a_bytes, void* pool_a, long long pool_a_stride,
@@ -413,9 +500,9 @@ int mla_cache_append(const void* a, long long a_stride, int a_bytes, void* pool_
   p.src_stride[1] = b_bytes > 0 ? b_stride : 0;
   p.slots = slots;
   p.T = T;
-  append_kernel<<<static_cast<unsigned>((static_cast<long long>(T) + kAppendWarps - 1) / kAppendWarps),
-                  32 * kAppendWarps, 0, stream>>>(p);
-  return launched();
+  return launch_dependent(append_kernel, p,
+                          dim3(static_cast<unsigned>((static_cast<long long>(T) + kAppendWarps - 1) / kAppendWarps)),
+                          32 * kAppendWarps, 0, stream);
 }
 
 int mla_cache_keep(void* pool_a, long long pool_a_stride, int a_bytes, void* pool_b,
@@ -443,13 +530,12 @@ int mla_cache_keep(void* pool_a, long long pool_a_stride, int a_bytes, void* poo
   p.path = path;
   p.keep = keep;
   p.max_blocks = max_blocks;
-  p.page = page_size;
+  p.page = Divisor(page_size);
   p.pool_pages = static_cast<int>(pool_rows / page_size);
   p.B = B;
   p.q = q_len;
-  const unsigned cols = (static_cast<unsigned>(p.r.units[0]) + p.r.units[1] + 31) / 32;
-  keep_kernel<<<dim3(cols, B < 65535 ? B : 65535), 32 * kKeepWarps, 0, stream>>>(p);
-  return launched();
+  const unsigned cols = (static_cast<unsigned>(p.r.units[0]) + p.r.units[1] + 32 * kKeepColumns - 1) / (32 * kKeepColumns);
+  return launch_dependent(keep_kernel, p, dim3(cols, B < 65535 ? B : 65535), 32 * kKeepWarps, 0, stream);
 }
 
 }  // extern "C"
