@@ -67,6 +67,11 @@ def _ints(name, t, *shape):
         raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, list(shape)))
 
 
+def _wrong_ints(**tensors):
+    for name, (t, *shape) in tensors.items():
+        _ints(name, t, *shape)
+
+
 # ---------------------------------------------------------------- attention
 
 def gqa_workspace_size(B: int, q_len: int, H: int, Hkv: int, D: int) -> int:
@@ -178,12 +183,14 @@ def blocks_extend(seq_lens, new_lens, block_table, page_size, free_pages, free_c
     """
     call = _f("mla_blocks_extend")
     B, max_blocks, n_free, n_slots = len(seq_lens), block_table.shape[-1], len(free_pages), len(slots)
-    _ints("seq_lens", seq_lens, B)
-    _ints("new_lens", new_lens, B)
-    _ints("block_table", block_table, B, max_blocks)
-    _ints("free_pages", free_pages, n_free)
-    _ints("free_count", free_count, 1)
-    _ints("slots", slots, n_slots)
+    i32 = _int32
+    if not (seq_lens.dtype is i32 and new_lens.dtype is i32 and block_table.dtype is i32 and free_pages.dtype is i32
+            and free_count.dtype is i32 and slots.dtype is i32 and seq_lens.dim() == 1 and new_lens.shape == (B,)
+            and block_table.shape == (B, max_blocks) and free_pages.dim() == 1 and free_count.shape == (1,)
+            and slots.dim() == 1 and seq_lens.is_contiguous() and new_lens.is_contiguous()
+            and block_table.is_contiguous() and free_pages.is_contiguous() and slots.is_contiguous()):
+        _wrong_ints(seq_lens=(seq_lens, B), new_lens=(new_lens, B), block_table=(block_table, B, max_blocks),
+                    free_pages=(free_pages, n_free), free_count=(free_count, 1), slots=(slots, n_slots))
     dev = seq_lens.get_device()
     if not (_on_current(dev) and dev == new_lens.get_device() == block_table.get_device() == free_pages.get_device()
             == free_count.get_device() == slots.get_device()):
@@ -200,11 +207,14 @@ def blocks_trim(seq_lens, keep_lens, block_table, page_size, free_pages, free_co
     released pages back on the stack: the inverse of ``blocks_extend``."""
     call = _f("mla_blocks_trim")
     B, max_blocks, n_free = len(seq_lens), block_table.shape[-1], len(free_pages)
-    _ints("seq_lens", seq_lens, B)
-    _ints("keep_lens", keep_lens, B)
-    _ints("block_table", block_table, B, max_blocks)
-    _ints("free_pages", free_pages, n_free)
-    _ints("free_count", free_count, 1)
+    i32 = _int32
+    if not (seq_lens.dtype is i32 and keep_lens.dtype is i32 and block_table.dtype is i32 and free_pages.dtype is i32
+            and free_count.dtype is i32 and seq_lens.dim() == 1 and keep_lens.shape == (B,)
+            and block_table.shape == (B, max_blocks) and free_pages.dim() == 1 and free_count.shape == (1,)
+            and seq_lens.is_contiguous() and keep_lens.is_contiguous() and block_table.is_contiguous()
+            and free_pages.is_contiguous()):
+        _wrong_ints(seq_lens=(seq_lens, B), keep_lens=(keep_lens, B), block_table=(block_table, B, max_blocks),
+                    free_pages=(free_pages, n_free), free_count=(free_count, 1))
     dev = seq_lens.get_device()
     if not (_on_current(dev) and dev == keep_lens.get_device() == block_table.get_device() == free_pages.get_device()
             == free_count.get_device()):
@@ -293,10 +303,12 @@ def _keep_tables(block_table, seq_lens, path, keep):
         raise ValueError("expected path [B,q] and block_table [B,max_blocks]")
     B, q_len = path.shape
     max_blocks = block_table.shape[1]
-    _ints("path", path, B, q_len)
-    _ints("keep", keep, B)
-    _ints("seq_lens", seq_lens, B)
-    _ints("block_table", block_table, B, max_blocks)
+    i32 = _int32
+    if not (path.dtype is i32 and keep.dtype is i32 and seq_lens.dtype is i32 and block_table.dtype is i32
+            and keep.shape == (B,) and seq_lens.shape == (B,) and block_table.shape == (B, max_blocks)
+            and path.is_contiguous() and keep.is_contiguous() and seq_lens.is_contiguous()
+            and block_table.is_contiguous()):
+        _wrong_ints(path=(path, B, q_len), keep=(keep, B), seq_lens=(seq_lens, B), block_table=(block_table, B, max_blocks))
     return B, q_len, max_blocks
 
 
