@@ -134,7 +134,7 @@ int byte_strides(const int64_t* given, const long long* sizes, int D, long long*
 }
 
 int encode(const DeviceCommon& d, CUtensorMap* map, const void* base, const Call& c, const long long* stride,
-           long long rows, int batches, int box_rows) {
+           long long rows, int batches, int box_rows, CUtensorMapL2promotion promotion) {
   const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(c.D / 64),
                               static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(batches)};
   const cuuint64_t strides[4] = {static_cast<cuuint64_t>(stride[1]), 128, static_cast<cuuint64_t>(stride[2]),
@@ -146,7 +146,7 @@ int encode(const DeviceCommon& d, CUtensorMap* map, const void* base, const Call
       d.encode(map, c.dtype == MLA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B,
-               c.D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+               promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_LAUNCH;
 }
 
@@ -189,9 +189,26 @@ int run(const Call& c) {
     const int low = c.page & -c.page;
     box = low >= kKeys ? kKeys : (low >= 8 ? low : 0);
   }
+  p.group_sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
+  p.group_members = (pl.groups + p.group_sets - 1) / p.group_sets;
+  // Heads side by side where a row of the cache holds them all: the most that
+  // leave fewer than 3 % of the CTAs without a team.
+  int heads = 1;
+  if (p.k_stride[2] < p.k_stride[1])
+    for (int h = 2; h <= c.Hkv && h * p.group_members <= grid; ++h) {
+      const int team = h * p.group_members;
+      if (c.Hkv % h == 0 && 100 * (grid % team) < 3 * grid) heads = h;
+    }
+  p.members = heads * p.group_members;
+  p.head_sets = c.Hkv / heads;
+  // Fetches of 256 bytes into L2 where the team wants all of them: two heads of
+  // 64 dims side by side (64 streams of 16k keys 347 -> 326 us; without teams
+  // such fetches cost 480 us against 397).
+  const CUtensorMapL2promotion promotion =
+      c.D == 128 || heads > 1 || c.Hkv == 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   CUtensorMap map_k = {}, map_v = {};
-  if (box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box) != MLA_OK ||
-                   encode(d, &map_v, c.v, c, p.v_stride, rows, batches, box) != MLA_OK))
+  if (box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box, promotion) != MLA_OK ||
+                   encode(d, &map_v, c.v, c, p.v_stride, rows, batches, box, promotion) != MLA_OK))
     return MLA_ERR_LAUNCH;
 
   uint8_t* const ws = static_cast<uint8_t*>(c.workspace);
@@ -220,10 +237,8 @@ int run(const Call& c) {
   p.desc_units = units <= grid;
   p.whole = c.Smax <= kWholeKeys;
   p.min_tiles = p.whole ? 1 : kMinTiles;
-  p.sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
-  p.members = (pl.groups + p.sets - 1) / p.sets;
   p.max_blocks = c.max_blocks;
-  p.page = c.page;
+  p.page = Divisor(paged ? c.page : 1);
   p.pool_pages = paged ? static_cast<int>(c.pool_rows / c.page) : 0;
   p.box_rows = box;
   p.test_stall = d.test_stall;
@@ -249,7 +264,7 @@ int run(const Call& c) {
   const int entries = p.desc_units ? static_cast<int>(units) : grid;
   const int pairs = ((rows_a_head < pl.part_rows ? rows_a_head : pl.part_rows) + 1) / 2;
   const bool many = p.desc_units && static_cast<long long>(entries) * pairs <= 3 * grid &&
-                    (grid / p.members) / (static_cast<long long>(c.B) * c.Hkv * p.sets) >= kManyParts;
+                    (grid / p.members) / (static_cast<long long>(c.B) * p.head_sets * p.group_sets) >= kManyParts;
   if (many) {
     cfg.gridDim = dim3(pairs, entries, 1);
   } else {

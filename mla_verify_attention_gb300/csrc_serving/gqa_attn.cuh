@@ -63,10 +63,12 @@ struct Params {
   float4* part_o;                  // [2 * grid][part_rows][D / 4]
   unsigned int* status;
   int B, q_len, H, Hkv, G, Smax, groups, part_rows, min_tiles;
-  int members, sets;               // row groups side by side, and one after the other
+  int members, group_members;      // CTAs a team: key heads x row groups side by side
+  int head_sets, group_sets;       // ... and one after the other
   int desc_units;                  // entries of `desc`: one a unit, or one a CTA
   int whole;                       // units are not cut (short caches): the work is counted in units
-  int max_blocks, page, pool_pages;
+  int max_blocks, pool_pages;
+  Divisor page;
   int box_rows;                    // rows a TMA box: 64 or a divisor that no page boundary cuts; 0: gather
   int test_stall;
   float scale_log2;
@@ -253,10 +255,11 @@ struct Segment {
 };
 
 // Walks a CTA's run of work [t, t1); every role walks it on its own.  The row
-// groups of a key head are taken side by side by `members` CTAs with the same
-// run, so that they read the same tiles at the same time and the caches come
-// from HBM once (one after the other, 1,024 rows a head over 8k keys read them
-// four times at 5.2 TB/s); a group that does not exist is skipped.
+// groups of a key head, and key heads whose rows interleave in the cache, are
+// taken side by side by the CTAs of a team, which have the same run: they read
+// the same tiles at the same time, so that the caches come from HBM once (one
+// after the other, 1,024 rows a head over 8k keys read them four times at 5.2
+// TB/s) and in whole rows.  A group that does not exist is skipped.
 struct Walk {
   long long t, t1, pre;
   int b, S, nt;
@@ -265,7 +268,8 @@ struct Walk {
     if (t < t1) nt = stream_tiles(p, b, S);
   }
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
-    const int units = p.Hkv * p.sets, member = static_cast<int>(blockIdx.x) % p.members;
+    const int units = p.head_sets * p.group_sets, member = static_cast<int>(blockIdx.x) % p.members;
+    const int head_member = member / p.group_members, group_member = member - head_member * p.group_members;
     while (t < t1) {
       while (t >= pre + static_cast<long long>(stream_work(p, nt)) * units) {
         pre += static_cast<long long>(stream_work(p, nt)) * units;
@@ -278,8 +282,9 @@ struct Walk {
       s.S = S;
       s.nt = nt;
       s.tile0 = local - u * work;
-      s.head = u / p.sets;
-      s.group = (u - s.head * p.sets) * p.members + member;
+      const int head_set = u / p.group_sets;
+      s.head = head_set * (p.members / p.group_members) + head_member;
+      s.group = (u - head_set * p.group_sets) * p.group_members + group_member;
       const long long left = t1 - t;
       const int n = left < work - s.tile0 ? static_cast<int>(left) : work - s.tile0;
       s.n = p.whole ? nt : n;
@@ -296,13 +301,15 @@ __device__ __forceinline__ int rows_of_group(const Params& p, int group) {
 
 // ------------------------------------------------------------ loads
 
-__device__ __forceinline__ int page_of(const Params& p, int b, int key) {
-  int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + key / p.page);
+// Pool row of a key of stream b.  A page outside the pool is reported, and page 0 read.
+__device__ __forceinline__ int pool_row(const Params& p, int b, int key) {
+  const int blk = p.page.of(key), size = static_cast<int>(p.page.d);
+  int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + blk);
   if (page < 0 || page >= p.pool_pages) {
     atomicOr(p.status, kBitPage);
     page = 0;
   }
-  return page;
+  return page * size + (key - blk * size);
 }
 
 // Position in a ring of stages.
@@ -338,8 +345,7 @@ __device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUt
       const int key = (s.tile0 + j) * kKeys + lane * R;
       if (!paged) return key;
       if (lane >= boxes || j >= s.n || key >= s.S) return 0;
-      const int page = page_of(p, s.b, key);
-      return page * p.page + key % p.page;
+      return pool_row(p, s.b, key);
     };
     const int batch = paged ? 0 : s.b;
     int row = row_of(0);
@@ -400,9 +406,7 @@ __device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk w
   while (w.next(p, s)) {
     auto row_of = [&](int j, int half) {       // -1 past the stream
       const int key = (s.tile0 + j) * kKeys + half * 32 + lane;
-      if (j >= s.n || key >= s.S) return -1;
-      const int page = page_of(p, s.b, key);
-      return page * p.page + key % p.page;
+      return j >= s.n || key >= s.S ? -1 : pool_row(p, s.b, key);
     };
     const uint8_t* const head = pool + s.head * head_stride + (lane % kUnits) * 16;
     int lo = row_of(0, 0), hi = row_of(0, 1);
@@ -892,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's run of tiles: each thread sums a run of streams, then a
   // scan over threads; the thread whose streams hold the first tile says which.
-  const int units = p.Hkv * p.sets;
+  const int units = p.head_sets * p.group_sets;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long sum = 0;
