@@ -401,7 +401,8 @@ enum mla_dtype { MLA_BF16 = 0, MLA_FP16 = 1 };
  *              stream with any other value outside [q_len, Smax] records MLA_ERR_SEQLEN and
  *              gets the same result.  Rows t < seq_lens[b] of k and v must be finite; the
  *              others may hold anything.
- *   tree_mask, scale, B, q_len, Smax and the errors as for mla_verify_attn; B < 2^20.
+ *   tree_mask, scale, q_len, Smax and the errors as for mla_verify_attn; B < 2^20, and
+ *              B * ceil(Smax / 64) * Hkv * ceil(q_len * H / Hkv / 128) < 2^31.
  *   workspace  at least mla_gqa_workspace_size(B, q_len, H, Hkv, D) bytes, 256-byte aligned;
  *              contents do not matter, not read after the call; calls that share it must not overlap.
  * Scores, softmax statistics and sums are fp32; the weights enter the product

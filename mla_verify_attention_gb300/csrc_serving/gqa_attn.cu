@@ -154,7 +154,9 @@ int run(const Call& c) {
   if (!shape_ok(c.B, c.q_len, c.H, c.Hkv, c.D) || c.Smax < 1 || c.Smax >= (1 << 24)) return MLA_ERR_SHAPE;
   if ((c.dtype != MLA_BF16 && c.dtype != MLA_FP16) || !std::isfinite(c.scale)) return MLA_ERR_ARG;
   const Plan pl = plan(c.q_len, c.H, c.Hkv);
-  if (static_cast<long long>((c.Smax + kKeys - 1) / kKeys) * c.Hkv * pl.groups >= (1ll << 31)) return MLA_ERR_SHAPE;
+  // The kernel counts the work, at most this, in 32 bits.
+  if (static_cast<long long>((c.Smax + kKeys - 1) / kKeys) * c.Hkv * pl.groups >= (1ll << 31) / (c.B > 0 ? c.B : 1))
+    return MLA_ERR_SHAPE;
   if (c.B == 0) return MLA_OK;
   if (!c.q || !c.k || !c.v || !c.seq_lens || !c.mask || !c.out || !c.lse) return MLA_ERR_NULLPTR;
   if (!aligned_to(c.q, 16) || !aligned_to(c.k, 16) || !aligned_to(c.v, 16) || !aligned_to(c.out, 16) ||

@@ -94,9 +94,7 @@ struct __align__(1024) Smem {
   // (qfree: one a segment parity.  The products can be through with a short
   // segment before a softmax warp asks for the one before it.)
   uint64_t qfull, qfree[2], ofull, ofree, mlx, drain[2];
-  long long total, start_pre;
-  long long warp_sum[kThreads / 32];
-  int start_b;
+  int warp_sum[kThreads / 32], start_b, start_pre;
   uint32_t tmem_base, abort_flag;
 };
 
@@ -254,6 +252,21 @@ struct Segment {
   int b, S, head, group, tile0, n, nt;   // tiles tile0 .. tile0 + n - 1 of the unit's nt
 };
 
+// The teams' runs of a total of work: equal, the first `more` one longer.
+struct Runs {
+  int teams, each, more;
+  __device__ __forceinline__ Runs(int total, int min_work, int all) {
+    teams = max(1, min(total / min_work, all));
+    each = total / teams;
+    more = total - each * teams;
+  }
+  __device__ __forceinline__ int start(int team) const { return team * each + min(team, more); }
+  __device__ __forceinline__ int team_of(int t) const {
+    const int longer = more * (each + 1);
+    return t < longer ? t / (each + 1) : more + (t - longer) / each;
+  }
+};
+
 // Walks a CTA's run of work [t, t1); every role walks it on its own.  The row
 // groups of a key head, and key heads whose rows interleave in the cache, are
 // taken side by side by the CTAs of a team, which have the same run: they read
@@ -261,9 +274,9 @@ struct Segment {
 // after the other, 1,024 rows a head over 8k keys read them four times at 5.2
 // TB/s) and in whole rows.  A group that does not exist is skipped.
 struct Walk {
-  long long t, t1, pre;
+  int t, t1, pre;                          // pre: work before stream b
   int b, S, nt;
-  __device__ __forceinline__ Walk(const Params& p, long long t0, long long t1_, int b0, long long pre0)
+  __device__ __forceinline__ Walk(const Params& p, int t0, int t1_, int b0, int pre0)
       : t(t0), t1(t1_), pre(pre0), b(b0), S(0), nt(0) {
     if (t < t1) nt = stream_tiles(p, b, S);
   }
@@ -271,11 +284,11 @@ struct Walk {
     const int units = p.head_sets * p.group_sets, member = static_cast<int>(blockIdx.x) % p.members;
     const int head_member = member / p.group_members, group_member = member - head_member * p.group_members;
     while (t < t1) {
-      while (t >= pre + static_cast<long long>(stream_work(p, nt)) * units) {
-        pre += static_cast<long long>(stream_work(p, nt)) * units;
+      while (t >= pre + stream_work(p, nt) * units) {
+        pre += stream_work(p, nt) * units;
         nt = stream_tiles(p, ++b, S);
       }
-      const int local = static_cast<int>(t - pre);
+      const int local = t - pre;
       const int work = stream_work(p, nt);
       const int u = local / work;
       s.b = b;
@@ -285,8 +298,7 @@ struct Walk {
       const int head_set = u / p.group_sets;
       s.head = head_set * (p.members / p.group_members) + head_member;
       s.group = (u - head_set * p.group_sets) * p.group_members + group_member;
-      const long long left = t1 - t;
-      const int n = left < work - s.tile0 ? static_cast<int>(left) : work - s.tile0;
+      const int n = min(t1 - t, work - s.tile0);
       s.n = p.whole ? nt : n;
       t += n;
       if (s.group < p.groups) return true;
@@ -821,7 +833,7 @@ __device__ __forceinline__ void drain_products(uint64_t& bar) {
 // business (0).  With p.desc_units there is an entry a unit, else one a CTA, for
 // the only unit that can be cut, its last.  Written before the first wait, so
 // that the merge finds it whatever becomes of the loads.
-__device__ __forceinline__ void note_cut_units(const Params& p, Walk w, long long t1, long long total, long long teams) {
+__device__ __forceinline__ void note_cut_units(const Params& p, Walk w, const Runs& runs) {
   const int cta = static_cast<int>(blockIdx.x);
   int4 d = make_int4(0, 0, 0, 0);
   Segment s;
@@ -829,9 +841,8 @@ __device__ __forceinline__ void note_cut_units(const Params& p, Walk w, long lon
     if (s.tile0 != 0) continue;
     const int hg = s.head * p.groups + s.group;
     if (s.n < s.nt) {
-      const long long end = t1 - s.n + s.nt;               // past the unit's last tile
-      const long long last = (end * teams - 1) / total;    // the team that has it
-      d = make_int4(s.b, hg, 2 * cta + (seg > 0 ? 1 : 0), static_cast<int>(last - cta / p.members) + 1);
+      const int last = runs.team_of(w.t1 - s.n + s.nt - 1);   // the team that has the unit's last tile
+      d = make_int4(s.b, hg, 2 * cta + (seg > 0 ? 1 : 0), last - cta / p.members + 1);
     }
     if (p.desc_units) p.desc[s.b * p.Hkv * p.groups + hg] = d;
   }
@@ -856,34 +867,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    if (p.box_rows) {
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-    }
+  if (warp == 3) {
     const uint32_t loaders = p.box_rows ? 1 : 32;
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = lane; i < C::kStages; i += 32) {
       mbar_init(smem_u32(&sm.kfull[i]), loaders);
       mbar_init(smem_u32(&sm.vfull[i]), loaders);
       mbar_init(smem_u32(&sm.kempty[i]), 1);
       mbar_init(smem_u32(&sm.vempty[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&sm.sfull[i >> 1][i & 1]), 1);
-      mbar_init(smem_u32(&sm.pfull[i >> 1][i & 1]), 4);
-      mbar_init(smem_u32(&sm.pvdone[i >> 1][i & 1]), 1);
+    if (lane >= 16 && lane < 20) {
+      const int g = (lane >> 1) & 1, i = lane & 1;
+      mbar_init(smem_u32(&sm.sfull[g][i]), 1);
+      mbar_init(smem_u32(&sm.pfull[g][i]), 4);
+      mbar_init(smem_u32(&sm.pvdone[g][i]), 1);
     }
-    mbar_init(smem_u32(&sm.qfull), 8);
-    mbar_init(smem_u32(&sm.qfree[0]), 1);
-    mbar_init(smem_u32(&sm.qfree[1]), 1);
-    mbar_init(smem_u32(&sm.ofull), 1);
-    mbar_init(smem_u32(&sm.ofree), 8);
-    mbar_init(smem_u32(&sm.mlx), 8);
-    mbar_init(smem_u32(&sm.drain[0]), 1);
-    mbar_init(smem_u32(&sm.drain[1]), 1);
-    sm.abort_flag = 0;
-    sm.start_b = 0;
-    sm.start_pre = 0;
+    if (lane == 20) {
+      mbar_init(smem_u32(&sm.qfull), 8);
+      mbar_init(smem_u32(&sm.qfree[0]), 1);
+      mbar_init(smem_u32(&sm.qfree[1]), 1);
+    }
+    if (lane == 21) {
+      mbar_init(smem_u32(&sm.ofull), 1);
+      mbar_init(smem_u32(&sm.ofree), 8);
+      mbar_init(smem_u32(&sm.mlx), 8);
+    }
+    if (lane == 22) {
+      mbar_init(smem_u32(&sm.drain[0]), 1);
+      mbar_init(smem_u32(&sm.drain[1]), 1);
+      sm.abort_flag = 0;
+    }
     fence_mbarrier_init_cluster();
     fence_proxy_async_smem();
   }
@@ -891,57 +903,91 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
     tmem_relinquish();
   }
+  if (tid == 0 && p.box_rows) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
   grid_dependency_wait();                                  // nothing of the caller's was touched so far
   if (tid == 0) grid_launch_dependents();
 
-  // ---- this CTA's run of tiles: each thread sums a run of streams, then a
-  // scan over threads; the thread whose streams hold the first tile says which.
+  // ---- this CTA's run of work: it starts in stream `start_b`, before which
+  // lie `start_pre` tiles (or units).
   const int units = p.head_sets * p.group_sets;
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long sum = 0;
-  int len;
-  for (int b = b0; b < b1; ++b) {
-    sum += static_cast<long long>(stream_work(p, stream_tiles(p, b, len))) * units;
-    if (blockIdx.x == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
-  }
-  long long inc = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
-  }
-  if (lane == 31) sm.warp_sum[warp] = inc;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i == warp) before = total;
-    total += sm.warp_sum[i];
-  }
-  // Teams of `members` CTAs share a run.
   const int all = static_cast<int>(gridDim.x) / p.members, team = static_cast<int>(blockIdx.x) / p.members;
-  long long teams = total / p.min_tiles;
-  teams = teams < 1 ? 1 : (teams < all ? teams : all);
-  const long long t0 = team < teams ? total * team / teams : total;
-  const long long t1 = team < teams ? total * (team + 1) / teams : total;
-  before += inc - sum;
-  if (t0 >= before && t0 < before + sum) {
-    int b = b0;
-    while (true) {
-      const long long n = static_cast<long long>(stream_work(p, stream_tiles(p, b, len))) * units;
-      if (t0 < before + n) break;
-      before += n;
-      ++b;
+  int len, total, start_b = 0, start_pre = 0;
+  if (p.B <= 32) {
+    // Every warp by itself, a stream a lane.
+    int work = 0;
+    if (lane < p.B) {
+      work = stream_work(p, stream_tiles(p, lane, len)) * units;
+      if (blockIdx.x == 0 && warp == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
     }
-    sm.start_b = b;
-    sm.start_pre = before;
+    int inc = work;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    const Runs runs(total, p.min_tiles, all);
+    if (team < runs.teams && total > 0) {
+      start_b = __ffs(__ballot_sync(0xFFFFFFFFu, inc > runs.start(team))) - 1;
+      start_pre = __shfl_sync(0xFFFFFFFFu, inc - work, start_b);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    // Each thread sums a run of streams, then a scan over threads; the thread
+    // whose streams hold the first tile says which.
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      sum += stream_work(p, stream_tiles(p, b, len)) * units;
+      if (blockIdx.x == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
+    }
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 31) sm.warp_sum[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i == warp) before = total;
+      total += sm.warp_sum[i];
+    }
+    const Runs runs(total, p.min_tiles, all);
+    const int t0 = team < runs.teams ? runs.start(team) : total;
+    before += inc - sum;
+    if (t0 >= before && t0 < before + sum) {
+      int b = b0;
+      while (true) {
+        const int n = stream_work(p, stream_tiles(p, b, len)) * units;
+        if (t0 < before + n) break;
+        before += n;
+        ++b;
+      }
+      sm.start_b = b;
+      sm.start_pre = before;
+    }
+    __syncthreads();
+    if (t0 < total) {
+      start_b = sm.start_b;
+      start_pre = sm.start_pre;
+    }
   }
-  __syncthreads();
   const uint32_t tmem = sm.tmem_base;
-  const Walk walk(p, t0, t1, sm.start_b, sm.start_pre);
+  const Runs runs(total, p.min_tiles, all);
+  const int t0 = team < runs.teams ? runs.start(team) : total;
+  const Walk walk(p, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
 
   if (warp == 0 || warp == 2) {
     if (p.box_rows == 0) load_gather<D>(sm, p, walk, warp == 2);
@@ -950,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ProductsQk<D, kBf16>(sm, p, tmem).run(walk);
     drain_products(sm.drain[0]);
   } else if (warp == 3) {
-    if (lane == 0 && !p.whole) note_cut_units(p, walk, t1, total, teams);
+    if (lane == 0 && !p.whole) note_cut_units(p, walk, runs);
     __syncwarp();
     ProductsPv<D, kBf16>(sm, p, tmem).run(walk);
     drain_products(sm.drain[1]);
