@@ -731,7 +731,9 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
     const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
     const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head;
     float m_off = m == -CUDART_INF_F ? -CUDART_INF_F : m - kShift;
-    // The groups' accumulators: their weights, from both maxima and sums.
+    // The groups' accumulators: their weights, from both maxima and sums.  (Not
+    // before the last segment's, in the same place, have been read.)
+    if (seg > 0 && !wait(sm, sm.ofree, (seg - 1) & 1, p)) return;
     sm.ml[g][r] = make_float2(m_off, l);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.mlx));

@@ -76,6 +76,42 @@ def test_matches_plain(B, q, H, Hkv, lens, D, dt):
     verify(c, *run(c))
 
 
+@pytest.mark.parametrize("B,q,H,Hkv,D,lens,dt", [
+    (1, 9, 40, 5, 64, [700], BF16),             # heads that no team divides evenly
+    (2, 3, 21, 3, 128, [600, 1290], FP16),      # seven heads a key head, three key heads
+    (1, 64, 40, 1, 64, [900], BF16),            # 2,560 rows: twenty row groups, two sets of them
+    (1, 64, 64, 2, 128, [1000], FP16),          # sixteen row groups
+    (3, 33, 24, 8, 64, [33, 2100, 800], BF16),  # heads side by side, 99 rows
+    (1, 1, 128, 128, 128, [1500], BF16),        # a key head a head, many of them
+    (60, 2, 16, 2, 128, list(range(2, 1202, 20)), BF16),   # many units, cut and whole
+])
+def test_heads_and_row_groups(B, q, H, Hkv, D, lens, dt):
+    c = case(B, q, H, Hkv, D, lens, dt)
+    verify(c, *run(c))
+
+
+@pytest.mark.parametrize("smax", [448, 512, 513, 600])
+def test_short_caches_whole_and_cut(smax):
+    # Up to 512 keys units are not cut, and there is no merge.
+    for lens in ([smax, 9, 0], [70, smax - 1, 64]):
+        c = case(3, 9, 16, 4, 128, lens, BF16, smax=smax)
+        verify(c, *run(c))
+
+
+def test_many_segments_of_one_tile():
+    # Single tiles one after the other: each is a segment of its own, with one
+    # softmax group idle; masked rows among them.
+    gen = torch.Generator().manual_seed(8)
+    lens = [int(x) for x in torch.randint(5, 70, (700,), generator=gen)]
+    for tree in ("random", "any"):
+        c = case(700, 5, 8, 1, 128, lens, BF16, smax=70, tree=tree)
+        a = run(c)
+        verify(c, *a)
+        for _ in range(3):
+            b = run(c)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("tree", ["chain", "any"])
 @pytest.mark.parametrize("q,G,n", [(9, 8, 9), (9, 8, 70), (40, 2, 41), (64, 4, 64), (64, 4, 129)])
 def test_masks(q, G, n, tree):

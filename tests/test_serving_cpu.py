@@ -32,7 +32,7 @@ PAGED = dict(q=16, k=16, v=16, strides=None, rows=640, table=16, max_blocks=5, p
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q_len=0), SHAPE), (dict(q_len=65), SHAPE), (dict(H=0), SHAPE), (dict(Hkv=0), SHAPE), (dict(H=63), SHAPE),
-    (dict(D=96), SHAPE), (dict(B=-1), SHAPE), (dict(B=1 << 20), SHAPE), (dict(Smax=0), SHAPE),
+    (dict(D=96), SHAPE), (dict(B=-1), SHAPE), (dict(B=1 << 20), SHAPE), (dict(B=1 << 16, Smax=1 << 18), SHAPE), (dict(Smax=0), SHAPE),
     (dict(Smax=1 << 24), SHAPE), (dict(dtype=2), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
     (dict(q=0), NULL), (dict(k=0), NULL), (dict(v=0), NULL), (dict(lens=0), NULL), (dict(mask=0), NULL),
     (dict(out=0), NULL), (dict(lse=0), NULL), (dict(k=24), ALIGN), (dict(out=8), ALIGN), (dict(ws=272), ALIGN),
