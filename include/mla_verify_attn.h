@@ -431,6 +431,23 @@ int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_p
                               int dtype, float scale, void* out, float* lse, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * The calls of this section with their arguments in one array of 64-bit values,
+ * in the order of their declarations: integers and addresses as such, a float
+ * as the bits of a double.  For bindings to which each argument costs more than
+ * its share of the launch.  Returns what the call returns, or MLA_ERR_ARG for an
+ * unknown `call`; an integer argument that does not fit its type is MLA_ERR_SHAPE.
+ */
+enum mla_packed {
+  MLA_CALL_BLOCKS_EXTEND = 0,
+  MLA_CALL_BLOCKS_TRIM = 1,
+  MLA_CALL_CACHE_APPEND = 2,
+  MLA_CALL_CACHE_KEEP = 3,
+  MLA_CALL_GQA_VERIFY_ATTN = 4,
+  MLA_CALL_GQA_VERIFY_ATTN_PAGED = 5
+};
+int mla_call_packed(int call, const int64_t* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,7 +26,7 @@ EXPORTED = ("mla_verify_attn", "mla_verify_attn_workspace_size", "mla_verify_att
             "mla_verify_attn_set_test_controls", "mla_verify_attn_noalloc",
             "mla_verify_attn_set_two_term_max_keys", "mla_blocks_extend", "mla_blocks_trim",
             "mla_cache_append", "mla_cache_keep", "mla_gqa_workspace_size", "mla_gqa_verify_attn",
-            "mla_gqa_verify_attn_paged")
+            "mla_gqa_verify_attn_paged", "mla_call_packed")
 
 _lock = threading.Lock()
 _lib = None
@@ -86,6 +86,8 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.mla_gqa_verify_attn_paged.argtypes = [P, P, P, P, L, P, I, I, P, P, I, I, I, I, I, I, F, P, P,
                                                   P, Z, P]
         lib.mla_gqa_verify_attn_paged.restype = I
+        lib.mla_call_packed.argtypes = [I, ctypes.c_char_p]
+        lib.mla_call_packed.restype = I
         _lib = lib
         return lib
 

@@ -8,33 +8,39 @@ raises ``MLAError``.  Problems only the GPU can see are in
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from ._lib import MLA_OK, MLAError, load_library
 
 _STRIDES = ctypes.c_longlong * 9
 LATENT, ROPE, ROW = 512, 64, 576
 
-# Bound by the first call: a verify step makes several of these calls, each a
-# few microseconds of GPU time, so they are kept as lean as checks allow.
-_fn = {}
-_torch = None
+# A verify step makes several of these calls, each a few microseconds of GPU
+# time, so they are kept as lean as checks allow: arguments are packed into one
+# array (ctypes takes 1.3 us to convert sixteen of them, 0.4 us for this), and
+# what is looked up once is bound by the first call.
+_EXTEND, _TRIM, _APPEND, _KEEP, _GQA, _GQA_PAGED = range(6)
+_pack_extend = struct.Struct("=13q").pack
+_pack_trim = struct.Struct("=10q").pack
+_pack_append = struct.Struct("=14q").pack
+_pack_keep = struct.Struct("=16q").pack
+_pack_gqa = struct.Struct("=13qd5q").pack
+_pack_paged = struct.Struct("=16qd5q").pack
+
+_torch = _call = None
 _current_device = _current_stream = _int32 = _bf16 = _fp16 = _fp32 = None
 
 
-def _f(name):
-    f = _fn.get(name)
-    if f is None:
-        global _torch, _current_device, _current_stream, _int32, _bf16, _fp16, _fp32
-        import torch
-        _torch, _int32 = torch, torch.int32
-        _bf16, _fp16, _fp32 = torch.bfloat16, torch.float16, torch.float32
-        f = getattr(load_library(), name)
-        if hasattr(torch._C, "_cuda_getDevice"):
-            _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-        else:                                        # a torch without CUDA: no tensor gets past the device check
-            _current_device = _current_stream = lambda *_: -2
-        _fn[name] = f
-    return f
+def _bind():
+    global _torch, _call, _current_device, _current_stream, _int32, _bf16, _fp16, _fp32
+    import torch
+    _torch, _int32 = torch, torch.int32
+    _bf16, _fp16, _fp32 = torch.bfloat16, torch.float16, torch.float32
+    if hasattr(torch._C, "_cuda_getDevice"):
+        _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    else:                                        # a torch without CUDA: no tensor gets past the device check
+        _current_device = _current_stream = lambda *_: -2
+    _call = load_library().mla_call_packed
 
 
 def _wrong_device(*tensors):
@@ -76,7 +82,7 @@ def _wrong_ints(**tensors):
 
 def gqa_workspace_size(B: int, q_len: int, H: int, Hkv: int, D: int) -> int:
     """Workspace bytes of the two calls below on the current device."""
-    return int(_f("mla_gqa_workspace_size")(B, q_len, H, Hkv, D))
+    return int(load_library().mla_gqa_workspace_size(B, q_len, H, Hkv, D))
 
 
 def _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, Hkv):
@@ -88,7 +94,7 @@ def _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, Hkv):
     if (tree_mask.element_size() != 4 or tree_mask.shape != (B, q_len, (q_len + 31) >> 5)
             or not tree_mask.is_contiguous() or tree_mask.is_floating_point()):
         raise ValueError("tree_mask must be contiguous 32-bit words [B,q,ceil(q/32)]")
-    strides = None
+    strides = 0
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
         qs, ks, vs = q.stride(), k.stride(), v.stride()
         if qs[3] != 1 or ks[-1] != 1 or vs[-1] != 1:
@@ -125,7 +131,8 @@ def gqa_verify_attn(q, k, v, seq_lens, tree_mask, scale, out=None, lse=None, wor
     Returns (out [B,q,H,D] in q's type, lse [B,q,H] fp32); a row whose mask
     leaves nothing has out 0 and lse -inf.
     """
-    call = _f("mla_gqa_verify_attn")
+    if _call is None:
+        _bind()
     shape = k.shape
     if q.dim() != 4 or len(shape) != 4 or v.shape != shape or shape[0] != q.shape[0] or shape[3] != q.shape[3]:
         raise ValueError("expected q [B,q,H,D], k and v [B,Smax,Hkv,D]")
@@ -136,9 +143,10 @@ def gqa_verify_attn(q, k, v, seq_lens, tree_mask, scale, out=None, lse=None, wor
     B, q_len, H, D, dt, strides, out, lse, ws, made = _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, shape[2])
     if not dev == out.get_device() == lse.get_device() == ws.get_device():
         _wrong_device(q, out, lse, ws)
-    st = call(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H,
-              shape[2], D, shape[1], dt, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-              ws.numel() * ws.element_size(), _handle(stream, dev, made))
+    st = _call(_GQA, _pack_gqa(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides and ctypes.addressof(strides), seq_lens.data_ptr(),
+        tree_mask.data_ptr(), B, q_len, H, shape[2], D, shape[1], dt, scale, out.data_ptr(), lse.data_ptr(),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev, made)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn")
     return out, lse
@@ -148,7 +156,8 @@ def gqa_verify_attn_paged(q, k_pool, v_pool, block_table, page_size, seq_lens, t
                           workspace=None, stream=None):
     """gqa_verify_attn over pools k_pool, v_pool [pool_rows,Hkv,D] of pages of
     page_size >= 1 rows, block_table [B,max_blocks] int32; read in place."""
-    call = _f("mla_gqa_verify_attn_paged")
+    if _call is None:
+        _bind()
     shape = k_pool.shape
     if (q.dim() != 4 or len(shape) != 3 or v_pool.shape != shape or shape[2] != q.shape[3] or block_table.dim() != 2):
         raise ValueError("expected q [B,q,H,D], k_pool and v_pool [rows,Hkv,D], block_table [B,max_blocks]")
@@ -162,9 +171,11 @@ def gqa_verify_attn_paged(q, k_pool, v_pool, block_table, page_size, seq_lens, t
                                                            shape[1])
     if not dev == out.get_device() == lse.get_device() == ws.get_device():
         _wrong_device(q, out, lse, ws)
-    st = call(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), strides, shape[0], block_table.data_ptr(), max_blocks,
-              int(page_size), seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H, shape[1], D, dt, float(scale), out.data_ptr(),
-              lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev, made))
+    st = _call(_GQA_PAGED, _pack_paged(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), strides and ctypes.addressof(strides), shape[0],
+        block_table.data_ptr(), max_blocks, page_size, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H, shape[1],
+        D, dt, scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _handle(stream, dev, made)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn_paged")
     return out, lse
@@ -181,8 +192,9 @@ def blocks_extend(seq_lens, new_lens, block_table, page_size, free_pages, free_c
     [B,max_blocks], free_pages [n], free_count [1], slots [>= new tokens].
     Either the whole batch grows or nothing does (``last_device_error`` tells).
     """
-    call = _f("mla_blocks_extend")
-    B, max_blocks, n_free, n_slots = len(seq_lens), block_table.shape[-1], len(free_pages), len(slots)
+    if _call is None:
+        _bind()
+    B, max_blocks, n_free, n_slots = (seq_lens.shape[0], block_table.shape[-1], free_pages.shape[0], slots.shape[0])
     i32 = _int32
     if not (seq_lens.dtype is i32 and new_lens.dtype is i32 and block_table.dtype is i32 and free_pages.dtype is i32
             and free_count.dtype is i32 and slots.dtype is i32 and seq_lens.dim() == 1 and new_lens.shape == (B,)
@@ -195,9 +207,10 @@ def blocks_extend(seq_lens, new_lens, block_table, page_size, free_pages, free_c
     if not (_on_current(dev) and dev == new_lens.get_device() == block_table.get_device() == free_pages.get_device()
             == free_count.get_device() == slots.get_device()):
         _wrong_device(seq_lens, new_lens, block_table, free_pages, free_count, slots)
-    st = call(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, int(page_size),
-              free_pages.data_ptr(), n_free, free_count.data_ptr(), int(pool_pages), slots.data_ptr(), n_slots,
-              _handle(stream, dev))
+    st = _call(_EXTEND, _pack_extend(
+        seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, page_size,
+        free_pages.data_ptr(), n_free, free_count.data_ptr(), pool_pages, slots.data_ptr(), n_slots,
+        _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_blocks_extend")
 
@@ -205,8 +218,9 @@ def blocks_extend(seq_lens, new_lens, block_table, page_size, free_pages, free_c
 def blocks_trim(seq_lens, keep_lens, block_table, page_size, free_pages, free_count, stream=None):
     """Shortens every stream to keep_lens[b] tokens, in place, and puts the
     released pages back on the stack: the inverse of ``blocks_extend``."""
-    call = _f("mla_blocks_trim")
-    B, max_blocks, n_free = len(seq_lens), block_table.shape[-1], len(free_pages)
+    if _call is None:
+        _bind()
+    B, max_blocks, n_free = seq_lens.shape[0], block_table.shape[-1], free_pages.shape[0]
     i32 = _int32
     if not (seq_lens.dtype is i32 and keep_lens.dtype is i32 and block_table.dtype is i32 and free_pages.dtype is i32
             and free_count.dtype is i32 and seq_lens.dim() == 1 and keep_lens.shape == (B,)
@@ -219,8 +233,9 @@ def blocks_trim(seq_lens, keep_lens, block_table, page_size, free_pages, free_co
     if not (_on_current(dev) and dev == keep_lens.get_device() == block_table.get_device() == free_pages.get_device()
             == free_count.get_device()):
         _wrong_device(seq_lens, keep_lens, block_table, free_pages, free_count)
-    st = call(seq_lens.data_ptr(), keep_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, int(page_size),
-              free_pages.data_ptr(), n_free, free_count.data_ptr(), _handle(stream, dev))
+    st = _call(_TRIM, _pack_trim(
+        seq_lens.data_ptr(), keep_lens.data_ptr(), block_table.data_ptr(), B, max_blocks, page_size,
+        free_pages.data_ptr(), n_free, free_count.data_ptr(), _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_blocks_trim")
 
@@ -261,19 +276,21 @@ def cache_append(kv_pool, latent, rope, slots, stream=None):
     may be column ranges of wider rows), slots [T] int32 as ``blocks_extend``
     makes them; a negative slot skips its token.
     """
-    call = _f("mla_cache_append")
-    T = len(slots)
+    if _call is None:
+        _bind()
+    T = slots.shape[0]
     pool_stride = _rows("kv_pool", kv_pool, ROW)
     a_stride, b_stride = _rows("latent", latent, LATENT), _rows("rope", rope, ROPE)
     _ints("slots", slots, T)
-    if len(latent) != T or len(rope) != T:
+    if latent.shape[0] != T or rope.shape[0] != T:
         raise ValueError("expected one slot a row")
     dev = kv_pool.get_device()
     if not (_on_current(dev) and dev == latent.get_device() == rope.get_device() == slots.get_device()):
         _wrong_device(kv_pool, latent, rope, slots)
     pool = kv_pool.data_ptr()
-    st = call(latent.data_ptr(), a_stride, 2 * LATENT, pool, pool_stride, rope.data_ptr(), b_stride, 2 * ROPE,
-              pool + 2 * LATENT, pool_stride, len(kv_pool), slots.data_ptr(), T, _handle(stream, dev))
+    st = _call(_APPEND, _pack_append(
+        latent.data_ptr(), a_stride, 2 * LATENT, pool, pool_stride, rope.data_ptr(), b_stride, 2 * ROPE,
+        pool + 2 * LATENT, pool_stride, kv_pool.shape[0], slots.data_ptr(), T, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_append")
 
@@ -281,19 +298,21 @@ def cache_append(kv_pool, latent, rope, slots, stream=None):
 def gqa_cache_append(k_pool, v_pool, k, v, slots, stream=None):
     """Key and value rows by slot: k_pool[slots[t]] = k[t], v_pool[slots[t]] = v[t];
     pools [rows,Hkv,D], k and v [T,Hkv,D] (column ranges of wider rows, too)."""
-    call = _f("mla_cache_append")
-    T = len(slots)
+    if _call is None:
+        _bind()
+    T = slots.shape[0]
     dt, rows, heads, width, k_stride, v_stride = _pools(k_pool, v_pool)
     a_stride, b_stride = _head_rows("k", k, dt, heads, width), _head_rows("v", v, dt, heads, width)
     _ints("slots", slots, T)
-    if len(k) != T or len(v) != T:
+    if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("expected one slot a row")
     dev = k_pool.get_device()
     if not (_on_current(dev) and dev == v_pool.get_device() == k.get_device() == v.get_device() == slots.get_device()):
         _wrong_device(k_pool, v_pool, k, v, slots)
     n = 2 * heads * width
-    st = call(k.data_ptr(), a_stride, n, k_pool.data_ptr(), k_stride, v.data_ptr(), b_stride, n, v_pool.data_ptr(),
-              v_stride, rows, slots.data_ptr(), T, _handle(stream, dev))
+    st = _call(_APPEND, _pack_append(
+        k.data_ptr(), a_stride, n, k_pool.data_ptr(), k_stride, v.data_ptr(), b_stride, n,
+        v_pool.data_ptr(), v_stride, rows, slots.data_ptr(), T, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_append")
 
@@ -320,22 +339,25 @@ def cache_keep(kv_pool, block_table, page_size, seq_lens, path, keep, stream=Non
     (``blocks_trim`` to prefix + keep follows).  A contiguous cache [B,Smax,576]
     is a pool of one page of Smax rows a stream.
     """
-    call = _f("mla_cache_keep")
+    if _call is None:
+        _bind()
     pool_stride = _rows("kv_pool", kv_pool, ROW)
     B, q_len, max_blocks = _keep_tables(block_table, seq_lens, path, keep)
     dev = kv_pool.get_device()
     if not (_on_current(dev) and dev == block_table.get_device() == seq_lens.get_device() == path.get_device()
             == keep.get_device()):
         _wrong_device(kv_pool, block_table, seq_lens, path, keep)
-    st = call(kv_pool.data_ptr(), pool_stride, 2 * ROW, None, 0, 0, len(kv_pool), block_table.data_ptr(), max_blocks,
-              int(page_size), seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev))
+    st = _call(_KEEP, _pack_keep(
+        kv_pool.data_ptr(), pool_stride, 2 * ROW, 0, 0, 0, kv_pool.shape[0], block_table.data_ptr(),
+        max_blocks, page_size, seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_keep")
 
 
 def gqa_cache_keep(k_pool, v_pool, block_table, page_size, seq_lens, path, keep, stream=None):
     """cache_keep for pools of separate keys and values [rows,Hkv,D]."""
-    call = _f("mla_cache_keep")
+    if _call is None:
+        _bind()
     _, rows, heads, width, k_stride, v_stride = _pools(k_pool, v_pool)
     B, q_len, max_blocks = _keep_tables(block_table, seq_lens, path, keep)
     dev = k_pool.get_device()
@@ -343,7 +365,8 @@ def gqa_cache_keep(k_pool, v_pool, block_table, page_size, seq_lens, path, keep,
             == path.get_device() == keep.get_device()):
         _wrong_device(k_pool, v_pool, block_table, seq_lens, path, keep)
     n = 2 * heads * width
-    st = call(k_pool.data_ptr(), k_stride, n, v_pool.data_ptr(), v_stride, n, rows, block_table.data_ptr(), max_blocks,
-              int(page_size), seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev))
+    st = _call(_KEEP, _pack_keep(
+        k_pool.data_ptr(), k_stride, n, v_pool.data_ptr(), v_stride, n, rows, block_table.data_ptr(),
+        max_blocks, page_size, seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_keep")

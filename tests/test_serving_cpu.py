@@ -107,6 +107,37 @@ def test_keep_arguments(lib, kw, want):
     assert call(lib.mla_cache_keep, KEEP, **kw) == want
 
 
+def test_packed_calls(lib):
+    # The same statuses as the calls themselves, argument by argument.
+    import struct
+    no_device()                           # (the addresses are made up)
+    names = dict(enumerate((EXTEND, TRIM, APPEND, KEEP, GQA, PAGED)))
+    fns = (lib.mla_blocks_extend, lib.mla_blocks_trim, lib.mla_cache_append, lib.mla_cache_keep,
+           lib.mla_gqa_verify_attn, lib.mla_gqa_verify_attn_paged)
+
+    def packed(which, args):
+        v = [x if x is not None else 0 for x in args.values()]
+        return lib.mla_call_packed(which, b"".join(struct.pack("=d" if isinstance(x, float) else "=q", x) for x in v))
+
+    for which, args in names.items():
+        for key, value in args.items():
+            if key in ("stream", "strides", "ws_bytes"):
+                continue
+            for bad in (0, -1, 2, 1 << 20):
+                a = dict(args)
+                a[key] = float(bad) if isinstance(value, float) else bad
+                want = call(fns[which], a)
+                if want not in (OK, NO_DEVICE):
+                    assert packed(which, a) == want, (which, key, bad)
+            if isinstance(value, int) and 0 < value < 4096 and value != 16 and key not in ("pb", "ws"):
+                a = dict(args)
+                a[key] = 1 << 40
+                assert packed(which, a) != OK
+    assert packed(1, dict(TRIM, B=(1 << 32) + 2)) == SHAPE          # more than an int holds
+    assert packed(4, dict(GQA, scale=float("nan"))) == ARG
+    assert lib.mla_call_packed(6, b"\0" * 200) == ARG and lib.mla_call_packed(0, None) == NULL
+
+
 def test_without_a_device(lib):
     no_device()
     for f, a in ((lib.mla_gqa_verify_attn, GQA), (lib.mla_gqa_verify_attn_paged, PAGED), (lib.mla_blocks_extend, EXTEND),
