@@ -17,8 +17,6 @@ namespace mla {
 namespace gqa {
 
 constexpr int kMaxDevices = 64;
-// Fewest tiles a CTA takes: below that, fewer CTAs share a short call's work.
-constexpr int kMinTiles = 2;
 // Caches of at most so many keys are not cut: a CTA then takes whole units, and
 // there is nothing to merge.
 constexpr int kWholeKeys = 512;
@@ -202,7 +200,12 @@ int run(const Call& c) {
       if (c.Hkv % h == 0 && 100 * (grid % team) < 3 * grid) heads = h;
     }
   p.members = heads * p.group_members;
+  p.head_members = heads;
   p.head_sets = c.Hkv / heads;
+  p.by_members = Divisor(p.members);
+  p.by_group_members = Divisor(p.group_members);
+  p.by_group_sets = Divisor(p.group_sets);
+  p.by_G = Divisor(c.H / c.Hkv);
   // Fetches of 256 bytes into L2 where the team wants all of them: two heads of
   // 64 dims side by side (64 streams of 16k keys 347 -> 326 us; without teams
   // such fetches cost 480 us against 397).
@@ -238,7 +241,6 @@ int run(const Call& c) {
   const long long units = static_cast<long long>(c.B) * c.Hkv * pl.groups;
   p.desc_units = units <= grid;
   p.whole = c.Smax <= kWholeKeys;
-  p.min_tiles = p.whole ? 1 : kMinTiles;
   p.max_blocks = c.max_blocks;
   p.page = Divisor(paged ? c.page : 1);
   p.pool_pages = paged ? static_cast<int>(c.pool_rows / c.page) : 0;

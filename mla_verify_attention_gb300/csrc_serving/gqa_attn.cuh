@@ -53,6 +53,8 @@ namespace gqa {
 constexpr int kKeys = 64;                  // keys a tile
 constexpr int kRows = 128;                 // rows a group's accumulator (MMA M)
 constexpr int kThreads = 384;              // 4 control warps + 2 x 4 softmax warps
+// Fewest tiles a team takes: below that, fewer teams share a short call's work.
+constexpr int kMinTiles = 2;
 constexpr float kLazy = 8.0f;              // log2 units a row's max may grow before O is rescaled
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -70,13 +72,13 @@ struct Params {
   float2* part_ml;                 // [2 * grid][part_rows]
   float4* part_o;                  // [2 * grid][part_rows][D / 4]
   unsigned int* status;
-  int B, q_len, H, Hkv, G, Smax, groups, part_rows, min_tiles;
-  int members, group_members;      // CTAs a team: key heads x row groups side by side
+  int B, q_len, H, Hkv, G, Smax, groups, part_rows;
+  int members, head_members, group_members;   // CTAs a team: key heads x row groups side by side
   int head_sets, group_sets;       // ... and one after the other
   int desc_units;                  // entries of `desc`: one a unit, or one a CTA
   int whole;                       // units are not cut (short caches): the work is counted in units
   int max_blocks, pool_pages;
-  Divisor page;
+  Divisor page, by_members, by_group_members, by_group_sets, by_G;
   int box_rows;                    // rows a TMA box: 64 or a divisor that no page boundary cuts; 0: gather
   int test_stall;
   float scale_log2;
@@ -261,10 +263,12 @@ struct Segment {
 };
 
 // The teams' runs of a total of work: equal, the first `more` one longer.
+// (Divisions are by products where the divisor is the call's: an integer
+// division by a variable cost a call half a microsecond at its start.)
 struct Runs {
   int teams, each, more;
-  __device__ __forceinline__ Runs(int total, int min_work, int all) {
-    teams = max(1, min(total / min_work, all));
+  __device__ __forceinline__ Runs(const Params& p, int total, int all) {
+    teams = max(1, min(p.whole ? total : total / kMinTiles, all));
     each = total / teams;
     more = total - each * teams;
   }
@@ -283,29 +287,29 @@ struct Runs {
 // TB/s) and in whole rows.  A group that does not exist is skipped.
 struct Walk {
   int t, t1, pre;                          // pre: work before stream b
-  int b, S, nt;
-  __device__ __forceinline__ Walk(const Params& p, int t0, int t1_, int b0, int pre0)
+  int b, S, nt, head0, group0;
+  __device__ __forceinline__ Walk(const Params& p, int member, int t0, int t1_, int b0, int pre0)
       : t(t0), t1(t1_), pre(pre0), b(b0), S(0), nt(0) {
+    head0 = p.by_group_members.of(member);
+    group0 = member - head0 * p.group_members;
     if (t < t1) nt = stream_tiles(p, b, S);
   }
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
-    const int units = p.head_sets * p.group_sets, member = static_cast<int>(blockIdx.x) % p.members;
-    const int head_member = member / p.group_members, group_member = member - head_member * p.group_members;
+    const int units = p.head_sets * p.group_sets;
     while (t < t1) {
       while (t >= pre + stream_work(p, nt) * units) {
         pre += stream_work(p, nt) * units;
         nt = stream_tiles(p, ++b, S);
       }
-      const int local = t - pre;
-      const int work = stream_work(p, nt);
-      const int u = local / work;
+      const int local = t - pre, work = stream_work(p, nt);
+      const int u = local < work ? 0 : local / work;
+      const int head_set = p.by_group_sets.of(u);
       s.b = b;
       s.S = S;
       s.nt = nt;
       s.tile0 = local - u * work;
-      const int head_set = u / p.group_sets;
-      s.head = head_set * (p.members / p.group_members) + head_member;
-      s.group = (u - head_set * p.group_sets) * p.group_members + group_member;
+      s.head = head_set * p.head_members + head0;
+      s.group = (u - head_set * p.group_sets) * p.group_members + group0;
       const int n = min(t1 - t, work - s.tile0);
       s.n = p.whole ? nt : n;
       t += n;
@@ -575,7 +579,7 @@ __device__ __forceinline__ void start_q(Smem<D>& sm, const Params& p, const Segm
   constexpr int kPer = 32 / kUnits;                        // rows a warp copies at once
   const int rows = rows_of_group(p, s.group);
   const int R = s.group * kRows + wq * 32 + lane;
-  const int i = R / p.G;
+  const int i = p.by_G.of(R);
   // Each lane knows its row's address; the lanes that copy a row ask for it.
   const long long base = wq * 32 + lane < rows ? s.b * p.q_stride[0] + i * p.q_stride[1] +
                                                      (s.head * p.G + (R - i * p.G)) * p.q_stride[2]
@@ -633,7 +637,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
     const int R = s.group * kRows + r;                     // row of the stream and head: draft * G + head in group
     const bool valid = r < rows;
     const bool warp_valid = wq * 32 < rows;
-    const int i = R / p.G;
+    const int i = p.by_G.of(R);
     const int head = s.head * p.G + (R - i * p.G);
     uint64_t mask64 = 0;
     if (valid) {
@@ -854,7 +858,7 @@ __device__ __forceinline__ void note_cut_units(const Params& p, Walk w, const Ru
     const int hg = s.head * p.groups + s.group;
     if (s.n < s.nt) {
       const int last = runs.team_of(w.t1 - s.n + s.nt - 1);   // the team that has the unit's last tile
-      d = make_int4(s.b, hg, 2 * cta + (seg > 0 ? 1 : 0), last - cta / p.members + 1);
+      d = make_int4(s.b, hg, 2 * cta + (seg > 0 ? 1 : 0), last - p.by_members.of(cta) + 1);
     }
     if (p.desc_units) p.desc[s.b * p.Hkv * p.groups + hg] = d;
   }
@@ -925,7 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- this CTA's run of work: it starts in stream `start_b`, before which
   // lie `start_pre` tiles (or units).
   const int units = p.head_sets * p.group_sets;
-  const int all = static_cast<int>(gridDim.x) / p.members, team = static_cast<int>(blockIdx.x) / p.members;
+  const int all = p.by_members.of(gridDim.x), team = p.by_members.of(blockIdx.x);
+  const int member = static_cast<int>(blockIdx.x) - team * p.members;
   int len, total, start_b = 0, start_pre = 0;
   if (p.B <= 32) {
     // Every warp by itself, a stream a lane.
@@ -941,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane >= d) inc += o;
     }
     total = __shfl_sync(0xFFFFFFFFu, inc, 31);
-    const Runs runs(total, p.min_tiles, all);
+    const Runs runs(p, total, all);
     if (team < runs.teams && total > 0) {
       start_b = __ffs(__ballot_sync(0xFFFFFFFFu, inc > runs.start(team))) - 1;
       start_pre = __shfl_sync(0xFFFFFFFFu, inc - work, start_b);
@@ -976,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i == warp) before = total;
       total += sm.warp_sum[i];
     }
-    const Runs runs(total, p.min_tiles, all);
+    const Runs runs(p, total, all);
     const int t0 = team < runs.teams ? runs.start(team) : total;
     before += inc - sum;
     if (t0 >= before && t0 < before + sum) {
@@ -997,9 +1002,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const uint32_t tmem = sm.tmem_base;
-  const Runs runs(total, p.min_tiles, all);
+  const Runs runs(p, total, all);
   const int t0 = team < runs.teams ? runs.start(team) : total;
-  const Walk walk(p, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
+  const Walk walk(p, member, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
 
   if (warp == 0 || warp == 2) {
     if (p.box_rows == 0) load_gather<D>(sm, p, walk, warp == 2);
@@ -1125,7 +1130,7 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
   }
   if (!valid) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int i = R / p.G;
+  const int i = p.by_G.of(R);
   const long long row = (static_cast<long long>(d.x) * p.q_len + i) * p.H + head * p.G + (R - i * p.G);
   reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (D * 2))[c4] =
       make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
