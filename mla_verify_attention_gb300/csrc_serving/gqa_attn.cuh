@@ -723,12 +723,11 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
         // Rows past the stream may hold anything: P is 0 there, but 0 * NaN is not.
         const int stage = (kt + j) % C::kStages;
         if (!wait(sm, sm.vfull[stage], ((kt + j) / C::kStages) & 1, p)) return;
-        const int z0 = s.S - k0, nz = kKeys - z0;
-        uint8_t* tile = sm.ring + stage * 2 * C::kTile + C::kTile;
-        for (int it = r; it < nz * (D / 8); it += kRows) {
-          const int rr = z0 + it / (D / 8), u = it % (D / 8);
-          *reinterpret_cast<uint4*>(tile + (u >> 3) * (kKeys * 128) + rr * 128 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        // Each thread one 16-byte column of every kRows / (D / 8)-th row.
+        const int u = r % (D / 8);
+        uint8_t* const column = sm.ring + stage * 2 * C::kTile + C::kTile + (u >> 3) * (kKeys * 128) + (u & 7) * 16;
+        for (int row = s.S - k0 + r / (D / 8); row < kKeys; row += kRows / (D / 8))
+          *reinterpret_cast<uint4*>(column + row * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
       __syncwarp();
