@@ -169,25 +169,32 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
     }
     __syncthreads();
 
-    // Four blocks a thread at a time: their reads are under way together.
-    for (int k0 = first; k0 < n_blocks; k0 += 4 * all_threads) {
-      int32_t* to[4];
+    // Four consecutive blocks a thread: one search (the searches' shared-memory
+    // reads are what a release of thousands of pages costs), and four reads
+    // under way together.
+    for (long long k4 = 4ll * first; k4 < n_blocks; k4 += 4ll * all_threads) {
+      const int k0 = static_cast<int>(k4), n = min(4, n_blocks - k0);
+      int b = find_stream(blk_pre, p.B, k0);
+      int end = blk_pre[b + 1];
+      int32_t* entry = p.table + static_cast<size_t>(b) * p.max_blocks + p.page.up(base_len[b]) + (k0 - blk_pre[b]);
+      int32_t* at[4];
       int page[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int k = k0 + e * all_threads;
-        to[e] = nullptr;
-        if (k < n_blocks) {
-          const int b = find_stream(blk_pre, p.B, k);
-          int32_t* const entry =
-              p.table + static_cast<size_t>(b) * p.max_blocks + p.page.up(base_len[b]) + (k - blk_pre[b]);
-          to[e] = kExtend ? entry : p.free_pages + fc + n_blocks - 1 - k;
-          page[e] = kExtend ? p.free_pages[fc - 1 - k] : *entry;
+        if (e >= n) break;
+        if (k0 + e >= end) {
+          do end = blk_pre[++b + 1]; while (k0 + e >= end);
+          entry = p.table + static_cast<size_t>(b) * p.max_blocks + p.page.up(base_len[b]);
         }
+        at[e] = entry++;
+        page[e] = kExtend ? p.free_pages[fc - 1 - (k0 + e)] : *at[e];
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (to[e] != nullptr) *to[e] = page[e];
+      for (int e = 0; e < 4; ++e) {
+        if (e >= n) break;
+        if (kExtend) *at[e] = page[e];
+        else p.free_pages[fc + n_blocks - 1 - (k0 + e)] = page[e];
+      }
     }
     if (kExtend) {
       // Four consecutive tokens a thread: one search, one 16-byte store.  The
