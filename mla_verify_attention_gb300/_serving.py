@@ -266,7 +266,8 @@ def _pools(k_pool, v_pool):
     if dt is not _bf16 and dt is not _fp16:
         raise ValueError("the pools must be bfloat16 or float16")
     rows, heads, width = k_pool.shape
-    return dt, rows, heads, width, _head_rows("k_pool", k_pool, dt, heads, width), _head_rows("v_pool", v_pool, dt, heads, width)
+    k_stride, v_stride = _head_rows("k_pool", k_pool, dt, heads, width), _head_rows("v_pool", v_pool, dt, heads, width)
+    return dt, rows, heads, width, k_stride, v_stride
 
 
 def cache_append(kv_pool, latent, rope, slots, stream=None):
@@ -327,7 +328,8 @@ def _keep_tables(block_table, seq_lens, path, keep):
             and keep.shape == (B,) and seq_lens.shape == (B,) and block_table.shape == (B, max_blocks)
             and path.is_contiguous() and keep.is_contiguous() and seq_lens.is_contiguous()
             and block_table.is_contiguous()):
-        _wrong_ints(path=(path, B, q_len), keep=(keep, B), seq_lens=(seq_lens, B), block_table=(block_table, B, max_blocks))
+        _wrong_ints(path=(path, B, q_len), keep=(keep, B), seq_lens=(seq_lens, B),
+                    block_table=(block_table, B, max_blocks))
     return B, q_len, max_blocks
 
 

@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
     }
   }
   const unsigned all_b = __shfl_sync(0xFFFFFFFFu, wb, 31), all_t = __shfl_sync(0xFFFFFFFFu, wt, 31);
-  const unsigned before_b = warp ? __shfl_sync(0xFFFFFFFFu, wb, warp - 1) : 0, before_t = warp ? __shfl_sync(0xFFFFFFFFu, wt, warp - 1) : 0;
+  const unsigned before_b = warp ? __shfl_sync(0xFFFFFFFFu, wb, warp - 1) : 0;
+  const unsigned before_t = warp ? __shfl_sync(0xFFFFFFFFu, wt, warp - 1) : 0;
 
   // Anything wrong: the batch stays as it was (the same verdict in every block).
   const bool no_pages = fc < 0 || fc > p.free_capacity ||
@@ -265,7 +266,9 @@ int launch_blocks(BlocksFn fn, const BlocksParams& p, unsigned blocks, unsigned 
 }
 
 // Threads of a block that has this many streams and items to see to.
-unsigned threads_for(long long n) { return n <= 128 ? 128 : (n >= kMaxThreads ? kMaxThreads : static_cast<unsigned>((n + 31) / 32 * 32)); }
+unsigned threads_for(long long n) {
+  return n <= 128 ? 128 : (n >= kMaxThreads ? kMaxThreads : static_cast<unsigned>((n + 31) / 32 * 32));
+}
 
 bool blocks_shape_ok(int B, int max_blocks, int page, int free_capacity) {
   return B >= 0 && B <= kMaxStreams && max_blocks >= 1 && page >= 1 && free_capacity >= 0 &&
@@ -446,9 +449,9 @@ int mla_blocks_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block
   const long long quads = (static_cast<long long>(max_tokens) + 3) / 4;
   if (max_tokens <= kOneBlockTokens)
     return launch_blocks(blocks_kernel<true, kAll>, p, 1, threads_for(quads > B ? quads : B), stream);
-  const long long blocks = (quads + kMaxThreads - 1) / kMaxThreads;
-  const int first = launch_blocks(blocks_kernel<true, kItems>, p,
-                                  static_cast<unsigned>(blocks < kMostBlocks ? blocks : kMostBlocks), kMaxThreads, stream);
+  const long long wanted = (quads + kMaxThreads - 1) / kMaxThreads;
+  const unsigned blocks = static_cast<unsigned>(wanted < kMostBlocks ? wanted : kMostBlocks);
+  const int first = launch_blocks(blocks_kernel<true, kItems>, p, blocks, kMaxThreads, stream);
   return first != MLA_OK ? first : launch_blocks(blocks_kernel<true, kCommit>, p, 1, threads_for(B), stream);
 }
 
@@ -529,7 +532,8 @@ int mla_cache_keep(void* pool_a, long long pool_a_stride, int a_bytes, void* poo
   p.pool_pages = static_cast<int>(pool_rows / page_size);
   p.B = B;
   p.q = q_len;
-  const unsigned cols = (static_cast<unsigned>(p.r.units[0]) + p.r.units[1] + 32 * kKeepColumns - 1) / (32 * kKeepColumns);
+  const unsigned units = static_cast<unsigned>(p.r.units[0]) + p.r.units[1];
+  const unsigned cols = (units + 32 * kKeepColumns - 1) / (32 * kKeepColumns);
   return launch_dependent(keep_kernel, p, dim3(cols, B < 65535 ? B : 65535), 32 * kKeepWarps, 0, stream);
 }
 

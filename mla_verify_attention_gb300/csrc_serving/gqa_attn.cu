@@ -81,7 +81,8 @@ bool g_ready[kMaxDevices][4];
 
 // The kernels for these sizes, ready on the current device.
 int pick(int D, int dtype, Variant* out) {
-  static const Variant all[4] = {variant<64, true>(), variant<64, false>(), variant<128, true>(), variant<128, false>()};
+  static const Variant all[4] = {variant<64, true>(), variant<64, false>(), variant<128, true>(),
+                                 variant<128, false>()};
   const int n = (D == 128 ? 2 : 0) + (dtype == MLA_FP16 ? 1 : 0);
   *out = all[n];
   int dev = -1;
@@ -143,8 +144,7 @@ int encode(const DeviceCommon& d, CUtensorMap* map, const void* base, const Call
   const CUresult r =
       d.encode(map, c.dtype == MLA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B,
-               promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+               CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_LAUNCH;
 }
 
@@ -206,11 +206,12 @@ int run(const Call& c) {
   p.by_group_members = Divisor(p.group_members);
   p.by_group_sets = Divisor(p.group_sets);
   p.by_G = Divisor(c.H / c.Hkv);
-  // Fetches of 256 bytes into L2 where the team wants all of them: two heads of
-  // 64 dims side by side (64 streams of 16k keys 347 -> 326 us; without teams
-  // such fetches cost 480 us against 397).
+  // Fetches of 256 bytes into L2 where the team wants all of them: also with 64
+  // dims a head, if two heads or two rows lie side by side (64 streams of 16k
+  // keys 347 -> 326 us; without teams such fetches cost 480 us against 397).
+  const bool fetch_256 = c.D == 128 || heads > 1 || p.k_stride[1] == 2 * c.D;
   const CUtensorMapL2promotion promotion =
-      c.D == 128 || heads > 1 || c.Hkv == 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+      fetch_256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   CUtensorMap map_k = {}, map_v = {};
   if (box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box, promotion) != MLA_OK ||
                    encode(d, &map_v, c.v, c, p.v_stride, rows, batches, box, promotion) != MLA_OK))

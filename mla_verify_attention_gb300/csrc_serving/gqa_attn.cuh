@@ -141,7 +141,7 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { retu
   " @" #pred " tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [" #bar "];\n"
 #define MLA_QK_BODY(chunks)                                                                                        \
   asm volatile("{\n .reg .pred e, z, c;\n .reg .b32 x, y;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n" \
-               " setp.ne.and.b32 c, %7, 0, e;\n setp.ne.b32 z, 0, 0;\n" chunks                                                \
+               " setp.ne.and.b32 c, %7, 0, e;\n setp.ne.b32 z, 0, 0;\n" chunks                                       \
                MLA_COMMIT(e, %4) MLA_COMMIT(e, %5) MLA_COMMIT(c, %6) "}" ::"r"(d),                                  \
                "r"(a), "r"(b), "r"(id), "r"(bar0), "r"(bar1), "r"(bar2), "r"(static_cast<uint32_t>(end)),           \
                "n"(kDescHi)                                                                                         \
@@ -175,8 +175,8 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uin
 }
 
 // One box of a cache by the elected lane of a converged warp.
-__device__ __forceinline__ void tma_box_elect(uint32_t dst, const CUtensorMap* map, int row, int chunk, int head, int batch,
-                                              uint32_t bar) {
+__device__ __forceinline__ void tma_box_elect(uint32_t dst, const CUtensorMap* map, int row, int chunk, int head,
+                                              int batch, uint32_t bar) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
       " @e cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -573,7 +573,8 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, const uint4* v, uint8_t
 // Starts the copies of a segment's Q rows into a swizzled tile, by all softmax
 // warps: each group half the rows of each warp's 32.
 template <int D>
-__device__ __forceinline__ void start_q(Smem<D>& sm, const Params& p, const Segment& s, int seg, int g, int wq, int lane) {
+__device__ __forceinline__ void start_q(Smem<D>& sm, const Params& p, const Segment& s, int seg, int g, int wq,
+                                        int lane) {
   using C = Shape<D>;
   constexpr int kUnits = D / 8;                            // 16-byte units a row
   constexpr int kPer = 32 / kUnits;                        // rows a warp copies at once
@@ -619,7 +620,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
   const float a = p.scale_log2;
   const bool pos = a > 0.f;
   const float a_eff = pos ? a : 1.f;
-  int kt = 0, seg = 0, n = 0;                              // n: tasks of this group so far
+  int kt = 0, seg = 0, n = 0;                              // n: tiles of this group so far
   Segment s, next;
   bool more = w.next(p, s);
   if (more) {
@@ -773,10 +774,9 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
       for (int e = 0; e < 4; ++e) {
         const int row = 8 * e + (lane >> 2);
         const long long orow = __shfl_sync(0xFFFFFFFFu, out_row, row);
+        const size_t part_row = static_cast<size_t>(slot) * p.part_rows + wq * 32 + row;
         uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) + (orow * D + c0) * 2
-                                   : reinterpret_cast<uint8_t*>(
-                                         p.part_o + (static_cast<size_t>(slot) * p.part_rows + wq * 32 + row) * (D / 4) +
-                                         c0 / 4);
+                                   : reinterpret_cast<uint8_t*>(p.part_o + part_row * (D / 4) + c0 / 4);
         dst[e] = wq * 32 + row < rows ? to + (lane & 3) * 16 : nullptr;
       }
 #pragma unroll 1
@@ -1066,7 +1066,8 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
   const int head = d.y / p.groups, R = (d.y - head * p.groups) * kRows + rr;
   const bool valid = rr < kRows && R < p.q_len * p.G;
   // Row rr of part k >= 1 lies in slot 2 * (CTA of part 0 + k * members).
-  const size_t row_k = static_cast<size_t>(2 * (d.z >> 1)) * p.part_rows + rr, row_0 = static_cast<size_t>(d.z) * p.part_rows + rr;
+  const size_t row_k = static_cast<size_t>(2 * (d.z >> 1)) * p.part_rows + rr;
+  const size_t row_0 = static_cast<size_t>(d.z) * p.part_rows + rr;
   const size_t step = static_cast<size_t>(2 * p.members) * p.part_rows;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -CUDART_INF_F, l = 0.f;

@@ -261,6 +261,22 @@ def test_pages_far_into_a_large_pool(page):
     verify(c, *run_paged(c, page, big, table))
 
 
+def test_streams_far_into_a_large_cache():
+    # The last stream's rows begin beyond 2^32 bytes of a contiguous cache.
+    smax = 1_100_000
+    c = case(3, 9, 16, 8, 128, [300, 9, 700], BF16)
+    big = []
+    for x in (c["k"], c["v"]):
+        y = torch.empty((3, smax, 8, 128), dtype=BF16, device="cuda")
+        y[:, :x.shape[1]] = x
+        big.append(y)
+    assert 2 * smax * 8 * 128 * 2 > 2 ** 32
+    out, lse = mva.gqa_verify_attn(c["q"], big[0], big[1], c["lens_t"], c["mask"], c["scale"])
+    torch.cuda.synchronize()
+    assert mva.last_device_error() == 0
+    verify(c, out, lse)
+
+
 @pytest.mark.parametrize("page", [64, 16, 5])
 def test_bad_page_is_reported(page):
     c = case(2, 9, 8, 1, 64, [300, 300], BF16)
