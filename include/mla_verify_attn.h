@@ -399,8 +399,11 @@ enum mla_dtype { MLA_BF16 = 0, MLA_FP16 = 1 };
  *              dimensions of size 1 are not used.
  *   seq_lens   as for mla_verify_attn, and 0 for an unused stream (out 0, lse -inf).  A
  *              stream with any other value outside [q_len, Smax] records MLA_ERR_SEQLEN and
- *              gets the same result.  Rows t < seq_lens[b] of k and v must be finite; the
- *              others may hold anything.
+ *              gets the same result.  Rows of k and v past seq_lens[b], and those of drafts
+ *              that no draft of the stream sees (a batch padded to one q_len), may hold anything
+ *              (NaN included).  A row of v that some draft sees must be finite, or the
+ *              stream's other drafts get its NaN, too; NaN in a row of q, or in a key that a
+ *              draft sees, gives that draft's rows NaN.
  *   tree_mask, scale, q_len, Smax and the errors as for mla_verify_attn; B < 2^20, and
  *              B * ceil(Smax / 64) * Hkv * ceil(q_len * H / Hkv / 128) < 2^31.
  *   workspace  at least mla_gqa_workspace_size(B, q_len, H, Hkv, D) bytes, 256-byte aligned;

@@ -22,11 +22,12 @@
 //
 // Split.  The work is a sequence of 64-key tiles: streams, then key heads,
 // then keys.  Every CTA (or team of CTAs, one a group of 128 rows) of one
-// persistent wave takes an equal run of that sequence, computed on the device from seq_lens, so that ragged
-// batches balance to one tile and nothing is planned on the host.  A (stream,
-// head, row group) unit that lies within one run is written to `out`; one that
-// is cut leaves unnormalised partials (at most two a CTA, which bounds the
-// workspace by the grid) that the combine kernels merge in order.
+// persistent wave takes an equal run of that sequence, computed on the device
+// from seq_lens, so that ragged batches balance to one tile and nothing is
+// planned on the host.  A (stream, head, row group) unit that lies within one run
+// is written to `out`; one that is cut leaves unnormalised partials (at most two a
+// CTA, which bounds the workspace by the grid) that the combine kernels merge in
+// order.
 //
 // CTA.  One warp loads K and V tiles (TMA boxes in the 128-byte swizzle), two
 // issue tcgen05.mma, eight softmax warps in two groups take the key tiles in
@@ -321,6 +322,28 @@ struct Walk {
 
 __device__ __forceinline__ int rows_of_group(const Params& p, int group) {
   return min(kRows, p.q_len * p.G - group * kRows);
+}
+
+// Keys k0 .. k0 + 63 that a row with draft mask `mask64` sees: those before the
+// drafts, np of which lie in the tile (np < 64, may be negative), then its drafts.
+__device__ __forceinline__ uint64_t visible(uint64_t mask64, int np) {
+  if (np > 0) return ((1ull << np) - 1ull) | mask64 << np;
+  return -np < 64 ? mask64 >> (-np) : 0ull;
+}
+
+// The drafts of stream b that any of its drafts sees, by a whole converged warp;
+// `word`: the lane's draft's mask, where one word holds it.
+__device__ __forceinline__ uint64_t seen_drafts(const Params& p, int b, uint32_t word, int lane) {
+  if (p.q_len <= 32) return __reduce_or_sync(0xFFFFFFFFu, word) & (~0u >> (32 - p.q_len));
+  const uint32_t* rows = p.mask + static_cast<size_t>(b) * p.q_len * 2;
+  uint32_t lo = 0, hi = 0;
+  for (int i = lane; i < p.q_len; i += 32) {
+    lo |= rows[2 * i];
+    hi |= rows[2 * i + 1];
+  }
+  lo = __reduce_or_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_or_sync(0xFFFFFFFFu, hi) & (~0u >> (64 - p.q_len));
+  return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
 // ------------------------------------------------------------ loads
@@ -641,6 +664,8 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
     const int i = p.by_G.of(R);
     const int head = s.head * p.G + (R - i * p.G);
     uint64_t mask64 = 0;
+    uint32_t word = 0;
+    if (p.q_len <= 32 && lane < p.q_len) word = p.mask[static_cast<size_t>(s.b) * p.q_len + lane];
     if (valid) {
       const int words = (p.q_len + 31) >> 5;
       const uint32_t* mrow = p.mask + (static_cast<size_t>(s.b) * p.q_len + i) * words;
@@ -653,8 +678,8 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
     for (int j = g; j < s.n; j += 2, ++n) {
       const int buf = n & 1;
       const uint32_t s_t = tmem + lanes + 256 + (2 * g + buf) * kKeys;
-      if (!wait(sm, sm.sfull[g][buf], (n >> 1) & 1, p)) return;
       const int k0 = (s.tile0 + j) * kKeys;
+      if (!wait(sm, sm.sfull[g][buf], (n >> 1) & 1, p)) return;
       if (warp_valid) {
         tc_fence_after();
         uint32_t sr[64];
@@ -666,9 +691,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
           for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a);
         }
         if (k0 + kKeys > prefix) {
-          const int np = prefix - k0;                      // prefix keys of this tile (may be <= 0)
-          uint64_t vis = np > 0 ? (1ull << np) - 1ull : 0ull;      // (np < 64 here)
-          vis |= np > 0 ? mask64 << np : (-np < 64 ? mask64 >> (-np) : 0ull);
+          const uint64_t vis = visible(mask64, prefix - k0);
           const uint32_t lo = static_cast<uint32_t>(vis), hi = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -720,16 +743,24 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
         tmem_st_wait();
         tc_fence_before();
       }
-      if (k0 + kKeys > s.S) {
-        // Rows past the stream may hold anything: P is 0 there, but 0 * NaN is not.
-        const int stage = (kt + j) % C::kStages;
-        if (!wait(sm, sm.vfull[stage], ((kt + j) / C::kStages) & 1, p)) return;
-        // Each thread one 16-byte column of every kRows / (D / 8)-th row.
-        const int u = r % (D / 8);
-        uint8_t* const column = sm.ring + stage * 2 * C::kTile + C::kTile + (u >> 3) * (kKeys * 128) + (u & 7) * 16;
-        for (int row = s.S - k0 + r / (D / 8); row < kKeys; row += kRows / (D / 8))
-          *reinterpret_cast<uint4*>(column + row * 128) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+      if (k0 + kKeys > prefix) {
+        // Rows past the stream, and drafts that none sees (a batch padded to one
+        // q_len), may hold anything: P is 0 there, but 0 * NaN is not.
+        const uint64_t used = visible(seen_drafts(p, s.b, word, lane), prefix - k0);
+        const uint32_t lo = static_cast<uint32_t>(used), hi = static_cast<uint32_t>(used >> 32);
+        if ((lo & hi) != ~0u) {
+          const int stage = (kt + j) % C::kStages;
+          if (!wait(sm, sm.vfull[stage], ((kt + j) / C::kStages) & 1, p)) return;
+          // Each thread one 16-byte column of every kRows / (D / 8)-th row.
+          constexpr int kStep = kRows / (D / 8);
+          const int u = r % (D / 8), row0 = r / (D / 8);
+          uint8_t* const at = sm.ring + stage * 2 * C::kTile + C::kTile + (u >> 3) * (kKeys * 128) + (u & 7) * 16 + row0 * 128;
+#pragma unroll
+          for (int row = 0; row < kKeys; row += kStep)
+            if (!(((row < 32 ? lo : hi) >> ((row & 31) + row0)) & 1u))
+              *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[g][buf]));
@@ -761,7 +792,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
     if (warp_valid) {
       tc_fence_after();
       if (direct) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;        // (a NaN stays one)
         w0 *= inv;
         w1 *= inv;
       }
@@ -821,7 +852,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
       }
       if (valid && g == 0) {
         if (direct)
-          p.lse[out_row] = l > 0.f ? (m_off + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+          p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (m_off + log2f(l)) * 0.6931471805599453f;
         else
           p.part_ml[static_cast<size_t>(slot) * p.part_rows + r] = make_float2(m_off, l);
       }
@@ -1129,12 +1160,12 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
     }
   }
   if (!valid) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;              // (a NaN stays one)
   const int i = p.by_G.of(R);
   const long long row = (static_cast<long long>(d.x) * p.q_len + i) * p.H + head * p.G + (R - i * p.G);
   reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (D * 2))[c4] =
       make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
-  if (c4 == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+  if (c4 == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D, bool kBf16>

@@ -119,6 +119,56 @@ def test_masks(q, G, n, tree):
     verify(c, *run(c))
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("q,used,n,page", [
+    (9, 5, 300, 0),            # the padding drafts end inside a tile
+    (9, 0, 9, 0),              # nothing but padding
+    (64, 33, 160, 0),          # drafts over two tiles, two mask words
+    (40, 12, 104, 16),         # pages that end inside a tile
+    (40, 20, 1000, 5),         # gathered rows, in several parts
+    (33, 32, 128, 0),          # one padding draft, the last key of a whole tile
+])
+def test_drafts_that_none_sees_hold_anything(q, used, n, page, what):
+    # A batch padded to one q_len: the drafts behind `used` see the prefix alone, and none sees them.
+    for D, dt in ((64, BF16), (128, FP16)):
+        c = case(2, q, 16, 2, D, [n, n + 64], dt)
+        c["seen"][0, used:] = False
+        c["seen"][0, :, used:] = False
+        c["mask"] = plain.mask_words(c["seen"]).cuda()
+        junk = {}
+        for name in "kv":
+            junk[name] = c[name].clone()
+            junk[name][0, n - q + used:n] = what
+        if page:
+            rows = -(-(n + 64) // page) * page
+            pools = []
+            for name in "kv":
+                pool = torch.zeros((2, rows, 2, D), dtype=dt, device="cuda")
+                pool[:, :n + 64] = junk[name]
+                pools.append(pool.view(2 * rows, 2, D))
+            table = torch.arange(2 * rows // page, dtype=torch.int32, device="cuda").view(2, -1)
+            out, lse = mva.gqa_verify_attn_paged(c["q"], *pools, table, page, c["lens_t"], c["mask"], c["scale"])
+        else:
+            out, lse = mva.gqa_verify_attn(c["q"], junk["k"], junk["v"], c["lens_t"], c["mask"], c["scale"])
+        assert mva.last_device_error() == 0
+        verify(c, out, lse)
+
+
+@pytest.mark.parametrize("n,smax", [(100, 128), (400, 600), (5000, 5000)])    # whole units, and cut ones
+def test_nan_of_a_row_stays_in_it(n, smax):
+    c = case(1, 5, 8, 2, 128, [n], BF16, smax=smax)
+    c["q"][0, 2, 3, 7] = float("nan")
+    c["k"][0, n - 1] = float("nan")                # a key that the last draft alone sees
+    c["seen"][0, :4, 4] = False
+    c["seen"][0, 4, 4] = True
+    c["mask"] = plain.mask_words(c["seen"]).cuda()
+    out, lse = run(c)
+    bad = torch.zeros((5, 8), dtype=torch.bool, device="cuda")
+    bad[2, 3] = bad[4] = True
+    assert torch.equal(torch.isnan(lse[0]), bad)
+    assert torch.equal(torch.isnan(out[0]).all(-1), bad) and torch.equal(torch.isnan(out[0]).any(-1), bad)
+
+
 def test_rows_that_see_nothing():
     c = case(1, 9, 8, 1, 64, [9], FP16)
     c["seen"][0, 3] = False
