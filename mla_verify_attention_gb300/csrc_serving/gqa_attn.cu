@@ -66,14 +66,15 @@ using CombineFn = void (*)(Params, int);
 
 struct Variant {
   AttnFn attn;
-  CombineFn combine[2];   // many units; many parts
+  CombineFn combine_parts, combine_few_chunks, combine_many_chunks;
   size_t smem;
 };
 template <int D, bool kBf16>
 Variant variant() {
   constexpr size_t smem = sizeof(Smem<D>);
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16>, {combine_many_units<D, kBf16>, combine_many_parts<D, kBf16>}, smem};
+  return {attn_kernel<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8>,
+          combine_many_units<D, kBf16, 3>, smem};
 }
 
 std::mutex g_ready_mutex;
@@ -270,15 +271,17 @@ int run(const Call& c) {
   const int pairs = ((rows_a_head < pl.part_rows ? rows_a_head : pl.part_rows) + 1) / 2;
   const bool many = p.desc_units && static_cast<long long>(entries) * pairs <= 3 * grid &&
                     (grid / p.members) / (static_cast<long long>(c.B) * p.head_sets * p.group_sets) >= kManyParts;
+  CombineFn combine = var.combine_parts;
   if (many) {
     cfg.gridDim = dim3(pairs, entries, 1);
   } else {
     const long long chunks = static_cast<long long>(entries) * (pl.part_rows / kMergeUnits);
-    cfg.gridDim = dim3(static_cast<unsigned>(chunks < 5 * grid ? chunks : 5 * grid), 1, 1);
+    combine = chunks <= 5 * grid ? var.combine_few_chunks : var.combine_many_chunks;
+    cfg.gridDim = dim3(static_cast<unsigned>(chunks < 8 * grid ? chunks : 8 * grid), 1, 1);
   }
   cfg.blockDim = dim3(c.D / 4 * kMergeUnits, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, var.combine[many ? 1 : 0], p, entries) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, combine, p, entries) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }

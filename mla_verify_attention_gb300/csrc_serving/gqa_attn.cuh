@@ -1081,14 +1081,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 //     chunk x of the unit of entry y;
 //   many units, few parts: eight rows and one part group; every block first lists
 //     the cut units (all entries read at once) and takes chunks of them in turn
-//     (a block a chunk and entry were 9,728 that mostly found nothing to do).
+//     (a block a chunk and entry were 9,728 that mostly found nothing to do).  A
+//     thread loads eight parts at once where there are no more chunks than blocks
+//     at a time (264 rows over 16k keys 32.6 -> 31.9 us against four), three where
+//     more blocks an SM count (1,024 rows in two parts each: three 50.3, four 51.0,
+//     eight 53.6 us).
 constexpr int kMaxParts = 320;               // CTAs of the split kernel at most
 constexpr int kMergeUnits = 8;               // rows x part groups of a block
 constexpr int kMergeParts = 4;               // part groups when there are many parts
-template <int D, bool kBf16, int kP>
+template <int D, bool kBf16, int kP, int kAtOnce>            // kAtOnce: parts a thread loads at once
 __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int chunk) {
   constexpr int kR = kMergeUnits / kP;
-  constexpr int kAtOnce = kP > 1 ? 8 : 4;                  // parts a thread loads at once
   constexpr int kGroup = D / 4 * kR;                       // threads a part group
   __shared__ float4 sums[kP > 1 ? kP - 1 : 1][kGroup];
   __shared__ float2 stats[kP > 1 ? kP - 1 : 1][kR];
@@ -1172,10 +1175,10 @@ template <int D, bool kBf16>
 __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_parts(const Params p, int) {
   grid_dependency_wait();
   const int4 d = __ldcg(p.desc + blockIdx.y);
-  if (d.w != 0) merge_rows<D, kBf16, kMergeParts>(p, d, blockIdx.x);
+  if (d.w != 0) merge_rows<D, kBf16, kMergeParts, 8>(p, d, blockIdx.x);
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, int kAtOnce>
 __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_units(const Params p, int entries) {
   constexpr int kThreadsM = D / 4 * kMergeUnits, kWarps = kThreadsM / 32;
   __shared__ int4 cut[kMaxParts];
@@ -1200,7 +1203,7 @@ __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_units(const 
   const int chunks = p.part_rows / kMergeUnits;
   for (int item = blockIdx.x; item < n_cut * chunks; item += gridDim.x) {
     const int u = item / chunks;
-    merge_rows<D, kBf16, 1>(p, cut[u], item - u * chunks);
+    merge_rows<D, kBf16, 1, kAtOnce>(p, cut[u], item - u * chunks);
   }
 }
 
