@@ -335,21 +335,25 @@ struct KeepParams {
   const int32_t* path;
   const int32_t* keep;
   int max_blocks, pool_pages, B, q;
+  int columns;                  // a block
   Divisor page;
 };
 
-// One block a stream and kKeepColumns 512-byte columns of the pool rows: eight
-// warps read the path's rows (eight rows a warp at most) into registers, and
-// after a barrier write them to their new places, so that any path is safe in
-// place.  Before that the block works out the rows (a thread a row; count,
-// length and path are read together, then the pages): two dependent reads that
-// the columns share.  256 streams, 17 of 33 rows of 4 KB on average: 8.8 us, of
-// which the bytes need 5.1; 8 streams x 9 latent rows 2.4 us.
+// One block a stream and one or two 512-byte columns of the pool rows: eight
+// warps read the path's rows (kRows a warp at most) into registers, and after a
+// barrier write them to their new places, so that any path is safe in place.
+// Before that the block works out the rows (a thread a row; count, length and
+// path are read together, then the pages): two dependent reads that the columns
+// share.  One column while those blocks all fit the device (8 streams x 9
+// latent rows 2.1 us, 2.5 with two); two beyond that (256 streams, 17 of 33 rows
+// of 4 KB on average: 6.4 us, of which the bytes need 5.1; one 6.7, four 7.3 us).
+// Fewer rows a warp leave registers for more blocks: six an SM with five rows
+// (6.8 us with eight rows and four blocks, 8.1 with three).
 constexpr int kKeepWarps = 8;
-constexpr int kKeepRows = 64 / kKeepWarps;
-constexpr int kKeepColumns = 2;
+constexpr int kKeepBlocks = 6;                     // an SM, about
 
-__global__ void __launch_bounds__(32 * kKeepWarps) keep_kernel(const KeepParams p) {
+template <int kRows>
+__global__ void __launch_bounds__(32 * kKeepWarps, kRows <= 5 ? kKeepBlocks : 4) keep_kernel(const KeepParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ int rows[2][64];                      // pool rows the j-th kept draft moves from / to
   grid_dependency_wait();
@@ -377,21 +381,22 @@ __global__ void __launch_bounds__(32 * kKeepWarps) keep_kernel(const KeepParams 
     if (wrong) atomicOr(p.r.status, wrong);
     if (__syncthreads_or(static_cast<int>(wrong))) continue;   // this stream stays as it was
 #pragma unroll 1
-    for (int col = 0; col < kKeepColumns; ++col) {
-      const int c = (static_cast<int>(blockIdx.x) * kKeepColumns + col) * 32 + lane;
-      const int which = c < p.r.units[0] ? 0 : 1;
-      uint8_t* const pool = p.r.pool[which] + 16ll * (which ? c - p.r.units[0] : c);
-      const long long stride = p.r.pool_stride[which];
-      uint4 v[kKeepRows];
+    for (int col = 0; col < p.columns; ++col) {
+      const int c = (static_cast<int>(blockIdx.x) * p.columns + col) * 32 + lane;
+      // (Selected, not indexed: an index would put the parameters on the stack.)
+      const bool second = c >= p.r.units[0];
+      uint8_t* const pool = second ? p.r.pool[1] + 16ll * (c - p.r.units[0]) : p.r.pool[0] + 16ll * c;
+      const long long stride = second ? p.r.pool_stride[1] : p.r.pool_stride[0];
+      uint4 v[kRows];
 #pragma unroll
-      for (int e = 0; e < kKeepRows; ++e) {
+      for (int e = 0; e < kRows; ++e) {
         const int j = warp + kKeepWarps * e;
         if (j < n && c < units && rows[0][j] != rows[1][j])
           v[e] = *reinterpret_cast<const uint4*>(pool + rows[0][j] * stride);
       }
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < kKeepRows; ++e) {
+      for (int e = 0; e < kRows; ++e) {
         const int j = warp + kKeepWarps * e;
         if (j < n && c < units && rows[0][j] != rows[1][j])
           *reinterpret_cast<uint4*>(pool + rows[1][j] * stride) = v[e];
@@ -532,9 +537,13 @@ int mla_cache_keep(void* pool_a, long long pool_a_stride, int a_bytes, void* poo
   p.pool_pages = static_cast<int>(pool_rows / page_size);
   p.B = B;
   p.q = q_len;
-  const unsigned units = static_cast<unsigned>(p.r.units[0]) + p.r.units[1];
-  const unsigned cols = (units + 32 * kKeepColumns - 1) / (32 * kKeepColumns);
-  return launch_dependent(keep_kernel, p, dim3(cols, B < 65535 ? B : 65535), 32 * kKeepWarps, 0, stream);
+  const unsigned cols = (static_cast<unsigned>(p.r.units[0]) + p.r.units[1] + 31) / 32;
+  p.columns = static_cast<long long>(cols) * B <= kKeepBlocks * d.sms ? 1 : 2;
+  const dim3 grid((cols + p.columns - 1) / p.columns, B < 65535 ? B : 65535);
+  void (*const fn)(KeepParams) = q_len <= 2 * kKeepWarps   ? keep_kernel<2>
+                                 : q_len <= 5 * kKeepWarps ? keep_kernel<5>
+                                                           : keep_kernel<8>;
+  return launch_dependent(fn, p, grid, 32 * kKeepWarps, 0, stream);
 }
 
 }  // extern "C"

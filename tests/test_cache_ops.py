@@ -282,6 +282,38 @@ def test_keep(B, q, latent, page):
         assert torch.equal(x.cpu().view(torch.int16), w.view(torch.int16))
 
 
+@pytest.mark.parametrize("B,q,heads,D", [
+    (400, 9, 0, 0),            # latent rows, three columns
+    (130, 16, 8, 128),
+    (130, 17, 8, 128),
+    (130, 40, 8, 128),
+    (130, 41, 8, 128),
+    (200, 64, 5, 72),          # rows of 45 units
+])
+def test_keep_of_many_streams(B, q, heads, D):
+    # More blocks than fit the device at once, every number of rows a warp.
+    page = 16
+    gen = torch.Generator().manual_seed(q)
+    lens = torch.randint(q, q + 40, (B,), generator=gen)
+    blocks = (q + 40) // page + 1
+    table = torch.randperm(B * blocks, generator=gen).view(B, blocks)
+    path, keep = torch.randint(0, q, (B, q), generator=gen), torch.randint(0, q + 1, (B,), generator=gen)
+    rows = B * blocks * page
+    row = lambda i: table.gather(1, (lens[:, None] - q + i) // page) * page + (lens[:, None] - q + i) % page
+    kept = torch.arange(q)[None, :] < keep[:, None]
+    src, dst = row(path)[kept], row(torch.arange(q).expand(B, q))[kept]
+    shape = (rows, 576) if heads == 0 else (rows, heads, D)
+    pools = [torch.randn(shape, generator=gen).to(BF16) for _ in range(1 if heads == 0 else 2)]
+    want = [x.index_copy(0, dst, x[src]) for x in pools]
+    got = [x.cuda() for x in pools]
+    call = mva.cache_keep if heads == 0 else mva.gqa_cache_keep
+    ints32 = lambda x: x.to(torch.int32).cuda()
+    call(*got, ints32(table), page, ints32(lens), ints32(path), ints32(keep))
+    ok()
+    for x, w in zip(got, want):
+        assert torch.equal(x.cpu().view(torch.int16), w.view(torch.int16))
+
+
 def test_keep_leaves_a_wrong_stream_as_it_was():
     page, q = 4, 3
     for what, status in (("path", -12), ("count", -12), ("length", -8), ("page", -10)):
