@@ -15,17 +15,22 @@ namespace mla {
 // A programmatic dependent of the grid before it (every kernel here waits for
 // that grid before it reads anything): its launch overlaps that grid's end.
 template <class P>
-int launch_dependent(void (*fn)(P), const P& p, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream) {
+int launch_dependent(void (*fn)(P), const P& p, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                     unsigned cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
@@ -43,15 +48,28 @@ int launch_dependent(void (*fn)(P), const P& p, dim3 grid, unsigned threads, siz
 // A call for a verify step is a chain of a few dependent reads, so it is one
 // block of as many threads as there are streams or token quads, launched as a
 // dependent of the grid before it: 3 us for 8 streams x 9 tokens (5.3 us with
-// 1,024 threads and a plain launch).  Many tokens (an extend of prompts) are
-// shared by as many blocks as they fill, each with a scan of its own, and a
-// second grid then writes the lengths and the free count, which every block of
-// the first has to have read: extend and trim of 512 prompts, 217k tokens,
-// 19 us (one cluster of eight blocks 27 us).
+// 1,024 threads and a plain launch).  More work is shared by a cluster of eight
+// blocks, each with a scan of its own; the first writes the lengths and the free
+// count once all have read them (the cluster's barrier).  Extends beyond that (of
+// prompts) are shared by as many blocks as they fill, and a second grid takes the
+// place of the barrier.  Extend and trim, us, with one block / a cluster / two
+// grids for the extend and a cluster for the trim:
+//   64 streams x 9 tokens, page 16     7.0    7.2    8.1
+//   64 x 64                            7.0    6.5    7.2
+//   8 x 4,096, page 64                13.7    6.9    6.9
+//   64 x 1,024, page 16               26.4    9.4    7.7
+//   512 x 64                          18.6    9.2    9.5
+//   512 x 424                         91.7   22.2    9.3
+// How many blocks a trim releases is not known on the host: one block of threads
+// does it where the table itself is small (an empty trim 1.7 us, 2.0 with a
+// cluster).
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxStreams = 16384;     // three int32 a stream in shared memory
-constexpr int kOneBlockTokens = 8192;  // up to here one block does it all
-constexpr int kMostBlocks = 128;
+constexpr int kOneBlockTokens = 2048;
+constexpr int kClusterTokens = 32768;
+constexpr int kOneBlockStreams = 16, kOneBlockEntries = 16384;
+constexpr unsigned kClusterBlocks = 8;
+constexpr int kMostBlocks = 152;
 constexpr unsigned kFull = 1u << 31;   // sums stay there: more than any limit they are held to
 
 struct BlocksParams {
@@ -78,7 +96,10 @@ __device__ __forceinline__ int find_stream(const int* pre, int n, int x) {
   return lo;
 }
 
-enum { kAll = 0, kItems = 1, kCommit = 2 };   // what a grid does: everything, or one of the two parts
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+
+// What a grid does: everything, in one block or in one cluster; or one of the two parts.
+enum { kAll = 0, kCluster = 1, kItems = 2, kCommit = 3 };
 
 template <bool kExtend, int kPart>
 __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksParams p) {
@@ -169,6 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
       if (kExtend) tok_pre[p.B] = n_tokens;
     }
     __syncthreads();
+    if (kPart == kCluster) cluster_arrive();         // this block has read the lengths and the free count
 
     // Four consecutive blocks a thread: one search (the searches' shared-memory
     // reads are what a release of thousands of pages costs), and four reads
@@ -238,6 +260,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
     }
   }
 
+  if (kPart == kCluster) {
+    __syncwarp();
+    cluster_wait();
+    if (blockIdx.x != 0) return;
+  }
   if (kPart != kItems) {
     // Every thread reads and writes its own streams; the lengths that the
     // searches above used are in shared memory.
@@ -255,20 +282,24 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
 
 using BlocksFn = void (*)(BlocksParams);
 
-int launch_blocks(BlocksFn fn, const BlocksParams& p, unsigned blocks, unsigned threads, cudaStream_t stream) {
+int launch_blocks(BlocksFn fn, const BlocksParams& p, unsigned blocks, unsigned threads, cudaStream_t stream,
+                  unsigned cluster = 1) {
   const size_t smem = (3 * static_cast<size_t>(p.B) + 2) * sizeof(int);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((3 * kMaxStreams + 2) * sizeof(int))) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }
-  return launch_dependent(fn, p, dim3(blocks), threads, smem, stream);
+  return launch_dependent(fn, p, dim3(blocks), threads, smem, stream, cluster);
 }
 
 // Threads of a block that has this many streams and items to see to.
 unsigned threads_for(long long n) {
   return n <= 128 ? 128 : (n >= kMaxThreads ? kMaxThreads : static_cast<unsigned>((n + 31) / 32 * 32));
 }
+
+// The same of blocks that share the work: 1,024 threads only to scan many streams.
+int shared_threads(int B) { return B > kMaxThreads / 2 ? kMaxThreads : kMaxThreads / 2; }
 
 bool blocks_shape_ok(int B, int max_blocks, int page, int free_capacity) {
   return B >= 0 && B <= kMaxStreams && max_blocks >= 1 && page >= 1 && free_capacity >= 0 &&
@@ -452,11 +483,14 @@ int mla_blocks_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block
   BlocksParams p = {seq_lens, new_lens, block_table, const_cast<int32_t*>(free_pages), free_count, slots,
                     d.status_word, B, max_blocks, free_capacity, pool_pages, max_tokens, Divisor(page_size)};
   const long long quads = (static_cast<long long>(max_tokens) + 3) / 4;
-  if (max_tokens <= kOneBlockTokens)
+  if (max_tokens <= kOneBlockTokens && B <= kMaxThreads)
     return launch_blocks(blocks_kernel<true, kAll>, p, 1, threads_for(quads > B ? quads : B), stream);
-  const long long wanted = (quads + kMaxThreads - 1) / kMaxThreads;
+  const int threads = shared_threads(B);
+  if (max_tokens <= kClusterTokens)
+    return launch_blocks(blocks_kernel<true, kCluster>, p, kClusterBlocks, threads, stream, kClusterBlocks);
+  const long long wanted = (quads + threads - 1) / threads;
   const unsigned blocks = static_cast<unsigned>(wanted < kMostBlocks ? wanted : kMostBlocks);
-  const int first = launch_blocks(blocks_kernel<true, kItems>, p, blocks, kMaxThreads, stream);
+  const int first = launch_blocks(blocks_kernel<true, kItems>, p, blocks, threads, stream);
   return first != MLA_OK ? first : launch_blocks(blocks_kernel<true, kCommit>, p, 1, threads_for(B), stream);
 }
 
@@ -476,7 +510,9 @@ int mla_blocks_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* 
   if (st != MLA_OK) return st;
   BlocksParams p = {seq_lens, keep_lens, const_cast<int32_t*>(block_table), free_pages, free_count, nullptr,
                     d.status_word, B, max_blocks, free_capacity, 0, 0, Divisor(page_size)};
-  return launch_blocks(blocks_kernel<false, kAll>, p, 1, threads_for(B > 16 ? kMaxThreads : B), stream);
+  if (B <= kOneBlockStreams && static_cast<long long>(B) * max_blocks <= kOneBlockEntries)
+    return launch_blocks(blocks_kernel<false, kAll>, p, 1, threads_for(B), stream);
+  return launch_blocks(blocks_kernel<false, kCluster>, p, kClusterBlocks, shared_threads(B), stream, kClusterBlocks);
 }
 
 int mla_cache_append(const void* a, long long a_stride, int a_bytes, void* pool_a, long long pool_a_stride,

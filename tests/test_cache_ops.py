@@ -174,6 +174,48 @@ def test_trim_refuses_growth_and_a_full_list():
         assert torch.equal(t[k], old[k]), k
 
 
+@pytest.mark.parametrize("room", [1000, 5000, 40000])
+def test_many_streams_all_or_nothing(room):
+    # One block, a cluster, two grids: every block of a call comes to the same verdict.
+    B, page = 200, 4
+    p = Pool([b % 9 for b in range(B)], page, 24, 600)
+    t = p.gpu(room)
+    old = {k: x.clone() for k, x in t.items()}
+    few = [1] * B                                  # (24 * page more than the last stream's one token: no room)
+    for new, status in (([-1] + few[1:], -8), (few[:-1] + [24 * page], -8), ([20] * B, -11 if room > 20 * B else -8)):
+        t["slots"].fill_(7)
+        extend(p, new)
+        ok(status)
+        for k in ("lens", "table", "free", "count"):
+            assert torch.equal(t[k], old[k]), k
+        assert (t["slots"] == -1).all()
+    for keep in ([0] * (B - 1) + [p.lens[-1] + 1], [-1] + [0] * (B - 1)):
+        trim(p, keep)
+        ok(-8)
+        for k in ("lens", "table", "free", "count"):
+            assert torch.equal(t[k], old[k]), k
+
+
+@pytest.mark.parametrize("B,most", [(3000, 4), (700, 100)])
+def test_streams_of_a_thread_are_read_before_they_change(B, most):
+    # Several streams a thread, which every block of the call reads twice.
+    rng = random.Random(B)
+    p = Pool([rng.randint(0, 9) for _ in range(B)], 4, (9 + most) // 4 + 2, B * (most // 4 + 2))
+    t = p.gpu(B * most)
+    start = {k: t[k].clone() for k in ("lens", "free", "count")}
+    new = [rng.randint(0, most) for _ in range(B)]
+    new_t, keep_t = ints(new), start["lens"].clone()
+    slots = p.extend(new)
+    for _ in range(30):
+        mva.blocks_extend(t["lens"], new_t, t["table"], 4, t["free"], t["count"], p.pages, t["slots"])
+        got, lens = t["slots"].clone(), t["lens"].clone()
+        mva.blocks_trim(t["lens"], keep_t, t["table"], 4, t["free"], t["count"])
+        ok()
+        assert got.tolist() == slots + [-1] * (B * most - len(slots)) and lens.tolist() == p.lens
+        for k, x in start.items():
+            assert torch.equal(t[k], x), k
+
+
 def test_bad_page_in_the_table_gives_no_slot():
     p = Pool([5, 5], 16, 4, 4)
     t = p.gpu(6)
