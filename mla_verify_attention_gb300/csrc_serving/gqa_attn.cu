@@ -73,8 +73,8 @@ template <int D, bool kBf16>
 Variant variant() {
   constexpr size_t smem = sizeof(Smem<D>);
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8>,
-          combine_many_units<D, kBf16, 3>, smem};
+  return {attn_kernel<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
+          combine_many_units<D, kBf16, 3, 2>, smem};
 }
 
 std::mutex g_ready_mutex;
@@ -275,8 +275,12 @@ int run(const Call& c) {
   if (many) {
     cfg.gridDim = dim3(pairs, entries, 1);
   } else {
-    const long long chunks = static_cast<long long>(entries) * (pl.part_rows / kMergeUnits);
-    combine = chunks <= 5 * grid ? var.combine_few_chunks : var.combine_many_chunks;
+    long long chunks = static_cast<long long>(entries) * (pl.part_rows / kMergeUnits);
+    combine = var.combine_few_chunks;
+    if (chunks > 5 * grid) {
+      combine = var.combine_many_chunks;
+      chunks /= 2;                                         // (twice the rows)
+    }
     cfg.gridDim = dim3(static_cast<unsigned>(chunks < 8 * grid ? chunks : 8 * grid), 1, 1);
   }
   cfg.blockDim = dim3(c.D / 4 * kMergeUnits, 1, 1);

@@ -1079,23 +1079,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 // is as little else in it as there can be.  Two shapes:
 //   few units, many parts: two rows and four part groups; block (x, y) takes
 //     chunk x of the unit of entry y;
-//   many units, few parts: eight rows and one part group; every block first lists
-//     the cut units (all entries read at once) and takes chunks of them in turn
-//     (a block a chunk and entry were 9,728 that mostly found nothing to do).  A
-//     thread loads eight parts at once where there are no more chunks than blocks
-//     at a time (264 rows over 16k keys 32.6 -> 31.9 us against four), three where
-//     more blocks an SM count (1,024 rows in two parts each: three 50.3, four 51.0,
-//     eight 53.6 us).
+//   many units, few parts: one part group; every block first lists the cut units
+//     (all entries read at once) and takes chunks of them in turn (a block a chunk
+//     and entry were 9,728 that mostly found nothing to do).  With no more chunks
+//     than blocks at a time a chunk is eight rows and a thread loads eight parts
+//     at once (264 rows over 16k keys 32.6 -> 31.9 us against four).  With more,
+//     what counts are blocks an SM and instructions a byte: three parts at once,
+//     and sixteen rows with eight columns a thread (1,024 rows in two parts each:
+//     48.7 us; four columns 50.3; and four parts at once 51.0, eight 53.6).
 constexpr int kMaxParts = 320;               // CTAs of the split kernel at most
-constexpr int kMergeUnits = 8;               // rows x part groups of a block
+constexpr int kMergeUnits = 8;               // rows x part groups of a block, four columns a thread
 constexpr int kMergeParts = 4;               // part groups when there are many parts
-template <int D, bool kBf16, int kP, int kAtOnce>            // kAtOnce: parts a thread loads at once
+// kAtOnce: parts a thread loads at once; kV: its columns, in fours, D / kV apart.
+template <int D, bool kBf16, int kP, int kAtOnce, int kV>
 __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int chunk) {
-  constexpr int kR = kMergeUnits / kP;
-  constexpr int kGroup = D / 4 * kR;                       // threads a part group
-  __shared__ float4 sums[kP > 1 ? kP - 1 : 1][kGroup];
+  constexpr int kLanes = D / 4 / kV;                       // threads a row
+  constexpr int kR = kMergeUnits * kV / kP;
+  constexpr int kGroup = kLanes * kR;                      // threads a part group
+  __shared__ float4 sums[kP > 1 ? kP - 1 : 1][kV][kGroup];
   __shared__ float2 stats[kP > 1 ? kP - 1 : 1][kR];
-  const int tid = threadIdx.x, c4 = tid % (D / 4), r = tid / (D / 4) % kR, group = tid / kGroup, t = tid % kGroup;
+  const int tid = threadIdx.x, c4 = tid % kLanes, r = tid / kLanes % kR, group = tid / kGroup, t = tid % kGroup;
   const int parts = d.w, rr = chunk * kR + r;
   const int head = d.y / p.groups, R = (d.y - head * p.groups) * kRows + rr;
   const bool valid = rr < kRows && R < p.q_len * p.G;
@@ -1103,42 +1106,50 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
   const size_t row_k = static_cast<size_t>(2 * (d.z >> 1)) * p.part_rows + rr;
   const size_t row_0 = static_cast<size_t>(d.z) * p.part_rows + rr;
   const size_t step = static_cast<size_t>(2 * p.members) * p.part_rows;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 o[kV] = {};
   float m = -CUDART_INF_F, l = 0.f;
+  auto scale = [&](float keep) {
+    l *= keep;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) o[v] = make_float4(o[v].x * keep, o[v].y * keep, o[v].z * keep, o[v].w * keep);
+  };
+  auto add = [&](float w, const float4& x, int v) {
+    o[v].x += w * x.x;
+    o[v].y += w * x.y;
+    o[v].z += w * x.z;
+    o[v].w += w * x.w;
+  };
   for (int k0 = group; valid && k0 < parts; k0 += kAtOnce * kP) {
-    float4 x[kAtOnce];
+    float4 x[kAtOnce][kV] = {};
     float2 y[kAtOnce];
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) {
       const int k = k0 + e * kP;
       y[e] = make_float2(-CUDART_INF_F, 0.f);
-      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k < parts) {
         const size_t row = k ? row_k + k * step : row_0;
         y[e] = __ldcg(p.part_ml + row);
-        x[e] = __ldcg(p.part_o + row * (D / 4) + c4);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) x[e][v] = __ldcg(p.part_o + row * (D / 4) + v * kLanes + c4);
       }
     }
     float top = m;
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) top = fmaxf(top, y[e].x);
-    const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    scale(m == -CUDART_INF_F ? 0.f : ex2(m - top));
     m = top;
-    l *= keep;
-    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) {
       const float w = y[e].x == -CUDART_INF_F ? 0.f : ex2(y[e].x - m);
       l += w * y[e].y;
-      o.x += w * x[e].x;
-      o.y += w * x[e].y;
-      o.z += w * x[e].z;
-      o.w += w * x[e].w;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) add(w, x[e][v], v);
     }
   }
   if (kP > 1) {
     if (group) {
-      sums[group - 1][t] = o;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) sums[group - 1][v][t] = o[v];
       if (c4 == 0) stats[group - 1][r] = make_float2(m, l);
     }
     __syncthreads();
@@ -1146,28 +1157,25 @@ __device__ __forceinline__ void merge_rows(const Params& p, const int4 d, int ch
     float top = m;
 #pragma unroll
     for (int g = 0; g < kP - 1; ++g) top = fmaxf(top, stats[g][r].x);
-    const float keep = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    scale(m == -CUDART_INF_F ? 0.f : ex2(m - top));
     m = top;
-    l *= keep;
-    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
     for (int g = 0; g < kP - 1; ++g) {
       const float2 y = stats[g][r];
-      const float4 x = sums[g][t];
       const float w = y.x == -CUDART_INF_F ? 0.f : ex2(y.x - m);
       l += w * y.y;
-      o.x += w * x.x;
-      o.y += w * x.y;
-      o.z += w * x.z;
-      o.w += w * x.w;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) add(w, sums[g][v][t], v);
     }
   }
   if (!valid) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;              // (a NaN stays one)
   const int i = p.by_G.of(R);
   const long long row = (static_cast<long long>(d.x) * p.q_len + i) * p.H + head * p.G + (R - i * p.G);
-  reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (D * 2))[c4] =
-      make_uint2(pack2<kBf16>(o.x * inv, o.y * inv), pack2<kBf16>(o.z * inv, o.w * inv));
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+    reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (D * 2))[v * kLanes + c4] =
+        make_uint2(pack2<kBf16>(o[v].x * inv, o[v].y * inv), pack2<kBf16>(o[v].z * inv, o[v].w * inv));
   if (c4 == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -1175,11 +1183,12 @@ template <int D, bool kBf16>
 __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_parts(const Params p, int) {
   grid_dependency_wait();
   const int4 d = __ldcg(p.desc + blockIdx.y);
-  if (d.w != 0) merge_rows<D, kBf16, kMergeParts, 8>(p, d, blockIdx.x);
+  if (d.w != 0) merge_rows<D, kBf16, kMergeParts, 8, 1>(p, d, blockIdx.x);
 }
 
-template <int D, bool kBf16, int kAtOnce>
+template <int D, bool kBf16, int kAtOnce, int kV>
 __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_units(const Params p, int entries) {
+  static_assert(kMergeUnits * kV <= 16, "a partial's rows are a multiple of 16");
   constexpr int kThreadsM = D / 4 * kMergeUnits, kWarps = kThreadsM / 32;
   __shared__ int4 cut[kMaxParts];
   __shared__ int warp_cut[kWarps];
@@ -1200,10 +1209,10 @@ __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_many_units(const 
     n_cut = at;
     __syncthreads();
   }
-  const int chunks = p.part_rows / kMergeUnits;
+  const int chunks = p.part_rows / (kMergeUnits * kV);
   for (int item = blockIdx.x; item < n_cut * chunks; item += gridDim.x) {
     const int u = item / chunks;
-    merge_rows<D, kBf16, 1, kAtOnce>(p, cut[u], item - u * chunks);
+    merge_rows<D, kBf16, 1, kAtOnce, kV>(p, cut[u], item - u * chunks);
   }
 }
 
