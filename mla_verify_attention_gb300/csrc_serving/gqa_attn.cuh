@@ -382,7 +382,9 @@ __device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUt
   uint64_t* const full = is_v ? sm.vfull : sm.kfull;
   uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
   const uint32_t ring = smem_u32(sm.ring) + (is_v ? C::kTile : 0);
-  const int R = p.box_rows, boxes = kKeys / R;             // boxes along the keys; lane i looks up box i's row
+  // Boxes along the keys.  The lanes look up the rows of 32 of them, `batch_tiles`
+  // tiles, together and a batch ahead.
+  const int R = p.box_rows, shift = __ffs(R) - 1, boxes = kKeys >> shift, batch_tiles = 32 / boxes;
   const bool paged = p.block_table != nullptr;
   Ring<C::kStages> at;
   int issued = 0;
@@ -391,31 +393,32 @@ __device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUt
     auto row_of = [&](int j) {
       const int key = (s.tile0 + j) * kKeys + lane * R;
       if (!paged) return key;
-      if (lane >= boxes || j >= s.n || key >= s.S) return 0;
-      return pool_row(p, s.b, key);
+      return key < s.S && key < (s.tile0 + s.n) * kKeys ? pool_row(p, s.b, key) : 0;
     };
     const int batch = paged ? 0 : s.b;
-    int row = row_of(0);
-    for (int j = 0; j < s.n; ++j, at.advance()) {
-      const int row_next = row_of(j + 1);
+    int row = 0, row_next = row_of(0), first = 0;          // `first`: lane of the tile's first box
+    for (int j = 0; j < s.n; ++j, at.advance(), first = (first + boxes) & 31) {
+      if (first == 0) {
+        row = row_next;
+        row_next = row_of(j + batch_tiles);
+      }
       if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
       const uint32_t bar = smem_u32(&full[at.stage]), dst = ring + at.stage * 2 * C::kTile;
       if (p.test_stall && is_v && issued == 0 && blockIdx.x == 0) goto out;       // this load never comes
       if (R == kKeys) {
         arrive_expect_elect(bar, C::kTile);
-        tma_box_elect(dst, map, __shfl_sync(0xFFFFFFFFu, row, 0), 0, s.head, batch, bar);
+        tma_box_elect(dst, map, __shfl_sync(0xFFFFFFFFu, row, first), 0, s.head, batch, bar);
       } else {
-        const int n = min(boxes, (s.S - (s.tile0 + j) * kKeys + R - 1) / R);       // boxes with keys of the stream
+        const int n = min(boxes, (s.S - (s.tile0 + j) * kKeys + R - 1) >> shift);  // boxes with keys of the stream
         arrive_expect_elect(bar, n * R * D * 2);
         for (int i = 0; i < n; ++i) {
-          const int r = __shfl_sync(0xFFFFFFFFu, row, i);
+          const int r = __shfl_sync(0xFFFFFFFFu, row, first + i);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
             tma_box_elect(dst + c * (kKeys * 128) + i * R * 128, map, r, c, s.head, batch, bar);
         }
       }
       ++issued;
-      row = row_next;
     }
   }
 out:
@@ -434,6 +437,7 @@ __device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk w
   constexpr int kUnits = D / 8;                // 16-byte units a row
   constexpr int kPer = 32 / kUnits;            // rows a warp copies at once
   constexpr int kAhead = C::kStages - 1 < 8 ? C::kStages - 1 : 8;   // stages in flight
+  constexpr int kTablesAhead = 6;              // tiles
   const int lane = threadIdx.x & 31;
   uint64_t* const full = is_v ? sm.vfull : sm.kfull;
   uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
@@ -455,9 +459,16 @@ __device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk w
       const int key = (s.tile0 + j) * kKeys + half * 32 + lane;
       return j >= s.n || key >= s.S ? -1 : pool_row(p, s.b, key);
     };
+    auto prefetch = [&](int j) {               // the table's entries for tile j, soon to be looked up
+      const int key = (s.tile0 + j) * kKeys + lane * 2;
+      if (j < s.n && key < s.S)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table + static_cast<size_t>(s.b) * p.max_blocks + p.page.of(key)));
+    };
+    for (int j = 1; j < kTablesAhead; ++j) prefetch(j);
     const uint8_t* const head = pool + s.head * head_stride + (lane % kUnits) * 16;
     int lo = row_of(0, 0), hi = row_of(0, 1);
     for (int j = 0; j < s.n; ++j, at.advance()) {
+      prefetch(j + kTablesAhead);
       const int lo_next = row_of(j + 1, 0), hi_next = row_of(j + 1, 1);
       if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
       const uint32_t dst = ring + at.stage * 2 * C::kTile + (lane % kUnits >> 3) * (kKeys * 128);
