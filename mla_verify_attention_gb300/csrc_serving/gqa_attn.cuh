@@ -14,9 +14,9 @@
 //
 // Measured (GPU time, bf16 D = 128 unless said, loads first: share of the
 // measured copy rate): 64 streams of 8k keys, one token, 8 heads a key head 317
-// us, 6.8 TB/s (100 %); the same at D = 64, 16k keys 317 us (100 %); one stream
+// us, 6.8 TB/s (100 %); the same at D = 64, 16k keys 325 us (98 %); one stream
 // of 64k keys, 9 drafts 50 us, 5.4 TB/s (79 %: ~6.5 us of start and end and ~4 us
-// of merge around the stream); 16 streams x 1,024 rows over 8k keys 198 us, 1,390
+// of merge around the stream); 16 streams x 1,024 rows over 8k keys 197 us, 1,395
 // TFLOP/s (71 % of the measured bf16 rate: the chain of a tile through products,
 // softmax and products again, not any one of them).
 //

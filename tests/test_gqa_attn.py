@@ -279,6 +279,14 @@ def test_pages(B, q, H, Hkv, D, lens, dt, page):
     verify(c, *run_paged(c, page, pools, table))
 
 
+@pytest.mark.parametrize("page", [64, 48, 32, 8, 5])
+def test_pages_of_long_runs(page):
+    # Runs of about fifty tiles: the pages are looked up in several batches.
+    c = case(3, 3, 16, 8, 64, [30000, 7001, 23333], BF16)
+    pools, table = paged(c, page)
+    verify(c, *run_paged(c, page, pools, table))
+
+
 def test_pages_equal_the_contiguous_call():
     c = case(2, 9, 16, 2, 128, [640, 333], BF16, smax=640)
     a = run(c)
