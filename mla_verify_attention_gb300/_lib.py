@@ -124,6 +124,22 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def empty_on(stream, shape, dtype, device, result=True):
+    """Memory for what a call on `stream` writes, which is not the current
+    stream.  It comes out of `stream`'s pool: a block of the current stream's
+    pool may still be used by work queued there, which `stream` does not wait
+    for.  A result is for the current stream to read (once that has waited for
+    `stream`), so it is recorded there: dropped, it is not handed out again
+    before the current stream's work of that time is done."""
+    import torch
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(current)
+    return t
+
+
 def verify_attn_raw(q_nope_ptr, q_rope_ptr, kv_ptr, seq_lens_ptr, mask_ptr, B, q_len, H, Smax,
                     scale, out_ptr, lse_ptr, workspace_ptr, workspace_bytes, stream_handle) -> int:
     """Direct C-ABI call with integer device pointers; returns the status."""

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from ._lib import MLA_OK, MLAError, load_library
+from ._lib import MLA_OK, MLAError, empty_on, load_library
 
 _STRIDES = ctypes.c_longlong * 9
 LATENT, ROPE, ROW = 512, 64, 576
@@ -55,17 +55,16 @@ def _on_current(dev):
     return dev >= 0 and dev == _current_device()
 
 
-def _handle(stream, dev, scratch=()):
-    """The stream's handle; memory made here for another stream than the
-    current one is recorded on it, so that it is not handed out too early."""
-    current = _current_stream(dev)
-    if stream is None:
-        return current
-    handle = int(stream.cuda_stream)
-    if handle != current:
-        for t in scratch:
-            t.record_stream(stream)
-    return handle
+def _handle(stream, dev):
+    return _current_stream(dev) if stream is None else int(stream.cuda_stream)
+
+
+def _empty(shape, dt, like, stream, result=True):
+    """Memory that a call on `stream` writes, out of that stream's pool."""
+    device = like.device
+    if stream is None or int(stream.cuda_stream) == _current_stream(like.get_device()):
+        return _torch.empty(shape, dtype=dt, device=device)
+    return empty_on(stream, shape, dt, device, result)
 
 
 def _ints(name, t, *shape):
@@ -85,7 +84,7 @@ def gqa_workspace_size(B: int, q_len: int, H: int, Hkv: int, D: int) -> int:
     return int(load_library().mla_gqa_workspace_size(B, q_len, H, Hkv, D))
 
 
-def _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, Hkv):
+def _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, Hkv, stream):
     B, q_len, H, D = q.shape
     dt = q.dtype
     if k.dtype is not dt or v.dtype is not dt or (dt is not _bf16 and dt is not _fp16):
@@ -102,23 +101,19 @@ def _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, Hkv):
         if len(ks) == 3:            # pools: no batch dimension
             ks, vs = (8,) + ks, (8,) + vs
         strides = _STRIDES(*qs[:3], *ks[:3], *vs[:3])
-    made = []
     if out is None:
-        out = _torch.empty((B, q_len, H, D), dtype=dt, device=q.device)
-        made.append(out)
+        out = _empty((B, q_len, H, D), dt, q, stream)
     elif out.dtype is not dt or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
     if lse is None:
-        lse = _torch.empty((B, q_len, H), dtype=_fp32, device=q.device)
-        made.append(lse)
+        lse = _empty((B, q_len, H), _fp32, q, stream)
     elif lse.dtype is not _fp32 or lse.shape != (B, q_len, H) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B,q,H]")
     if workspace is None:
-        workspace = _torch.empty(gqa_workspace_size(B, q_len, H, Hkv, D), dtype=_torch.uint8, device=q.device)
-        made.append(workspace)
+        workspace = _empty(gqa_workspace_size(B, q_len, H, Hkv, D), _torch.uint8, q, stream, result=False)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return B, q_len, H, D, 0 if dt is _bf16 else 1, strides, out, lse, workspace, made
+    return B, q_len, H, D, 0 if dt is _bf16 else 1, strides, out, lse, workspace
 
 
 def gqa_verify_attn(q, k, v, seq_lens, tree_mask, scale, out=None, lse=None, workspace=None, stream=None):
@@ -129,7 +124,8 @@ def gqa_verify_attn(q, k, v, seq_lens, tree_mask, scale, out=None, lse=None, wor
     dimension is contiguous.  seq_lens [B] int32 counts the drafts' own rows
     (0: unused stream), tree_mask [B,q,ceil(q/32)] as for ``verify_attn``.
     Returns (out [B,q,H,D] in q's type, lse [B,q,H] fp32); a row whose mask
-    leaves nothing has out 0 and lse -inf.
+    leaves nothing has out 0 and lse -inf.  Without out, lse or workspace they
+    are made, out of `stream`'s own pool where that is another stream.
     """
     if _call is None:
         _bind()
@@ -140,13 +136,14 @@ def gqa_verify_attn(q, k, v, seq_lens, tree_mask, scale, out=None, lse=None, wor
     if not (_on_current(dev) and dev == k.get_device() == v.get_device() == seq_lens.get_device()
             == tree_mask.get_device()):
         _wrong_device(q, k, v, seq_lens, tree_mask)
-    B, q_len, H, D, dt, strides, out, lse, ws, made = _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, shape[2])
+    B, q_len, H, D, dt, strides, out, lse, ws = _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, shape[2],
+                                                     stream)
     if not dev == out.get_device() == lse.get_device() == ws.get_device():
         _wrong_device(q, out, lse, ws)
     st = _call(_GQA, _pack_gqa(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), strides and ctypes.addressof(strides), seq_lens.data_ptr(),
         tree_mask.data_ptr(), B, q_len, H, shape[2], D, shape[1], dt, scale, out.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev, made)))
+        ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn")
     return out, lse
@@ -167,15 +164,15 @@ def gqa_verify_attn_paged(q, k_pool, v_pool, block_table, page_size, seq_lens, t
     if not (_on_current(dev) and dev == k_pool.get_device() == v_pool.get_device() == seq_lens.get_device()
             == tree_mask.get_device() == block_table.get_device()):
         _wrong_device(q, k_pool, v_pool, seq_lens, tree_mask, block_table)
-    B, q_len, H, D, dt, strides, out, lse, ws, made = _gqa(q, k_pool, v_pool, seq_lens, tree_mask, out, lse, workspace,
-                                                           shape[1])
+    B, q_len, H, D, dt, strides, out, lse, ws = _gqa(q, k_pool, v_pool, seq_lens, tree_mask, out, lse, workspace, shape[1],
+                                                     stream)
     if not dev == out.get_device() == lse.get_device() == ws.get_device():
         _wrong_device(q, out, lse, ws)
     st = _call(_GQA_PAGED, _pack_paged(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), strides and ctypes.addressof(strides), shape[0],
         block_table.data_ptr(), max_blocks, page_size, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H, shape[1],
         D, dt, scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-        _handle(stream, dev, made)))
+        _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn_paged")
     return out, lse
