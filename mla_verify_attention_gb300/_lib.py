@@ -125,14 +125,16 @@ def _stream_handle(stream) -> int:
 
 
 def empty_on(stream, shape, dtype, device, result=True):
-    """Memory for what a call on `stream` writes, which is not the current
-    stream.  It comes out of `stream`'s pool: a block of the current stream's
+    """Memory for what a call on `stream` writes.  Where that is not the current
+    stream it comes out of `stream`'s pool: a block of the current stream's
     pool may still be used by work queued there, which `stream` does not wait
     for.  A result is for the current stream to read (once that has waited for
     `stream`), so it is recorded there: dropped, it is not handed out again
     before the current stream's work of that time is done."""
     import torch
     current = torch.cuda.current_stream(device)
+    if stream is None or int(stream.cuda_stream) == int(current.cuda_stream):
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if result:
@@ -170,12 +172,12 @@ def verify_attn(q_nope, q_rope, kv, seq_lens, tree_mask, scale, out=None, lse=No
         raise ValueError("tree_mask must be a contiguous CUDA 32-bit tensor")
     dev = q_nope.device
     if out is None:
-        out = torch.empty((B, q, H, 512), dtype=torch.float32, device=dev)
+        out = empty_on(stream, (B, q, H, 512), torch.float32, dev)
     if lse is None:
-        lse = torch.empty((B, q, H), dtype=torch.float32, device=dev)
+        lse = empty_on(stream, (B, q, H), torch.float32, dev)
     need = workspace_size(B, q, H, Smax)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = empty_on(stream, need, torch.uint8, dev, result=False)
     ws_ptr = workspace.data_ptr() if workspace is not None else 0
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = verify_attn_raw(q_nope.data_ptr(), q_rope.data_ptr(), kv.data_ptr(), seq_lens.data_ptr(),
@@ -213,12 +215,12 @@ def verify_attn_paged(q_nope, q_rope, kv_pool, block_table, page_size, seq_lens,
         raise ValueError("tree_mask must be a contiguous CUDA 32-bit tensor")
     dev = q_nope.device
     if out is None:
-        out = torch.empty((B, q, H, 512), dtype=torch.float32, device=dev)
+        out = empty_on(stream, (B, q, H, 512), torch.float32, dev)
     if lse is None:
-        lse = torch.empty((B, q, H), dtype=torch.float32, device=dev)
+        lse = empty_on(stream, (B, q, H), torch.float32, dev)
     need = paged_workspace_size(B, q, H, max_blocks, int(page_size))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = empty_on(stream, need, torch.uint8, dev, result=False)
     ws_ptr = workspace.data_ptr() if workspace is not None else 0
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = int(load_library().mla_verify_attn_paged(

@@ -61,10 +61,9 @@ def _handle(stream, dev):
 
 def _empty(shape, dt, like, stream, result=True):
     """Memory that a call on `stream` writes, out of that stream's pool."""
-    device = like.device
-    if stream is None or int(stream.cuda_stream) == _current_stream(like.get_device()):
-        return _torch.empty(shape, dtype=dt, device=device)
-    return empty_on(stream, shape, dt, device, result)
+    if stream is None:
+        return _torch.empty(shape, dtype=dt, device=like.device)
+    return empty_on(stream, shape, dt, like.device, result)
 
 
 def _ints(name, t, *shape):

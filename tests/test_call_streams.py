@@ -11,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import mla_verify_attention_gb300 as mva
-from mla_verify_attention_gb300 import _serving
+from mla_verify_attention_gb300 import _lib, _serving
 
 BF16 = torch.bfloat16
 CURRENT, SIDE = 0, 77
@@ -94,6 +94,17 @@ def pool(monkeypatch):
     monkeypatch.setattr(_serving, "_current_device", lambda: 0)
     monkeypatch.setattr(_serving, "_current_stream", lambda dev: p.now[-1].cuda_stream)
     monkeypatch.setattr(_serving, "gqa_workspace_size", lambda *a: 4096)
+
+    class Library:
+        @staticmethod
+        def mla_verify_attn(*a):
+            p.launched.append(a[-1])
+            return 0
+        mla_verify_attn_paged = mla_verify_attn
+
+    monkeypatch.setattr(_lib, "load_library", Library)
+    monkeypatch.setattr(_lib, "workspace_size", lambda *a: 4096)
+    monkeypatch.setattr(_lib, "paged_workspace_size", lambda *a: 4096)
     return p
 
 
@@ -140,6 +151,31 @@ def test_grouped_heads_memory_of_the_caller(pool, call):
     assert out is given["out"] and lse is given["lse"] and not pool.made and pool.launched == [SIDE]
 
 
+def latent(**kw):
+    return mva.verify_attn(half(1, 5, 8, 512), half(1, 5, 8, 64), half(1, 90, 576), ints(1), ints(1, 5, 1), 0.1, **kw)
+
+
+def latent_paged(**kw):
+    return mva.verify_attn_paged(half(1, 5, 8, 512), half(1, 5, 8, 64), half(96, 576), ints(1, 6), 16, ints(1),
+                                 ints(1, 5, 1), 0.1, **kw)
+
+
+@pytest.mark.parametrize("call", [latent, latent_paged])
+def test_latent_memory_is_the_streams_own(pool, call):
+    out, lse = call(stream=Stream(SIDE))
+    assert pool.launched == [SIDE] and [t.made_on for t in pool.made] == [SIDE] * 3
+    assert out.recorded == [CURRENT] and lse.recorded == [CURRENT]
+    assert [t.recorded for t in pool.made[2:]] == [[]]
+
+
+@pytest.mark.parametrize("call", [latent, latent_paged])
+@pytest.mark.parametrize("stream", [None, Stream(CURRENT)])
+def test_latent_memory_on_the_current_stream(pool, call, stream):
+    out, lse = call(stream=stream)
+    assert pool.launched == [CURRENT] and [t.made_on for t in pool.made] == [CURRENT] * 3
+    assert not out.recorded and not lse.recorded
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("page", [0, 16])
 def test_calls_on_two_streams_share_no_memory(page, monkeypatch):
@@ -179,6 +215,50 @@ def test_calls_on_two_streams_share_no_memory(page, monkeypatch):
     monkeypatch.undo()
     torch.cuda.synchronize()
     assert mva.last_device_error() == 0
+    for other in (used[0], used[2]):
+        assert used[1][1] <= other[0] or other[1] <= used[1][0]
+    for got, ref in ((first, want[0]), (second, want[1]), (third, want[0])):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [0, 16])
+def test_latent_calls_on_two_streams_share_no_memory(page, monkeypatch):
+    gen = torch.Generator().manual_seed(4)
+    rand = lambda *s: torch.randn(s, generator=gen).to(BF16).cuda()
+    B, q, H, n = 1, 9, 64, 4000
+    lens = torch.full((B,), n, dtype=torch.int32).cuda()
+    mask = torch.tensor([(2 << i) - 1 for i in range(q)], dtype=torch.int32).view(1, q, 1).cuda()
+    kv, table = rand(n, 576), torch.arange(n // 16, dtype=torch.int32).view(B, -1).cuda()
+    queries = [(rand(B, q, H, 512), rand(B, q, H, 64)) for _ in range(2)]
+
+    def call(x, stream=None):
+        if page:
+            return mva.verify_attn_paged(*x, kv, table, page, lens, mask, 0.07, stream=stream)
+        return mva.verify_attn(*x, kv.view(B, n, 576), lens, mask, 0.07, stream=stream)
+
+    want = [call(x) for x in queries]
+    work = torch.randn((8192, 8192), device="cuda")
+    side = torch.cuda.Stream()
+    used = []
+    empty = torch.empty
+
+    def noted(shape, **kw):
+        t = empty(shape, **kw)
+        if t.dtype == torch.uint8:
+            used.append((t.data_ptr(), t.data_ptr() + t.numel()))
+        return t
+
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", noted)
+    for _ in range(4):
+        torch.mm(work, work)                       # the current stream's calls wait behind this
+    first = call(queries[0])
+    second = call(queries[1], stream=side)
+    third = call(queries[0])
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert mva.last_device_error() == 0 and len(used) == 3
     for other in (used[0], used[2]):
         assert used[1][1] <= other[0] or other[1] <= used[1][0]
     for got, ref in ((first, want[0]), (second, want[1]), (third, want[0])):
