@@ -309,7 +309,8 @@ int mla_verify_attn_noalloc(const void* q_nope_abs, const void* q_rope, const vo
  *                token slot -1 and MLA_ERR_PAGE.
  *   slots        [max_tokens] int32 (may be NULL when max_tokens is 0).
  *   0 <= B <= 16384, page_size >= 1, max_blocks >= 1, max_blocks * page_size < 2^31,
- *   pool_pages * page_size < 2^31; all pointers 4-byte aligned (slots: 16).
+ *   pool_pages * page_size < 2^31, free_capacity and max_tokens <= 2^31 - 2; all pointers
+ *   4-byte aligned (slots: 16).
  *
  * Either the whole batch grows or nothing does: with too few free pages
  * (MLA_ERR_POOL), or a negative length, a stream that would outgrow its table

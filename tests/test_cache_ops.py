@@ -196,6 +196,32 @@ def test_many_streams_all_or_nothing(room):
             assert torch.equal(t[k], old[k]), k
 
 
+@pytest.mark.parametrize("B", [2, 3, 4, 7, 8, 16, 64, 1500])
+@pytest.mark.parametrize("room", [8, 5000, 40000])
+def test_more_new_tokens_than_32_bits_count(B, room):
+    # 2^30 - 1 new tokens a stream in a block it already has: eight times as many are more than 2^32.
+    lens, new = ints([1] * B), ints([2 ** 30 - 1] * B)
+    table, free, count = ints([[0]] * B), ints([0]), ints([1])
+    slots = torch.full((room,), 7, dtype=torch.int32, device="cuda")
+    mva.blocks_extend(lens, new, table, 2 ** 30, free, count, 1, slots)
+    ok(-8)
+    assert lens.tolist() == [1] * B and count.tolist() == [1] and free.tolist() == [0]
+    assert table.tolist() == [[0]] * B and (slots == -1).all()
+
+
+def test_more_blocks_than_32_bits_count():
+    # Four streams of 2^30 blocks each.
+    table = torch.empty((4, 2 ** 30), dtype=torch.int32, device="cuda")
+    lens, free, count = ints([2 ** 30] * 4), ints(list(range(9))), ints([2])
+    mva.blocks_trim(lens, ints([0] * 4), table, 1, free, count)
+    ok(-11)
+    assert lens.tolist() == [2 ** 30] * 4 and free.tolist() == list(range(9)) and count.tolist() == [2]
+    lens, slots = ints([0] * 4), torch.full((100,), 7, dtype=torch.int32, device="cuda")
+    mva.blocks_extend(lens, ints([2 ** 30] * 4), table, 1, free, count, 9, slots)
+    ok(-8)
+    assert lens.tolist() == [0] * 4 and count.tolist() == [2] and (slots == -1).all()
+
+
 @pytest.mark.parametrize("B,most", [(3000, 4), (700, 100)])
 def test_streams_of_a_thread_are_read_before_they_change(B, most):
     # Several streams a thread, which every block of the call reads twice.

@@ -77,6 +77,17 @@ def test_extend_arguments(lib, kw, want):
     assert call(lib.mla_blocks_extend, EXTEND, **kw) == want
 
 
+def test_block_counts_that_sums_cannot_tell_apart(lib):
+    # Sums stop at 2^31 - 1, which has to be more than any limit.
+    most = 2 ** 31 - 2
+    assert call(lib.mla_blocks_extend, EXTEND, tokens=most + 1) == SHAPE
+    assert call(lib.mla_blocks_extend, EXTEND, cap=most + 1) == SHAPE
+    assert call(lib.mla_blocks_trim, TRIM, cap=most + 1) == SHAPE
+    no_device()
+    assert call(lib.mla_blocks_extend, EXTEND, tokens=most, cap=most) == NO_DEVICE
+    assert call(lib.mla_blocks_trim, TRIM, cap=most) == NO_DEVICE
+
+
 @pytest.mark.parametrize("kw,want", [
     (dict(B=16385), SHAPE), (dict(page=0), SHAPE), (dict(cap=-1), SHAPE), (dict(keep=0), NULL), (dict(count=0), NULL),
     (dict(table=2), ALIGN), (dict(B=0), OK)])
