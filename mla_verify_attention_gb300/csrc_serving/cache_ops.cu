@@ -288,8 +288,10 @@ using BlocksFn = void (*)(BlocksParams);
 
 int launch_blocks(BlocksFn fn, const BlocksParams& p, unsigned blocks, unsigned threads, cudaStream_t stream,
                   unsigned cluster = 1) {
+  // Beyond 48 KB, the kernel's own arrays (256 bytes, room for 1 KB) counted, a
+  // block's shared memory has to be asked for.
   const size_t smem = (3 * static_cast<size_t>(p.B) + 2) * sizeof(int);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 47 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((3 * kMaxStreams + 2) * sizeof(int))) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;

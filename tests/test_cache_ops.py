@@ -146,6 +146,38 @@ def test_largest_batch():
     assert p.t["slots"].tolist() == slots + [-1] * (2 * B - len(slots))
 
 
+SHARED_MEMORY = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch, mla_verify_attention_gb300 as mva
+ints = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+for B in (4010, 4011, 4074, 4075, 4095, 4096):
+    lens, table, count = ints(B), ints(B, 3), ints(1) + 2 * B
+    free = torch.arange(2 * B, dtype=torch.int32, device="cuda")
+    for room in (2 * B, 40000):
+        slots = ints(room) + 7
+        mva.blocks_extend(lens, ints(B) + 2, table, 4, free, count, 2 * B, slots)
+        torch.cuda.synchronize()
+        b = torch.arange(B, device="cuda")
+        want = (4 * (2 * B - 1 - b)[:, None] + torch.arange(2, device="cuda")).view(-1)
+        assert mva.last_device_error() == 0 and (lens == 2).all() and count.item() == B
+        assert torch.equal(slots[:2 * B].long(), want) and (slots[2 * B:] == -1).all()
+        mva.blocks_trim(lens, ints(B), table, 4, free, count)
+        torch.cuda.synchronize()
+        assert mva.last_device_error() == 0 and (lens == 0).all() and count.item() == 2 * B
+        assert torch.equal(free.long(), torch.arange(2 * B, device="cuda"))
+"""
+
+
+def test_batches_around_the_shared_memory_that_is_not_asked_for():
+    # In a process of its own: a larger batch before it would have asked.
+    import subprocess
+    import sys
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", SHARED_MEMORY, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("why,new,status", [
     ("pages", [10, 40, 0], -11), ("negative", [1, -1, 0], -8), ("table", [0, 0, 90], -8), ("slots", [20, 12, 0], -8)])
 def test_extend_all_or_nothing(why, new, status):
