@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
   bad |= kExtend && all_t > static_cast<unsigned>(p.max_tokens);
   if (bad || no_pages) {
     if (kExtend && kPart != kCommit)
-      for (int t = first; t < p.max_tokens; t += all_threads) p.slots[t] = -1;
+      for (long long t = first; t < p.max_tokens; t += all_threads) p.slots[t] = -1;
     if (kPart != kItems && first == 0) atomicOr(p.status, bad ? kBitSeqLen : kBitPool);
     return;
   }
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) blocks_kernel(const BlocksPara
             s[e] = row0 < 0 ? -1 : row0 + (pos - blk * static_cast<int>(p.page.d));
           }
         }
-        if (t0 + 4 <= p.max_tokens) {
+        if (p.max_tokens - t0 >= 4) {
           *reinterpret_cast<int4*>(p.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
         } else {
           for (int e = 0; t0 + e < p.max_tokens; ++e) p.slots[t0 + e] = s[e];

@@ -146,6 +146,22 @@ def test_largest_batch():
     assert p.t["slots"].tolist() == slots + [-1] * (2 * B - len(slots))
 
 
+@pytest.mark.parametrize("n", [2 ** 31 - 2, 2 ** 31 - 5, 2 ** 31 - 100000])
+def test_largest_slot_map(n):
+    # Nearly 2^31 entries: the last ones are still counted in range, and nothing beside them is written.
+    raw = torch.full((n + 8,), 7, dtype=torch.int32, device="cuda")
+    slots = raw[4:4 + n]
+    lens, table, free, count = ints([3, 5]), ints([[0, -1], [1, 2]]), ints([3]), ints([1])
+    for new, status, want in (([2, 9], -8, []), ([4, 1], 0, [3, 12, 13, 14, 9])):
+        slots.fill_(7)
+        mva.blocks_extend(lens, ints(new), table, 4, free, count, 4, slots)
+        ok(status)
+        assert slots[:len(want)].tolist() == want
+        for part in slots[len(want):].split(2 ** 28):
+            assert (part == -1).all()
+        assert (raw[:4] == 7).all() and (raw[4 + n:] == 7).all()
+
+
 SHARED_MEMORY = """
 import sys
 sys.path.insert(0, sys.argv[1])
