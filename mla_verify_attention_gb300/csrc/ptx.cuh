@@ -105,6 +105,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 // ---------------------------------------------------------------- grid dependencies
 // Block until the grids this one depends on programmatically have completed
 // and their memory is visible (a no-op for a launch without that dependency).
+// What those grids may have written is then read with ordinary loads: a
+// read-only one (__ldg, ld.global.nc) promises that nobody writes the address
+// while this grid runs, which began before they ended, and may be moved up
+// across this wait.
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

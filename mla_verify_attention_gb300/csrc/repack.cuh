@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kRepackThreads, 4) repack_kernel(const RepackP
         const int r = idx / kRowPieces;
         const int c = idx - r * kRowPieces;
         if (r < nk)
-          v[i] = __ldg(reinterpret_cast<const uint4*>(p.pool + static_cast<size_t>(rows[r]) * (kRowPieces * 16)) + c);
+          v[i] = reinterpret_cast<const uint4*>(p.pool + static_cast<size_t>(rows[r]) * (kRowPieces * 16))[c];
       }
 #pragma unroll
       for (int i = 0; i < kRepackBatch; ++i) {

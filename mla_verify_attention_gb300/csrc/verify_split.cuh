@@ -321,7 +321,7 @@ template <bool kPaged>
 __device__ __forceinline__ int2 tile_origin(const SplitParams& p, const Unit& u, int key) {
   if (!kPaged) return make_int2(key, u.b);
   const int blk = key / p.page_size;
-  int page = __ldg(p.block_table + static_cast<size_t>(u.b) * p.max_blocks + blk);
+  int page = p.block_table[static_cast<size_t>(u.b) * p.max_blocks + blk];
   if (page < 0 || page >= p.pool_pages) {
     atomicOr(p.status, kStatusPage);
     page = 0;

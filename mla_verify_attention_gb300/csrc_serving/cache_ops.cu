@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
       uint4 v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c + 32 * e < n) v[e] = __ldg(src + c + 32 * e);
+        if (c + 32 * e < n) v[e] = src[c + 32 * e];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (c + 32 * e < n) dst[c + 32 * e] = v[e];

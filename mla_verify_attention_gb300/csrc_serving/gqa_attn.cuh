@@ -251,7 +251,7 @@ __device__ __forceinline__ bool wait2(S& sm, uint64_t& bar0, uint32_t parity0, u
 
 // Key tiles of stream b; 0 for an unused stream and for one whose length is out of range.
 __device__ __forceinline__ int stream_tiles(const Params& p, int b, int& S) {
-  S = __ldg(p.seq_lens + b);
+  S = p.seq_lens[b];
   return S < p.q_len || S > p.Smax ? 0 : (S + kKeys - 1) / kKeys;
 }
 
@@ -352,7 +352,7 @@ __device__ __forceinline__ uint64_t seen_drafts(const Params& p, int b, uint32_t
 // before its value is looked at (a check straight after the load waited for it, a
 // tile: 64 streams of 8k keys on 4-row pages took 610 us).
 __device__ __forceinline__ int table_entry(const Params& p, int b, int key) {
-  return __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + p.page.of(key));
+  return p.block_table[static_cast<size_t>(b) * p.max_blocks + p.page.of(key)];
 }
 // A page outside the pool is reported, and page 0 read.
 __device__ __forceinline__ int pool_row(const Params& p, int page, int key) {
