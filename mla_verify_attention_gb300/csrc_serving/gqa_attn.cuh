@@ -236,7 +236,9 @@ __device__ __forceinline__ bool wait(S& sm, uint64_t& bar, uint32_t parity, cons
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// For two barriers at once: half the lanes ask for each.
+// For two barriers at once: half the lanes ask for each.  A lane has then only
+// seen what is ordered before its own barrier; __syncwarp orders that before what
+// any lane does next (a vote alone orders no memory).
 template <class S>
 __device__ __forceinline__ bool wait2(S& sm, uint64_t& bar0, uint32_t parity0, uint64_t& bar1, uint32_t parity1,
                                       const Params& p) {
@@ -244,7 +246,9 @@ __device__ __forceinline__ bool wait2(S& sm, uint64_t& bar0, uint32_t parity0, u
   const uint32_t bar = odd ? smem_u32(&bar1) : smem_u32(&bar0), parity = odd ? parity1 : parity0;
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) ok = wait_slow(sm, bar, parity, p);
-  return __all_sync(0xFFFFFFFFu, ok);
+  ok = __all_sync(0xFFFFFFFFu, ok);
+  __syncwarp();
+  return ok;
 }
 
 // ------------------------------------------------------------ work

@@ -112,6 +112,20 @@ def test_many_segments_of_one_tile():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("D,page", [(64, 0), (128, 0), (128, 16), (64, 5)])
+def test_products_see_what_both_their_barriers_guard(D, page):
+    # Tiles, weights and results pass between warps all the time: the same bits every time.
+    gen = torch.Generator().manual_seed(D + page)
+    lens = [int(x) for x in torch.randint(5, 400, (300,), generator=gen)] + [9000]
+    c = case(301, 5, 16, 2, D, lens, BF16)
+    call = run if not page else lambda c, p=paged(c, page): run_paged(c, page, *p)
+    a = call(c)
+    verify(c, *a)
+    for _ in range(50):
+        b = call(c)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("tree", ["chain", "any"])
 @pytest.mark.parametrize("q,G,n", [(9, 8, 9), (9, 8, 70), (40, 2, 41), (64, 4, 64), (64, 4, 129)])
 def test_masks(q, G, n, tree):
