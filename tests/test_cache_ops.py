@@ -290,6 +290,33 @@ def test_streams_of_a_thread_are_read_before_they_change(B, most):
             assert torch.equal(t[k], x), k
 
 
+@pytest.mark.parametrize("B,most,page", [(3000, 20, 4), (1500, 60, 16), (16384, 9, 3)])
+def test_streams_of_a_thread_with_many_tokens(B, most, page):
+    # Two grids for the extend, each with several streams a thread.
+    rng = random.Random(B)
+    p = Pool([rng.randint(0, 30) for _ in range(B)], page, (30 + 3 * most) // page + 2, B * (2 * most // page + 2))
+    t = p.gpu(B * most + 3)
+    for _ in range(2):
+        before = list(p.lens)
+        new = [rng.randint(0, most) for _ in range(B)]
+        slots = p.extend(new)
+        extend(p, new)
+        ok()
+        p.same()
+        assert t["slots"].tolist() == slots + [-1] * (B * most + 3 - len(slots))
+        keep = [rng.choice([0, n, m, rng.randint(n, m)]) for n, m in zip(before, p.lens)]
+        p.trim(keep)
+        trim(p, keep)
+        ok()
+        p.same()
+    old = {k: x.clone() for k, x in t.items()}
+    extend(p, [0] * (B - 1) + [10 ** 6])
+    ok(-8)
+    for k in ("lens", "table", "free", "count"):
+        assert torch.equal(t[k], old[k]), k
+    assert (t["slots"] == -1).all()
+
+
 def test_bad_page_in_the_table_gives_no_slot():
     p = Pool([5, 5], 16, 4, 4)
     t = p.gpu(6)

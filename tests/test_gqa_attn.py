@@ -90,6 +90,23 @@ def test_heads_and_row_groups(B, q, H, Hkv, D, lens, dt):
     verify(c, *run(c))
 
 
+@pytest.mark.parametrize("G,Hkv,D,lens,smax,dt", [
+    (34, 1, 128, [900], 900, BF16),                        # 17 row groups: nine and eight
+    (38, 2, 64, [64, 2500, 700], 2500, FP16),              # 19 groups of two key heads
+    (34, 2, 128, [1300, 80, 3000, 0, 511], 3000, BF16),    # more units than CTAs
+    (68, 1, 64, [640, 5000], 5000, BF16),                  # 34 groups: three sets of twelve, two missing
+    (70, 3, 64, [900, 64, 1700], 1700, FP16),              # 35 groups, three key heads
+    (34, 2, 64, [300, 512, 64, 100], 512, BF16),           # units that are not cut
+])
+def test_row_groups_that_a_set_lacks(G, Hkv, D, lens, smax, dt):
+    # Row groups that sets of CTAs do not divide evenly: in the last set some have none.
+    c = case(len(lens), 64, G * Hkv, Hkv, D, lens, dt, smax=smax)
+    a = run(c)
+    verify(c, *a)
+    b = run(c)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("smax", [448, 512, 513, 600])
 def test_short_caches_whole_and_cut(smax):
     # Up to 512 keys units are not cut, and there is no merge.
