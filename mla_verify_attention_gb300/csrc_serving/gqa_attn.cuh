@@ -1012,10 +1012,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int sum = 0;
+    bool off = false;                  // (reported after the loop: an atomic in it would hold up the next loads)
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) {
       sum += stream_work(p, stream_tiles(p, b, len)) * units;
-      if (blockIdx.x == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
+      off |= len != 0 && (len < p.q_len || len > p.Smax);
     }
+    if (off && blockIdx.x == 0) atomicOr(p.status, kBitSeqLen);
     int inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
