@@ -263,3 +263,34 @@ def test_latent_calls_on_two_streams_share_no_memory(page, monkeypatch):
         assert used[1][1] <= other[0] or other[1] <= used[1][0]
     for got, ref in ((first, want[0]), (second, want[1]), (third, want[0])):
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.gpu
+def test_captured_calls_on_two_streams():
+    """A capture that forks and joins, with memory that the calls make themselves on either stream."""
+    gen = torch.Generator().manual_seed(5)
+    rand = lambda *s: torch.randn(s, generator=gen).to(BF16).cuda()
+    B, q, H, Hkv, D, n = 2, 9, 16, 2, 128, 900
+    lens = torch.tensor([n, n - 30], dtype=torch.int32).cuda()
+    mask = torch.tensor([(2 << i) - 1 for i in range(q)], dtype=torch.int32).view(1, q, 1).expand(B, q, 1).contiguous().cuda()
+    k, v, queries = rand(B, n, Hkv, D), rand(B, n, Hkv, D), [rand(B, q, H, D) for _ in range(3)]
+    kv, qn, qr = rand(B, n, 576), rand(B, q, 64, 512), rand(B, q, 64, 64)
+    grouped = lambda x, **kw: mva.gqa_verify_attn(x, k, v, lens, mask, 0.1, **kw)
+    latent = lambda **kw: mva.verify_attn(qn, qr, kv, lens, mask, 0.07, **kw)
+    want = [grouped(x) for x in queries] + [latent()]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        first = queries[0] + 0                     # work of another kind before the fork
+        side.wait_stream(here)
+        on_side = grouped(queries[1], stream=side), latent(stream=side)
+        on_main = grouped(first)
+        here.wait_stream(side)
+        joined = grouped(queries[2])               # behind both streams
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert mva.last_device_error() == 0
+    for got, ref in zip((on_main, on_side[0], joined, on_side[1]), want):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
