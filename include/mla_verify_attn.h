@@ -344,7 +344,7 @@ int mla_blocks_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* 
  * and pool_b the pool's address + 1024, both with a row stride of 1152 bytes;
  * for separate keys and values a = k, b = v.  A contiguous cache is a pool of
  * B * Smax rows.
- *   a, b          T rows at a_stride / b_stride bytes.
+ *   a, b          T rows at a_stride / b_stride bytes, apart from the pools.
  *   pool_rows     rows in the pool(s), < 2^31; row strides in bytes.
  *   slots         [T] int32; a negative slot skips its token; one at or beyond
  *                 pool_rows skips it too and records MLA_ERR_SLOT.
@@ -393,7 +393,8 @@ enum mla_dtype { MLA_BF16 = 0, MLA_FP16 = 1 };
  * q_len = 1 with mask bit 0 set is ordinary decoding.
  *
  *   q, out     [B, q_len, H, D], k and v [B, Smax, Hkv, D], all of type `dtype`, D = 64 or 128,
- *              H a multiple of Hkv; 16-byte aligned; out and lse [B, q_len, H] fp32 contiguous.
+ *              H a multiple of Hkv; 16-byte aligned; out and lse [B, q_len, H] fp32 contiguous
+ *              and apart from all inputs (q is still read while rows are written).
  *   strides    NULL for contiguous tensors, or a host array of nine element strides
  *              {q: batch, draft, head; k: batch, row, head; v: batch, row, head}, multiples
  *              of 8 in [8, 2^38); the innermost dimension is contiguous.  Strides of

@@ -379,11 +379,13 @@ struct KeepParams {
 // One block a stream and one or two 512-byte columns of the pool rows: eight
 // warps read the path's rows (kRows a warp at most) into registers, and after a
 // barrier write them to their new places, so that any path is safe in place.
+// Rows that stay where they are are neither read nor written.
 // Before that the block works out the rows (a thread a row; count, length and
 // path are read together, then the pages): two dependent reads that the columns
 // share.  One column while those blocks all fit the device (8 streams x 9
 // latent rows 2.1 us, 2.5 with two); two beyond that (256 streams, 17 of 33 rows
-// of 4 KB on average: 6.4 us, of which the bytes need 5.1; one 6.7, four 7.3 us).
+// of 4 KB on average, of which 13 move: 6.4 us; one 6.7, four 7.3 us.  Reading and
+// writing the kept rows at the copy rate would take 5.1 us, those that move 4.2).
 // Fewer rows a warp leave registers for more blocks: six an SM with five rows
 // (6.8 us with eight rows and four blocks, 8.1 with three).
 constexpr int kKeepWarps = 8;
