@@ -132,8 +132,10 @@ def empty_on(stream, shape, dtype, device, result=True):
     `stream`), so it is recorded there: dropped, it is not handed out again
     before the current stream's work of that time is done."""
     import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     current = torch.cuda.current_stream(device)
-    if stream is None or int(stream.cuda_stream) == int(current.cuda_stream):
+    if int(stream.cuda_stream) == int(current.cuda_stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
