@@ -436,8 +436,39 @@ int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_p
                               int dtype, float scale, void* out, float* lse, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Long caches kept small, for grouped heads: a window over the cache, a cache
+ * held in 4 bits, and eviction by the weight that keys got.
+ */
+
 /*
- * The calls of this section with their arguments in one array of 64-bit values,
+ * mla_gqa_verify_attn and mla_gqa_verify_attn_paged with a sliding window: of
+ * the keys that draft i sees by its mask, in the cache's order, it attends to
+ * the last `window` and to those in the cache's first `sinks` rows.  For a mask of
+ * ancestors (itself among them) that is what a window over positions gives: a
+ * draft at depth n sees `window` - n - 1 keys of the prefix, and the sinks.
+ *   window   >= 1; sinks >= 0 (MLA_ERR_SHAPE).
+ * Rows of the cache from `sinks` up to max(0, seq_lens[b] - q_len - window) are not
+ * used: they may hold anything (NaN included), and block_table entries of
+ * pages that lie wholly there are not read, so such pages may have been given
+ * away.  Tiles of 64 keys that lie there are not read either.  All other
+ * arguments, results, errors and the workspace as for the calls without a window.
+ */
+int mla_gqa_verify_attn_window(const void* q, const void* k, const void* v, const int64_t* strides,
+                               const int32_t* seq_lens, const uint32_t* tree_mask, int B, int q_len, int H,
+                               int Hkv, int D, int Smax, int dtype, float scale, int window, int sinks,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+int mla_gqa_verify_attn_window_paged(const void* q, const void* k_pool, const void* v_pool,
+                                     const int64_t* strides, long long pool_rows, const int32_t* block_table,
+                                     int max_blocks, int page_size, const int32_t* seq_lens,
+                                     const uint32_t* tree_mask, int B, int q_len, int H, int Hkv, int D,
+                                     int dtype, float scale, int window, int sinks, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The calls of the two sections above with their arguments in one array of 64-bit values,
  * in the order of their declarations: integers and addresses as such, a float
  * as the bits of a double.  For bindings to which each argument costs more than
  * its share of the launch.  Returns what the call returns, or MLA_ERR_ARG for an
@@ -449,7 +480,10 @@ enum mla_packed {
   MLA_CALL_CACHE_APPEND = 2,
   MLA_CALL_CACHE_KEEP = 3,
   MLA_CALL_GQA_VERIFY_ATTN = 4,
-  MLA_CALL_GQA_VERIFY_ATTN_PAGED = 5
+  MLA_CALL_GQA_VERIFY_ATTN_PAGED = 5,
+  /* 6 and 7 are not calls */
+  MLA_CALL_GQA_VERIFY_ATTN_WINDOW = 8,
+  MLA_CALL_GQA_VERIFY_ATTN_WINDOW_PAGED = 9
 };
 int mla_call_packed(int call, const int64_t* args);
 

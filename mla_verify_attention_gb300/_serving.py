@@ -20,12 +20,15 @@ LATENT, ROPE, ROW = 512, 64, 576
 # array (ctypes takes 1.3 us to convert sixteen of them, 0.4 us for this), and
 # what is looked up once is bound by the first call.
 _EXTEND, _TRIM, _APPEND, _KEEP, _GQA, _GQA_PAGED = range(6)
+_WINDOW, _WINDOW_PAGED = range(8, 10)
 _pack_extend = struct.Struct("=13q").pack
 _pack_trim = struct.Struct("=10q").pack
 _pack_append = struct.Struct("=14q").pack
 _pack_keep = struct.Struct("=16q").pack
 _pack_gqa = struct.Struct("=13qd5q").pack
 _pack_paged = struct.Struct("=16qd5q").pack
+_pack_window = struct.Struct("=13qd7q").pack
+_pack_window_paged = struct.Struct("=16qd7q").pack
 
 _torch = _call = None
 _current_device = _current_stream = _int32 = _bf16 = _fp16 = _fp32 = None
@@ -174,6 +177,64 @@ def gqa_verify_attn_paged(q, k_pool, v_pool, block_table, page_size, seq_lens, t
         _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_verify_attn_paged")
+    return out, lse
+
+
+def gqa_verify_attn_window(q, k, v, seq_lens, tree_mask, scale, window, sinks=0, out=None, lse=None, workspace=None,
+                           stream=None):
+    """gqa_verify_attn with a sliding window: of the keys that its mask shows a
+    draft, in the cache's order, it attends to the last ``window`` (>= 1) and to
+    those in the cache's first ``sinks`` rows.  Rows from ``sinks`` up to
+    seq_lens[b] - q - window are not used and may hold anything."""
+    if _call is None:
+        _bind()
+    shape = k.shape
+    if q.dim() != 4 or len(shape) != 4 or v.shape != shape or shape[0] != q.shape[0] or shape[3] != q.shape[3]:
+        raise ValueError("expected q [B,q,H,D], k and v [B,Smax,Hkv,D]")
+    dev = q.get_device()
+    if not (_on_current(dev) and dev == k.get_device() == v.get_device() == seq_lens.get_device()
+            == tree_mask.get_device()):
+        _wrong_device(q, k, v, seq_lens, tree_mask)
+    B, q_len, H, D, dt, strides, out, lse, ws = _gqa(q, k, v, seq_lens, tree_mask, out, lse, workspace, shape[2],
+                                                     stream)
+    if not dev == out.get_device() == lse.get_device() == ws.get_device():
+        _wrong_device(q, out, lse, ws)
+    st = _call(_WINDOW, _pack_window(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides and ctypes.addressof(strides), seq_lens.data_ptr(),
+        tree_mask.data_ptr(), B, q_len, H, shape[2], D, shape[1], dt, scale, window, sinks, out.data_ptr(),
+        lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_gqa_verify_attn_window")
+    return out, lse
+
+
+def gqa_verify_attn_window_paged(q, k_pool, v_pool, block_table, page_size, seq_lens, tree_mask, scale, window, sinks=0,
+                                 out=None, lse=None, workspace=None, stream=None):
+    """gqa_verify_attn_paged with a sliding window (see ``gqa_verify_attn_window``);
+    table entries of pages that lie wholly between the first ``sinks`` rows and
+    row seq_lens[b] - q - window are not read."""
+    if _call is None:
+        _bind()
+    shape = k_pool.shape
+    if (q.dim() != 4 or len(shape) != 3 or v_pool.shape != shape or shape[2] != q.shape[3] or block_table.dim() != 2):
+        raise ValueError("expected q [B,q,H,D], k_pool and v_pool [rows,Hkv,D], block_table [B,max_blocks]")
+    max_blocks = block_table.shape[1]
+    _ints("block_table", block_table, q.shape[0], max_blocks)
+    dev = q.get_device()
+    if not (_on_current(dev) and dev == k_pool.get_device() == v_pool.get_device() == seq_lens.get_device()
+            == tree_mask.get_device() == block_table.get_device()):
+        _wrong_device(q, k_pool, v_pool, seq_lens, tree_mask, block_table)
+    B, q_len, H, D, dt, strides, out, lse, ws = _gqa(q, k_pool, v_pool, seq_lens, tree_mask, out, lse, workspace,
+                                                     shape[1], stream)
+    if not dev == out.get_device() == lse.get_device() == ws.get_device():
+        _wrong_device(q, out, lse, ws)
+    st = _call(_WINDOW_PAGED, _pack_window_paged(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), strides and ctypes.addressof(strides), shape[0],
+        block_table.data_ptr(), max_blocks, page_size, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H, shape[1],
+        D, dt, scale, window, sinks, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_gqa_verify_attn_window_paged")
     return out, lse
 
 

@@ -1,6 +1,6 @@
-// Host side of mla_gqa_verify_attn and mla_gqa_verify_attn_paged: argument
-// checks, tensor maps and the two launches (attention, then the merge of the
-// units that the even split of the work has cut).
+// Host side of mla_gqa_verify_attn, mla_gqa_verify_attn_window and their paged
+// forms: argument checks, tensor maps and the two launches (attention, then the
+// merge of the units that the even split of the work has cut).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "gqa_attn.cuh"
+#include "gqa_variants.h"
 #include "internal.h"
 #include "mla_verify_attn.h"
 
@@ -64,7 +65,6 @@ Layout layout(const Plan& pl, int grid, int D) {
   return l;
 }
 
-using AttnFn = void (*)(CUtensorMap, CUtensorMap, Params);
 using CombineFn = void (*)(Params, int);
 
 struct Variant {
@@ -76,29 +76,30 @@ template <int D, bool kBf16>
 Variant variant() {
   constexpr size_t smem = sizeof(Smem<D>);
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
+  return {attn_kernel<D, kBf16, kWhole>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
           combine_many_units<D, kBf16, 3, 2>, smem};
 }
 
 std::mutex g_ready_mutex;
-bool g_ready[kMaxDevices][4];
+bool g_ready[kMaxDevices][2][4];
 
 // The kernels for these sizes, ready on the current device.
-int pick(int D, int dtype, Variant* out) {
+int pick(int D, int dtype, Mode mode, Variant* out) {
   static const Variant all[4] = {variant<64, true>(), variant<64, false>(), variant<128, true>(),
                                  variant<128, false>()};
   const int n = (D == 128 ? 2 : 0) + (dtype == MLA_FP16 ? 1 : 0);
   *out = all[n];
+  if (mode == kWindow) out->attn = window_kernel(D, dtype == MLA_BF16);
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED_DEVICE;
   std::lock_guard<std::mutex> lock(g_ready_mutex);
-  if (!g_ready[dev][n]) {
+  if (!g_ready[dev][mode][n]) {
     if (cudaFuncSetAttribute(out->attn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(out->smem)) !=
         cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_LAUNCH;
     }
-    g_ready[dev][n] = true;
+    g_ready[dev][mode][n] = true;
   }
   return MLA_OK;
 }
@@ -118,6 +119,8 @@ struct Call {
   const int32_t* table;   // paged
   int max_blocks, page;
   long long pool_rows;
+  Mode mode;
+  int window, sinks;
 };
 
 // Byte strides of one tensor from element strides (or contiguous ones); a
@@ -154,6 +157,7 @@ int encode(const DeviceCommon& d, CUtensorMap* map, const void* base, const Call
 
 int run(const Call& c) {
   if (!shape_ok(c.B, c.q_len, c.H, c.Hkv, c.D) || c.Smax < 1 || c.Smax >= (1 << 24)) return MLA_ERR_SHAPE;
+  if (c.mode == kWindow && (c.window < 1 || c.sinks < 0)) return MLA_ERR_SHAPE;
   if ((c.dtype != MLA_BF16 && c.dtype != MLA_FP16) || !std::isfinite(c.scale)) return MLA_ERR_ARG;
   const Plan pl = plan(c.q_len, c.H, c.Hkv);
   // The kernel counts the work, at most this, in 32 bits.
@@ -182,7 +186,7 @@ int run(const Call& c) {
   const Layout lay = layout(pl, grid, c.D);
   if (!c.workspace || c.workspace_bytes < lay.bytes) return MLA_ERR_WORKSPACE;
   Variant var;
-  st = pick(c.D, c.dtype, &var);
+  st = pick(c.D, c.dtype, c.mode, &var);
   if (st != MLA_OK) return st;
 
   // Rows a TMA box: whole 64-key tiles, or the largest power of two that no
@@ -245,7 +249,15 @@ int run(const Call& c) {
   const int rows_a_head = c.q_len * (c.H / c.Hkv);
   const long long units = static_cast<long long>(c.B) * c.Hkv * pl.groups;
   p.desc_units = units <= grid;
-  p.whole = c.Smax <= kWholeKeys;
+  long long most_tiles = (c.Smax + kKeys - 1) / kKeys;     // of a stream
+  if (c.mode == kWindow) {
+    const long long seen = (static_cast<long long>(c.sinks) + kKeys - 1) / kKeys +
+                           (static_cast<long long>(c.window) + c.q_len + 2 * kKeys - 2) / kKeys;
+    if (seen < most_tiles) most_tiles = seen;
+  }
+  p.whole = most_tiles <= kWholeKeys / kKeys;
+  p.window = c.window;
+  p.sinks = c.sinks;
   p.max_blocks = c.max_blocks;
   p.page = Divisor(paged ? c.page : 1);
   p.pool_pages = paged ? static_cast<int>(c.pool_rows / c.page) : 0;
@@ -313,9 +325,45 @@ int mla_gqa_verify_attn(const void* q, const void* k, const void* v, const int64
                         int Hkv, int D, int Smax, int dtype, float scale, void* out, float* lse,
                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   const mla::gqa::Call c = {q, k, v, strides, seq_lens, tree_mask, B, q_len, H, Hkv, D, Smax, dtype, scale,
-                            out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0};
+                            out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0, mla::gqa::kWhole, 0, 0};
   return mla::gqa::run(c);
 }
+
+int mla_gqa_verify_attn_window(const void* q, const void* k, const void* v, const int64_t* strides,
+                               const int32_t* seq_lens, const uint32_t* tree_mask, int B, int q_len, int H,
+                               int Hkv, int D, int Smax, int dtype, float scale, int window, int sinks,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+  const mla::gqa::Call c = {q, k, v, strides, seq_lens, tree_mask, B, q_len, H, Hkv, D, Smax, dtype, scale,
+                            out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0, mla::gqa::kWindow,
+                            window, sinks};
+  return mla::gqa::run(c);
+}
+
+}  // extern "C"
+
+namespace mla {
+namespace gqa {
+
+// What the paged calls check before the others.
+int run_paged(Call c, const int32_t* block_table, int max_blocks, int page_size, long long pool_rows) {
+  if (page_size < 1 || max_blocks < 1 || static_cast<long long>(max_blocks) * page_size >= (1ll << 24) ||
+      pool_rows < 1 || pool_rows % page_size != 0 || pool_rows >= (1ll << 31))
+    return MLA_ERR_SHAPE;
+  if (c.B > 0 && !block_table) return MLA_ERR_NULLPTR;
+  if (!aligned_to(block_table, 4)) return MLA_ERR_ALIGN;
+  c.table = block_table;
+  c.max_blocks = max_blocks;
+  c.page = page_size;
+  c.pool_rows = pool_rows;
+  c.Smax = max_blocks * page_size;
+  return run(c);
+}
+
+}  // namespace gqa
+}  // namespace mla
+
+extern "C" {
 
 int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_pool,
                               const int64_t* strides, long long pool_rows, const int32_t* block_table,
@@ -323,15 +371,21 @@ int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_p
                               const uint32_t* tree_mask, int B, int q_len, int H, int Hkv, int D,
                               int dtype, float scale, void* out, float* lse, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
-  if (page_size < 1 || max_blocks < 1 || static_cast<long long>(max_blocks) * page_size >= (1ll << 24) ||
-      pool_rows < 1 || pool_rows % page_size != 0 || pool_rows >= (1ll << 31))
-    return MLA_ERR_SHAPE;
-  if (B > 0 && !block_table) return MLA_ERR_NULLPTR;
-  if (!mla::aligned_to(block_table, 4)) return MLA_ERR_ALIGN;
-  const mla::gqa::Call c = {q, k_pool, v_pool, strides, seq_lens, tree_mask, B, q_len, H, Hkv, D,
-                            max_blocks * page_size, dtype, scale, out, lse, workspace, workspace_bytes, stream,
-                            block_table, max_blocks, page_size, pool_rows};
-  return mla::gqa::run(c);
+  const mla::gqa::Call c = {q, k_pool, v_pool, strides, seq_lens, tree_mask, B, q_len, H, Hkv, D, 0, dtype, scale,
+                            out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0, mla::gqa::kWhole, 0, 0};
+  return mla::gqa::run_paged(c, block_table, max_blocks, page_size, pool_rows);
+}
+
+int mla_gqa_verify_attn_window_paged(const void* q, const void* k_pool, const void* v_pool,
+                                     const int64_t* strides, long long pool_rows, const int32_t* block_table,
+                                     int max_blocks, int page_size, const int32_t* seq_lens,
+                                     const uint32_t* tree_mask, int B, int q_len, int H, int Hkv, int D,
+                                     int dtype, float scale, int window, int sinks, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const mla::gqa::Call c = {q, k_pool, v_pool, strides, seq_lens, tree_mask, B, q_len, H, Hkv, D, 0, dtype, scale,
+                            out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0, mla::gqa::kWindow,
+                            window, sinks};
+  return mla::gqa::run_paged(c, block_table, max_blocks, page_size, pool_rows);
 }
 
 }  // extern "C"

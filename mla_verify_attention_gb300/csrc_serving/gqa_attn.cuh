@@ -65,6 +65,10 @@ constexpr int kMinTiles = 2;
 constexpr float kLazy = 8.0f;              // log2 units a row's max may grow before O is rescaled
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// What the kernel attends over: a stream's whole cache, or its first keys and a
+// sliding window (see Window below).
+enum Mode { kWhole, kWindow };
+
 struct Params {
   const uint8_t* q;
   const uint8_t* k;
@@ -89,6 +93,7 @@ struct Params {
   int box_rows;                    // rows a TMA box: 64 or a divisor that no page boundary cuts; 0: gather
   int test_stall;
   float scale_log2;
+  int window, sinks;               // kWindow
 };
 
 template <int D>
@@ -259,10 +264,29 @@ __device__ __forceinline__ bool wait2(S& sm, uint64_t& bar0, uint32_t parity0, u
 
 // ------------------------------------------------------------ work
 
-// Key tiles of stream b; 0 for an unused stream and for one whose length is out of range.
+// With a window a draft sees the last `window` of the keys that its mask shows
+// it, and those in the first `sinks` rows of the cache.  Prefix keys from `sinks`
+// to `start` = prefix - window are seen by no draft, whatever its mask; whole
+// tiles of them are skipped: of the stream's tiles, `first` lie before the gap.
+// (A draft whose mask shows n drafts sees the prefix from prefix - window + n:
+// the n - 1 keys or fewer between are left to the mask.)
+struct Window {
+  int start, first, gap;
+  __device__ __forceinline__ Window(const Params& p, int S) {
+    start = max(0, S - p.q_len - p.window);
+    first = (min(p.sinks, start) + kKeys - 1) / kKeys;
+    gap = max(0, start / kKeys - first);
+  }
+};
+
+// Key tiles of stream b that are read; 0 for an unused stream and for one whose length is out of range.
+template <Mode kMode>
 __device__ __forceinline__ int stream_tiles(const Params& p, int b, int& S) {
   S = p.seq_lens[b];
-  return S < p.q_len || S > p.Smax ? 0 : (S + kKeys - 1) / kKeys;
+  if (S < p.q_len || S > p.Smax) return 0;
+  const int nt = (S + kKeys - 1) / kKeys;
+  if constexpr (kMode == kWindow) return nt - Window(p, S).gap;
+  return nt;
 }
 
 // Its work a unit: tiles, or with p.whole the unit itself.
@@ -271,6 +295,14 @@ __device__ __forceinline__ int stream_work(const Params& p, int nt) { return p.w
 // A CTA's part of one unit.
 struct Segment {
   int b, S, head, group, tile0, n, nt;   // tiles tile0 .. tile0 + n - 1 of the unit's nt
+  int start, first, gap;                 // kWindow
+  // First key of the segment's tile j.
+  template <Mode kMode>
+  __device__ __forceinline__ int key(int j) const {
+    int t = tile0 + j;
+    if constexpr (kMode == kWindow) t += t < first ? 0 : gap;
+    return t * kKeys;
+  }
 };
 
 // The teams' runs of a total of work: equal, the first `more` one longer.
@@ -296,6 +328,7 @@ struct Runs {
 // the same tiles at the same time, so that the caches come from HBM once (one
 // after the other, 1,024 rows a head over 8k keys read them four times at 5.2
 // TB/s) and in whole rows.  A group that does not exist is skipped.
+template <Mode kMode>
 struct Walk {
   int t, t1, pre;                          // pre: work before stream b
   int b, S, nt, head0, group0;
@@ -303,14 +336,14 @@ struct Walk {
       : t(t0), t1(t1_), pre(pre0), b(b0), S(0), nt(0) {
     head0 = p.by_group_members.of(member);
     group0 = member - head0 * p.group_members;
-    if (t < t1) nt = stream_tiles(p, b, S);
+    if (t < t1) nt = stream_tiles<kMode>(p, b, S);
   }
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
     const int units = p.head_sets * p.group_sets;
     while (t < t1) {
       while (t >= pre + stream_work(p, nt) * units) {
         pre += stream_work(p, nt) * units;
-        nt = stream_tiles(p, ++b, S);
+        nt = stream_tiles<kMode>(p, ++b, S);
       }
       const int local = t - pre, work = stream_work(p, nt);
       const int u = local < work ? 0 : local / work;
@@ -318,6 +351,12 @@ struct Walk {
       s.b = b;
       s.S = S;
       s.nt = nt;
+      if constexpr (kMode == kWindow) {
+        const Window w(p, S);
+        s.start = w.start;
+        s.first = w.first;
+        s.gap = w.gap;
+      }
       s.tile0 = local - u * work;
       s.head = head_set * p.head_members + head0;
       s.group = (u - head_set * p.group_sets) * p.group_members + group0;
@@ -339,6 +378,13 @@ __device__ __forceinline__ int rows_of_group(const Params& p, int group) {
 __device__ __forceinline__ uint64_t visible(uint64_t mask64, int np) {
   if (np > 0) return ((1ull << np) - 1ull) | mask64 << np;
   return -np < 64 ? mask64 >> (-np) : 0ull;
+}
+
+// Of keys k0 .. k0 + 63, those from row `from` of the cache to row `to`.
+__device__ __forceinline__ uint64_t between(int k0, int from, int to) {
+  const int lo = max(from - k0, 0), hi = min(to - k0, kKeys);
+  if (lo >= hi) return 0ull;
+  return (~0ull >> (kKeys - (hi - lo))) << lo;
 }
 
 // The drafts of stream b that any of its drafts sees, by a whole converged warp;
@@ -390,8 +436,9 @@ struct Ring {
 // Warps 0 (K) and 2 (V): tiles by TMA.  A tile is one box of 64 rows, or boxes
 // of box_rows rows and 64 dims when pages are shorter than a tile.  (One warp
 // for both took longer to issue a tile's copies than the memory to deliver them.)
-template <int D>
-__device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUtensorMap* map, Walk w, bool is_v) {
+// With a window, boxes without a key that a draft may see are left out.
+template <int D, Mode kMode>
+__device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUtensorMap* map, Walk<kMode> w, bool is_v) {
   using C = Shape<D>;
   const int lane = threadIdx.x & 31;
   uint64_t* const full = is_v ? sm.vfull : sm.kfull;
@@ -406,13 +453,24 @@ __device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUt
   Segment s;
   while (w.next(p, s)) {
     const int end = min(s.S, (s.tile0 + s.n) * kKeys);
-    auto key_of = [&](int j) { return (s.tile0 + j) * kKeys + lane * R; };
-    auto entry_of = [&](int j) { return paged && key_of(j) < end ? table_entry(p, s.b, key_of(j)) : 0; };
+    auto key_of = [&](int j) {
+      if constexpr (kMode == kWindow) return s.template key<kMode>(j + (lane >> (6 - shift))) + (lane & (boxes - 1)) * R;
+      return (s.tile0 + j) * kKeys + lane * R;
+    };
+    auto wanted = [&](int j) {
+      const int key = key_of(j);
+      if constexpr (kMode == kWindow)
+        return j + (lane >> (6 - shift)) < s.n && key < s.S && (key < p.sinks || key + R > s.start);
+      return key < end;
+    };
+    auto entry_of = [&](int j) { return paged && wanted(j) ? table_entry(p, s.b, key_of(j)) : 0; };
     const int batch = paged ? 0 : s.b;
     int row = 0, entry = entry_of(0), first = 0;           // `first`: lane of the tile's first box
+    uint32_t wanted_lanes = 0;                             // (kWindow)
     for (int j = 0; j < s.n; ++j, at.advance(), first = (first + boxes) & 31) {
       if (first == 0) {
-        row = !paged ? key_of(j) : (key_of(j) < end ? pool_row(p, entry, key_of(j)) : 0);
+        row = !paged ? key_of(j) : (wanted(j) ? pool_row(p, entry, key_of(j)) : 0);
+        if constexpr (kMode == kWindow) wanted_lanes = __ballot_sync(0xFFFFFFFFu, wanted(j));
         entry = entry_of(j + batch_tiles);
       }
       if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
@@ -422,9 +480,12 @@ __device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUt
         arrive_expect_elect(bar, C::kTile);
         tma_box_elect(dst, map, __shfl_sync(0xFFFFFFFFu, row, first), 0, s.head, batch, bar);
       } else {
-        const int n = min(boxes, (s.S - (s.tile0 + j) * kKeys + R - 1) >> shift);  // boxes with keys of the stream
-        arrive_expect_elect(bar, n * R * D * 2);
+        int n = min(boxes, (s.S - s.template key<kMode>(j) + R - 1) >> shift);     // boxes with keys of the stream
+        int left_out = 0;
+        if constexpr (kMode == kWindow) left_out = n - __popc(wanted_lanes >> first & ((1u << n) - 1u));
+        arrive_expect_elect(bar, (n - left_out) * R * D * 2);
         for (int i = 0; i < n; ++i) {
+          if (kMode == kWindow && !(wanted_lanes >> (first + i) & 1u)) continue;
           const int r = __shfl_sync(0xFFFFFFFFu, row, first + i);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
@@ -444,8 +505,8 @@ out:
 // multiple of 8): rows copied 16 bytes a lane, into the layout the boxes would
 // leave; rows past the stream are zeros.  A lane looks up the pages of two rows
 // of the next tile while it copies this one.
-template <int D>
-__device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk w, bool is_v) {
+template <int D, Mode kMode>
+__device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk<kMode> w, bool is_v) {
   using C = Shape<D>;
   constexpr int kUnits = D / 8;                // 16-byte units a row
   constexpr int kPer = 32 / kUnits;            // rows a warp copies at once
@@ -468,15 +529,19 @@ __device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk w
   };
   Segment s;
   while (w.next(p, s)) {
-    auto key_of = [&](int j, int half) { return (s.tile0 + j) * kKeys + half * 32 + lane; };
-    auto entry_of = [&](int j, int half) {
-      return j < s.n && key_of(j, half) < s.S ? table_entry(p, s.b, key_of(j, half)) : 0;
+    auto key_of = [&](int j, int half) { return s.template key<kMode>(j) + half * 32 + lane; };
+    auto wanted = [&](int key) {
+      if constexpr (kMode == kWindow) return key < s.S && (key < p.sinks || key >= s.start);
+      return key < s.S;
     };
-    auto row_of = [&](int j, int half, int entry) {        // -1 past the stream
-      return key_of(j, half) < s.S ? pool_row(p, entry, key_of(j, half)) : -1;
+    auto entry_of = [&](int j, int half) {
+      return j < s.n && wanted(key_of(j, half)) ? table_entry(p, s.b, key_of(j, half)) : 0;
+    };
+    auto row_of = [&](int j, int half, int entry) {        // -1 past the stream, or in the gap
+      return wanted(key_of(j, half)) ? pool_row(p, entry, key_of(j, half)) : -1;
     };
     auto prefetch = [&](int j) {               // the table's entries for tile j, soon to be looked up
-      const int key = (s.tile0 + j) * kKeys + lane * 2;
+      const int key = s.template key<kMode>(j) + lane * 2;
       if (j < s.n && key < s.S)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table + static_cast<size_t>(s.b) * p.max_blocks +
                                                       p.page.of(key)));
@@ -523,7 +588,7 @@ out:
 // gained nothing.)
 
 // Warp 1: S of every tile.
-template <int D, bool kBf16>
+template <int D, bool kBf16, Mode kMode>
 struct ProductsQk {
   using C = Shape<D>;
   static constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
@@ -548,7 +613,7 @@ struct ProductsQk {
     return true;
   }
 
-  __device__ __forceinline__ void run(Walk w) {
+  __device__ __forceinline__ void run(Walk<kMode> w) {
     int seg = 0;
     Segment s;
     while (w.next(p, s)) {
@@ -563,7 +628,7 @@ struct ProductsQk {
 };
 
 // Warp 3: O += P V of every tile.
-template <int D, bool kBf16>
+template <int D, bool kBf16, Mode kMode>
 struct ProductsPv {
   using C = Shape<D>;
   static constexpr uint32_t kId = idesc<kBf16>(D, 1);
@@ -588,7 +653,7 @@ struct ProductsPv {
     return true;
   }
 
-  __device__ __forceinline__ void run(Walk w) {
+  __device__ __forceinline__ void run(Walk<kMode> w) {
     int seg = 0;
     Segment s;
     while (w.next(p, s)) {
@@ -659,8 +724,8 @@ __device__ __forceinline__ void finish_q(Smem<D>& sm, int lane) {
 }
 
 // Warps 4..11: group g = 0, 1, warp wq of the group, one row a thread.
-template <int D, bool kBf16>
-__device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t tmem, Walk w, int g, int wq,
+template <int D, bool kBf16, Mode kMode>
+__device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t tmem, Walk<kMode> w, int g, int wq,
                                         int lane) {
   using C = Shape<D>;
   // fp16 weights are kept 2^7 larger: the largest, 2^(8 + 7), is in range and
@@ -704,11 +769,23 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
       if (p.q_len < 64) mask64 &= (1ull << p.q_len) - 1ull;
     }
     const int prefix = s.S - p.q_len;
+    // With a window: prefix keys from `sinks` to `hide` are hidden from this row,
+    // and of more drafts than the window holds the first ones that are no sinks.
+    int hide = 0, hide_most = 0;
+    if constexpr (kMode == kWindow) {
+      const int n_seen = __popcll(mask64);
+      hide = prefix - min(prefix, max(0, p.window - n_seen));
+      hide_most = prefix - min(prefix, max(0, p.window - p.q_len));
+      uint64_t last = mask64;
+      for (int x = n_seen; x > p.window; --x) last &= last - 1ull;
+      mask64 = last | (mask64 & between(prefix, 0, p.sinks));
+    }
     float m = -CUDART_INF_F, l = 0.f;
     for (int j = g; j < s.n; j += 2, ++n) {
       const int buf = n & 1;
       const uint32_t s_t = tmem + lanes + 256 + (2 * g + buf) * kKeys;
-      const int k0 = (s.tile0 + j) * kKeys;
+      const int k0 = s.template key<kMode>(j);
+      const bool edge = kMode == kWindow && k0 < hide_most && k0 + kKeys > p.sinks;   // some row's window starts here
       if (!wait(sm, sm.sfull[g][buf], (n >> 1) & 1, p)) return;
       if (warp_valid) {
         tc_fence_after();
@@ -720,8 +797,9 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
 #pragma unroll
           for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a);
         }
-        if (k0 + kKeys > prefix) {
-          const uint64_t vis = visible(mask64, prefix - k0);
+        if (k0 + kKeys > prefix || edge) {
+          uint64_t vis = kMode == kWindow && k0 + kKeys <= prefix ? ~0ull : visible(mask64, prefix - k0);
+          if constexpr (kMode == kWindow) vis &= ~between(k0, p.sinks, hide);
           const uint32_t lo = static_cast<uint32_t>(vis), hi = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -773,10 +851,11 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
         tmem_st_wait();
         tc_fence_before();
       }
-      if (k0 + kKeys > prefix) {
-        // Rows past the stream, and drafts that none sees (a batch padded to one
-        // q_len), may hold anything: P is 0 there, but 0 * NaN is not.
-        const uint64_t used = visible(seen_drafts(p, s.b, word, lane), prefix - k0);
+      if (k0 + kKeys > prefix || (kMode == kWindow && k0 < s.start && k0 + kKeys > p.sinks)) {
+        // Rows past the stream, drafts that none sees (a batch padded to one q_len)
+        // and keys in the gap may hold anything: P is 0 there, but 0 * NaN is not.
+        uint64_t used = k0 + kKeys > prefix ? visible(seen_drafts(p, s.b, word, lane), prefix - k0) : ~0ull;
+        if constexpr (kMode == kWindow) used &= ~between(k0, p.sinks, s.start);
         const uint32_t lo = static_cast<uint32_t>(used), hi = static_cast<uint32_t>(used >> 32);
         if ((lo & hi) != ~0u) {
           const int stage = (kt + j) % C::kStages;
@@ -909,7 +988,8 @@ __device__ __forceinline__ void drain_products(uint64_t& bar) {
 // business (0).  With p.desc_units there is an entry a unit, else one a CTA, for
 // the only unit that can be cut, its last.  Written before the first wait, so
 // that the merge finds it whatever becomes of the loads.
-__device__ __forceinline__ void note_cut_units(const Params& p, Walk w, const Runs& runs) {
+template <Mode kMode>
+__device__ __forceinline__ void note_cut_units(const Params& p, Walk<kMode> w, const Runs& runs) {
   const int cta = static_cast<int>(blockIdx.x);
   int4 d = make_int4(0, 0, 0, 0);
   Segment s;
@@ -925,7 +1005,7 @@ __device__ __forceinline__ void note_cut_units(const Params& p, Walk w, const Ru
   if (!p.desc_units) p.desc[cta] = d;
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
   using S = Smem<D>;
@@ -996,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Every warp by itself, a stream a lane.
     int work = 0;
     if (lane < p.B) {
-      work = stream_work(p, stream_tiles(p, lane, len)) * units;
+      work = stream_work(p, stream_tiles<kMode>(p, lane, len)) * units;
       if (blockIdx.x == 0 && warp == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
     }
     int inc = work;
@@ -1023,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool off = false;                  // (reported after the loop: an atomic in it would hold up the next loads)
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-      sum += stream_work(p, stream_tiles(p, b, len)) * units;
+      sum += stream_work(p, stream_tiles<kMode>(p, b, len)) * units;
       off |= len != 0 && (len < p.q_len || len > p.Smax);
     }
     if (off && blockIdx.x == 0) atomicOr(p.status, kBitSeqLen);
@@ -1050,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (t0 >= before && t0 < before + sum) {
       int b = b0;
       while (true) {
-        const int n = stream_work(p, stream_tiles(p, b, len)) * units;
+        const int n = stream_work(p, stream_tiles<kMode>(p, b, len)) * units;
         if (t0 < before + n) break;
         before += n;
         ++b;
@@ -1067,25 +1147,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   const Runs runs(p, total, all);
   const int t0 = team < runs.teams ? runs.start(team) : total;
-  const Walk walk(p, member, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
+  const Walk<kMode> walk(p, member, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
 
   if (warp == 0 || warp == 2) {
-    if (p.box_rows == 0) load_gather<D>(sm, p, walk, warp == 2);
-    else load_tma<D>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
+    if (p.box_rows == 0) load_gather<D, kMode>(sm, p, walk, warp == 2);
+    else load_tma<D, kMode>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
   } else if (warp == 1) {
-    ProductsQk<D, kBf16>(sm, p, tmem).run(walk);
+    ProductsQk<D, kBf16, kMode>(sm, p, tmem).run(walk);
     drain_products(sm.drain[0]);
   } else if (warp == 3) {
     if (lane == 0 && !p.whole) note_cut_units(p, walk, runs);
     __syncwarp();
-    ProductsPv<D, kBf16>(sm, p, tmem).run(walk);
+    ProductsPv<D, kBf16, kMode>(sm, p, tmem).run(walk);
     drain_products(sm.drain[1]);
   } else if (warp >= 4) {
-    softmax<D, kBf16>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
+    softmax<D, kBf16, kMode>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
   }
   // Streams without keys.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (stream_tiles(p, b, len) != 0) continue;
+    if (stream_tiles<kMode>(p, b, len) != 0) continue;
     if (p.desc_units && !p.whole)
       for (int u = tid; u < p.Hkv * p.groups; u += kThreads) p.desc[b * p.Hkv * p.groups + u] = make_int4(0, 0, 0, 0);
     const long long rows = static_cast<long long>(p.q_len) * p.H;

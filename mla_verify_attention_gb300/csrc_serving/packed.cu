@@ -49,6 +49,8 @@ extern "C" int mla_call_packed(int which, const int64_t* args) {
     case MLA_CALL_CACHE_KEEP: return call(mla_cache_keep, args);
     case MLA_CALL_GQA_VERIFY_ATTN: return call(mla_gqa_verify_attn, args);
     case MLA_CALL_GQA_VERIFY_ATTN_PAGED: return call(mla_gqa_verify_attn_paged, args);
+    case MLA_CALL_GQA_VERIFY_ATTN_WINDOW: return call(mla_gqa_verify_attn_window, args);
+    case MLA_CALL_GQA_VERIFY_ATTN_WINDOW_PAGED: return call(mla_gqa_verify_attn_window_paged, args);
     default: return MLA_ERR_ARG;
   }
 }
