@@ -468,6 +468,84 @@ int mla_gqa_verify_attn_window_paged(const void* q, const void* k_pool, const vo
                                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * A cache of Hkv heads x D values in 4 bits.  A pool row is
+ *   Hkv * D / 2 bytes of codes (E2M1; heads in order, dimension 2 i in the low
+ *     half of a head's byte i),
+ *   Hkv * D / 16 bytes of steps (E4M3), one for every 16 values of a head,
+ *   padding up to a multiple of 16 bytes, never read or written,
+ * mla_gqa_fp4_row_bytes in all (0 for sizes that are not supported: D is 64 or
+ * 128, Hkv <= MLA_FP4_MAX_HEADS), and stands for the values
+ *   E2M1(code) * E4M3(step) * factor
+ * with one factor for all rows of a pool, a positive number between 2^-64 and
+ * 2^64 (MLA_ERR_ARG).  Rows move like any other: mla_cache_keep and
+ * mla_cache_compact take them as bytes.
+ */
+#define MLA_FP4_MAX_HEADS 4096
+size_t mla_gqa_fp4_row_bytes(int Hkv, int D);
+
+/*
+ * mla_cache_append into such pools: for every t with slots[t] >= 0 row slots[t] of
+ * k_pool and v_pool takes k[t] and v[t], of type `dtype`.  For each 16 values x
+ *   step = the E4M3 nearest to min(448, max|x| / (6 factor)),
+ *   code = the E2M1 nearest to x / (step factor)   (both ties to even; 0 where the step is 0);
+ * a group with a NaN gets a NaN step.
+ *   k, v            T rows [Hkv, D] at k_stride / v_stride bytes; 16-byte aligned, as all
+ *                   rows and strides here; apart from the pools.
+ *   k_held, v_held  NULL, or T rows [Hkv, D] of type `dtype` that take the values that
+ *                   the pools now hold for each token (rounded to `dtype`; rows of skipped
+ *                   tokens stay as they are): a prompt that attends to itself then
+ *                   sees what later tokens will.
+ * Slots as for mla_cache_append.  0 <= T < 2^30.
+ */
+int mla_gqa_cache_append_fp4(const void* k, long long k_stride, const void* v, long long v_stride, int Hkv, int D,
+                             int dtype, float k_factor, float v_factor, void* k_pool, long long k_pool_stride,
+                             void* v_pool, long long v_pool_stride, long long pool_rows, const int32_t* slots, int T,
+                             void* k_held, long long k_held_stride, void* v_held, long long v_held_stride,
+                             cudaStream_t stream);
+
+/*
+ * Which keys of each stream stay, by the weight that they got.  A stream of S =
+ * seq_lens[b] > budget keys keeps its first `sinks`, its last `recent`, and of the
+ * keys between those with the largest totals, to `budget` in all; of equal totals
+ * the first.  The total of key t is the fp32 sum of weights[b][h][t] over the heads
+ * h, in order (NaN counts as the largest).  A stream of at most `budget` keys
+ * keeps them all.
+ *   weights    [B, Hkv, Smax] fp32; only t < seq_lens[b] is read.
+ *   kept       [B, budget] int32, out: the kept positions in order, -1 behind them.
+ *   keep_lens  [B] int32, out: min(seq_lens[b], budget), as mla_blocks_trim takes it.
+ *   workspace  mla_evict_workspace_size(B, Smax) bytes, 4-byte aligned (NULL where that
+ *              is 0, as up to 393,216 keys); contents do not matter.
+ *   0 <= B < 2^20, 1 <= Smax < 2^24, 1 <= Hkv <= 65536, sinks, recent >= 0 and
+ *   sinks + recent <= budget (MLA_ERR_SHAPE).
+ * A seq_lens[b] outside [0, Smax] records MLA_ERR_SEQLEN and keeps nothing.
+ */
+size_t mla_evict_workspace_size(int B, int Smax);
+
+int mla_evict_select(const float* weights, const int32_t* seq_lens, int B, int Hkv, int Smax, int sinks, int recent,
+                     int32_t* kept, int budget, int32_t* keep_lens, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
+/*
+ * The rows that stay move together, in place: row j of stream b takes the value
+ * that row kept[b][j] had before the call, for every j < keep_lens[b]; what is left
+ * behind them keeps no particular value.  seq_lens stays as it is: mla_blocks_trim to keep_lens follows.
+ *   pool_a, pool_b, block_table, max_blocks, page_size  as for mla_cache_keep.
+ *   weights    NULL, or [B, Hkv, max_blocks * page_size] fp32 that move along; entries
+ *              from keep_lens[b] up to seq_lens[b] become 0.
+ *   kept       [B, budget] int32, increasing in each stream, as mla_evict_select leaves it.
+ *   keep_lens  [B] int32 in [0, min(seq_lens[b], budget)]
+ * An entry of kept below its own place or not below seq_lens[b] records
+ * MLA_ERR_SLOT and its row stays; entries in another order leave rows with
+ * undefined contents.  A count or length out of range (MLA_ERR_SLOT,
+ * MLA_ERR_SEQLEN) leaves the stream as it was; a row whose page lies outside the pool
+ * (MLA_ERR_PAGE) is not moved.  No page may belong to two streams.
+ */
+int mla_cache_compact(void* pool_a, long long pool_a_stride, int a_bytes, void* pool_b, long long pool_b_stride,
+                      int b_bytes, long long pool_rows, float* weights, int Hkv, const int32_t* block_table,
+                      int max_blocks, int page_size, const int32_t* seq_lens, const int32_t* kept, int budget,
+                      const int32_t* keep_lens, int B, cudaStream_t stream);
+
+/*
  * The calls of the two sections above with their arguments in one array of 64-bit values,
  * in the order of their declarations: integers and addresses as such, a float
  * as the bits of a double.  For bindings to which each argument costs more than
@@ -483,7 +561,10 @@ enum mla_packed {
   MLA_CALL_GQA_VERIFY_ATTN_PAGED = 5,
   /* 6 and 7 are not calls */
   MLA_CALL_GQA_VERIFY_ATTN_WINDOW = 8,
-  MLA_CALL_GQA_VERIFY_ATTN_WINDOW_PAGED = 9
+  MLA_CALL_GQA_VERIFY_ATTN_WINDOW_PAGED = 9,
+  MLA_CALL_GQA_CACHE_APPEND_FP4 = 10,
+  MLA_CALL_EVICT_SELECT = 11,
+  MLA_CALL_CACHE_COMPACT = 12
 };
 int mla_call_packed(int call, const int64_t* args);
 

@@ -27,7 +27,8 @@ EXPORTED = ("mla_verify_attn", "mla_verify_attn_workspace_size", "mla_verify_att
             "mla_verify_attn_set_two_term_max_keys", "mla_blocks_extend", "mla_blocks_trim",
             "mla_cache_append", "mla_cache_keep", "mla_gqa_workspace_size", "mla_gqa_verify_attn",
             "mla_gqa_verify_attn_paged", "mla_call_packed", "mla_gqa_verify_attn_window",
-            "mla_gqa_verify_attn_window_paged")
+            "mla_gqa_verify_attn_window_paged", "mla_gqa_fp4_row_bytes", "mla_gqa_cache_append_fp4",
+            "mla_evict_workspace_size", "mla_evict_select", "mla_cache_compact")
 
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +93,16 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.mla_gqa_verify_attn_window_paged.argtypes = [P, P, P, P, L, P, I, I, P, P, I, I, I, I, I, I, F, I, I,
                                                          P, P, P, Z, P]
         lib.mla_gqa_verify_attn_window_paged.restype = I
+        lib.mla_gqa_fp4_row_bytes.argtypes = [I, I]
+        lib.mla_gqa_fp4_row_bytes.restype = Z
+        lib.mla_gqa_cache_append_fp4.argtypes = [P, L, P, L, I, I, I, F, F, P, L, P, L, L, P, I, P, L, P, L, P]
+        lib.mla_gqa_cache_append_fp4.restype = I
+        lib.mla_evict_workspace_size.argtypes = [I, I]
+        lib.mla_evict_workspace_size.restype = Z
+        lib.mla_evict_select.argtypes = [P, P, I, I, I, I, I, P, I, P, P, Z, P]
+        lib.mla_evict_select.restype = I
+        lib.mla_cache_compact.argtypes = [P, L, I, P, L, I, L, P, I, P, I, I, P, P, I, P, I, P]
+        lib.mla_cache_compact.restype = I
         lib.mla_call_packed.argtypes = [I, ctypes.c_char_p]
         lib.mla_call_packed.restype = I
         _lib = lib

@@ -20,7 +20,7 @@ LATENT, ROPE, ROW = 512, 64, 576
 # array (ctypes takes 1.3 us to convert sixteen of them, 0.4 us for this), and
 # what is looked up once is bound by the first call.
 _EXTEND, _TRIM, _APPEND, _KEEP, _GQA, _GQA_PAGED = range(6)
-_WINDOW, _WINDOW_PAGED = range(8, 10)
+_WINDOW, _WINDOW_PAGED, _APPEND_FP4, _SELECT, _COMPACT = range(8, 13)
 _pack_extend = struct.Struct("=13q").pack
 _pack_trim = struct.Struct("=10q").pack
 _pack_append = struct.Struct("=14q").pack
@@ -29,16 +29,19 @@ _pack_gqa = struct.Struct("=13qd5q").pack
 _pack_paged = struct.Struct("=16qd5q").pack
 _pack_window = struct.Struct("=13qd7q").pack
 _pack_window_paged = struct.Struct("=16qd7q").pack
+_pack_append_fp4 = struct.Struct("=7q2d12q").pack
+_pack_select = struct.Struct("=13q").pack
+_pack_compact = struct.Struct("=18q").pack
 
 _torch = _call = None
-_current_device = _current_stream = _int32 = _bf16 = _fp16 = _fp32 = None
+_current_device = _current_stream = _int32 = _bf16 = _fp16 = _fp32 = _uint8 = None
 
 
 def _bind():
-    global _torch, _call, _current_device, _current_stream, _int32, _bf16, _fp16, _fp32
+    global _torch, _call, _current_device, _current_stream, _int32, _bf16, _fp16, _fp32, _uint8
     import torch
     _torch, _int32 = torch, torch.int32
-    _bf16, _fp16, _fp32 = torch.bfloat16, torch.float16, torch.float32
+    _bf16, _fp16, _fp32, _uint8 = torch.bfloat16, torch.float16, torch.float32, torch.uint8
     if hasattr(torch._C, "_cuda_getDevice"):
         _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     else:                                        # a torch without CUDA: no tensor gets past the device check
@@ -429,3 +432,198 @@ def gqa_cache_keep(k_pool, v_pool, block_table, page_size, seq_lens, path, keep,
         max_blocks, page_size, seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_keep")
+
+
+# ---------------------------------------------------------------- a cache in 4 bits
+
+_row_bytes = {}
+
+
+def gqa_fp4_row_bytes(Hkv: int, D: int) -> int:
+    """Bytes of a pool row that holds Hkv heads of D = 64 or 128 values in 4 bits (0: not supported)."""
+    n = _row_bytes.get((Hkv, D))
+    if n is None:
+        n = _row_bytes[Hkv, D] = int(load_library().mla_gqa_fp4_row_bytes(Hkv, D))
+    return n
+
+
+def _byte_rows(name, t, width):
+    """Byte stride of uint8 rows [rows, width] whose bytes are contiguous."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is not _uint8 or len(shape) != 2 or shape[1] != width or st[1] != 1:
+        raise ValueError("%s must be uint8 [rows,%d] with contiguous rows" % (name, width))
+    return st[0] if shape[0] > 1 else width
+
+
+def _byte_pools(k_pool, v_pool):
+    if k_pool.dim() != 2 or v_pool.shape != k_pool.shape:
+        raise ValueError("expected k_pool and v_pool uint8 [rows,bytes]")
+    rows, width = k_pool.shape
+    return rows, width, _byte_rows("k_pool", k_pool, width), _byte_rows("v_pool", v_pool, width)
+
+
+def gqa_cache_append_fp4(k_pool, v_pool, k, v, slots, k_scale=1.0, v_scale=1.0, k_held=None, v_held=None, stream=None):
+    """Key and value rows by slot into pools held in 4 bits: uint8
+    [rows, gqa_fp4_row_bytes(Hkv, D)], k and v [T,Hkv,D] bf16 or fp16 (column
+    ranges of wider rows, too).
+
+    Every 16 values share a step; k_scale and v_scale are the pools' own factors
+    (a value is code * step * factor; steps reach from 2^-9 to 448).  With k_held,
+    v_held [T,Hkv,D] of k's type, those take the values that the pools now hold.
+    """
+    if _call is None:
+        _bind()
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("expected k and v [T,Hkv,D]")
+    T, heads, width = k.shape
+    dt = k.dtype
+    if dt is not _bf16 and dt is not _fp16:
+        raise ValueError("k and v must be bfloat16 or float16")
+    rows, n_bytes, kp_stride, vp_stride = _byte_pools(k_pool, v_pool)
+    if n_bytes != gqa_fp4_row_bytes(heads, width):
+        raise ValueError("k_pool and v_pool must be uint8 [rows,%d]" % gqa_fp4_row_bytes(heads, width))
+    a_stride, b_stride = _head_rows("k", k, dt, heads, width), _head_rows("v", v, dt, heads, width)
+    _ints("slots", slots, T)
+    kh = vh = kh_stride = vh_stride = 0
+    dev = k_pool.get_device()
+    for name, t in (("k_held", k_held), ("v_held", v_held)):
+        if t is None:
+            continue
+        if t.shape != k.shape:
+            raise ValueError("%s must have k's shape" % name)
+        st = _head_rows(name, t, dt, heads, width)
+        if t.get_device() != dev:
+            _wrong_device(k_pool, t)
+        if t is k_held:
+            kh, kh_stride = t.data_ptr(), st
+        if t is v_held:
+            vh, vh_stride = t.data_ptr(), st
+    if not (_on_current(dev) and dev == v_pool.get_device() == k.get_device() == v.get_device() == slots.get_device()):
+        _wrong_device(k_pool, v_pool, k, v, slots)
+    st = _call(_APPEND_FP4, _pack_append_fp4(
+        k.data_ptr(), a_stride, v.data_ptr(), b_stride, heads, width, 0 if dt is _bf16 else 1, k_scale, v_scale,
+        k_pool.data_ptr(), kp_stride, v_pool.data_ptr(), vp_stride, rows, slots.data_ptr(), T, kh, kh_stride, vh,
+        vh_stride, _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_gqa_cache_append_fp4")
+
+
+def gqa_cache_keep_fp4(k_pool, v_pool, block_table, page_size, seq_lens, path, keep, stream=None):
+    """gqa_cache_keep for pools held in 4 bits, uint8 [rows,bytes]."""
+    if _call is None:
+        _bind()
+    rows, n, k_stride, v_stride = _byte_pools(k_pool, v_pool)
+    B, q_len, max_blocks = _keep_tables(block_table, seq_lens, path, keep)
+    dev = k_pool.get_device()
+    if not (_on_current(dev) and dev == v_pool.get_device() == block_table.get_device() == seq_lens.get_device()
+            == path.get_device() == keep.get_device()):
+        _wrong_device(k_pool, v_pool, block_table, seq_lens, path, keep)
+    st = _call(_KEEP, _pack_keep(
+        k_pool.data_ptr(), k_stride, n, v_pool.data_ptr(), v_stride, n, rows, block_table.data_ptr(),
+        max_blocks, page_size, seq_lens.data_ptr(), path.data_ptr(), keep.data_ptr(), B, q_len, _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_cache_keep")
+
+
+# ---------------------------------------------------------------- eviction
+
+def evict_workspace_size(B: int, Smax: int) -> int:
+    """Workspace bytes of evict_select (0 for streams of up to 393,216 keys)."""
+    return int(load_library().mla_evict_workspace_size(B, Smax))
+
+
+def evict_select(weights, seq_lens, sinks, recent, kept, keep_lens, workspace=None, stream=None):
+    """Which keys of each stream stay: the first ``sinks``, the last ``recent`` and,
+    to kept.shape[1] in all, those between with the largest sums of weights over
+    the heads (of equal ones the first).
+
+    weights [B,Hkv,Smax] fp32 as ``gqa_attn_weights`` adds them up, seq_lens [B].
+    Writes kept [B,budget] (positions in order, -1 behind them) and keep_lens [B],
+    both int32: ``gqa_cache_compact`` and ``blocks_trim`` to keep_lens follow.
+    """
+    if _call is None:
+        _bind()
+    if weights.dim() != 3 or weights.dtype is not _fp32 or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous float32 [B,Hkv,Smax]")
+    B, heads, Smax = weights.shape
+    budget = kept.shape[-1]
+    _ints("seq_lens", seq_lens, B)
+    _ints("kept", kept, B, budget)
+    _ints("keep_lens", keep_lens, B)
+    dev = weights.get_device()
+    if not (_on_current(dev) and dev == seq_lens.get_device() == kept.get_device() == keep_lens.get_device()):
+        _wrong_device(weights, seq_lens, kept, keep_lens)
+    at = size = 0
+    if workspace is None and Smax > 49152:           # (shorter streams need none)
+        n = evict_workspace_size(B, Smax)
+        workspace = _empty(n, _uint8, weights, stream, result=False) if n else None
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if workspace.get_device() != dev:
+            _wrong_device(weights, workspace)
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _call(_SELECT, _pack_select(
+        weights.data_ptr(), seq_lens.data_ptr(), B, heads, Smax, sinks, recent, kept.data_ptr(), budget,
+        keep_lens.data_ptr(), at, size, _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_evict_select")
+
+
+def _compact(pool_a, a_stride, a_bytes, pool_b, b_stride, b_bytes, rows, weights, block_table, page_size, seq_lens, kept,
+             keep_lens, stream):
+    if block_table.dim() != 2 or kept.dim() != 2:
+        raise ValueError("expected block_table [B,max_blocks] and kept [B,budget]")
+    B, max_blocks = block_table.shape
+    budget = kept.shape[1]
+    _ints("block_table", block_table, B, max_blocks)
+    _ints("seq_lens", seq_lens, B)
+    _ints("kept", kept, B, budget)
+    _ints("keep_lens", keep_lens, B)
+    w = heads = 0
+    dev = pool_a.get_device()
+    if not (_on_current(dev) and dev == pool_b.get_device() == block_table.get_device() == seq_lens.get_device()
+            == kept.get_device() == keep_lens.get_device()):
+        _wrong_device(pool_a, pool_b, block_table, seq_lens, kept, keep_lens)
+    if weights is not None:
+        heads = weights.shape[1] if weights.dim() == 3 else 0
+        if (weights.dtype is not _fp32 or weights.shape != (B, heads, max_blocks * page_size)
+                or not weights.is_contiguous()):
+            raise ValueError("weights must be contiguous float32 [B,Hkv,max_blocks * page_size]")
+        if weights.get_device() != dev:
+            _wrong_device(pool_a, weights)
+        w = weights.data_ptr()
+    st = _call(_COMPACT, _pack_compact(
+        pool_a.data_ptr(), a_stride, a_bytes, pool_b.data_ptr() if b_bytes else 0, b_stride, b_bytes, rows, w, heads,
+        block_table.data_ptr(), max_blocks, page_size, seq_lens.data_ptr(), kept.data_ptr(), budget,
+        keep_lens.data_ptr(), B, _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_cache_compact")
+
+
+def gqa_cache_compact(k_pool, v_pool, block_table, page_size, seq_lens, kept, keep_lens, weights=None, stream=None):
+    """Moves the rows that stay together, in place: row j of stream b takes what row
+    kept[b,j] held, for j < keep_lens[b] (both as ``evict_select`` leaves them).
+
+    Pools [rows,Hkv,D] bf16 or fp16, or uint8 [rows,bytes] held in 4 bits; weights
+    [B,Hkv,max_blocks * page_size] move along, with zeros behind.  seq_lens stays
+    as it is (``blocks_trim`` to keep_lens follows).
+    """
+    if _call is None:
+        _bind()
+    if k_pool.dtype is _uint8:
+        rows, n, k_stride, v_stride = _byte_pools(k_pool, v_pool)
+    else:
+        _, rows, heads, width, k_stride, v_stride = _pools(k_pool, v_pool)
+        n = 2 * heads * width
+    _compact(k_pool, k_stride, n, v_pool, v_stride, n, rows, weights, block_table, page_size, seq_lens, kept, keep_lens,
+             stream)
+
+
+def cache_compact(kv_pool, block_table, page_size, seq_lens, kept, keep_lens, weights=None, stream=None):
+    """gqa_cache_compact for a latent pool [rows,576] bf16."""
+    if _call is None:
+        _bind()
+    stride = _rows("kv_pool", kv_pool, ROW)
+    _compact(kv_pool, stride, 2 * ROW, kv_pool, 0, 0, kv_pool.shape[0], weights, block_table, page_size, seq_lens, kept,
+             keep_lens, stream)

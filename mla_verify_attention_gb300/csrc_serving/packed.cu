@@ -51,6 +51,9 @@ extern "C" int mla_call_packed(int which, const int64_t* args) {
     case MLA_CALL_GQA_VERIFY_ATTN_PAGED: return call(mla_gqa_verify_attn_paged, args);
     case MLA_CALL_GQA_VERIFY_ATTN_WINDOW: return call(mla_gqa_verify_attn_window, args);
     case MLA_CALL_GQA_VERIFY_ATTN_WINDOW_PAGED: return call(mla_gqa_verify_attn_window_paged, args);
+    case MLA_CALL_GQA_CACHE_APPEND_FP4: return call(mla_gqa_cache_append_fp4, args);
+    case MLA_CALL_EVICT_SELECT: return call(mla_evict_select, args);
+    case MLA_CALL_CACHE_COMPACT: return call(mla_cache_compact, args);
     default: return MLA_ERR_ARG;
   }
 }

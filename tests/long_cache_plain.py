@@ -92,3 +92,66 @@ def rows_of(table_row, page, n):
     """Pool rows of a stream's first n keys."""
     t = torch.arange(n)
     return (table_row.cpu().long()[t // page] * page + t % page).clamp_min(0)
+
+
+# ---------------------------------------------------------------- rows in 4 bits
+
+LEVELS = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def e4m3_values():
+    """The 8-bit type's values by code, 0 .. 126, in 64 bits."""
+    return torch.tensor([(c & 7) * 2.0 ** -9 if c < 8 else (8 + (c & 7)) * 2.0 ** ((c >> 3) - 10) for c in range(127)],
+                        dtype=torch.float64)
+
+
+def nearest_even(x, values):
+    """Index of the nearest of rising values, of two as near the even index; beyond the last, the last."""
+    mid = (values[1:] + values[:-1]) / 2
+    lo = torch.searchsorted(mid, x.contiguous())                 # mids below x: x on a mid goes down
+    on = (lo < len(mid)) & (x == mid[lo.clamp(max=len(mid) - 1)])
+    return torch.where(on & (lo % 2 == 1), lo + 1, lo)
+
+
+def pack_fp4(x, factor):
+    """Rows x [T,Hkv,D] (CPU) as pool rows [T,bytes] without their padding."""
+    T, Hkv, D = x.shape
+    g = x.double().view(T, Hkv, D // 16, 16)
+    f32 = lambda v: torch.tensor(v, dtype=torch.float32).double()
+    top = g.abs().amax(-1)
+    # The definition's quotients are fp32 ones.
+    step = nearest_even((top.float() / f32(6 * factor).float()).double(), e4m3_values())
+    step = torch.where(top.isnan(), 127, step)
+    d = (torch.cat([e4m3_values(), torch.tensor([float("nan")]).double()])[step].float() * f32(factor).float())[..., None]
+    q = torch.where(d > 0, g.float() / d, torch.zeros(())).double().nan_to_num(nan=0.0)
+    code = nearest_even(q.abs(), torch.tensor(LEVELS, dtype=torch.float64)) | (torch.signbit(q).long() << 3)
+    code = code.view(T, Hkv * D // 2, 2)
+    return torch.cat([code[..., 0] | code[..., 1] << 4, step.view(T, -1)], 1).to(torch.uint8)
+
+
+def unpack_fp4(rows, Hkv, D, factor):
+    """The values [...,Hkv,D] of pool rows (CPU), in 64 bits (their products fp32's, as the factor is)."""
+    level = torch.tensor(LEVELS + [-x for x in LEVELS], dtype=torch.float64)
+    step = torch.cat([e4m3_values(), torch.tensor([float("nan")]).double()])
+    step = torch.cat([step, -step])
+    n = Hkv * D // 2
+    code = rows[..., :n].long()
+    code = torch.stack([code & 15, code >> 4], -1).view(*rows.shape[:-1], Hkv, D // 16, 16)
+    s = step[rows[..., n:n + Hkv * D // 16].long()].view(*rows.shape[:-1], Hkv, D // 16, 1)
+    return (level[code] * s * factor).view(*rows.shape[:-1], Hkv, D)
+
+
+# ---------------------------------------------------------------- eviction
+
+def select(weights, S, sinks, recent, budget):
+    """Kept positions of one stream: weights [Hkv,>=S] fp32 (CPU), summed in order."""
+    if S <= budget:
+        return list(range(S))
+    total = weights[0, :S].clone()
+    for h in range(1, weights.shape[0]):
+        total += weights[h, :S]
+    total = total.tolist()
+    key = [(-float("inf") if x != x else -x, t) for t, x in enumerate(total)]
+    nan_first = [(0 if total[t] != total[t] else 1, *key[t]) for t in range(sinks, S - recent)]
+    chosen = [k[2] for k in sorted(nan_first)[:budget - sinks - recent]]
+    return sorted(list(range(sinks)) + chosen + list(range(S - recent, S)))
