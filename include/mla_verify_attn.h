@@ -504,6 +504,31 @@ int mla_gqa_cache_append_fp4(const void* k, long long k_stride, const void* v, l
                              cudaStream_t stream);
 
 /*
+ * The attention weight that each key got from a verify (or decoding) step, added
+ * to what is there: for key head g of stream b and every key t < seq_lens[b]
+ *   weights[b][g][t] += sum exp(s - lse[b,i,h])
+ * over the drafts i that see t by their mask and the query heads h of g, s the
+ * score as in mla_gqa_verify_attn.  With the lse of that call over the same keys a
+ * row's weights add up to 1.
+ *   q, k, strides (q's three and k's three), seq_lens, tree_mask, the sizes, the
+ *              types, the paged form and the errors as for mla_gqa_verify_attn
+ *              (streams of another length than q_len .. Smax get nothing).
+ *   lse        [B, q_len, H] fp32.  A row with lse +inf or -inf adds nothing, whatever
+ *              its q holds: +inf leaves out drafts that were not accepted, or padding.
+ *   weights    [B, Hkv, Smax] fp32 (Smax = max_blocks * page_size), in and out; entries
+ *              from seq_lens[b] on are neither read nor written.
+ * Scores, exponentials and sums are fp32; deterministic.  No workspace.
+ */
+int mla_gqa_attn_weights(const void* q, const void* k, const int64_t* strides, const int32_t* seq_lens,
+                         const uint32_t* tree_mask, const float* lse, int B, int q_len, int H, int Hkv, int D, int Smax,
+                         int dtype, float scale, float* weights, cudaStream_t stream);
+
+int mla_gqa_attn_weights_paged(const void* q, const void* k_pool, const int64_t* strides, long long pool_rows,
+                               const int32_t* block_table, int max_blocks, int page_size, const int32_t* seq_lens,
+                               const uint32_t* tree_mask, const float* lse, int B, int q_len, int H, int Hkv, int D,
+                               int dtype, float scale, float* weights, cudaStream_t stream);
+
+/*
  * Which keys of each stream stay, by the weight that they got.  A stream of S =
  * seq_lens[b] > budget keys keeps its first `sinks`, its last `recent`, and of the
  * keys between those with the largest totals, to `budget` in all; of equal totals
@@ -564,7 +589,9 @@ enum mla_packed {
   MLA_CALL_GQA_VERIFY_ATTN_WINDOW_PAGED = 9,
   MLA_CALL_GQA_CACHE_APPEND_FP4 = 10,
   MLA_CALL_EVICT_SELECT = 11,
-  MLA_CALL_CACHE_COMPACT = 12
+  MLA_CALL_CACHE_COMPACT = 12,
+  MLA_CALL_GQA_ATTN_WEIGHTS = 13,
+  MLA_CALL_GQA_ATTN_WEIGHTS_PAGED = 14
 };
 int mla_call_packed(int call, const int64_t* args);
 

@@ -20,7 +20,7 @@ LATENT, ROPE, ROW = 512, 64, 576
 # array (ctypes takes 1.3 us to convert sixteen of them, 0.4 us for this), and
 # what is looked up once is bound by the first call.
 _EXTEND, _TRIM, _APPEND, _KEEP, _GQA, _GQA_PAGED = range(6)
-_WINDOW, _WINDOW_PAGED, _APPEND_FP4, _SELECT, _COMPACT = range(8, 13)
+_WINDOW, _WINDOW_PAGED, _APPEND_FP4, _SELECT, _COMPACT, _WEIGHTS, _WEIGHTS_PAGED = range(8, 15)
 _pack_extend = struct.Struct("=13q").pack
 _pack_trim = struct.Struct("=10q").pack
 _pack_append = struct.Struct("=14q").pack
@@ -32,6 +32,8 @@ _pack_window_paged = struct.Struct("=16qd7q").pack
 _pack_append_fp4 = struct.Struct("=7q2d12q").pack
 _pack_select = struct.Struct("=13q").pack
 _pack_compact = struct.Struct("=18q").pack
+_pack_weights = struct.Struct("=13qd2q").pack
+_pack_weights_paged = struct.Struct("=16qd2q").pack
 
 _torch = _call = None
 _current_device = _current_stream = _int32 = _bf16 = _fp16 = _fp32 = _uint8 = None
@@ -530,6 +532,79 @@ def gqa_cache_keep_fp4(k_pool, v_pool, block_table, page_size, seq_lens, path, k
 def evict_workspace_size(B: int, Smax: int) -> int:
     """Workspace bytes of evict_select (0 for streams of up to 393,216 keys)."""
     return int(load_library().mla_evict_workspace_size(B, Smax))
+
+
+def _weights(q, k, seq_lens, tree_mask, lse, weights, Hkv, Smax):
+    B, q_len, H, D = q.shape
+    dt = q.dtype
+    if k.dtype is not dt or (dt is not _bf16 and dt is not _fp16):
+        raise ValueError("q and k must have one type, bfloat16 or float16")
+    _ints("seq_lens", seq_lens, B)
+    if (tree_mask.element_size() != 4 or tree_mask.shape != (B, q_len, (q_len + 31) >> 5)
+            or not tree_mask.is_contiguous() or tree_mask.is_floating_point()):
+        raise ValueError("tree_mask must be contiguous 32-bit words [B,q,ceil(q/32)]")
+    if lse.dtype is not _fp32 or lse.shape != (B, q_len, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B,q,H]")
+    if weights.dtype is not _fp32 or weights.shape != (B, Hkv, Smax) or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous float32 [B,Hkv,%d]" % Smax)
+    strides = 0
+    if not (q.is_contiguous() and k.is_contiguous()):
+        qs, ks = q.stride(), k.stride()
+        if qs[3] != 1 or ks[-1] != 1:
+            raise ValueError("the innermost dimension of q and k must be contiguous")
+        if len(ks) == 3:            # pools: no batch dimension
+            ks = (8,) + ks
+        strides = _STRIDES(*qs[:3], *ks[:3], 0, 0, 0)
+    return B, q_len, H, D, 0 if dt is _bf16 else 1, strides
+
+
+def gqa_attn_weights(q, k, seq_lens, tree_mask, lse, scale, weights, stream=None):
+    """Adds the attention weight that each cached key got, in place: weights[b,g,t]
+    += sum of exp(score - lse) over the drafts that see key t and the query heads of
+    key head g.
+
+    q, k, seq_lens and tree_mask as for ``gqa_verify_attn``, lse [B,q,H] as it
+    returns it (rows with lse +inf or -inf add nothing: +inf leaves out drafts
+    that were not accepted), weights [B,Hkv,Smax] fp32.
+    """
+    if _call is None:
+        _bind()
+    shape = k.shape
+    if q.dim() != 4 or len(shape) != 4 or shape[0] != q.shape[0] or shape[3] != q.shape[3]:
+        raise ValueError("expected q [B,q,H,D], k [B,Smax,Hkv,D]")
+    dev = q.get_device()
+    if not (_on_current(dev) and dev == k.get_device() == seq_lens.get_device() == tree_mask.get_device()
+            == lse.get_device() == weights.get_device()):
+        _wrong_device(q, k, seq_lens, tree_mask, lse, weights)
+    B, q_len, H, D, dt, strides = _weights(q, k, seq_lens, tree_mask, lse, weights, shape[2], shape[1])
+    st = _call(_WEIGHTS, _pack_weights(
+        q.data_ptr(), k.data_ptr(), strides and ctypes.addressof(strides), seq_lens.data_ptr(), tree_mask.data_ptr(),
+        lse.data_ptr(), B, q_len, H, shape[2], D, shape[1], dt, scale, weights.data_ptr(), _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_gqa_attn_weights")
+
+
+def gqa_attn_weights_paged(q, k_pool, block_table, page_size, seq_lens, tree_mask, lse, scale, weights, stream=None):
+    """gqa_attn_weights over a pool k_pool [pool_rows,Hkv,D] of pages of page_size >= 1
+    rows, block_table [B,max_blocks] int32, weights [B,Hkv,max_blocks * page_size]."""
+    if _call is None:
+        _bind()
+    shape = k_pool.shape
+    if q.dim() != 4 or len(shape) != 3 or shape[2] != q.shape[3] or block_table.dim() != 2:
+        raise ValueError("expected q [B,q,H,D], k_pool [rows,Hkv,D], block_table [B,max_blocks]")
+    max_blocks = block_table.shape[1]
+    _ints("block_table", block_table, q.shape[0], max_blocks)
+    dev = q.get_device()
+    if not (_on_current(dev) and dev == k_pool.get_device() == seq_lens.get_device() == tree_mask.get_device()
+            == block_table.get_device() == lse.get_device() == weights.get_device()):
+        _wrong_device(q, k_pool, seq_lens, tree_mask, block_table, lse, weights)
+    B, q_len, H, D, dt, strides = _weights(q, k_pool, seq_lens, tree_mask, lse, weights, shape[1], max_blocks * page_size)
+    st = _call(_WEIGHTS_PAGED, _pack_weights_paged(
+        q.data_ptr(), k_pool.data_ptr(), strides and ctypes.addressof(strides), shape[0], block_table.data_ptr(),
+        max_blocks, page_size, seq_lens.data_ptr(), tree_mask.data_ptr(), lse.data_ptr(), B, q_len, H, shape[1], D, dt,
+        scale, weights.data_ptr(), _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_gqa_attn_weights_paged")
 
 
 def evict_select(weights, seq_lens, sinks, recent, kept, keep_lens, workspace=None, stream=None):

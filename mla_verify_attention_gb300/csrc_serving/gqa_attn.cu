@@ -10,7 +10,7 @@
 #include <mutex>
 
 #include "gqa_attn.cuh"
-#include "gqa_variants.h"
+#include "gqa_host.h"
 #include "internal.h"
 #include "mla_verify_attn.h"
 
@@ -104,25 +104,6 @@ int pick(int D, int dtype, Mode mode, Variant* out) {
   return MLA_OK;
 }
 
-struct Call {
-  const void *q, *k, *v;
-  const int64_t* strides;
-  const int32_t* seq_lens;
-  const uint32_t* mask;
-  int B, q_len, H, Hkv, D, Smax, dtype;
-  float scale;
-  void* out;
-  float* lse;
-  void* workspace;
-  size_t workspace_bytes;
-  cudaStream_t stream;
-  const int32_t* table;   // paged
-  int max_blocks, page;
-  long long pool_rows;
-  Mode mode;
-  int window, sinks;
-};
-
 // Byte strides of one tensor from element strides (or contiguous ones); a
 // dimension of size 1 gets the contiguous stride.
 int byte_strides(const int64_t* given, const long long* sizes, int D, long long* out) {
@@ -139,14 +120,34 @@ int byte_strides(const int64_t* given, const long long* sizes, int D, long long*
   return MLA_OK;
 }
 
+// Rows a TMA box: whole 64-key tiles, or the largest power of two that no
+// page boundary cuts, down to the 8 rows of a swizzle group; other page
+// sizes are gathered row by row (0).
+int box_rows(const Call& c) {
+  if (c.table == nullptr) return kKeys;
+  const int low = c.page & -c.page;
+  return low >= kKeys ? kKeys : (low >= 8 ? low : 0);
+}
+
+// Heads side by side where a row of the cache holds them all: the most that
+// leave fewer than 3 % of the CTAs without a team.
+int heads_side_by_side(const long long* stride, int Hkv, int group_members, int grid) {
+  int heads = 1;
+  if (stride[2] < stride[1])
+    for (int h = 2; h <= Hkv && h * group_members <= grid; ++h) {
+      const int team = h * group_members;
+      if (Hkv % h == 0 && 100 * (grid % team) < 3 * grid) heads = h;
+    }
+  return heads;
+}
+
 int encode(const DeviceCommon& d, CUtensorMap* map, const void* base, const Call& c, const long long* stride,
-           long long rows, int batches, int box_rows, CUtensorMapL2promotion promotion) {
+           long long rows, int batches, int box_rows, int box_chunks, CUtensorMapL2promotion promotion) {
   const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(c.D / 64),
                               static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(batches)};
   const cuuint64_t strides[4] = {static_cast<cuuint64_t>(stride[1]), 128, static_cast<cuuint64_t>(stride[2]),
                                  static_cast<cuuint64_t>(stride[0])};
-  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows),
-                             static_cast<cuuint32_t>(box_rows == kKeys ? c.D / 64 : 1), 1, 1};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks), 1, 1};
   const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
   const CUresult r =
       d.encode(map, c.dtype == MLA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
@@ -189,24 +190,10 @@ int run(const Call& c) {
   st = pick(c.D, c.dtype, c.mode, &var);
   if (st != MLA_OK) return st;
 
-  // Rows a TMA box: whole 64-key tiles, or the largest power of two that no
-  // page boundary cuts, down to the 8 rows of a swizzle group; other page
-  // sizes are gathered row by row.
-  int box = kKeys;
-  if (paged) {
-    const int low = c.page & -c.page;
-    box = low >= kKeys ? kKeys : (low >= 8 ? low : 0);
-  }
+  const int box = box_rows(c);
   p.group_sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
   p.group_members = (pl.groups + p.group_sets - 1) / p.group_sets;
-  // Heads side by side where a row of the cache holds them all: the most that
-  // leave fewer than 3 % of the CTAs without a team.
-  int heads = 1;
-  if (p.k_stride[2] < p.k_stride[1])
-    for (int h = 2; h <= c.Hkv && h * p.group_members <= grid; ++h) {
-      const int team = h * p.group_members;
-      if (c.Hkv % h == 0 && 100 * (grid % team) < 3 * grid) heads = h;
-    }
+  const int heads = heads_side_by_side(p.k_stride, c.Hkv, p.group_members, grid);
   p.members = heads * p.group_members;
   p.head_members = heads;
   p.head_sets = c.Hkv / heads;
@@ -221,8 +208,8 @@ int run(const Call& c) {
   const CUtensorMapL2promotion promotion =
       fetch_256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   CUtensorMap map_k = {}, map_v = {};
-  if (box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box, promotion) != MLA_OK ||
-                   encode(d, &map_v, c.v, c, p.v_stride, rows, batches, box, promotion) != MLA_OK))
+  if (box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box, box == kKeys ? c.D / 64 : 1, promotion) != MLA_OK ||
+                   encode(d, &map_v, c.v, c, p.v_stride, rows, batches, box, box == kKeys ? c.D / 64 : 1, promotion) != MLA_OK))
     return MLA_ERR_LAUNCH;
 
   uint8_t* const ws = static_cast<uint8_t*>(c.workspace);

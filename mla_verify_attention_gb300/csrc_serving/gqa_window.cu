@@ -1,6 +1,6 @@
 // The attention kernel with a sliding window and first tokens that stay visible.
 #include "gqa_attn.cuh"
-#include "gqa_variants.h"
+#include "gqa_host.h"
 
 namespace mla {
 namespace gqa {

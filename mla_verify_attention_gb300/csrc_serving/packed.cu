@@ -54,6 +54,8 @@ extern "C" int mla_call_packed(int which, const int64_t* args) {
     case MLA_CALL_GQA_CACHE_APPEND_FP4: return call(mla_gqa_cache_append_fp4, args);
     case MLA_CALL_EVICT_SELECT: return call(mla_evict_select, args);
     case MLA_CALL_CACHE_COMPACT: return call(mla_cache_compact, args);
+    case MLA_CALL_GQA_ATTN_WEIGHTS: return call(mla_gqa_attn_weights, args);
+    case MLA_CALL_GQA_ATTN_WEIGHTS_PAGED: return call(mla_gqa_attn_weights_paged, args);
     default: return MLA_ERR_ARG;
   }
 }
