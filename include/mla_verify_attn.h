@@ -504,6 +504,29 @@ int mla_gqa_cache_append_fp4(const void* k, long long k_stride, const void* v, l
                              cudaStream_t stream);
 
 /*
+ * mla_gqa_verify_attn_paged over such pools: the formula with the values that the
+ * rows stand for as k and v.
+ *   q, out, q_strides  of type `dtype`; q_strides NULL or q's three element strides.
+ *   k_pool, v_pool     [pool_rows] rows at k_pool_stride / v_pool_stride bytes (multiples of
+ *                      16 of at least mla_gqa_fp4_row_bytes(Hkv, D)); 16-byte aligned.
+ *   k_factor, v_factor the pools' factors; scale * k_factor finite (MLA_ERR_ARG).
+ *   workspace          mla_gqa_fp4_workspace_size(B, q_len, H, Hkv, D) bytes.
+ * A contiguous cache [B, Smax] is a pool of one page of Smax rows a stream.  All
+ * other arguments, results and errors as for mla_gqa_verify_attn_paged (a step of
+ * NaN is a row that is not finite).  A row of q enters the products in fp16,
+ * brought to its range by a power of two: values below 2^-28 of the row's largest
+ * lose digits.  The weights are fp16, too.
+ */
+size_t mla_gqa_fp4_workspace_size(int B, int q_len, int H, int Hkv, int D);
+
+int mla_gqa_verify_attn_fp4_paged(const void* q, const int64_t* q_strides, const void* k_pool, long long k_pool_stride,
+                                  const void* v_pool, long long v_pool_stride, long long pool_rows,
+                                  const int32_t* block_table, int max_blocks, int page_size, const int32_t* seq_lens,
+                                  const uint32_t* tree_mask, int B, int q_len, int H, int Hkv, int D, int dtype,
+                                  float scale, float k_factor, float v_factor, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * The attention weight that each key got from a verify (or decoding) step, added
  * to what is there: for key head g of stream b and every key t < seq_lens[b]
  *   weights[b][g][t] += sum exp(s - lse[b,i,h])
@@ -591,7 +614,8 @@ enum mla_packed {
   MLA_CALL_EVICT_SELECT = 11,
   MLA_CALL_CACHE_COMPACT = 12,
   MLA_CALL_GQA_ATTN_WEIGHTS = 13,
-  MLA_CALL_GQA_ATTN_WEIGHTS_PAGED = 14
+  MLA_CALL_GQA_ATTN_WEIGHTS_PAGED = 14,
+  MLA_CALL_GQA_VERIFY_ATTN_FP4_PAGED = 15
 };
 int mla_call_packed(int call, const int64_t* args);
 

@@ -11,16 +11,18 @@ from ._lib import (TWO_TERM_MAX_KEYS_DEFAULT, MLAError, forced, last_device_erro
                    paged_workspace_size, plan, set_timing_events, set_two_term_max_keys, strerror,
                    verify_attn, verify_attn_paged, verify_attn_raw, workspace_size)
 from ._serving import (blocks_extend, blocks_trim, cache_append, cache_compact, cache_keep, evict_select,
-                       evict_workspace_size, gqa_attn_weights, gqa_attn_weights_paged, gqa_cache_append, gqa_cache_append_fp4, gqa_cache_compact, gqa_cache_keep,
-                       gqa_cache_keep_fp4, gqa_fp4_row_bytes, gqa_verify_attn, gqa_verify_attn_paged, gqa_verify_attn_window,
-                       gqa_verify_attn_window_paged, gqa_workspace_size)
+                       evict_workspace_size, gqa_attn_weights, gqa_attn_weights_paged, gqa_cache_append,
+                       gqa_cache_append_fp4, gqa_cache_compact, gqa_cache_keep, gqa_cache_keep_fp4,
+                       gqa_fp4_row_bytes, gqa_fp4_workspace_size, gqa_verify_attn, gqa_verify_attn_fp4_paged,
+                       gqa_verify_attn_paged, gqa_verify_attn_window, gqa_verify_attn_window_paged,
+                       gqa_workspace_size)
 from ._build import build
 
-__all__ = ["TWO_TERM_MAX_KEYS_DEFAULT", "MLAError", "blocks_extend", "blocks_trim", "build", "cache_append",
+__all__ = ["MLAError", "TWO_TERM_MAX_KEYS_DEFAULT", "blocks_extend", "blocks_trim", "build", "cache_append",
            "cache_compact", "cache_keep", "evict_select", "evict_workspace_size", "forced", "gqa_attn_weights",
-           "gqa_attn_weights_paged", "gqa_cache_append",
-           "gqa_cache_append_fp4", "gqa_cache_compact", "gqa_cache_keep", "gqa_cache_keep_fp4", "gqa_fp4_row_bytes",
-           "gqa_verify_attn",
-           "gqa_verify_attn_paged", "gqa_verify_attn_window", "gqa_verify_attn_window_paged", "gqa_workspace_size", "last_device_error", "load_library",
-           "paged_workspace_size", "plan", "set_timing_events", "set_two_term_max_keys", "strerror",
-           "verify_attn", "verify_attn_paged", "verify_attn_raw", "workspace_size"]
+           "gqa_attn_weights_paged", "gqa_cache_append", "gqa_cache_append_fp4", "gqa_cache_compact",
+           "gqa_cache_keep", "gqa_cache_keep_fp4", "gqa_fp4_row_bytes", "gqa_fp4_workspace_size", "gqa_verify_attn",
+           "gqa_verify_attn_fp4_paged", "gqa_verify_attn_paged", "gqa_verify_attn_window",
+           "gqa_verify_attn_window_paged", "gqa_workspace_size", "last_device_error", "load_library",
+           "paged_workspace_size", "plan", "set_timing_events", "set_two_term_max_keys", "strerror", "verify_attn",
+           "verify_attn_paged", "verify_attn_raw", "workspace_size"]

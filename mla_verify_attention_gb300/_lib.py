@@ -29,7 +29,8 @@ EXPORTED = ("mla_verify_attn", "mla_verify_attn_workspace_size", "mla_verify_att
             "mla_gqa_verify_attn_paged", "mla_call_packed", "mla_gqa_verify_attn_window",
             "mla_gqa_verify_attn_window_paged", "mla_gqa_fp4_row_bytes", "mla_gqa_cache_append_fp4",
             "mla_evict_workspace_size", "mla_evict_select", "mla_cache_compact",
-            "mla_gqa_attn_weights", "mla_gqa_attn_weights_paged")
+            "mla_gqa_attn_weights", "mla_gqa_attn_weights_paged", "mla_gqa_fp4_workspace_size",
+            "mla_gqa_verify_attn_fp4_paged")
 
 _lock = threading.Lock()
 _lib = None
@@ -108,6 +109,11 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.mla_gqa_attn_weights.restype = I
         lib.mla_gqa_attn_weights_paged.argtypes = [P, P, P, L, P, I, I, P, P, P, I, I, I, I, I, I, F, P, P]
         lib.mla_gqa_attn_weights_paged.restype = I
+        lib.mla_gqa_fp4_workspace_size.argtypes = [I, I, I, I, I]
+        lib.mla_gqa_fp4_workspace_size.restype = Z
+        lib.mla_gqa_verify_attn_fp4_paged.argtypes = [P, P, P, L, P, L, L, P, I, I, P, P, I, I, I, I, I, I, F, F, F, P, P,
+                                                      P, Z, P]
+        lib.mla_gqa_verify_attn_fp4_paged.restype = I
         lib.mla_call_packed.argtypes = [I, ctypes.c_char_p]
         lib.mla_call_packed.restype = I
         _lib = lib

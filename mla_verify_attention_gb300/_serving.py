@@ -20,7 +20,7 @@ LATENT, ROPE, ROW = 512, 64, 576
 # array (ctypes takes 1.3 us to convert sixteen of them, 0.4 us for this), and
 # what is looked up once is bound by the first call.
 _EXTEND, _TRIM, _APPEND, _KEEP, _GQA, _GQA_PAGED = range(6)
-_WINDOW, _WINDOW_PAGED, _APPEND_FP4, _SELECT, _COMPACT, _WEIGHTS, _WEIGHTS_PAGED = range(8, 15)
+_WINDOW, _WINDOW_PAGED, _APPEND_FP4, _SELECT, _COMPACT, _WEIGHTS, _WEIGHTS_PAGED, _FP4_PAGED = range(8, 16)
 _pack_extend = struct.Struct("=13q").pack
 _pack_trim = struct.Struct("=10q").pack
 _pack_append = struct.Struct("=14q").pack
@@ -30,6 +30,7 @@ _pack_paged = struct.Struct("=16qd5q").pack
 _pack_window = struct.Struct("=13qd7q").pack
 _pack_window_paged = struct.Struct("=16qd7q").pack
 _pack_append_fp4 = struct.Struct("=7q2d12q").pack
+_pack_fp4_paged = struct.Struct("=18q3d5q").pack
 _pack_select = struct.Struct("=13q").pack
 _pack_compact = struct.Struct("=18q").pack
 _pack_weights = struct.Struct("=13qd2q").pack
@@ -508,6 +509,67 @@ def gqa_cache_append_fp4(k_pool, v_pool, k, v, slots, k_scale=1.0, v_scale=1.0, 
         vh_stride, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_cache_append_fp4")
+
+
+def gqa_fp4_workspace_size(B: int, q_len: int, H: int, Hkv: int, D: int) -> int:
+    """Workspace bytes of gqa_verify_attn_fp4_paged on the current device."""
+    return int(load_library().mla_gqa_fp4_workspace_size(B, q_len, H, Hkv, D))
+
+
+def gqa_verify_attn_fp4_paged(q, k_pool, v_pool, kv_heads, block_table, page_size, seq_lens, tree_mask, scale,
+                              k_scale=1.0, v_scale=1.0, out=None, lse=None, workspace=None, stream=None):
+    """gqa_verify_attn_paged over pools held in 4 bits, uint8
+    [pool_rows, gqa_fp4_row_bytes(kv_heads, D)] as ``gqa_cache_append_fp4`` fills them
+    with the same k_scale and v_scale; q [B,q,H,D] bf16 or fp16."""
+    if _call is None:
+        _bind()
+    if q.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("expected q [B,q,H,D], block_table [B,max_blocks]")
+    B, q_len, H, D = q.shape
+    dt = q.dtype
+    if dt is not _bf16 and dt is not _fp16:
+        raise ValueError("q must be bfloat16 or float16")
+    rows, width, k_stride, v_stride = _byte_pools(k_pool, v_pool)
+    if width != gqa_fp4_row_bytes(kv_heads, D):
+        raise ValueError("k_pool and v_pool must be uint8 [rows,%d]" % gqa_fp4_row_bytes(kv_heads, D))
+    max_blocks = block_table.shape[1]
+    _ints("block_table", block_table, B, max_blocks)
+    _ints("seq_lens", seq_lens, B)
+    if (tree_mask.element_size() != 4 or tree_mask.shape != (B, q_len, (q_len + 31) >> 5)
+            or not tree_mask.is_contiguous() or tree_mask.is_floating_point()):
+        raise ValueError("tree_mask must be contiguous 32-bit words [B,q,ceil(q/32)]")
+    dev = q.get_device()
+    if not (_on_current(dev) and dev == k_pool.get_device() == v_pool.get_device() == seq_lens.get_device()
+            == tree_mask.get_device() == block_table.get_device()):
+        _wrong_device(q, k_pool, v_pool, seq_lens, tree_mask, block_table)
+    strides = 0
+    if not q.is_contiguous():
+        qs = q.stride()
+        if qs[3] != 1:
+            raise ValueError("the innermost dimension of q must be contiguous")
+        strides = _STRIDES(*qs[:3], 0, 0, 0, 0, 0, 0)
+    if out is None:
+        out = _empty((B, q_len, H, D), dt, q, stream)
+    elif out.dtype is not dt or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is None:
+        lse = _empty((B, q_len, H), _fp32, q, stream)
+    elif lse.dtype is not _fp32 or lse.shape != (B, q_len, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B,q,H]")
+    if workspace is None:
+        workspace = _empty(gqa_fp4_workspace_size(B, q_len, H, kv_heads, D), _uint8, q, stream, result=False)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if not dev == out.get_device() == lse.get_device() == workspace.get_device():
+        _wrong_device(q, out, lse, workspace)
+    st = _call(_FP4_PAGED, _pack_fp4_paged(
+        q.data_ptr(), strides and ctypes.addressof(strides), k_pool.data_ptr(), k_stride, v_pool.data_ptr(), v_stride,
+        rows, block_table.data_ptr(), max_blocks, page_size, seq_lens.data_ptr(), tree_mask.data_ptr(), B, q_len, H,
+        kv_heads, D, 0 if dt is _bf16 else 1, scale, k_scale, v_scale, out.data_ptr(), lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _handle(stream, dev)))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_gqa_verify_attn_fp4_paged")
+    return out, lse
 
 
 def gqa_cache_keep_fp4(k_pool, v_pool, block_table, page_size, seq_lens, path, keep, stream=None):

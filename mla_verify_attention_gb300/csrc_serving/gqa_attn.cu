@@ -71,17 +71,18 @@ struct Variant {
   AttnFn attn;
   CombineFn combine_parts, combine_few_chunks, combine_many_chunks;
   size_t smem;
+  int threads;
 };
 template <int D, bool kBf16>
 Variant variant() {
-  constexpr size_t smem = sizeof(Smem<D>);
+  constexpr size_t smem = sizeof(Smem<D, kWhole>);
   static_assert(smem <= 232448, "one CTA's shared memory");
   return {attn_kernel<D, kBf16, kWhole>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
-          combine_many_units<D, kBf16, 3, 2>, smem};
+          combine_many_units<D, kBf16, 3, 2>, smem, kThreads};
 }
 
 std::mutex g_ready_mutex;
-bool g_ready[kMaxDevices][2][4];
+bool g_ready[kMaxDevices][3][4];
 
 // The kernels for these sizes, ready on the current device.
 int pick(int D, int dtype, Mode mode, Variant* out) {
@@ -90,6 +91,7 @@ int pick(int D, int dtype, Mode mode, Variant* out) {
   const int n = (D == 128 ? 2 : 0) + (dtype == MLA_FP16 ? 1 : 0);
   *out = all[n];
   if (mode == kWindow) out->attn = window_kernel(D, dtype == MLA_BF16);
+  if (mode == kFp4) out->attn = fp4_kernel(D, dtype == MLA_BF16, &out->smem, &out->threads);
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED_DEVICE;
   std::lock_guard<std::mutex> lock(g_ready_mutex);
@@ -176,8 +178,16 @@ int run(const Call& c) {
   const int batches = paged ? 1 : c.B;
   const long long q_sizes[3] = {c.B, c.q_len, c.H}, kv_sizes[3] = {batches, rows, c.Hkv};
   int st = byte_strides(c.strides, q_sizes, c.D, p.q_stride);
-  if (st == MLA_OK) st = byte_strides(c.strides ? c.strides + 3 : nullptr, kv_sizes, c.D, p.k_stride);
-  if (st == MLA_OK) st = byte_strides(c.strides ? c.strides + 6 : nullptr, kv_sizes, c.D, p.v_stride);
+  if (c.mode == kFp4) {
+    p.k_stride[1] = c.pool_stride[0];
+    p.v_stride[1] = c.pool_stride[1];
+    p.k_stride[2] = p.v_stride[2] = c.D / 2;
+    p.steps_at = fp4::code_bytes(c.Hkv, c.D);
+    p.v_factor = c.v_factor;
+  } else {
+    if (st == MLA_OK) st = byte_strides(c.strides ? c.strides + 3 : nullptr, kv_sizes, c.D, p.k_stride);
+    if (st == MLA_OK) st = byte_strides(c.strides ? c.strides + 6 : nullptr, kv_sizes, c.D, p.v_stride);
+  }
   if (st != MLA_OK) return st;
 
   DeviceCommon d;
@@ -190,7 +200,7 @@ int run(const Call& c) {
   st = pick(c.D, c.dtype, c.mode, &var);
   if (st != MLA_OK) return st;
 
-  const int box = box_rows(c);
+  const int box = c.mode == kFp4 ? 0 : box_rows(c);
   p.group_sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
   p.group_members = (pl.groups + p.group_sets - 1) / p.group_sets;
   const int heads = heads_side_by_side(p.k_stride, c.Hkv, p.group_members, grid);
@@ -257,7 +267,7 @@ int run(const Call& c) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(var.threads, 1, 1);
   cfg.dynamicSmemBytes = var.smem;
   cfg.stream = c.stream;
   cfg.attrs = attr;
@@ -360,6 +370,31 @@ int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_p
                               size_t workspace_bytes, cudaStream_t stream) {
   const mla::gqa::Call c = {q, k_pool, v_pool, strides, seq_lens, tree_mask, B, q_len, H, Hkv, D, 0, dtype, scale,
                             out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0, mla::gqa::kWhole, 0, 0};
+  return mla::gqa::run_paged(c, block_table, max_blocks, page_size, pool_rows);
+}
+
+size_t mla_gqa_fp4_workspace_size(int B, int q_len, int H, int Hkv, int D) {
+  return Hkv > MLA_FP4_MAX_HEADS ? 0 : mla_gqa_workspace_size(B, q_len, H, Hkv, D);
+}
+
+int mla_gqa_verify_attn_fp4_paged(const void* q, const int64_t* q_strides, const void* k_pool, long long k_pool_stride,
+                                  const void* v_pool, long long v_pool_stride, long long pool_rows,
+                                  const int32_t* block_table, int max_blocks, int page_size, const int32_t* seq_lens,
+                                  const uint32_t* tree_mask, int B, int q_len, int H, int Hkv, int D, int dtype,
+                                  float scale, float k_factor, float v_factor, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+  const long long row = static_cast<long long>(mla_gqa_fp4_row_bytes(Hkv, D)), limit = 1ll << 32;
+  if (row == 0 || k_pool_stride < row || v_pool_stride < row || k_pool_stride > limit || v_pool_stride > limit)
+    return MLA_ERR_SHAPE;
+  if (!mla::fp4::factor_ok(k_factor) || !mla::fp4::factor_ok(v_factor) || !std::isfinite(scale) ||
+      !std::isfinite(scale * k_factor))
+    return MLA_ERR_ARG;
+  if (k_pool_stride % 16 || v_pool_stride % 16) return MLA_ERR_ALIGN;
+  mla::gqa::Call c = {q, k_pool, v_pool, q_strides, seq_lens, tree_mask, B, q_len, H, Hkv, D, 0, dtype, scale * k_factor,
+                      out, lse, workspace, workspace_bytes, stream, nullptr, 0, 0, 0, mla::gqa::kFp4, 0, 0};
+  c.pool_stride[0] = k_pool_stride;
+  c.pool_stride[1] = v_pool_stride;
+  c.v_factor = v_factor;
   return mla::gqa::run_paged(c, block_table, max_blocks, page_size, pool_rows);
 }
 

@@ -47,10 +47,12 @@
 // two terms would remove the rest for a second product a tile.
 #pragma once
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include <cstdint>
 
+#include "fp4_format.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -65,9 +67,9 @@ constexpr int kMinTiles = 2;
 constexpr float kLazy = 8.0f;              // log2 units a row's max may grow before O is rescaled
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// What the kernel attends over: a stream's whole cache, or its first keys and a
-// sliding window (see Window below).
-enum Mode { kWhole, kWindow };
+// What the kernel attends over: a stream's whole cache, its first keys and a
+// sliding window (see Window below), or a whole cache held in 4 bits (gqa_fp4.cuh).
+enum Mode { kWhole, kWindow, kFp4 };
 
 struct Params {
   const uint8_t* q;
@@ -94,30 +96,50 @@ struct Params {
   int test_stall;
   float scale_log2;
   int window, sinks;               // kWindow
+  int steps_at;                    // kFp4: where a row's steps begin
+  float v_factor;
 };
 
-template <int D>
+template <int D, Mode kMode>
 struct Shape {
+  static constexpr int kThreads = kMode == kFp4 ? 512 : gqa::kThreads;
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = kKeys * D * 2;          // bytes of a K or V tile
   static constexpr int kQTile = kRows * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 10;    // 160 KB of K and V tiles
+  // 160 KB of K and V tiles, or 96 KB in 16 bits and 54 or 72 KB in 4.
+  static constexpr int kStages = (kMode == kFp4 ? 3 : 5) * (D == 128 ? 1 : 2);
   static constexpr int kRing = 2 * kStages * kTile;
+  static constexpr int kCodes = kKeys * D / 2, kSteps = kKeys * D / 16;      // bytes of a tile in 4 bits
+  static constexpr int kPacked = D == 128 ? 6 : 16;    // stages of them
 };
 
+// What only some forms have.
+template <int D, Mode kMode>
+struct Extra {};
 template <int D>
+struct Extra<D, kFp4> {
+  using C = Shape<D, kFp4>;
+  __align__(16) uint8_t codes[2][C::kPacked][C::kCodes];   // [K, V]
+  __align__(16) uint8_t steps[2][C::kPacked][C::kSteps];
+  float q_unit[2][kRows];                              // what a row of Q was divided by
+  uint64_t packed_full[2][C::kPacked], packed_empty[2][C::kPacked];
+};
+
+template <int D, Mode kMode>
 struct __align__(1024) Smem {
-  uint8_t q[2 * Shape<D>::kQTile];                     // this segment's rows and the next one's
-  uint8_t ring[Shape<D>::kRing];                       // stage s: K tile, V tile
+  using C = Shape<D, kMode>;
+  uint8_t q[2 * C::kQTile];                            // this segment's rows and the next one's
+  uint8_t ring[C::kRing];                              // stage s: K tile, V tile
   float2 ml[2][kRows];
-  uint64_t kfull[Shape<D>::kStages], kempty[Shape<D>::kStages];
-  uint64_t vfull[Shape<D>::kStages], vempty[Shape<D>::kStages];
+  uint64_t kfull[C::kStages], kempty[C::kStages];
+  uint64_t vfull[C::kStages], vempty[C::kStages];
   uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];     // [group][buffer]
   // (qfree: one a segment parity.  The products can be through with a short
   // segment before a softmax warp asks for the one before it.)
   uint64_t qfull, qfree[2], ofull, ofree, mlx, drain[2];
-  int warp_sum[kThreads / 32], start_b, start_pre;
+  int warp_sum[C::kThreads / 32], start_b, start_pre;
   uint32_t tmem_base, abort_flag;
+  Extra<D, kMode> extra;
 };
 
 // ------------------------------------------------------------ instructions
@@ -225,7 +247,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // Bounded; gives up at once when another warp of the CTA has.
 template <class S>
-__device__ __noinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
+__device__ __forceinline__ bool wait_loop(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
   for (int i = 0; i < 64; ++i)       // (reading the timer takes longer than most waits)
     if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
@@ -238,6 +260,25 @@ __device__ __noinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, con
       return false;
     }
   }
+}
+// Out of line, except where warps have register counts of their own (a call's
+// registers cannot be allocated there).
+template <class S>
+__device__ __noinline__ bool wait_call(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
+  return wait_loop(sm, bar, parity, p);
+}
+template <class S>
+struct InlineWaits {
+  static constexpr bool value = false;
+};
+template <int D>
+struct InlineWaits<Smem<D, kFp4>> {
+  static constexpr bool value = true;
+};
+template <class S>
+__device__ __forceinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
+  if constexpr (InlineWaits<S>::value) return wait_loop(sm, bar, parity, p);
+  else return wait_call(sm, bar, parity, p);
 }
 // By a whole converged warp; the result is warp-uniform.
 template <class S>
@@ -438,8 +479,8 @@ struct Ring {
 // for both took longer to issue a tile's copies than the memory to deliver them.)
 // With a window, boxes without a key that a draft may see are left out.
 template <int D, Mode kMode>
-__device__ __forceinline__ void load_tma(Smem<D>& sm, const Params& p, const CUtensorMap* map, Walk<kMode> w, bool is_v) {
-  using C = Shape<D>;
+__device__ __forceinline__ void load_tma(Smem<D, kMode>& sm, const Params& p, const CUtensorMap* map, Walk<kMode> w, bool is_v) {
+  using C = Shape<D, kMode>;
   const int lane = threadIdx.x & 31;
   uint64_t* const full = is_v ? sm.vfull : sm.kfull;
   uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
@@ -506,8 +547,8 @@ out:
 // leave; rows past the stream are zeros.  A lane looks up the pages of two rows
 // of the next tile while it copies this one.
 template <int D, Mode kMode>
-__device__ __forceinline__ void load_gather(Smem<D>& sm, const Params& p, Walk<kMode> w, bool is_v) {
-  using C = Shape<D>;
+__device__ __forceinline__ void load_gather(Smem<D, kMode>& sm, const Params& p, Walk<kMode> w, bool is_v) {
+  using C = Shape<D, kMode>;
   constexpr int kUnits = D / 8;                // 16-byte units a row
   constexpr int kPer = 32 / kUnits;            // rows a warp copies at once
   constexpr int kAhead = C::kStages - 1 < 8 ? C::kStages - 1 : 8;   // stages in flight
@@ -576,6 +617,131 @@ out:
   cp_async_wait<0>();
 }
 
+// ------------------------------------------------------------ loads of a cache in 4 bits
+//
+// Warps 0 (K) and 2 (V) copy a tile's codes and steps, row by row, into a ring in 4
+// bits; two more warps each (12 and 13, 14 and 15) turn them into the 16-bit tiles of the
+// products.  (A code times its step is exact in fp16, whatever the type of Q; the
+// pools' factors go to the scale and to the result.)
+
+// 4, 8 or 16 bytes to shared memory, or as many zero bytes when !full.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool full) {
+  static_assert(kBytes == 4 || kBytes == 8, "");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(full ? kBytes : 0)
+               : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void load_packed(Smem<D, kFp4>& sm, const Params& p, Walk<kFp4> w, bool is_v) {
+  using C = Shape<D, kFp4>;
+  constexpr int kUnits = D / 32, kPer = 32 / kUnits;     // 16-byte units of a row's codes, rows a warp copies at once
+  constexpr int kAhead = C::kPacked - 1 < 8 ? C::kPacked - 1 : 8;
+  const int lane = threadIdx.x & 31;
+  uint64_t* const full = sm.extra.packed_full[is_v];
+  uint64_t* const empty = sm.extra.packed_empty[is_v];
+  const uint8_t* const pool = is_v ? p.v : p.k;
+  const long long row_stride = is_v ? p.v_stride[1] : p.k_stride[1];
+  const bool withheld = p.test_stall && is_v && blockIdx.x == 0;
+  Ring<C::kPacked> at, landed;
+  int started = 0;
+  auto publish = [&]() {                       // the oldest tile's copies of this lane have landed
+    if (!withheld) mbar_arrive(smem_u32(&full[landed.stage]));
+    landed.advance();
+  };
+  Segment s;
+  while (w.next(p, s)) {
+    auto key_of = [&](int j, int half) { return s.template key<kFp4>(j) + half * 32 + lane; };
+    auto entry_of = [&](int j, int half) {
+      return j < s.n && key_of(j, half) < s.S ? table_entry(p, s.b, key_of(j, half)) : 0;
+    };
+    auto row_of = [&](int j, int half, int entry) {        // -1 past the stream
+      return key_of(j, half) < s.S ? pool_row(p, entry, key_of(j, half)) : -1;
+    };
+    const uint8_t* const codes = pool + s.head * (D / 2) + (lane % kUnits) * 16;
+    const uint8_t* const steps = pool + p.steps_at + s.head * (D / 16);
+    // Entries two tiles ahead, rows one.
+    int entry[2] = {entry_of(0, 0), entry_of(0, 1)}, next[2] = {entry_of(1, 0), entry_of(1, 1)};
+    for (int j = 0; j < s.n; ++j, at.advance()) {
+      const int row[2] = {row_of(j, 0, entry[0]), row_of(j, 1, entry[1])};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        entry[h] = next[h];
+        next[h] = entry_of(j + 2, h);
+      }
+      if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
+      const uint32_t dst = smem_u32(sm.extra.codes[is_v][at.stage]) + lane * 16;
+#pragma unroll
+      for (int e = 0; e < kKeys / kPer; ++e) {
+        const int r = __shfl_sync(0xFFFFFFFFu, row[e * kPer >= 32], (e * kPer & 31) + lane / kUnits);
+        cp_async_16(dst + e * 512, codes + (r < 0 ? 0 : r) * row_stride, r >= 0);
+      }
+      const uint32_t dst_steps = smem_u32(sm.extra.steps[is_v][at.stage]) + lane * (D / 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        cp_async_small<D / 16>(dst_steps + h * 32 * (D / 16), steps + (row[h] < 0 ? 0 : row[h]) * row_stride, row[h] >= 0);
+      cp_async_commit();
+      if (++started >= kAhead) {
+        cp_async_wait<kAhead - 1>();
+        publish();
+      }
+    }
+  }
+  cp_async_wait<0>();
+  for (int n = min(started, kAhead - 1); n > 0; --n) publish();
+  return;
+out:
+  cp_async_wait<0>();
+}
+
+// One of the two warps of K or V: every second 32 units of 16 bytes of codes.
+template <int D>
+__device__ __forceinline__ void unpack_tiles(Smem<D, kFp4>& sm, const Params& p, Walk<kFp4> w, bool is_v, int half) {
+  using C = Shape<D, kFp4>;
+  constexpr int kUnits = D / 32;
+  const int lane = threadIdx.x & 31;
+  uint64_t* const full = is_v ? sm.vfull : sm.kfull;
+  uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
+  Ring<C::kPacked> from;
+  Ring<C::kStages> to;
+  Segment s;
+  while (w.next(p, s)) {
+    for (int j = 0; j < s.n; ++j, from.advance(), to.advance()) {
+      if (!wait2(sm, sm.extra.packed_full[is_v][from.stage], from.phase, empty[to.stage], to.phase ^ 1, p)) return;
+      uint8_t* const tile = sm.ring + to.stage * 2 * C::kTile + (is_v ? C::kTile : 0);
+      const uint8_t* const codes = sm.extra.codes[is_v][from.stage];
+      const uint8_t* const steps = sm.extra.steps[is_v][from.stage];
+#pragma unroll
+      for (int e = 0; e < C::kCodes / 16 / 64; ++e) {
+        const int x = (2 * e + half) * 32 + lane, row = x / kUnits, u = x % kUnits;   // 32 values
+        const uint4 c = *reinterpret_cast<const uint4*>(codes + x * 16);
+        const uint32_t two = fp4::from_e4m3x2(*reinterpret_cast<const uint16_t*>(steps + x * 2));
+        const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+        uint8_t* const dst = tile + (u >> 1) * (kKeys * 128) + row * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 step = __half2half2(i < 2 ? __low2half(*reinterpret_cast<const __half2*>(&two))
+                                                  : __high2half(*reinterpret_cast<const __half2*>(&two)));
+          uint32_t h[4];
+          fp4::from_e2m1x8(words[i], h);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[y]), step);
+            h[y] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(dst + ((((u & 1) * 4 + i) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&full[to.stage]));
+        mbar_arrive(smem_u32(&sm.extra.packed_empty[is_v][from.stage]));
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ products
 
 // A segment's tiles are taken by the two softmax groups in turn.  Issuing one
@@ -590,14 +756,14 @@ out:
 // Warp 1: S of every tile.
 template <int D, bool kBf16, Mode kMode>
 struct ProductsQk {
-  using C = Shape<D>;
-  static constexpr uint32_t kId = idesc<kBf16>(kKeys, 0);
-  Smem<D>& sm;
+  using C = Shape<D, kMode>;
+  static constexpr uint32_t kId = idesc<kBf16 && kMode != kFp4>(kKeys, 0);
+  Smem<D, kMode>& sm;
   const Params& p;
   uint32_t tmem, q0, k0;
   Ring<C::kStages> at;
   int done[2] = {0, 0};                        // tiles of each group so far
-  __device__ __forceinline__ ProductsQk(Smem<D>& sm_, const Params& p_, uint32_t tmem_)
+  __device__ __forceinline__ ProductsQk(Smem<D, kMode>& sm_, const Params& p_, uint32_t tmem_)
       : sm(sm_), p(p_), tmem(tmem_), q0(desc_lo(smem_u32(sm_.q), 16)), k0(desc_lo(smem_u32(sm_.ring), 16)) {}
 
   template <int g>
@@ -630,14 +796,14 @@ struct ProductsQk {
 // Warp 3: O += P V of every tile.
 template <int D, bool kBf16, Mode kMode>
 struct ProductsPv {
-  using C = Shape<D>;
-  static constexpr uint32_t kId = idesc<kBf16>(D, 1);
-  Smem<D>& sm;
+  using C = Shape<D, kMode>;
+  static constexpr uint32_t kId = idesc<kBf16 && kMode != kFp4>(D, 1);
+  Smem<D, kMode>& sm;
   const Params& p;
   uint32_t tmem, v0;
   Ring<C::kStages> at;
   int done[2] = {0, 0};
-  __device__ __forceinline__ ProductsPv(Smem<D>& sm_, const Params& p_, uint32_t tmem_)
+  __device__ __forceinline__ ProductsPv(Smem<D, kMode>& sm_, const Params& p_, uint32_t tmem_)
       : sm(sm_), p(p_), tmem(tmem_), v0(desc_lo(smem_u32(sm_.ring) + C::kTile, kKeys * 128)) {}
 
   // `first`: the group's first of the segment, O starts at 0.
@@ -690,10 +856,10 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, const uint4* v, uint8_t
 
 // Starts the copies of a segment's Q rows into a swizzled tile, by all softmax
 // warps: each group half the rows of each warp's 32.
-template <int D>
-__device__ __forceinline__ void start_q(Smem<D>& sm, const Params& p, const Segment& s, int seg, int g, int wq,
+template <int D, bool kBf16, Mode kMode>
+__device__ __forceinline__ void start_q(Smem<D, kMode>& sm, const Params& p, const Segment& s, int seg, int g, int wq,
                                         int lane) {
-  using C = Shape<D>;
+  using C = Shape<D, kMode>;
   constexpr int kUnits = D / 8;                            // 16-byte units a row
   constexpr int kPer = 32 / kUnits;                        // rows a warp copies at once
   const int rows = rows_of_group(p, s.group);
@@ -705,18 +871,48 @@ __device__ __forceinline__ void start_q(Smem<D>& sm, const Params& p, const Segm
                                                : 0;
   const uint32_t tile = smem_u32(sm.q) + (seg & 1) * C::kQTile;
   const int r0 = g * 16 + lane / kUnits, u = lane % kUnits;
+  if constexpr (kMode == kFp4 && kBf16) {
+    // The products are fp16's (a code times its step is not always bf16's): a row's
+    // largest magnitude is brought to 2^14 by a power of two, which leaves every
+    // value down to 2^-28 of it as it is.
+    uint4 v[16 / kPer];
 #pragma unroll
-  for (int e = 0; e < 16 / kPer; ++e) {
-    const long long off = __shfl_sync(0xFFFFFFFFu, base, r0 + e * kPer);
-    const int row = wq * 32 + r0 + e * kPer;
-    if (row < rows)
-      cp_async_16(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), p.q + off + u * 16, true);
+    for (int e = 0; e < 16 / kPer; ++e) {
+      const long long off = __shfl_sync(0xFFFFFFFFu, base, r0 + e * kPer);
+      v[e] = wq * 32 + r0 + e * kPer < rows ? *reinterpret_cast<const uint4*>(p.q + off + u * 16) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < 16 / kPer; ++e) {
+      const int row = wq * 32 + r0 + e * kPer;
+      uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w}, top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+      for (int x = 1; x < kUnits; x <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+      const int exponent = min(max(127 + 14 + 127 - static_cast<int>(top >> 7), 1), 253);   // of the power of two
+      const float times = __uint_as_float(static_cast<uint32_t>(exponent) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack2<false>(bf16lo_to_f32(w[i]) * times, bf16hi_to_f32(w[i]) * times);
+      *reinterpret_cast<uint4*>(sm.q + (seg & 1) * C::kQTile + (u >> 3) * (kRows * 128) + row * 128 +
+                                (((u & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (u == 0) sm.extra.q_unit[seg & 1][row] = __uint_as_float(static_cast<uint32_t>(254 - exponent) << 23);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16 / kPer; ++e) {
+      const long long off = __shfl_sync(0xFFFFFFFFu, base, r0 + e * kPer);
+      const int row = wq * 32 + r0 + e * kPer;
+      if (row < rows)
+        cp_async_16(tile + (u >> 3) * (kRows * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), p.q + off + u * 16, true);
+    }
+    cp_async_commit();
   }
-  cp_async_commit();
 }
 // The copies have landed: hands the tile to the products.
-template <int D>
-__device__ __forceinline__ void finish_q(Smem<D>& sm, int lane) {
+template <int D, Mode kMode>
+__device__ __forceinline__ void finish_q(Smem<D, kMode>& sm, int lane) {
   cp_async_wait<0>();
   fence_proxy_async_smem();
   __syncwarp();
@@ -725,32 +921,33 @@ __device__ __forceinline__ void finish_q(Smem<D>& sm, int lane) {
 
 // Warps 4..11: group g = 0, 1, warp wq of the group, one row a thread.
 template <int D, bool kBf16, Mode kMode>
-__device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t tmem, Walk<kMode> w, int g, int wq,
+__device__ __forceinline__ void softmax(Smem<D, kMode>& sm, const Params& p, uint32_t tmem, Walk<kMode> w, int g, int wq,
                                         int lane) {
-  using C = Shape<D>;
+  using C = Shape<D, kMode>;
   // fp16 weights are kept 2^7 larger: the largest, 2^(8 + 7), is in range and
   // the smallest that is not rounded to a subnormal is 2^-14 / 2^7 of a row's
   // largest weight or more.  bf16 has fp32's range.
-  constexpr float kShift = kBf16 ? 0.f : 7.f;
+  constexpr bool kBf16P = kBf16 && kMode != kFp4;
+  constexpr float kShift = kBf16P ? 0.f : 7.f;
   const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
   const int r = wq * 32 + lane;
   const uint32_t o_t = tmem + lanes + g * D;
-  const float a = p.scale_log2;
+  float a = p.scale_log2;
   const bool pos = a > 0.f;
-  const float a_eff = pos ? a : 1.f;
+  float a_eff = pos ? a : 1.f;
   int kt = 0, seg = 0, n = 0;                              // n: tiles of this group so far
   Segment s, next;
   bool more = w.next(p, s);
   if (more) {
-    start_q<D>(sm, p, s, 0, g, wq, lane);
-    finish_q<D>(sm, lane);
+    start_q<D, kBf16, kMode>(sm, p, s, 0, g, wq, lane);
+    finish_q<D, kMode>(sm, lane);
   }
   for (; more; s = next) {
     more = w.next(p, next);
     if (more) {
       // The next segment's Q lands while this one's tiles are worked on.
       if (seg > 0 && !wait(sm, sm.qfree[(seg - 1) & 1], ((seg - 1) >> 1) & 1, p)) return;
-      start_q<D>(sm, p, next, seg + 1, g, wq, lane);
+      start_q<D, kBf16, kMode>(sm, p, next, seg + 1, g, wq, lane);
     }
     const int rows = rows_of_group(p, s.group);
     const int R = s.group * kRows + r;                     // row of the stream and head: draft * G + head in group
@@ -779,6 +976,11 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
       uint64_t last = mask64;
       for (int x = n_seen; x > p.window; --x) last &= last - 1ull;
       mask64 = last | (mask64 & between(prefix, 0, p.sinks));
+    }
+    if constexpr (kMode == kFp4 && kBf16) {
+      if (!wait(sm, sm.qfull, seg & 1, p)) return;
+      a = p.scale_log2 * sm.extra.q_unit[seg & 1][r];
+      a_eff = pos ? a : 1.f;
     }
     float m = -CUDART_INF_F, l = 0.f;
     for (int j = g; j < s.n; j += 2, ++n) {
@@ -841,7 +1043,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
           f2unpack(ffma2(f2pack(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), a2, m2), x0, x1);
           const float p0 = ex2(x0), p1 = ex2(x1);
           sum[c & 1] = fadd2(sum[c & 1], f2pack(p0, p1));
-          pw[c] = pack2<kBf16>(p0, p1);
+          pw[c] = pack2<kBf16P>(p0, p1);
         }
         MLA_TMEM_ST_32x32b_X32(s_t, pw);
         float s0, s1, s2, s3;
@@ -879,7 +1081,7 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
     // products then start while this one's results are written.
     if (more) {
       if (!wait(sm, sm.qfull, seg & 1, p)) return;         // (a group without a tile has not seen it)
-      finish_q<D>(sm, lane);
+      finish_q<D, kMode>(sm, lane);
     }
     const bool direct = s.n == s.nt;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
@@ -904,6 +1106,10 @@ __device__ __forceinline__ void softmax(Smem<D>& sm, const Params& p, uint32_t t
         const float inv = l == 0.f ? 0.f : 1.f / l;        // (a NaN stays one)
         w0 *= inv;
         w1 *= inv;
+      }
+      if constexpr (kMode == kFp4) {
+        w0 *= p.v_factor;
+        w1 *= p.v_factor;
       }
       const int c0 = g * (D / 2), c1 = c0 + D / 2;         // each group writes half the columns
       // The products are through with this segment's Q: the first 2 KB of the
@@ -1006,10 +1212,11 @@ __device__ __forceinline__ void note_cut_units(const Params& p, Walk<kMode> w, c
 }
 
 template <int D, bool kBf16, Mode kMode>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
-  using S = Smem<D>;
-  using C = Shape<D>;
+  using S = Smem<D, kMode>;
+  using C = Shape<D, kMode>;
+  constexpr int kThreads = C::kThreads;
   // Shared memory is full to the last KB: the tiles' alignment is asked for, and
   // checked, instead of made with a spare KB.
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1024,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 3) {
-    const uint32_t loaders = p.box_rows ? 1 : 32;
+    const uint32_t loaders = kMode == kFp4 ? 2 : p.box_rows ? 1 : 32;
     for (int i = lane; i < C::kStages; i += 32) {
       mbar_init(smem_u32(&sm.kfull[i]), loaders);
       mbar_init(smem_u32(&sm.vfull[i]), loaders);
@@ -1047,6 +1254,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.ofree), 8);
       mbar_init(smem_u32(&sm.mlx), 8);
     }
+    if constexpr (kMode == kFp4) {
+      for (int i = lane; i < 2 * C::kPacked; i += 32) {
+        mbar_init(smem_u32(&sm.extra.packed_full[0][i]), 32);
+        mbar_init(smem_u32(&sm.extra.packed_empty[0][i]), 2);
+      }
+    }
     if (lane == 22) {
       mbar_init(smem_u32(&sm.drain[0]), 1);
       mbar_init(smem_u32(&sm.drain[1]), 1);
@@ -1059,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
     tmem_relinquish();
   }
-  if (tid == 0 && p.box_rows) {
+  if (kMode != kFp4 && tid == 0 && p.box_rows) {
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
@@ -1149,7 +1362,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t0 = team < runs.teams ? runs.start(team) : total;
   const Walk<kMode> walk(p, member, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
 
-  if (warp == 0 || warp == 2) {
+  if constexpr (kMode == kFp4) {
+    // 512 threads of 128 registers: the softmax warps take 168, the others 88.
+    if (warp >= 4 && warp < 12) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+      softmax<D, kBf16, kMode>(sm, p, tmem, walk, (warp - 4) >> 2, warp & 3, lane);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp >= 12) {
+        unpack_tiles<D>(sm, p, walk, warp >= 14, warp & 1);
+      } else if (warp == 0 || warp == 2) {
+        load_packed<D>(sm, p, walk, warp == 2);
+      } else if (warp == 1) {
+        ProductsQk<D, kBf16, kMode>(sm, p, tmem).run(walk);
+        drain_products(sm.drain[0]);
+      } else {
+        if (lane == 0 && !p.whole) note_cut_units(p, walk, runs);
+        __syncwarp();
+        ProductsPv<D, kBf16, kMode>(sm, p, tmem).run(walk);
+        drain_products(sm.drain[1]);
+      }
+    }
+  } else if (warp == 0 || warp == 2) {
     if (p.box_rows == 0) load_gather<D, kMode>(sm, p, walk, warp == 2);
     else load_tma<D, kMode>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
   } else if (warp == 1) {

@@ -29,6 +29,8 @@ struct Call {
   long long pool_rows;
   Mode mode;
   int window, sinks;
+  long long pool_stride[2];   // kFp4: bytes, K and V
+  float v_factor;
 };
 
 bool shape_ok(int B, int q, int H, int Hkv, int D);
@@ -42,6 +44,7 @@ int cta_count(const DeviceCommon& d);
 // Forms of the attention kernel that are compiled on their own.
 using AttnFn = void (*)(CUtensorMap, CUtensorMap, Params);
 AttnFn window_kernel(int D, bool bf16);    // gqa_window.cu
+AttnFn fp4_kernel(int D, bool bf16, size_t* smem, int* threads);   // gqa_fp4.cu
 
 }  // namespace gqa
 }  // namespace mla

@@ -56,6 +56,7 @@ extern "C" int mla_call_packed(int which, const int64_t* args) {
     case MLA_CALL_CACHE_COMPACT: return call(mla_cache_compact, args);
     case MLA_CALL_GQA_ATTN_WEIGHTS: return call(mla_gqa_attn_weights, args);
     case MLA_CALL_GQA_ATTN_WEIGHTS_PAGED: return call(mla_gqa_attn_weights_paged, args);
+    case MLA_CALL_GQA_VERIFY_ATTN_FP4_PAGED: return call(mla_gqa_verify_attn_fp4_paged, args);
     default: return MLA_ERR_ARG;
   }
 }
