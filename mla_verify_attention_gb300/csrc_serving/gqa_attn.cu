@@ -27,9 +27,6 @@ constexpr int kWholeKeys = 512;
 // Row groups of a head that CTAs take side by side, at most.
 constexpr int kMaxMembers = 16;
 
-// Parts a unit from which four part groups share the merge of a row.
-constexpr int kManyParts = 8;
-
 struct Plan {
   int groups;          // groups of 128 rows a key head
   int part_rows;       // rows of a partial, a multiple of 16
@@ -194,10 +191,11 @@ int run(const Call& c) {
   st = device_common(&d);
   if (st != MLA_OK) return st;
   const int grid = cta_count(d);
-  const Layout lay = layout(pl, grid, c.D);
+  const bool few = c.mode == kFp4 && few_rows(c.q_len, c.H, c.Hkv);
+  const Layout lay = layout(pl, few ? grid * few_heads(c.q_len, c.H, c.Hkv) : grid, c.D);
   if (!c.workspace || c.workspace_bytes < lay.bytes) return MLA_ERR_WORKSPACE;
-  Variant var;
-  st = pick(c.D, c.dtype, c.mode, &var);
+  Variant var = {};
+  if (!few) st = pick(c.D, c.dtype, c.mode, &var);
   if (st != MLA_OK) return st;
 
   const int box = c.mode == kFp4 ? 0 : box_rows(c);
@@ -261,6 +259,8 @@ int run(const Call& c) {
   p.box_rows = box;
   p.test_stall = d.test_stall;
   p.scale_log2 = c.scale * 1.4426950408889634f;
+
+  if (few) return run_few(c, p, d, grid);
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -374,7 +374,12 @@ int mla_gqa_verify_attn_paged(const void* q, const void* k_pool, const void* v_p
 }
 
 size_t mla_gqa_fp4_workspace_size(int B, int q_len, int H, int Hkv, int D) {
-  return Hkv > MLA_FP4_MAX_HEADS ? 0 : mla_gqa_workspace_size(B, q_len, H, Hkv, D);
+  using namespace mla;
+  if (!gqa::shape_ok(B, q_len, H, Hkv, D) || Hkv > MLA_FP4_MAX_HEADS) return 0;
+  DeviceCommon d;
+  if (device_common(&d) != MLA_OK) return 0;
+  const int parts = gqa::cta_count(d) * (gqa::few_rows(q_len, H, Hkv) ? gqa::few_heads(q_len, H, Hkv) : 1);
+  return gqa::layout(gqa::plan(q_len, H, Hkv), parts, D).bytes;
 }
 
 int mla_gqa_verify_attn_fp4_paged(const void* q, const int64_t* q_strides, const void* k_pool, long long k_pool_stride,

@@ -1,0 +1,737 @@
+// Attention over a cache held in 4 bits for few query rows a key head (decoding, short
+// drafts): the other kernel behind mla_gqa_verify_attn_fp4_paged.
+//
+// Mathematics.  That of the attention kernel (gqa_attn.cuh), turned around: S^T = K Q^T
+// and O^T = V^T P with the keys, then the dimensions, as the 16 rows of a warp's
+// mma.sync and 8 query rows as its columns, so that 8 rows cost a sixteenth of the 128
+// that a tcgen05 product has.  Codes become fp16 in the registers of the lanes that
+// feed the product: nothing is written back to shared memory.
+//   K: lane 4 g + c holds keys g and g + 8 of 16, and a contiguous quarter c of their
+//      dimensions: 16 bytes (8 at D = 64).  The order of the dimensions in a
+//      product is free if Q has the same: a lane's quarter of a row of Q as it lies.
+//   V: lane 4 g + c holds dimensions 16 g .. 16 g + 15 (8 at D = 64) of keys 2 c, 2 c + 1,
+//      2 c + 8, 2 c + 9; the halves of two keys' bytes are interleaved before they
+//      are converted, so that a pair of keys lies in a register as the product wants.
+// S^T's layout is P's but for a transpose of 8 x 8 (movmatrix).  The keys' order in
+// shared memory is permuted (kOrder) so that neither K's nor V's reads collide.
+//
+// What bounds it: 1,152 bytes a key of 8 heads at D = 128, 23 bytes a cycle and SM; the
+// conversions (78 values a cycle and SM measured) take about half of that time.
+//
+// Split.  Equal runs of 64-key tiles as in the attention kernel, but a CTA takes all (up
+// to 16) key heads of a run: whole rows of the cache come in by bulk copies of one row
+// each, any page size, by a warp of their own.  Its other warps are shared out
+// among the heads; those of one head take 16 keys in turn and are put together at a
+// unit's end.  The heads of a CTA count as a team's members for the merge.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "gqa_attn.cuh"
+#include "gqa_host.h"
+#include "mla_verify_attn.h"
+
+namespace mla {
+namespace gqa {
+namespace few {
+
+constexpr int kMostStages = 8;
+constexpr uint32_t kOrder = 0x57463120u;   // key of row i of 8, four bits each
+
+struct FewParams : Params {
+  int heads, head_warps;           // key heads a CTA, warps a head
+  int stage_keys, stages, pitch;   // a stage: stage_keys rows of K, then of V, pitch bytes apart
+  int codes;                       // bytes copied of a row: all of them,
+  int split;                       // or (not 0) the heads' codes, and their steps on their own
+};
+
+// kN: query rows in eights; more of them want more registers.
+template <int kN>
+struct Shape8 {
+  static constexpr int kWarps = kN == 1 ? 16 : 8;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+};
+
+template <int kN>
+struct __align__(128) Head {
+  uint64_t full[kMostStages], empty[kMostStages], meet[Shape8<kN>::kWarps];
+  float2 ml[Shape8<kN>::kWarps][8 * kN];
+  int warp_sum[Shape8<kN>::kWarps + 1], start_b, start_pre;
+  uint32_t abort_flag;
+};
+
+template <int D>
+constexpr int kSumPitch = D + 4;           // floats a row of the warps' sums
+template <int D, int kN>
+constexpr int kSums = Shape8<kN>::kWarps * 8 * kN * kSumPitch<D> * 4;
+
+__device__ __forceinline__ void copy_row(uint32_t dst, const uint8_t* src, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t low2(uint32_t x) { return __byte_perm(x, x, 0x1010); }
+__device__ __forceinline__ uint32_t high2(uint32_t x) { return __byte_perm(x, x, 0x3232); }
+
+// The last warp: a row of K and one of V a lane.
+template <int kN>
+__device__ __forceinline__ void load_rows(Head<kN>& sm, const FewParams& p, uint32_t ring, int step_bytes, Walk<kWhole> w) {
+  const int lane = threadIdx.x & 31;
+  const bool withheld = p.test_stall && blockIdx.x == 0;
+  const int stage_bytes = 2 * p.stage_keys * p.pitch;
+  int stage = 0, issued = 0;
+  uint32_t phase = 0;
+  Segment s;
+  while (w.next(p, s)) {
+    const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys);
+    // The heads' steps, from one multiple of 16 bytes to another.
+    const int from = p.split ? (s.head * step_bytes) & ~15 : 0;
+    const int steps = p.split ? (((s.head + p.heads) * step_bytes + 15) & ~15) - from : 0;
+    const int codes_at = p.split ? s.head * step_bytes * 8 : 0;
+    const int row_bytes = p.codes + steps;
+    int next = begin + lane < end ? table_entry(p, s.b, begin + lane) : 0;
+    for (int k0 = begin; k0 < end; k0 += p.stage_keys) {
+      if (!wait(sm, sm.empty[stage], phase ^ 1, p)) goto out;
+      const uint32_t bar = smem_u32(&sm.full[stage]);
+      const int n = min(p.stage_keys, end - k0);
+      if (withheld && issued == 0) goto out;               // this load never comes
+      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * n * row_bytes);
+      __syncwarp();
+      for (int r = lane; r - lane < n; r += 32) {
+        const int entry = next, key = k0 + r;
+        // (the entry of this lane's next row, in this stage or the next)
+        const int ahead = r + 32 - lane < n ? key + 32 : k0 + p.stage_keys + lane;
+        next = ahead < end ? table_entry(p, s.b, ahead) : 0;
+        if (r < n) {
+          const long long row = pool_row(p, entry, key);
+          const uint32_t dst = ring + stage * stage_bytes + r * p.pitch, dst_v = dst + p.stage_keys * p.pitch;
+          const uint8_t* const k = p.k + row * p.k_stride[1];
+          const uint8_t* const v = p.v + row * p.v_stride[1];
+          copy_row(dst, k + codes_at, p.codes, bar);
+          copy_row(dst_v, v + codes_at, p.codes, bar);
+          if (p.split) {
+            copy_row(dst + p.codes, k + p.steps_at + from, steps, bar);
+            copy_row(dst_v + p.codes, v + p.steps_at + from, steps, bar);
+          }
+        }
+      }
+      ++issued;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+out:
+  for (int n = issued - 1; n >= 0 && n >= issued - p.stages; --n)
+    mbar_wait(smem_u32(&sm.full[n % p.stages]), (n / p.stages) & 1, kWaitNs / 2);
+}
+
+// All warps of a head are here; false: some wait has run out.
+template <int kN>
+__device__ __forceinline__ bool meet(Head<kN>& sm, const FewParams& p, int head, uint32_t& times) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.meet[head]));
+  return wait(sm, sm.meet[head], times++ & 1u, p);
+}
+
+template <int D, bool kBf16, int kN>
+__device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const uint8_t* ring, float* sums, Walk<kWhole> w,
+                                       int warp, int lane) {
+  constexpr int kTiles = D / 16;             // of 16 dimensions (or rows of O^T)
+  constexpr int kQ = D / 8;                  // registers of a row of Q a lane
+  constexpr float kShift = 7.f;              // (see the attention kernel's softmax)
+  const int g = lane >> 2, c = lane & 3;
+  const int head_local = warp / p.head_warps, j = warp - head_local * p.head_warps;
+  const int rows = p.q_len * p.G;
+  const int key_g = kOrder >> (4 * g) & 7, key_c = kOrder >> (8 * c) & 7, key_c1 = kOrder >> (8 * c + 4) & 7;
+  const int stage_bytes = 2 * p.stage_keys * p.pitch, v_at = p.stage_keys * p.pitch;
+  int stage = 0, seg = 0;
+  uint32_t phase = 0, met = 0;
+  Segment s;
+  for (; w.next(p, s); ++seg) {
+    const int head = s.head + head_local;
+    const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys), prefix = s.S - p.q_len;
+    // ---- rows of Q: row 8 t + g, this lane's quarter; in fp16, brought to its range
+    // by a power of two where they are bf16.
+    uint32_t q[kN][kQ];
+    float a[kN][2];                          // scale of rows 8 t + 2 c, + 1
+    uint64_t mask[kN][2];
+    float m[kN][2], l[kN][2], o[kN][kTiles][4];
+#pragma unroll
+    for (int t = 0; t < kN; ++t) {
+      const int R = 8 * t + g, i = p.by_G.of(R);
+      float unit = 1.f;
+      const uint8_t* const src =
+          p.q + s.b * p.q_stride[0] + i * p.q_stride[1] + (head * p.G + (R - i * p.G)) * p.q_stride[2] + c * (D / 2);
+#pragma unroll
+      for (int e = 0; e < kQ / 4; ++e) {
+        const uint4 x = R < rows ? reinterpret_cast<const uint4*>(src)[e] : make_uint4(0, 0, 0, 0);
+        q[t][4 * e] = x.x;
+        q[t][4 * e + 1] = x.y;
+        q[t][4 * e + 2] = x.z;
+        q[t][4 * e + 3] = x.w;
+      }
+      if (kBf16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < kQ; ++e) top = __vmaxu2(top, q[t][e] & 0x7FFF7FFFu);
+        top = max(top & 0xFFFFu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const int exponent = min(max(127 + 14 + 127 - static_cast<int>(top >> 7), 1), 253);
+        const float by = __uint_as_float(static_cast<uint32_t>(exponent) << 23);
+        unit = __uint_as_float(static_cast<uint32_t>(254 - exponent) << 23);
+#pragma unroll
+        for (int e = 0; e < kQ; ++e) q[t][e] = pack2<false>(bf16lo_to_f32(q[t][e]) * by, bf16hi_to_f32(q[t][e]) * by);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        a[t][e] = p.scale_log2 * __shfl_sync(0xFFFFFFFFu, unit, (2 * c + e) * 4);
+        const int row = 8 * t + 2 * c + e, draft = p.by_G.of(row);
+        mask[t][e] = 0;
+        if (row < rows) {
+          const int words = (p.q_len + 31) >> 5;
+          const uint32_t* const word = p.mask + (static_cast<size_t>(s.b) * p.q_len + draft) * words;
+          mask[t][e] = word[0];
+          if (words > 1) mask[t][e] |= static_cast<uint64_t>(word[1]) << 32;
+          if (p.q_len < 64) mask[t][e] &= (1ull << p.q_len) - 1ull;
+        }
+        m[t][e] = -CUDART_INF_F;
+        l[t][e] = 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][x][e] = 0.f;
+    }
+    uint64_t used = 0;                       // drafts that some row sees
+#pragma unroll
+    for (int t = 0; t < kN; ++t) used |= mask[t][0] | mask[t][1];
+    used |= __shfl_xor_sync(0xFFFFFFFFu, used, 1);
+    used |= __shfl_xor_sync(0xFFFFFFFFu, used, 2);
+    const int steps_at = (p.split ? p.codes + ((s.head * (D / 16)) & 15) : p.steps_at) + head_local * (D / 16);
+
+    // ---- the run's stages
+    for (int k1 = begin; k1 < end; k1 += p.stage_keys) {
+      if (!wait(sm, sm.full[stage], phase, p)) return;
+      const uint8_t* const base = ring + stage * stage_bytes;
+      for (int step = j; step * 16 < p.stage_keys; step += p.head_warps) {
+        const int k0 = k1 + step * 16;
+        if (k0 >= end) break;
+        const bool edge = k0 + 16 > min(prefix, end);
+        float x[kN][4];
+#pragma unroll
+        for (int t = 0; t < kN; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+        {
+          // S^T = K Q^T
+          const uint8_t* const ka = base + (step * 16 + key_g) * p.pitch;
+          const uint8_t* const kb = ka + 8 * p.pitch;
+          uint32_t wa[D / 32], wb[D / 32], sa, sb;
+          if constexpr (D == 128) {
+            const uint4 va = *reinterpret_cast<const uint4*>(ka + head_local * 64 + c * 16);
+            const uint4 vb = *reinterpret_cast<const uint4*>(kb + head_local * 64 + c * 16);
+            wa[0] = va.x, wa[1] = va.y, wa[2] = va.z, wa[3] = va.w;
+            wb[0] = vb.x, wb[1] = vb.y, wb[2] = vb.z, wb[3] = vb.w;
+            sa = fp4::from_e4m3x2(*reinterpret_cast<const uint16_t*>(ka + steps_at + 2 * c));
+            sb = fp4::from_e4m3x2(*reinterpret_cast<const uint16_t*>(kb + steps_at + 2 * c));
+          } else {
+            const uint2 va = *reinterpret_cast<const uint2*>(ka + head_local * 32 + c * 8);
+            const uint2 vb = *reinterpret_cast<const uint2*>(kb + head_local * 32 + c * 8);
+            wa[0] = va.x, wa[1] = va.y;
+            wb[0] = vb.x, wb[1] = vb.y;
+            sa = fp4::from_e4m3x2(ka[steps_at + c]);
+            sb = fp4::from_e4m3x2(kb[steps_at + c]);
+          }
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            uint32_t ha[4], hb[4];
+            fp4::from_e2m1x8(wa[e], ha);
+            fp4::from_e2m1x8(wb[e], hb);
+            const uint32_t ta = e < 2 ? low2(sa) : high2(sa), tb = e < 2 ? low2(sb) : high2(sb);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t f[4] = {times(ha[2 * y], ta), times(hb[2 * y], tb), times(ha[2 * y + 1], ta),
+                                     times(hb[2 * y + 1], tb)};
+#pragma unroll
+              for (int t = 0; t < kN; ++t) mma(x[t], f, q[t][4 * e + 2 * y], q[t][4 * e + 2 * y + 1]);
+            }
+          }
+        }
+        // ---- softmax: x[t][0..1] are key g's scores of rows 2 c, 2 c + 1, x[t][2..3] key g + 8's.
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < kN; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][e] *= a[t][e & 1];
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = k0 + key_g + (e >> 1) * 8;
+              const bool seen = key < end && (key < prefix || (mask[t][e & 1] >> (key - prefix) & 1ull));
+              if (!seen) x[t][e] = -CUDART_INF_F;
+            }
+          }
+          grow |= fmaxf(x[t][0], x[t][2]) > m[t][0] + kLazy || fmaxf(x[t][1], x[t][3]) > m[t][1] + kLazy;
+        }
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+          for (int t = 0; t < kN; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(x[t][e], x[t][e + 2]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+              if (top > m[t][e] + kLazy) {
+                const float alpha = ex2(m[t][e] - top);    // 0 when nothing was visible before
+                m[t][e] = top;
+                l[t][e] *= alpha;
+#pragma unroll
+                for (int y = 0; y < kTiles; ++y) {
+                  o[t][y][e] *= alpha;
+                  o[t][y][e + 2] *= alpha;
+                }
+              }
+            }
+        }
+        uint32_t pb[kN][2];
+#pragma unroll
+        for (int t = 0; t < kN; ++t) {
+          const float m0 = m[t][0] == -CUDART_INF_F ? 0.f : m[t][0] - kShift;
+          const float m1 = m[t][1] == -CUDART_INF_F ? 0.f : m[t][1] - kShift;
+          const float p0 = ex2(x[t][0] - m0), p1 = ex2(x[t][1] - m1), p2 = ex2(x[t][2] - m0), p3 = ex2(x[t][3] - m1);
+          l[t][0] += p0 + p2;
+          l[t][1] += p1 + p3;
+          pb[t][0] = transposed(pack2<false>(p0, p1));
+          pb[t][1] = transposed(pack2<false>(p2, p3));
+        }
+        {
+          // O^T += V^T P, keys 2 c, 2 c + 1 and those 8 behind
+          uint32_t f[kTiles][4];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint8_t* const v0 = base + v_at + (step * 16 + 8 * half + key_c) * p.pitch;
+            const uint8_t* const v1 = base + v_at + (step * 16 + 8 * half + key_c1) * p.pitch;
+            const int step_at = steps_at + (D == 128 ? g : g >> 1);
+            uint32_t s0 = v0[step_at], s1 = v1[step_at];
+            if (edge) {
+              // Rows past the run, and drafts that none sees, may hold anything.
+              const int t0 = k0 + 8 * half + key_c, t1 = k0 + 8 * half + key_c1;
+              if (!(t0 < end && (t0 < prefix || (used >> (t0 - prefix) & 1ull)))) s0 = 0;
+              if (!(t1 < end && (t1 < prefix || (used >> (t1 - prefix) & 1ull)))) s1 = 0;
+            }
+            const uint32_t scale = fp4::from_e4m3x2(s0 | s1 << 8);
+            uint32_t w0[D / 64], w1[D / 64];
+            if constexpr (D == 128) {
+              const uint2 x0 = *reinterpret_cast<const uint2*>(v0 + head_local * 64 + g * 8);
+              const uint2 x1 = *reinterpret_cast<const uint2*>(v1 + head_local * 64 + g * 8);
+              w0[0] = x0.x, w0[1] = x0.y;
+              w1[0] = x1.x, w1[1] = x1.y;
+            } else {
+              w0[0] = *reinterpret_cast<const uint32_t*>(v0 + head_local * 32 + g * 4);
+              w1[0] = *reinterpret_cast<const uint32_t*>(v1 + head_local * 32 + g * 4);
+            }
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+              uint32_t even[4], odd[4];
+              fp4::from_e2m1x8((w0[e] & 0x0F0F0F0Fu) | (w1[e] << 4 & 0xF0F0F0F0u), even);
+              fp4::from_e2m1x8((w0[e] >> 4 & 0x0F0F0F0Fu) | (w1[e] & 0xF0F0F0F0u), odd);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                f[4 * e + y][2 * half] = times(even[y], scale);
+                f[4 * e + y][2 * half + 1] = times(odd[y], scale);
+              }
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+            for (int t = 0; t < kN; ++t) mma(o[t][y], f[y], pb[t][0], pb[t][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.empty[stage]));
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // ---- the unit's end: the warps of a head are put together.
+    const bool direct = s.n == s.nt;
+    const int slot = 2 * (static_cast<int>(blockIdx.x) * p.heads + head_local) + (seg > 0 ? 1 : 0);
+    float w_mine[kN][2], m_all[kN][2], l_all[kN][2];
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], d);
+        m[t][e] = m[t][e] == -CUDART_INF_F ? -CUDART_INF_F : m[t][e] - kShift;
+        m_all[t][e] = m[t][e];
+        l_all[t][e] = l[t][e];
+        w_mine[t][e] = 1.f;
+        if (p.head_warps > 1 && g == 0) sm.ml[warp][8 * t + 2 * c + e] = make_float2(m[t][e], l[t][e]);
+      }
+    if (p.head_warps > 1) {
+      if (!meet(sm, p, head_local, met)) return;
+#pragma unroll
+      for (int t = 0; t < kN; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = -CUDART_INF_F, sum = 0.f;
+          for (int x = 0; x < p.head_warps; ++x) top = fmaxf(top, sm.ml[head_local * p.head_warps + x][8 * t + 2 * c + e].x);
+          for (int x = 0; x < p.head_warps; ++x) {
+            const float2 y = sm.ml[head_local * p.head_warps + x][8 * t + 2 * c + e];
+            sum += (y.x == -CUDART_INF_F ? 0.f : ex2(y.x - top)) * y.y;
+          }
+          w_mine[t][e] = m[t][e] == -CUDART_INF_F ? 0.f : ex2(m[t][e] - top);
+          m_all[t][e] = top;
+          l_all[t][e] = sum;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * t + 2 * c + e, i = p.by_G.of(row);
+        const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head * p.G + (row - i * p.G);
+        float by = w_mine[t][e] * p.v_factor;
+        if (direct) by *= l_all[t][e] == 0.f ? 0.f : 1.f / l_all[t][e];       // (a NaN stays one)
+        if (j == 0 && g == 0 && row < rows) {
+          if (direct)
+            p.lse[out_row] = l_all[t][e] == 0.f ? -CUDART_INF_F : (m_all[t][e] + log2f(l_all[t][e])) * 0.6931471805599453f;
+          else
+            p.part_ml[static_cast<size_t>(slot) * p.part_rows + row] = make_float2(m_all[t][e], l_all[t][e]);
+        }
+        // Dimensions g D / 8 .. of row `row`, in order.
+        float v[2 * kTiles];
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y) {
+          v[2 * y] = o[t][y][e] * by;
+          v[2 * y + 1] = o[t][y][e + 2] * by;
+        }
+        if (p.head_warps > 1) {
+          float4* const to = reinterpret_cast<float4*>(sums + (warp * 8 * kN + row) * kSumPitch<D> + g * (D / 8));
+#pragma unroll
+          for (int y = 0; y < D / 32; ++y) to[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+        } else if (row < rows) {
+          if (direct) {
+            uint4* const to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (out_row * D + g * (D / 8)) * 2);
+#pragma unroll
+            for (int y = 0; y < D / 64; ++y)
+              to[y] = make_uint4(pack2<kBf16>(v[8 * y], v[8 * y + 1]), pack2<kBf16>(v[8 * y + 2], v[8 * y + 3]),
+                                 pack2<kBf16>(v[8 * y + 4], v[8 * y + 5]), pack2<kBf16>(v[8 * y + 6], v[8 * y + 7]));
+          } else {
+            float4* const to = p.part_o + (static_cast<size_t>(slot) * p.part_rows + row) * (D / 4) + g * (D / 32);
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y) to[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          }
+        }
+      }
+    if (p.head_warps > 1) {
+      if (!meet(sm, p, head_local, met)) return;
+      for (int x = j * 32 + lane; x < rows * (D / 4); x += 32 * p.head_warps) {
+        const int row = x / (D / 4), col = x % (D / 4);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < p.head_warps; ++y) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              sums + ((head_local * p.head_warps + y) * 8 * kN + row) * kSumPitch<D> + col * 4);
+          sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+        }
+        if (direct) {
+          const int i = p.by_G.of(row);
+          const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head * p.G + (row - i * p.G);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (out_row * D + col * 4) * 2) =
+              make_uint2(pack2<kBf16>(sum.x, sum.y), pack2<kBf16>(sum.z, sum.w));
+        } else {
+          p.part_o[(static_cast<size_t>(slot) * p.part_rows + row) * (D / 4) + col] = sum;
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool kBf16, int kN>
+__global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const FewParams p) {
+  using C = Shape8<kN>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Head<kN>& sm = *reinterpret_cast<Head<kN>*>(smem_raw);
+  float* const sums = reinterpret_cast<float*>(smem_raw + sizeof(Head<kN>));
+  uint8_t* const ring = smem_raw + sizeof(Head<kN>) + (p.head_warps > 1 ? kSums<D, kN> : 0);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 0) {
+    if (lane < p.stages) {
+      mbar_init(smem_u32(&sm.full[lane]), 1);
+      mbar_init(smem_u32(&sm.empty[lane]), p.heads * p.head_warps);
+    }
+    if (lane < p.heads) mbar_init(smem_u32(&sm.meet[lane]), p.head_warps);
+    if (lane == 0) sm.abort_flag = 0;
+    fence_mbarrier_init_cluster();
+    fence_proxy_async_smem();
+  }
+  grid_dependency_wait();
+  if (tid == 0) grid_launch_dependents();
+
+  // This CTA's run (as in the attention kernel, with a CTA a team).
+  const int units = p.head_sets, team = blockIdx.x;
+  const int per = (p.B + C::kThreads - 1) / C::kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int sum = 0, len;
+  bool off = false;
+  for (int b = b0; b < b1; ++b) {
+    sum += stream_work(p, stream_tiles<kWhole>(p, b, len)) * units;
+    off |= len != 0 && (len < p.q_len || len > p.Smax);
+  }
+  if (off && blockIdx.x == 0) atomicOr(p.status, kBitSeqLen);
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) sm.warp_sum[warp] = inc;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < C::kWarps + 1; ++i) {
+    if (i == warp) before = total;
+    total += sm.warp_sum[i];
+  }
+  const Runs runs(p, total, gridDim.x);
+  const int t0 = team < runs.teams ? runs.start(team) : total;
+  before += inc - sum;
+  if (t0 >= before && t0 < before + sum) {
+    int b = b0;
+    while (true) {
+      const int n = stream_work(p, stream_tiles<kWhole>(p, b, len)) * units;
+      if (t0 < before + n) break;
+      before += n;
+      ++b;
+    }
+    sm.start_b = b;
+    sm.start_pre = before;
+  }
+  __syncthreads();
+  const bool any = t0 < total;
+  const Walk<kWhole> walk(p, 0, t0, any ? runs.start(team + 1) : total, any ? sm.start_b : 0, any ? sm.start_pre : 0);
+
+  if (warp == C::kWarps) {
+    if (lane == 0 && !p.whole) {
+      // The merge's list: the units that start in this run and are cut (see note_cut_units).
+      int4 d = make_int4(0, 0, 0, 0);
+      Walk<kWhole> w = walk;
+      Segment s;
+      for (int seg = 0; w.next(p, s); ++seg) {
+        if (s.tile0 != 0) continue;
+        const bool cut = s.n < s.nt;
+        const int parts = cut ? runs.team_of(w.t1 - s.n + s.nt - 1) - team + 1 : 0;
+        if (cut) d = make_int4(s.b, s.head, 2 * team * p.heads + (seg > 0 ? 1 : 0), parts);
+        if (p.desc_units)
+          for (int h = 0; h < p.heads; ++h)
+            p.desc[s.b * p.Hkv + s.head + h] = cut ? make_int4(s.b, s.head + h, d.z + 2 * h, parts) : make_int4(0, 0, 0, 0);
+      }
+      if (!p.desc_units) p.desc[team] = d;
+    }
+    __syncwarp();
+    load_rows<kN>(sm, p, smem_u32(ring), D / 16, walk);
+  } else if (warp < p.heads * p.head_warps) {
+    attend<D, kBf16, kN>(sm, p, ring, sums, walk, warp, lane);
+  }
+  // Streams without keys.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (stream_tiles<kWhole>(p, b, len) != 0) continue;
+    if (p.desc_units && !p.whole)
+      for (int u = tid; u < p.Hkv; u += C::kThreads) p.desc[b * p.Hkv + u] = make_int4(0, 0, 0, 0);
+    const long long rows = static_cast<long long>(p.q_len) * p.H;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + b * rows * (D * 2));
+    for (long long x = tid; x < rows * (D / 8); x += C::kThreads) o[x] = make_uint4(0, 0, 0, 0);
+    for (long long x = tid; x < rows; x += C::kThreads) p.lse[b * rows + x] = -CUDART_INF_F;
+  }
+}
+
+// The merge where each entry stands for a CTA's cut unit of every head (entries a
+// head: combine_many_parts of the attention kernel).  A block lists the cut units,
+// and takes chunks of eight rows of their heads in turn.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_heads(const FewParams p, int entries) {
+  constexpr int kThreadsM = D / 4 * kMergeUnits, kWarps = kThreadsM / 32;
+  __shared__ int4 cut[kMaxParts];
+  __shared__ int warp_cut[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  grid_dependency_wait();
+  int n_cut = 0;
+  for (int base = 0; base < entries; base += kThreadsM) {
+    const int4 d = base + tid < entries ? __ldcg(p.desc + base + tid) : make_int4(0, 0, 0, 0);
+    const unsigned ballot = __ballot_sync(0xFFFFFFFFu, d.w != 0);
+    if ((tid & 31) == 0) warp_cut[warp] = __popc(ballot);
+    __syncthreads();
+    int at = n_cut;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp && d.w != 0) cut[at + __popc(ballot & ((1u << (tid & 31)) - 1u))] = d;
+      at += warp_cut[w];
+    }
+    n_cut = at;
+    __syncthreads();
+  }
+  const int chunks = (p.q_len * p.G + kMergeUnits - 1) / kMergeUnits;
+  for (int item = blockIdx.x; item < n_cut * p.heads * chunks; item += gridDim.x) {
+    const int u = item / (p.heads * chunks), rest = item - u * p.heads * chunks, h = rest / chunks;
+    int4 d = cut[u];
+    d.y += h;
+    d.z += 2 * h;
+    merge_rows<D, kBf16, 1, 8, 1>(p, d, rest - h * chunks);
+  }
+}
+
+// ------------------------------------------------------------ host
+
+using Fn = void (*)(FewParams);
+using MergeFn = void (*)(FewParams, int);
+using PartsFn = void (*)(Params, int);
+struct Variant {
+  Fn attn;
+  MergeFn merge;
+  PartsFn parts, units;
+  int threads, warps, head_bytes, sum_bytes;
+};
+template <int D, bool kBf16, int kN>
+Variant variant() {
+  return {few_kernel<D, kBf16, kN>, combine_heads<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
+          Shape8<kN>::kThreads, Shape8<kN>::kWarps, static_cast<int>(sizeof(Head<kN>)), kSums<D, kN>};
+}
+
+constexpr int kSharedBytes = 232448;
+constexpr int kStageBytes = 40 << 10;      // a stage, about
+
+std::mutex g_mutex;
+bool g_ready[64][8];
+
+// Key heads a CTA: the most that divide Hkv and leave no more than a quarter of the warps idle.
+int heads_a_cta(int Hkv, int warps) {
+  int best = 1;
+  for (int h = 2; h <= warps && h <= Hkv; ++h)
+    if (Hkv % h == 0 && 4 * h * (warps / h) >= 3 * warps) best = h;
+  return best;
+}
+
+// Bytes of the longest run of steps that a CTA's heads have, from one multiple of 16 to another.
+int most_step_bytes(int Hkv, int heads, int each) {
+  int most = 0;
+  for (int h = 0; h < Hkv; h += heads) {
+    const int bytes = (((h + heads) * each + 15) & ~15) - ((h * each) & ~15);
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
+}  // namespace few
+
+// Rows a key head up to which this kernel takes a call.
+constexpr long long kFewRows = 16;
+bool few_rows(int q_len, int H, int Hkv) { return q_len * (H / Hkv) <= kFewRows; }
+int few_heads(int q_len, int H, int Hkv) {
+  return few::heads_a_cta(Hkv, q_len * (H / Hkv) <= 8 ? few::Shape8<1>::kWarps : few::Shape8<2>::kWarps);
+}
+
+int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid) {
+  using namespace few;
+  const int rows = c.q_len * (c.H / c.Hkv);
+  const bool bf16 = c.dtype == MLA_BF16;
+  static const Variant all[8] = {variant<64, true, 1>(),  variant<64, true, 2>(),  variant<64, false, 1>(),
+                                 variant<64, false, 2>(), variant<128, true, 1>(), variant<128, true, 2>(),
+                                 variant<128, false, 1>(), variant<128, false, 2>()};
+  const int n = (c.D == 128 ? 4 : 0) + (bf16 ? 0 : 2) + (rows > 8 ? 1 : 0);
+  const Variant& v = all[n];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_UNSUPPORTED_DEVICE;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_ready[dev][n]) {
+      if (cudaFuncSetAttribute(v.attn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes) != cudaSuccess) {
+        cudaGetLastError();
+        return MLA_ERR_LAUNCH;
+      }
+      g_ready[dev][n] = true;
+    }
+  }
+  FewParams p = {};
+  static_cast<Params&>(p) = shared;
+  p.heads = heads_a_cta(c.Hkv, v.warps);
+  p.head_warps = v.warps / p.heads;
+  p.members = p.head_members = p.heads;
+  p.head_sets = c.Hkv / p.heads;
+  p.by_members = Divisor(p.heads);
+  p.groups = p.group_members = p.group_sets = 1;
+  p.by_group_members = p.by_group_sets = Divisor(1);
+  // Whole rows where a CTA has all heads, else their codes and their steps apart.
+  p.split = p.heads != c.Hkv;
+  p.codes = p.split ? p.heads * (c.D / 2) : fp4::row_bytes(c.Hkv, c.D);
+  // Rows lie an odd multiple of 32 bytes apart, which is what kOrder wants.
+  const int row = p.codes + (p.split ? most_step_bytes(c.Hkv, p.heads, c.D / 16) : 0);
+  p.pitch = ((row + 31) / 32 | 1) * 32;
+  p.stage_keys = 16 * p.head_warps;
+  while (2 * p.stage_keys <= kKeys && 4 * p.stage_keys * p.pitch <= kStageBytes) p.stage_keys *= 2;
+  const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), stage = 2 * p.stage_keys * p.pitch;
+  p.stages = (kSharedBytes - fixed) / stage;
+  if (p.stages > kMostStages) p.stages = kMostStages;
+  if (p.stages < 2) return MLA_ERR_SHAPE;                  // (no number of heads gives less)
+
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(v.threads, 1, 1);
+  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, v.attn, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_LAUNCH;
+  }
+  if (p.whole) return MLA_OK;
+  const int entries = p.desc_units ? c.B * c.Hkv : grid, pairs = (rows + 1) / 2;
+  cfg.blockDim = dim3(c.D / 4 * kMergeUnits, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  cudaError_t err;
+  if (p.desc_units && static_cast<long long>(entries) * pairs <= 3 * grid && grid / (c.B * p.head_sets) >= kManyParts) {
+    cfg.gridDim = dim3(pairs, entries, 1);
+    err = cudaLaunchKernelEx(&cfg, v.parts, static_cast<Params>(p), entries);
+  } else {
+    const long long chunks = static_cast<long long>(entries) * (p.desc_units ? 1 : p.heads) * 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(chunks < 8 * grid ? chunks : 8 * grid), 1, 1);
+    err = p.desc_units ? cudaLaunchKernelEx(&cfg, v.units, static_cast<Params>(p), entries)
+                       : cudaLaunchKernelEx(&cfg, v.merge, p, entries);
+  }
+  if (err != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_LAUNCH;
+  }
+  return MLA_OK;
+}
+
+}  // namespace gqa
+}  // namespace mla
