@@ -19,10 +19,12 @@
 // conversions (78 values a cycle and SM measured) take about half of that time.
 //
 // Split.  Equal runs of 64-key tiles as in the attention kernel, but a CTA takes all (up
-// to 16) key heads of a run: whole rows of the cache come in by bulk copies of one row
-// each, any page size, by a warp of their own.  Its other warps are shared out
-// among the heads; those of one head take 16 keys in turn and are put together at a
-// unit's end.  The heads of a CTA count as a team's members for the merge.
+// to 16) key heads of a run: whole rows of the cache come in by TMA boxes of eight rows
+// or more (a bulk copy a row took 64 cycles each, 2.6 TB/s in all; boxes of eight 7.1),
+// or, where pages are not a multiple of eight rows, by four warps' 16-byte copies.
+// The other warps are shared out among the heads; those of one head take 16 keys in
+// turn and are put together at a unit's end.  The heads of a CTA count as a team's
+// members for the merge.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,39 +41,76 @@ namespace gqa {
 namespace few {
 
 constexpr int kMostStages = 8;
-constexpr uint32_t kOrder = 0x57463120u;   // key of row i of 8, four bits each
+constexpr int kLoaders = 4;                // warps that load
 
 struct FewParams : Params {
   int heads, head_warps;           // key heads a CTA, warps a head
-  int stage_keys, stages, pitch;   // a stage: stage_keys rows of K, then of V, pitch bytes apart
-  int codes;                       // bytes copied of a row: all of them,
-  int split;                       // or (not 0) the heads' codes, and their steps on their own
+  // A stage: stage_keys rows of K, then of V (stage_bytes / 2 behind).  Whole rows where a CTA
+  // has all heads; else (split) the heads' codes, then their steps, which begin at a
+  // multiple of 16 bytes.
+  int stage_keys, stages, stage_bytes, split;
+  int code_pitch, step_pitch;      // bytes between rows
+  int code_bytes, step_bytes;      // copied of a row (step_bytes: split)
+  int row_end;                     // bytes of a pool row
+  uint32_t order;                  // key of row i of 8, four bits each
+  Divisor by_units;                // 16-byte units of a row
 };
 
 // kN: query rows in eights; more of them want more registers.
 template <int kN>
 struct Shape8 {
   static constexpr int kWarps = kN == 1 ? 16 : 8;
-  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kThreads = 32 * (kWarps + kLoaders);
+};
+
+// A warp's place in its run, kept in shared memory between the ends of segments: the
+// stages want all registers.
+struct Place {
+  Walk<kWhole> walk;
+  Segment s;
+  int seg;
 };
 
 template <int kN>
 struct __align__(128) Head {
   uint64_t full[kMostStages], empty[kMostStages], meet[Shape8<kN>::kWarps];
   float2 ml[Shape8<kN>::kWarps][8 * kN];
-  int warp_sum[Shape8<kN>::kWarps + 1], start_b, start_pre;
+  Place place[Shape8<kN>::kWarps];
+  int warp_sum[Shape8<kN>::kWarps + kLoaders], start_b, start_pre;
   uint32_t abort_flag;
 };
+
+}  // namespace few
+template <int kN>
+struct InlineWaits<few::Head<kN>> {
+  static constexpr bool value = true;
+};
+namespace few {
 
 template <int D>
 constexpr int kSumPitch = D + 4;           // floats a row of the warps' sums
 template <int D, int kN>
 constexpr int kSums = Shape8<kN>::kWarps * 8 * kN * kSumPitch<D> * 4;
 
-__device__ __forceinline__ void copy_row(uint32_t dst, const uint8_t* src, int bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at));
+  return r;
+}
+// kWords 32-bit words.
+template <int kWords>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
+  if constexpr (kWords == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+  else if constexpr (kWords == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -92,46 +131,48 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t low2(uint32_t x) { return __byte_perm(x, x, 0x1010); }
 __device__ __forceinline__ uint32_t high2(uint32_t x) { return __byte_perm(x, x, 0x3232); }
 
-// The last warp: a row of K and one of V a lane.
+struct Maps {
+  CUtensorMap codes[2], steps[2];            // of K and V
+};
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(bar)
+               : "memory");
+}
+
+// The first loader: a box of K and one of V a lane.
 template <int kN>
-__device__ __forceinline__ void load_rows(Head<kN>& sm, const FewParams& p, uint32_t ring, int step_bytes, Walk<kWhole> w) {
-  const int lane = threadIdx.x & 31;
-  const bool withheld = p.test_stall && blockIdx.x == 0;
-  const int stage_bytes = 2 * p.stage_keys * p.pitch;
+__device__ __forceinline__ void load_boxes(Head<kN>& sm, const FewParams& p, const Maps& maps, uint32_t ring, int each, Walk<kWhole> w) {
+  const int lane = threadIdx.x & 31, R = p.box_rows;
   int stage = 0, issued = 0;
   uint32_t phase = 0;
   Segment s;
   while (w.next(p, s)) {
     const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys);
-    // The heads' steps, from one multiple of 16 bytes to another.
-    const int from = p.split ? (s.head * step_bytes) & ~15 : 0;
-    const int steps = p.split ? (((s.head + p.heads) * step_bytes + 15) & ~15) - from : 0;
-    const int codes_at = p.split ? s.head * step_bytes * 8 : 0;
-    const int row_bytes = p.codes + steps;
-    int next = begin + lane < end ? table_entry(p, s.b, begin + lane) : 0;
+    const int code_x = p.split ? s.head * each : 0;                          // in 8 bytes
+    const int step_x = (p.steps_at + ((s.head * each) & ~15)) >> 3;
+    auto entry_of = [&](int k0) {
+      const int key = k0 + lane * R;
+      return lane * R < p.stage_keys && key < end ? table_entry(p, s.b, key) : 0;
+    };
+    int next = entry_of(begin);
     for (int k0 = begin; k0 < end; k0 += p.stage_keys) {
+      const int n = (min(p.stage_keys, end - k0) + R - 1) / R;               // boxes
+      const int row = lane < n ? pool_row(p, next, k0 + lane * R) : 0;
+      next = entry_of(k0 + p.stage_keys);
       if (!wait(sm, sm.empty[stage], phase ^ 1, p)) goto out;
       const uint32_t bar = smem_u32(&sm.full[stage]);
-      const int n = min(p.stage_keys, end - k0);
-      if (withheld && issued == 0) goto out;               // this load never comes
-      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * n * row_bytes);
+      if (p.test_stall && blockIdx.x == 0 && issued == 0) goto out;          // this load never comes
+      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * n * R * (p.code_bytes + p.step_bytes));
       __syncwarp();
-      for (int r = lane; r - lane < n; r += 32) {
-        const int entry = next, key = k0 + r;
-        // (the entry of this lane's next row, in this stage or the next)
-        const int ahead = r + 32 - lane < n ? key + 32 : k0 + p.stage_keys + lane;
-        next = ahead < end ? table_entry(p, s.b, ahead) : 0;
-        if (r < n) {
-          const long long row = pool_row(p, entry, key);
-          const uint32_t dst = ring + stage * stage_bytes + r * p.pitch, dst_v = dst + p.stage_keys * p.pitch;
-          const uint8_t* const k = p.k + row * p.k_stride[1];
-          const uint8_t* const v = p.v + row * p.v_stride[1];
-          copy_row(dst, k + codes_at, p.codes, bar);
-          copy_row(dst_v, v + codes_at, p.codes, bar);
-          if (p.split) {
-            copy_row(dst + p.codes, k + p.steps_at + from, steps, bar);
-            copy_row(dst_v + p.codes, v + p.steps_at + from, steps, bar);
-          }
+      if (lane < n) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t dst = ring + stage * p.stage_bytes + v * (p.stage_bytes >> 1);
+          tma_box(dst + lane * R * p.code_pitch, &maps.codes[v], code_x, row, bar);
+          if (p.split)
+            tma_box(dst + p.stage_keys * p.code_pitch + lane * R * p.step_pitch, &maps.steps[v], step_x, row, bar);
         }
       }
       ++issued;
@@ -146,6 +187,59 @@ out:
     mbar_wait(smem_u32(&sm.full[n % p.stages]), (n / p.stages) & 1, kWaitNs / 2);
 }
 
+// All loaders where no box fits the pages: a quarter of a stage's rows each, 16 bytes a lane.
+template <int kN>
+__device__ __forceinline__ void load_rows(Head<kN>& sm, const FewParams& p, uint32_t ring, int each, Walk<kWhole> w, int loader) {
+  const int lane = threadIdx.x & 31, units = static_cast<int>(p.by_units.d), code_units = p.code_bytes >> 4;
+  const int keys = p.stage_keys / kLoaders, first = loader * keys;           // (no more than 64)
+  int stage = 0;
+  uint32_t phase = 0;
+  Segment s;
+  while (w.next(p, s)) {
+    const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys);
+    const int code_at = p.split ? s.head * each * 8 : 0, step_at = p.steps_at + ((s.head * each) & ~15);
+    auto entry_of = [&](int k0, int h) {
+      const int r = h * 32 + lane, key = k0 + first + r;
+      return r < keys && key < end ? table_entry(p, s.b, key) : 0;
+    };
+    int next[2] = {entry_of(begin, 0), entry_of(begin, 1)};
+    for (int k0 = begin; k0 < end; k0 += p.stage_keys) {
+      const int n = min(keys, end - k0 - first);                             // rows (none: negative)
+      int row[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        row[h] = h * 32 + lane < n ? pool_row(p, next[h], k0 + first + h * 32 + lane) : 0;
+        next[h] = entry_of(k0 + p.stage_keys, h);
+      }
+      if (!wait(sm, sm.empty[stage], phase ^ 1, p)) goto out;
+      const uint32_t dst = ring + stage * p.stage_bytes;
+      for (int x = lane; x - lane < n * units; x += 32) {
+        const int r = p.by_units.of(x), u = x - r * units;
+        const int lo = __shfl_sync(0xFFFFFFFFu, row[0], r & 31), hi = __shfl_sync(0xFFFFFFFFu, row[1], r & 31);
+        if (x >= n * units) continue;
+        const long long at = r < 32 ? lo : hi;
+        const int key = first + r;
+        const bool step = u >= code_units;
+        // (Of a split row's steps, those behind the row's end are not there.)
+        const int from = step ? step_at + (u - code_units) * 16 : code_at + u * 16;
+        const uint32_t to = dst + (step ? p.stage_keys * p.code_pitch + key * p.step_pitch + (u - code_units) * 16
+                                        : key * p.code_pitch + u * 16);
+        const bool there = !step || from < p.row_end;
+        cp_async_16(to, p.k + at * p.k_stride[1] + (there ? from : 0), there);
+        cp_async_16(to + (p.stage_bytes >> 1), p.v + at * p.v_stride[1] + (there ? from : 0), there);
+      }
+      if (!(p.test_stall && blockIdx.x == 0))
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.full[stage])) : "memory");
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+out:
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // All warps of a head are here; false: some wait has run out.
 template <int kN>
 __device__ __forceinline__ bool meet(Head<kN>& sm, const FewParams& p, int head, uint32_t& times) {
@@ -154,35 +248,62 @@ __device__ __forceinline__ bool meet(Head<kN>& sm, const FewParams& p, int head,
   return wait(sm, sm.meet[head], times++ & 1u, p);
 }
 
+// Whether draft i of stream b sees draft d; whether some draft sees a key of the run.
+__device__ __forceinline__ bool sees(const Params& p, int b, int i, int d) {
+  const int words = (p.q_len + 31) >> 5;
+  return p.mask[(static_cast<size_t>(b) * p.q_len + i) * words + (d >> 5)] >> (d & 31) & 1u;
+}
+__device__ __forceinline__ bool used(const Params& p, int b, int key, int prefix, int end) {
+  if (key >= end || key < prefix) return key < end;
+  bool any = false;
+  for (int i = 0; i < p.q_len; ++i) any |= sees(p, b, i, key - prefix);
+  return any;
+}
+
 template <int D, bool kBf16, int kN>
-__device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const uint8_t* ring, float* sums, Walk<kWhole> w,
-                                       int warp, int lane) {
+__device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_t ring, float* sums, int warp, int lane) {
   constexpr int kTiles = D / 16;             // of 16 dimensions (or rows of O^T)
   constexpr int kQ = D / 8;                  // registers of a row of Q a lane
   constexpr float kShift = 7.f;              // (see the attention kernel's softmax)
+  constexpr float kNothing = -1e30f;
   const int g = lane >> 2, c = lane & 3;
   const int head_local = warp / p.head_warps, j = warp - head_local * p.head_warps;
   const int rows = p.q_len * p.G;
-  const int key_g = kOrder >> (4 * g) & 7, key_c = kOrder >> (8 * c) & 7, key_c1 = kOrder >> (8 * c + 4) & 7;
-  const int stage_bytes = 2 * p.stage_keys * p.pitch, v_at = p.stage_keys * p.pitch;
-  int stage = 0, seg = 0;
+  const int key_g = p.order >> (4 * g) & 7, key_c = p.order >> (8 * c) & 7, key_c1 = p.order >> (8 * c + 4) & 7;
+  // Where this lane reads, from a stage's start and of the first 16 keys: K's codes (and
+  // their steps, from where the head's steps are), the same of V, and from there to
+  // the second key's.
+  const int k_codes = key_g * p.code_pitch + head_local * (D / 2) + c * (D / 8), k_steps = key_g * p.step_pitch + c * (D / 64);
+  const int v_codes = (p.stage_bytes >> 1) + key_c * p.code_pitch + head_local * (D / 2) + g * (D / 16);
+  const int v_steps = (p.stage_bytes >> 1) + key_c * p.step_pitch + (D == 128 ? g : g >> 1);
+  int stage = 0;
   uint32_t phase = 0, met = 0;
-  Segment s;
-  for (; w.next(p, s); ++seg) {
-    const int head = s.head + head_local;
+  while (true) {
+    Segment s;
+    {
+      Walk<kWhole> w = sm.place[warp].walk;
+      if (!w.next(p, s)) return;
+      __syncwarp();
+      if (lane == 0) {
+        sm.place[warp].walk = w;
+        sm.place[warp].s = s;
+        ++sm.place[warp].seg;
+      }
+    }
     const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys), prefix = s.S - p.q_len;
     // ---- rows of Q: row 8 t + g, this lane's quarter; in fp16, brought to its range
     // by a power of two where they are bf16.
     uint32_t q[kN][kQ];
     float a[kN][2];                          // scale of rows 8 t + 2 c, + 1
-    uint64_t mask[kN][2];
-    float m[kN][2], l[kN][2], o[kN][kTiles][4];
+    // ms: what a row's exponents are taken off, its maximum less kShift; kNothing
+    // until it has seen a key.
+    float ms[kN][2], l[kN][2], o[kN][kTiles][4];
 #pragma unroll
     for (int t = 0; t < kN; ++t) {
       const int R = 8 * t + g, i = p.by_G.of(R);
       float unit = 1.f;
       const uint8_t* const src =
-          p.q + s.b * p.q_stride[0] + i * p.q_stride[1] + (head * p.G + (R - i * p.G)) * p.q_stride[2] + c * (D / 2);
+          p.q + s.b * p.q_stride[0] + i * p.q_stride[1] + ((s.head + head_local) * p.G + (R - i * p.G)) * p.q_stride[2] + c * (D / 2);
 #pragma unroll
       for (int e = 0; e < kQ / 4; ++e) {
         const uint4 x = R < rows ? reinterpret_cast<const uint4*>(src)[e] : make_uint4(0, 0, 0, 0);
@@ -207,16 +328,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         a[t][e] = p.scale_log2 * __shfl_sync(0xFFFFFFFFu, unit, (2 * c + e) * 4);
-        const int row = 8 * t + 2 * c + e, draft = p.by_G.of(row);
-        mask[t][e] = 0;
-        if (row < rows) {
-          const int words = (p.q_len + 31) >> 5;
-          const uint32_t* const word = p.mask + (static_cast<size_t>(s.b) * p.q_len + draft) * words;
-          mask[t][e] = word[0];
-          if (words > 1) mask[t][e] |= static_cast<uint64_t>(word[1]) << 32;
-          if (p.q_len < 64) mask[t][e] &= (1ull << p.q_len) - 1ull;
-        }
-        m[t][e] = -CUDART_INF_F;
+        ms[t][e] = kNothing;
         l[t][e] = 0.f;
       }
 #pragma unroll
@@ -224,20 +336,16 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][x][e] = 0.f;
     }
-    uint64_t used = 0;                       // drafts that some row sees
-#pragma unroll
-    for (int t = 0; t < kN; ++t) used |= mask[t][0] | mask[t][1];
-    used |= __shfl_xor_sync(0xFFFFFFFFu, used, 1);
-    used |= __shfl_xor_sync(0xFFFFFFFFu, used, 2);
-    const int steps_at = (p.split ? p.codes + ((s.head * (D / 16)) & 15) : p.steps_at) + head_local * (D / 16);
+    // Of the stage's row 0: this head's steps.
+    const int steps_at = (p.split ? p.stage_keys * p.code_pitch + ((s.head * (D / 16)) & 15) : p.steps_at) + head_local * (D / 16);
 
     // ---- the run's stages
     for (int k1 = begin; k1 < end; k1 += p.stage_keys) {
       if (!wait(sm, sm.full[stage], phase, p)) return;
-      const uint8_t* const base = ring + stage * stage_bytes;
-      for (int step = j; step * 16 < p.stage_keys; step += p.head_warps) {
-        const int k0 = k1 + step * 16;
-        if (k0 >= end) break;
+      const uint32_t base = ring + stage * p.stage_bytes;
+      const int last = min(k1 + p.stage_keys, end);
+      for (int k0 = k1 + 16 * j; k0 < last; k0 += 16 * p.head_warps) {
+        const uint32_t codes = base + (k0 - k1) * p.code_pitch, steps = base + (k0 - k1) * p.step_pitch + steps_at;
         const bool edge = k0 + 16 > min(prefix, end);
         float x[kN][4];
 #pragma unroll
@@ -246,128 +354,129 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
           for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
         {
           // S^T = K Q^T
-          const uint8_t* const ka = base + (step * 16 + key_g) * p.pitch;
-          const uint8_t* const kb = ka + 8 * p.pitch;
           uint32_t wa[D / 32], wb[D / 32], sa, sb;
+          lds<D / 32>(codes + k_codes, wa);
+          lds<D / 32>(codes + k_codes + 8 * p.code_pitch, wb);
           if constexpr (D == 128) {
-            const uint4 va = *reinterpret_cast<const uint4*>(ka + head_local * 64 + c * 16);
-            const uint4 vb = *reinterpret_cast<const uint4*>(kb + head_local * 64 + c * 16);
-            wa[0] = va.x, wa[1] = va.y, wa[2] = va.z, wa[3] = va.w;
-            wb[0] = vb.x, wb[1] = vb.y, wb[2] = vb.z, wb[3] = vb.w;
-            sa = fp4::from_e4m3x2(*reinterpret_cast<const uint16_t*>(ka + steps_at + 2 * c));
-            sb = fp4::from_e4m3x2(*reinterpret_cast<const uint16_t*>(kb + steps_at + 2 * c));
+            sa = fp4::from_e4m3x2(lds_u16(steps + k_steps));
+            sb = fp4::from_e4m3x2(lds_u16(steps + k_steps + 8 * p.step_pitch));
           } else {
-            const uint2 va = *reinterpret_cast<const uint2*>(ka + head_local * 32 + c * 8);
-            const uint2 vb = *reinterpret_cast<const uint2*>(kb + head_local * 32 + c * 8);
-            wa[0] = va.x, wa[1] = va.y;
-            wb[0] = vb.x, wb[1] = vb.y;
-            sa = fp4::from_e4m3x2(ka[steps_at + c]);
-            sb = fp4::from_e4m3x2(kb[steps_at + c]);
+            sa = fp4::from_e4m3x2(lds_u8(steps + k_steps));
+            sb = fp4::from_e4m3x2(lds_u8(steps + k_steps + 8 * p.step_pitch));
           }
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) {
             uint32_t ha[4], hb[4];
             fp4::from_e2m1x8(wa[e], ha);
             fp4::from_e2m1x8(wb[e], hb);
-            const uint32_t ta = e < 2 ? low2(sa) : high2(sa), tb = e < 2 ? low2(sb) : high2(sb);
+            const uint32_t fa = e < 2 ? low2(sa) : high2(sa), fb = e < 2 ? low2(sb) : high2(sb);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint32_t f[4] = {times(ha[2 * y], ta), times(hb[2 * y], tb), times(ha[2 * y + 1], ta),
-                                     times(hb[2 * y + 1], tb)};
+              const uint32_t f[4] = {times(ha[2 * y], fa), times(hb[2 * y], fb), times(ha[2 * y + 1], fa),
+                                     times(hb[2 * y + 1], fb)};
 #pragma unroll
               for (int t = 0; t < kN; ++t) mma(x[t], f, q[t][4 * e + 2 * y], q[t][4 * e + 2 * y + 1]);
             }
           }
         }
         // ---- softmax: x[t][0..1] are key g's scores of rows 2 c, 2 c + 1, x[t][2..3] key g + 8's.
-        bool grow = false;
+        uint32_t hidden = 0;
+        if (edge) {
 #pragma unroll
-        for (int t = 0; t < kN; ++t) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[t][e] *= a[t][e & 1];
-          if (edge) {
+          for (int t = 0; t < kN; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = k0 + key_g + (e >> 1) * 8;
-              const bool seen = key < end && (key < prefix || (mask[t][e & 1] >> (key - prefix) & 1ull));
-              if (!seen) x[t][e] = -CUDART_INF_F;
+              const int key = k0 + key_g + (e >> 1) * 8, row = 8 * t + 2 * c + (e & 1);
+              if (key >= end || (key >= prefix && !(row < rows && sees(p, s.b, p.by_G.of(row), key - prefix))))
+                hidden |= 1u << (4 * t + e);
             }
-          }
-          grow |= fmaxf(x[t][0], x[t][2]) > m[t][0] + kLazy || fmaxf(x[t][1], x[t][3]) > m[t][1] + kLazy;
         }
+        float y[kN][4];
+        auto shifted = [&]() {
+#pragma unroll
+          for (int t = 0; t < kN; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[t][e] = fmaf(x[t][e], a[t][e & 1], -ms[t][e & 1]);
+              if (edge && (hidden >> (4 * t + e) & 1u)) y[t][e] = -CUDART_INF_F;
+            }
+        };
+        shifted();
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < kN; ++t)
+          grow |= fmaxf(fmaxf(y[t][0], y[t][1]), fmaxf(y[t][2], y[t][3])) > kLazy + kShift;
         if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
           for (int t = 0; t < kN; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(x[t][e], x[t][e + 2]);
+              float top = -CUDART_INF_F;
+#pragma unroll
+              for (int z = e; z < 4; z += 2)
+                if (!(hidden >> (4 * t + z) & 1u)) top = fmaxf(top, x[t][z] * a[t][e]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-              if (top > m[t][e] + kLazy) {
-                const float alpha = ex2(m[t][e] - top);    // 0 when nothing was visible before
-                m[t][e] = top;
+              if (top - ms[t][e] > kLazy + kShift) {
+                const float alpha = ex2(ms[t][e] - (top - kShift));    // 0 when nothing was visible before
+                ms[t][e] = top - kShift;
                 l[t][e] *= alpha;
 #pragma unroll
-                for (int y = 0; y < kTiles; ++y) {
-                  o[t][y][e] *= alpha;
-                  o[t][y][e + 2] *= alpha;
+                for (int z = 0; z < kTiles; ++z) {
+                  o[t][z][e] *= alpha;
+                  o[t][z][e + 2] *= alpha;
                 }
               }
             }
+          shifted();
         }
         uint32_t pb[kN][2];
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
-          const float m0 = m[t][0] == -CUDART_INF_F ? 0.f : m[t][0] - kShift;
-          const float m1 = m[t][1] == -CUDART_INF_F ? 0.f : m[t][1] - kShift;
-          const float p0 = ex2(x[t][0] - m0), p1 = ex2(x[t][1] - m1), p2 = ex2(x[t][2] - m0), p3 = ex2(x[t][3] - m1);
+          const float p0 = ex2(y[t][0]), p1 = ex2(y[t][1]), p2 = ex2(y[t][2]), p3 = ex2(y[t][3]);
           l[t][0] += p0 + p2;
           l[t][1] += p1 + p3;
           pb[t][0] = transposed(pack2<false>(p0, p1));
           pb[t][1] = transposed(pack2<false>(p2, p3));
         }
         {
-          // O^T += V^T P, keys 2 c, 2 c + 1 and those 8 behind
-          uint32_t f[kTiles][4];
+          // O^T += V^T P: two pairs of keys, 2 c and 2 c + 1 and those 8 behind.
+          const int code_next = (key_c1 - key_c) * p.code_pitch, step_next = (key_c1 - key_c) * p.step_pitch;
+          uint32_t w[2][2][D / 64], scale[2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint8_t* const v0 = base + v_at + (step * 16 + 8 * half + key_c) * p.pitch;
-            const uint8_t* const v1 = base + v_at + (step * 16 + 8 * half + key_c1) * p.pitch;
-            const int step_at = steps_at + (D == 128 ? g : g >> 1);
-            uint32_t s0 = v0[step_at], s1 = v1[step_at];
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = steps + v_steps + 8 * h * p.step_pitch;
+            uint32_t s0 = lds_u8(at), s1 = lds_u8(at + step_next);
             if (edge) {
               // Rows past the run, and drafts that none sees, may hold anything.
-              const int t0 = k0 + 8 * half + key_c, t1 = k0 + 8 * half + key_c1;
-              if (!(t0 < end && (t0 < prefix || (used >> (t0 - prefix) & 1ull)))) s0 = 0;
-              if (!(t1 < end && (t1 < prefix || (used >> (t1 - prefix) & 1ull)))) s1 = 0;
+              if (!used(p, s.b, k0 + 8 * h + key_c, prefix, end)) s0 = 0;
+              if (!used(p, s.b, k0 + 8 * h + key_c1, prefix, end)) s1 = 0;
             }
-            const uint32_t scale = fp4::from_e4m3x2(s0 | s1 << 8);
-            uint32_t w0[D / 64], w1[D / 64];
-            if constexpr (D == 128) {
-              const uint2 x0 = *reinterpret_cast<const uint2*>(v0 + head_local * 64 + g * 8);
-              const uint2 x1 = *reinterpret_cast<const uint2*>(v1 + head_local * 64 + g * 8);
-              w0[0] = x0.x, w0[1] = x0.y;
-              w1[0] = x1.x, w1[1] = x1.y;
-            } else {
-              w0[0] = *reinterpret_cast<const uint32_t*>(v0 + head_local * 32 + g * 4);
-              w1[0] = *reinterpret_cast<const uint32_t*>(v1 + head_local * 32 + g * 4);
-            }
+            scale[h] = fp4::from_e4m3x2(s0 | s1 << 8);
+            lds<D / 64>(codes + v_codes + 8 * h * p.code_pitch, w[h][0]);
+            lds<D / 64>(codes + v_codes + 8 * h * p.code_pitch + code_next, w[h][1]);
+          }
 #pragma unroll
-            for (int e = 0; e < D / 64; ++e) {
-              uint32_t even[4], odd[4];
-              fp4::from_e2m1x8((w0[e] & 0x0F0F0F0Fu) | (w1[e] << 4 & 0xF0F0F0F0u), even);
-              fp4::from_e2m1x8((w0[e] >> 4 & 0x0F0F0F0Fu) | (w1[e] & 0xF0F0F0F0u), odd);
+          for (int e = 0; e < D / 64; ++e) {
+            // Tiles 4 e and 4 e + 1: the even dimensions of the eight; then the odd ones.
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                f[4 * e + y][2 * half] = times(even[y], scale);
-                f[4 * e + y][2 * half + 1] = times(odd[y], scale);
+            for (int odd = 0; odd < 2; ++odd) {
+              uint32_t x2[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a0 = w[h][0][e], a1 = w[h][1][e];
+                fp4::from_e2m1x8(odd ? (a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u)
+                                     : (a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), x2[h]);
+              }
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t f[4] = {times(x2[0][2 * z], scale[0]), times(x2[0][2 * z + 1], scale[0]),
+                                       times(x2[1][2 * z], scale[1]), times(x2[1][2 * z + 1], scale[1])};
+#pragma unroll
+                for (int t = 0; t < kN; ++t) mma(o[t][4 * e + 2 * odd + z], f, pb[t][0], pb[t][1]);
               }
             }
           }
-#pragma unroll
-          for (int y = 0; y < kTiles; ++y)
-#pragma unroll
-            for (int t = 0; t < kN; ++t) mma(o[t][y], f[y], pb[t][0], pb[t][1]);
         }
       }
       __syncwarp();
@@ -379,8 +488,11 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
     }
 
     // ---- the unit's end: the warps of a head are put together.
+    __syncwarp();
+    s = sm.place[warp].s;
+    const int head = s.head + head_local;
     const bool direct = s.n == s.nt;
-    const int slot = 2 * (static_cast<int>(blockIdx.x) * p.heads + head_local) + (seg > 0 ? 1 : 0);
+    const int slot = 2 * (static_cast<int>(blockIdx.x) * p.heads + head_local) + (sm.place[warp].seg > 1 ? 1 : 0);
     float w_mine[kN][2], m_all[kN][2], l_all[kN][2];
 #pragma unroll
     for (int t = 0; t < kN; ++t)
@@ -388,11 +500,11 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], d);
-        m[t][e] = m[t][e] == -CUDART_INF_F ? -CUDART_INF_F : m[t][e] - kShift;
-        m_all[t][e] = m[t][e];
+        if (ms[t][e] == kNothing) ms[t][e] = -CUDART_INF_F;
+        m_all[t][e] = ms[t][e];
         l_all[t][e] = l[t][e];
         w_mine[t][e] = 1.f;
-        if (p.head_warps > 1 && g == 0) sm.ml[warp][8 * t + 2 * c + e] = make_float2(m[t][e], l[t][e]);
+        if (p.head_warps > 1 && g == 0) sm.ml[warp][8 * t + 2 * c + e] = make_float2(ms[t][e], l[t][e]);
       }
     if (p.head_warps > 1) {
       if (!meet(sm, p, head_local, met)) return;
@@ -406,7 +518,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
             const float2 y = sm.ml[head_local * p.head_warps + x][8 * t + 2 * c + e];
             sum += (y.x == -CUDART_INF_F ? 0.f : ex2(y.x - top)) * y.y;
           }
-          w_mine[t][e] = m[t][e] == -CUDART_INF_F ? 0.f : ex2(m[t][e] - top);
+          w_mine[t][e] = ms[t][e] == -CUDART_INF_F ? 0.f : ex2(ms[t][e] - top);
           m_all[t][e] = top;
           l_all[t][e] = sum;
         }
@@ -429,8 +541,9 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
         float v[2 * kTiles];
 #pragma unroll
         for (int y = 0; y < kTiles; ++y) {
-          v[2 * y] = o[t][y][e] * by;
-          v[2 * y + 1] = o[t][y][e + 2] * by;
+          const int at = (y >> 2) * 8 + (y & 1) * 4 + (y >> 1 & 1);
+          v[at] = o[t][y][e] * by;
+          v[at + 2] = o[t][y][e + 2] * by;
         }
         if (p.head_warps > 1) {
           float4* const to = reinterpret_cast<float4*>(sums + (warp * 8 * kN + row) * kSumPitch<D> + g * (D / 8));
@@ -474,7 +587,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, const u
 }
 
 template <int D, bool kBf16, int kN>
-__global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const __grid_constant__ Maps maps, const FewParams p) {
   using C = Shape8<kN>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Head<kN>& sm = *reinterpret_cast<Head<kN>*>(smem_raw);
@@ -483,7 +596,7 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const FewP
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
     if (lane < p.stages) {
-      mbar_init(smem_u32(&sm.full[lane]), 1);
+      mbar_init(smem_u32(&sm.full[lane]), p.box_rows ? 1 : 32 * kLoaders);
       mbar_init(smem_u32(&sm.empty[lane]), p.heads * p.head_warps);
     }
     if (lane < p.heads) mbar_init(smem_u32(&sm.meet[lane]), p.head_warps);
@@ -514,7 +627,7 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const FewP
   __syncthreads();
   int before = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < C::kWarps + 1; ++i) {
+  for (int i = 0; i < C::kWarps + kLoaders; ++i) {
     if (i == warp) before = total;
     total += sm.warp_sum[i];
   }
@@ -536,8 +649,8 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const FewP
   const bool any = t0 < total;
   const Walk<kWhole> walk(p, 0, t0, any ? runs.start(team + 1) : total, any ? sm.start_b : 0, any ? sm.start_pre : 0);
 
-  if (warp == C::kWarps) {
-    if (lane == 0 && !p.whole) {
+  if (warp >= C::kWarps) {
+    if (warp == C::kWarps && lane == 0 && !p.whole) {
       // The merge's list: the units that start in this run and are cut (see note_cut_units).
       int4 d = make_int4(0, 0, 0, 0);
       Walk<kWhole> w = walk;
@@ -554,9 +667,15 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const FewP
       if (!p.desc_units) p.desc[team] = d;
     }
     __syncwarp();
-    load_rows<kN>(sm, p, smem_u32(ring), D / 16, walk);
+    if (p.box_rows == 0) load_rows<kN>(sm, p, smem_u32(ring), D / 16, walk, warp - C::kWarps);
+    else if (warp == C::kWarps) load_boxes<kN>(sm, p, maps, smem_u32(ring), D / 16, walk);
   } else if (warp < p.heads * p.head_warps) {
-    attend<D, kBf16, kN>(sm, p, ring, sums, walk, warp, lane);
+    if (lane == 0) {
+      sm.place[warp].walk = walk;
+      sm.place[warp].seg = 0;
+    }
+    __syncwarp();
+    attend<D, kBf16, kN>(sm, p, smem_u32(ring), sums, warp, lane);
   }
   // Streams without keys.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -607,7 +726,7 @@ __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_heads(const FewPa
 
 // ------------------------------------------------------------ host
 
-using Fn = void (*)(FewParams);
+using Fn = void (*)(Maps, FewParams);
 using MergeFn = void (*)(FewParams, int);
 using PartsFn = void (*)(Params, int);
 struct Variant {
@@ -685,18 +804,43 @@ int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid
   p.by_members = Divisor(p.heads);
   p.groups = p.group_members = p.group_sets = 1;
   p.by_group_members = p.by_group_sets = Divisor(1);
-  // Whole rows where a CTA has all heads, else their codes and their steps apart.
   p.split = p.heads != c.Hkv;
-  p.codes = p.split ? p.heads * (c.D / 2) : fp4::row_bytes(c.Hkv, c.D);
-  // Rows lie an odd multiple of 32 bytes apart, which is what kOrder wants.
-  const int row = p.codes + (p.split ? most_step_bytes(c.Hkv, p.heads, c.D / 16) : 0);
-  p.pitch = ((row + 31) / 32 | 1) * 32;
+  p.row_end = fp4::row_bytes(c.Hkv, c.D);
+  p.code_bytes = p.split ? p.heads * (c.D / 2) : p.row_end;
+  p.step_bytes = p.split ? most_step_bytes(c.Hkv, p.heads, c.D / 16) : 0;
+  p.code_pitch = p.code_bytes;
+  p.step_pitch = p.split ? p.step_bytes : p.code_bytes;
+  p.by_units = Divisor((p.code_bytes + p.step_bytes) / 16);
+  // Rows 2 i and 2 i + 1 of K are read together, 64 bytes each, and rows 0, 2, 4 and 6 of
+  // V, 32 bytes each: keys whose rows lie in different banks, as far as the pitch allows.
+  p.order = p.code_pitch % 128 == 64 ? 0x67542310u : p.code_pitch % 64 == 32 ? 0x57463120u : 0x73625140u;
+  const int key_bytes = 2 * (p.code_bytes + p.step_bytes);
   p.stage_keys = 16 * p.head_warps;
-  while (2 * p.stage_keys <= kKeys && 4 * p.stage_keys * p.pitch <= kStageBytes) p.stage_keys *= 2;
-  const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), stage = 2 * p.stage_keys * p.pitch;
+  while (2 * p.stage_keys <= kKeys && 2 * p.stage_keys * key_bytes <= kStageBytes) p.stage_keys *= 2;
+  p.stage_bytes = p.stage_keys * key_bytes;
+  const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), stage = p.stage_bytes;
   p.stages = (kSharedBytes - fixed) / stage;
   if (p.stages > kMostStages) p.stages = kMostStages;
   if (p.stages < 2) return MLA_ERR_SHAPE;                  // (no number of heads gives less)
+  // Boxes of at least eight rows (they begin at 128 bytes of shared memory) that neither
+  // a page's nor a stage's end cuts.
+  const int whole = p.stage_keys & -p.stage_keys, box = box_rows(c);
+  p.box_rows = box < whole ? box : whole;
+  Maps maps = {};
+  for (int i = 0; i < 2 && p.box_rows; ++i) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.row_end) / 8, static_cast<cuuint64_t>(c.pool_rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.pool_stride[i])};
+    const cuuint32_t elem[2] = {1, 1};
+    for (int part = 0; part <= p.split; ++part) {
+      const cuuint32_t size[2] = {static_cast<cuuint32_t>(part ? p.step_bytes : p.code_bytes) / 8,
+                                 static_cast<cuuint32_t>(p.box_rows)};
+      if (d.encode(part ? &maps.steps[i] : &maps.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT64, 2,
+                   const_cast<void*>(i ? c.v : c.k), dims, strides, size, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return MLA_ERR_LAUNCH;
+    }
+  }
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -708,7 +852,7 @@ int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, v.attn, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, v.attn, maps, p) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }
