@@ -31,6 +31,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "gqa_attn.cuh"
 #include "gqa_host.h"
@@ -56,11 +57,12 @@ struct FewParams : Params {
   Divisor by_units;                // 16-byte units of a row
 };
 
-// kN: query rows in eights; more of them want more registers.
+// kN: query rows in eights; with more of them a warp takes fewer keys at a time.
 template <int kN>
 struct Shape8 {
-  static constexpr int kWarps = kN == 1 ? 16 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * (kWarps + kLoaders);
+  static constexpr int kTogether = kN == 1 ? 2 : 1;        // sixteens of keys
 };
 
 // A warp's place in its run, kept in shared memory between the ends of segments: the
@@ -114,14 +116,13 @@ __device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
 }
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
@@ -264,6 +265,7 @@ template <int D, bool kBf16, int kN>
 __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_t ring, float* sums, int warp, int lane) {
   constexpr int kTiles = D / 16;             // of 16 dimensions (or rows of O^T)
   constexpr int kQ = D / 8;                  // registers of a row of Q a lane
+  constexpr int kS = Shape8<kN>::kTogether;
   constexpr float kShift = 7.f;              // (see the attention kernel's softmax)
   constexpr float kNothing = -1e30f;
   const int g = lane >> 2, c = lane & 3;
@@ -340,144 +342,165 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
     const int steps_at = (p.split ? p.stage_keys * p.code_pitch + ((s.head * (D / 16)) & 15) : p.steps_at) + head_local * (D / 16);
 
     // ---- the run's stages
-    for (int k1 = begin; k1 < end; k1 += p.stage_keys) {
-      if (!wait(sm, sm.full[stage], phase, p)) return;
-      const uint32_t base = ring + stage * p.stage_bytes;
-      const int last = min(k1 + p.stage_keys, end);
-      for (int k0 = k1 + 16 * j; k0 < last; k0 += 16 * p.head_warps) {
-        const uint32_t codes = base + (k0 - k1) * p.code_pitch, steps = base + (k0 - k1) * p.step_pitch + steps_at;
-        const bool edge = k0 + 16 > min(prefix, end);
-        float x[kN][4];
+    const int code_next = (key_c1 - key_c) * p.code_pitch, step_next = (key_c1 - key_c) * p.step_pitch;
+    auto keys = [&](auto at_edge, uint32_t codes, uint32_t steps, int k0) {
+      constexpr bool kEdge = decltype(at_edge)::value;
+      // Everything of the 16 kS keys that this lane has: K's codes and steps of two keys,
+      // V's of four, a sixteen.
+      uint32_t wk[kS][2][D / 32], sk[kS][2], wv[kS][2][2][D / 64], sv[kS][2][2];
+#pragma unroll
+      for (int i = 0; i < kS; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t c0 = codes + (16 * i + 8 * h) * p.code_pitch, s0 = steps + (16 * i + 8 * h) * p.step_pitch;
+          lds<D / 32>(c0 + k_codes, wk[i][h]);
+          sk[i][h] = D == 128 ? lds_u16(s0 + k_steps) : lds_u8(s0 + k_steps);
+          lds<D / 64>(c0 + v_codes, wv[i][h][0]);
+          lds<D / 64>(c0 + v_codes + code_next, wv[i][h][1]);
+          sv[i][h][0] = lds_u8(s0 + v_steps);
+          sv[i][h][1] = lds_u8(s0 + v_steps + step_next);
+        }
+      }
+      // S^T = K Q^T (two sums: a product waits for the last one's)
+      float x[kS][kN][4];
+#pragma unroll
+      for (int i = 0; i < kS; ++i) {
+        const uint32_t sa = fp4::from_e4m3x2(sk[i][0]), sb = fp4::from_e4m3x2(sk[i][1]);
+        float x2[kN][4];
 #pragma unroll
         for (int t = 0; t < kN; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-        {
-          // S^T = K Q^T
-          uint32_t wa[D / 32], wb[D / 32], sa, sb;
-          lds<D / 32>(codes + k_codes, wa);
-          lds<D / 32>(codes + k_codes + 8 * p.code_pitch, wb);
-          if constexpr (D == 128) {
-            sa = fp4::from_e4m3x2(lds_u16(steps + k_steps));
-            sb = fp4::from_e4m3x2(lds_u16(steps + k_steps + 8 * p.step_pitch));
-          } else {
-            sa = fp4::from_e4m3x2(lds_u8(steps + k_steps));
-            sb = fp4::from_e4m3x2(lds_u8(steps + k_steps + 8 * p.step_pitch));
-          }
+          for (int e = 0; e < 4; ++e) x[i][t][e] = x2[t][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            uint32_t ha[4], hb[4];
-            fp4::from_e2m1x8(wa[e], ha);
-            fp4::from_e2m1x8(wb[e], hb);
-            const uint32_t fa = e < 2 ? low2(sa) : high2(sa), fb = e < 2 ? low2(sb) : high2(sb);
+        for (int e = 0; e < D / 32; ++e) {
+          uint32_t ha[4], hb[4];
+          fp4::from_e2m1x8(wk[i][0][e], ha);
+          fp4::from_e2m1x8(wk[i][1][e], hb);
+          const uint32_t fa = e < 2 ? low2(sa) : high2(sa), fb = e < 2 ? low2(sb) : high2(sb);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t f[4] = {times(ha[2 * y], fa), times(hb[2 * y], fb), times(ha[2 * y + 1], fa),
-                                     times(hb[2 * y + 1], fb)};
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t f[4] = {times(ha[2 * y], fa), times(hb[2 * y], fb), times(ha[2 * y + 1], fa),
+                                   times(hb[2 * y + 1], fb)};
 #pragma unroll
-              for (int t = 0; t < kN; ++t) mma(x[t], f, q[t][4 * e + 2 * y], q[t][4 * e + 2 * y + 1]);
-            }
+            for (int t = 0; t < kN; ++t) mma(y ? x2[t] : x[i][t], f, q[t][4 * e + 2 * y], q[t][4 * e + 2 * y + 1]);
           }
         }
-        // ---- softmax: x[t][0..1] are key g's scores of rows 2 c, 2 c + 1, x[t][2..3] key g + 8's.
-        uint32_t hidden = 0;
-        if (edge) {
+#pragma unroll
+        for (int t = 0; t < kN; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][t][e] += x2[t][e];
+      }
+      // Softmax: x[i][t][0..1] are key g's scores of rows 2 c, 2 c + 1, [2..3] key g + 8's.
+      uint32_t hidden = 0;
+      if constexpr (kEdge) {
+#pragma unroll
+        for (int i = 0; i < kS; ++i)
 #pragma unroll
           for (int t = 0; t < kN; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = k0 + key_g + (e >> 1) * 8, row = 8 * t + 2 * c + (e & 1);
+              const int key = k0 + 16 * i + key_g + (e >> 1) * 8, row = 8 * t + 2 * c + (e & 1);
               if (key >= end || (key >= prefix && !(row < rows && sees(p, s.b, p.by_G.of(row), key - prefix))))
-                hidden |= 1u << (4 * t + e);
+                hidden |= 1u << ((i * kN + t) * 4 + e);
             }
-        }
-        float y[kN][4];
-        auto shifted = [&]() {
+      }
+      float y[kS][kN][4];
+      auto shifted = [&]() {
+#pragma unroll
+        for (int i = 0; i < kS; ++i)
 #pragma unroll
           for (int t = 0; t < kN; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              y[t][e] = fmaf(x[t][e], a[t][e & 1], -ms[t][e & 1]);
-              if (edge && (hidden >> (4 * t + e) & 1u)) y[t][e] = -CUDART_INF_F;
+              y[i][t][e] = fmaf(x[i][t][e], a[t][e & 1], -ms[t][e & 1]);
+              if (kEdge && (hidden >> ((i * kN + t) * 4 + e) & 1u)) y[i][t][e] = -CUDART_INF_F;
             }
-        };
-        shifted();
-        bool grow = false;
+      };
+      shifted();
+      float most = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < kS; ++i)
 #pragma unroll
         for (int t = 0; t < kN; ++t)
-          grow |= fmaxf(fmaxf(y[t][0], y[t][1]), fmaxf(y[t][2], y[t][3])) > kLazy + kShift;
-        if (__any_sync(0xFFFFFFFFu, grow)) {
+          most = fmaxf(most, fmaxf(fmaxf(y[i][t][0], y[i][t][1]), fmaxf(y[i][t][2], y[i][t][3])));
+      if (__any_sync(0xFFFFFFFFu, most > kLazy + kShift)) {
 #pragma unroll
-          for (int t = 0; t < kN; ++t)
+        for (int t = 0; t < kN; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float top = -CUDART_INF_F;
+          for (int e = 0; e < 2; ++e) {
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < kS; ++i)
 #pragma unroll
               for (int z = e; z < 4; z += 2)
-                if (!(hidden >> (4 * t + z) & 1u)) top = fmaxf(top, x[t][z] * a[t][e]);
+                if (!kEdge || !(hidden >> ((i * kN + t) * 4 + z) & 1u)) top = fmaxf(top, x[i][t][z] * a[t][e]);
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-              if (top - ms[t][e] > kLazy + kShift) {
-                const float alpha = ex2(ms[t][e] - (top - kShift));    // 0 when nothing was visible before
-                ms[t][e] = top - kShift;
-                l[t][e] *= alpha;
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            if (top - ms[t][e] > kLazy + kShift) {
+              const float alpha = ex2(ms[t][e] - (top - kShift));      // 0 when nothing was visible before
+              ms[t][e] = top - kShift;
+              l[t][e] *= alpha;
 #pragma unroll
-                for (int z = 0; z < kTiles; ++z) {
-                  o[t][z][e] *= alpha;
-                  o[t][z][e + 2] *= alpha;
-                }
+              for (int z = 0; z < kTiles; ++z) {
+                o[t][z][e] *= alpha;
+                o[t][z][e + 2] *= alpha;
               }
             }
-          shifted();
-        }
-        uint32_t pb[kN][2];
+          }
+        shifted();
+      }
+      // O^T += V^T P: two pairs of keys, 2 c and 2 c + 1 and those 8 behind.
+#pragma unroll
+      for (int i = 0; i < kS; ++i) {
+        uint32_t pb[kN][2], scale[2];
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
-          const float p0 = ex2(y[t][0]), p1 = ex2(y[t][1]), p2 = ex2(y[t][2]), p3 = ex2(y[t][3]);
+          const float p0 = ex2(y[i][t][0]), p1 = ex2(y[i][t][1]), p2 = ex2(y[i][t][2]), p3 = ex2(y[i][t][3]);
           l[t][0] += p0 + p2;
           l[t][1] += p1 + p3;
           pb[t][0] = transposed(pack2<false>(p0, p1));
           pb[t][1] = transposed(pack2<false>(p2, p3));
         }
-        {
-          // O^T += V^T P: two pairs of keys, 2 c and 2 c + 1 and those 8 behind.
-          const int code_next = (key_c1 - key_c) * p.code_pitch, step_next = (key_c1 - key_c) * p.step_pitch;
-          uint32_t w[2][2][D / 64], scale[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t at = steps + v_steps + 8 * h * p.step_pitch;
-            uint32_t s0 = lds_u8(at), s1 = lds_u8(at + step_next);
-            if (edge) {
-              // Rows past the run, and drafts that none sees, may hold anything.
-              if (!used(p, s.b, k0 + 8 * h + key_c, prefix, end)) s0 = 0;
-              if (!used(p, s.b, k0 + 8 * h + key_c1, prefix, end)) s1 = 0;
-            }
-            scale[h] = fp4::from_e4m3x2(s0 | s1 << 8);
-            lds<D / 64>(codes + v_codes + 8 * h * p.code_pitch, w[h][0]);
-            lds<D / 64>(codes + v_codes + 8 * h * p.code_pitch + code_next, w[h][1]);
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (kEdge) {
+            // Rows past the run, and drafts that none sees, may hold anything.
+            if (!used(p, s.b, k0 + 16 * i + 8 * h + key_c, prefix, end)) sv[i][h][0] = 0;
+            if (!used(p, s.b, k0 + 16 * i + 8 * h + key_c1, prefix, end)) sv[i][h][1] = 0;
           }
+          scale[h] = fp4::from_e4m3x2(sv[i][h][0] | sv[i][h][1] << 8);
+        }
 #pragma unroll
-          for (int e = 0; e < D / 64; ++e) {
-            // Tiles 4 e and 4 e + 1: the even dimensions of the eight; then the odd ones.
+        for (int e = 0; e < D / 64; ++e) {
+          // Tiles 4 e and 4 e + 1: the even dimensions of the eight; then the odd ones.
 #pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-              uint32_t x2[2][4];
+          for (int odd = 0; odd < 2; ++odd) {
+            uint32_t v2[2][4];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a0 = w[h][0][e], a1 = w[h][1][e];
-                fp4::from_e2m1x8(odd ? (a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u)
-                                     : (a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), x2[h]);
-              }
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = wv[i][h][0][e], a1 = wv[i][h][1][e];
+              fp4::from_e2m1x8(odd ? (a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u)
+                                   : (a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), v2[h]);
+            }
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const uint32_t f[4] = {times(x2[0][2 * z], scale[0]), times(x2[0][2 * z + 1], scale[0]),
-                                       times(x2[1][2 * z], scale[1]), times(x2[1][2 * z + 1], scale[1])};
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t f[4] = {times(v2[0][2 * z], scale[0]), times(v2[0][2 * z + 1], scale[0]),
+                                     times(v2[1][2 * z], scale[1]), times(v2[1][2 * z + 1], scale[1])};
 #pragma unroll
-                for (int t = 0; t < kN; ++t) mma(o[t][4 * e + 2 * odd + z], f, pb[t][0], pb[t][1]);
-              }
+              for (int t = 0; t < kN; ++t) mma(o[t][4 * e + 2 * odd + z], f, pb[t][0], pb[t][1]);
             }
           }
         }
+      }
+    };
+    for (int k1 = begin; k1 < end; k1 += p.stage_keys) {
+      if (!wait(sm, sm.full[stage], phase, p)) return;
+      const uint32_t base = ring + stage * p.stage_bytes;
+      const int last = min(k1 + p.stage_keys, end);
+      for (int k0 = k1 + 16 * kS * j; k0 < last; k0 += 16 * kS * p.head_warps) {
+        const uint32_t codes = base + (k0 - k1) * p.code_pitch, steps = base + (k0 - k1) * p.step_pitch + steps_at;
+        if (k0 + 16 * kS > min(prefix, end)) keys(std::true_type(), codes, steps, k0);
+        else keys(std::false_type(), codes, steps, k0);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.empty[stage]));
@@ -733,12 +756,12 @@ struct Variant {
   Fn attn;
   MergeFn merge;
   PartsFn parts, units;
-  int threads, warps, head_bytes, sum_bytes;
+  int threads, warps, together, head_bytes, sum_bytes;
 };
 template <int D, bool kBf16, int kN>
 Variant variant() {
   return {few_kernel<D, kBf16, kN>, combine_heads<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
-          Shape8<kN>::kThreads, Shape8<kN>::kWarps, static_cast<int>(sizeof(Head<kN>)), kSums<D, kN>};
+          Shape8<kN>::kThreads, Shape8<kN>::kWarps, Shape8<kN>::kTogether, static_cast<int>(sizeof(Head<kN>)), kSums<D, kN>};
 }
 
 constexpr int kSharedBytes = 232448;
@@ -815,7 +838,7 @@ int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid
   // V, 32 bytes each: keys whose rows lie in different banks, as far as the pitch allows.
   p.order = p.code_pitch % 128 == 64 ? 0x67542310u : p.code_pitch % 64 == 32 ? 0x57463120u : 0x73625140u;
   const int key_bytes = 2 * (p.code_bytes + p.step_bytes);
-  p.stage_keys = 16 * p.head_warps;
+  p.stage_keys = 16 * v.together * p.head_warps;
   while (2 * p.stage_keys <= kKeys && 2 * p.stage_keys * key_bytes <= kStageBytes) p.stage_keys *= 2;
   p.stage_bytes = p.stage_keys * key_bytes;
   const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), stage = p.stage_bytes;
