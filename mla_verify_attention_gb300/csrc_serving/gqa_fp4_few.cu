@@ -765,7 +765,7 @@ Variant variant() {
 }
 
 constexpr int kSharedBytes = 232448;
-constexpr int kStageBytes = 40 << 10;      // a stage, about
+constexpr int kStageBytes = 80 << 10;      // a stage, about
 
 std::mutex g_mutex;
 bool g_ready[64][8];
