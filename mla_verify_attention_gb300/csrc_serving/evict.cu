@@ -20,13 +20,19 @@ namespace evict {
 // n largest totals (of the key heads' weights) stay, of equal ones the first.  A
 // cluster of blocks takes a stream, each a run of its keys: they sum the heads, in order,
 // into an unsigned number that orders as the total does, and keep it in shared
-// memory.  Three passes of a histogram (11, 11 and 10 bits, each over what shares
-// the leading bits found so far), added up over the cluster by every block for
-// itself, give the n-th largest total and how many equal to it stay; a scan over the
-// keys then gives each kept one its place.  Weights are read once, and nothing but the
-// histograms and counts passes between blocks.
-constexpr int kThreads = 1024;
-constexpr int kBins = 2048;
+// memory.  Four passes of a histogram of eight bits, each over what shares the leading
+// bits found so far, give the n-th largest total and how many equal to it stay; a scan
+// over the keys then gives each kept one its place.  Weights are read once.
+//
+// What bounds it beside that read: chains of barriers and reads.  Blocks send their
+// histograms and counts to all others' shared memory and meet once a pass: read from
+// there after the barrier instead, 2,048 bins took 8,000 cycles a pass, more than
+// two passes of 256 take in all (one stream of 64k keys, 8 heads 30.6 -> 15.7 us).
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 256;
+constexpr int kPasses = 4;
+constexpr int kMostBlocks = 8;
 constexpr int kMaxDevices = 64;
 constexpr int kMostKeys = 49152;           // a block holds in shared memory
 
@@ -41,9 +47,11 @@ struct SelectParams {
 };
 
 struct SelectShared {
-  uint32_t hist[3][kBins];
-  unsigned long long warp_sum[32];
-  unsigned long long counts;               // this block's: above the threshold (upper half), equal to it
+  uint32_t mine[kPasses][kBins];                           // this block's histograms
+  uint32_t all[2][kMostBlocks][kBins];     // and everyone's, of every second pass (there is a barrier between)
+  uint64_t counts[kMostBlocks];            // keys above the threshold (upper half), equal to it
+  uint64_t warp_counts[kWarps];
+  uint32_t warp_sum[kBins / 32];
   uint32_t digit, left;
 };
 
@@ -54,52 +62,28 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 
 template <class T>
-__device__ __forceinline__ T remote(const T* mine, uint32_t rank) {
+__device__ __forceinline__ void send(T* mine, uint32_t rank, T x) {
   const uint32_t at = mapa_shared(smem_u32(mine), rank);
-  if constexpr (sizeof(T) == 8) {
-    unsigned long long r;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(at) : "memory");
-    return static_cast<T>(r);
-  } else {
-    uint32_t r;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
-    return static_cast<T>(r);
-  }
+  if constexpr (sizeof(T) == 8) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
+  else asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
 }
 
-// Sum of x over the threads before this one (and, in `total`, over all).
-__device__ __forceinline__ unsigned long long scan_before(unsigned long long x, unsigned long long* warp_sum,
-                                                          unsigned long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long inc = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
-  }
-  __syncthreads();                                         // (the sums of the last scan have been read)
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  unsigned long long w = warp_sum[lane];
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, w, d);
-    if (lane >= d) w += o;
-  }
-  total = __shfl_sync(0xFFFFFFFFu, w, 31);
-  const unsigned long long before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
-  return (warp > 0 ? before : 0ull) + inc - x;
+// All threads of a cluster; what they have sent has arrived.
+template <int kBlocks>
+__device__ __forceinline__ void sync_blocks() {
+  if (kBlocks > 1) cluster_sync_all();
+  else __syncthreads();
 }
 
 // kBlocks: of a stream's cluster.
 template <int kBlocks>
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t shared_keys[];
   __shared__ SelectShared sm;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = kBlocks > 1 ? cluster_ctarank() : 0u;
   const int b = static_cast<int>(blockIdx.x / kBlocks);
-  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  for (int i = tid; i < kPasses * kBins; i += kThreads) sm.mine[0][i] = 0;
   grid_dependency_wait();
   if (tid == 0) grid_launch_dependents();
   int S = p.seq_lens[b];
@@ -110,93 +94,127 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
   const int n = min(S, p.budget);
   int32_t* const kept = p.kept + static_cast<size_t>(b) * p.budget;
   if (tid == 0 && rank == 0) p.keep[b] = n;
-  const int all = kBlocks * kThreads, me = static_cast<int>(rank) * kThreads + tid;
-  for (int j = n + me; j < p.budget; j += all) kept[j] = -1;
+  const int threads = kBlocks * kThreads, me = static_cast<int>(rank) * kThreads + tid;
+  for (int j = n + me; j < p.budget; j += threads) kept[j] = -1;
   if (S <= p.budget) {                                     // (the whole cluster)
-    for (int j = me; j < n; j += all) kept[j] = j;
+    for (int j = me; j < n; j += threads) kept[j] = j;
     return;
   }
   const int run = (S + kBlocks - 1) / kBlocks, t0 = min(S, static_cast<int>(rank) * run), t1 = min(S, t0 + run);
   uint32_t* const keys = p.spill ? p.spill + static_cast<size_t>(b) * p.Smax + t0 : shared_keys;
-  const int from = p.sinks, to = S - p.recent;             // the keys that are chosen from
-  const float* const w = p.weights + static_cast<size_t>(b) * p.Hkv * p.Smax;
+  const int from = max(t0, p.sinks), to = min(t1, S - p.recent);   // of this block's keys, those that are chosen from
   __syncthreads();
-  for (int t = t0 + tid; t < t1; t += kThreads) {
-    if (t < from || t >= to) continue;
-    float sum = w[t];
-#pragma unroll 8
-    for (int h = 1; h < p.Hkv; ++h) sum += w[static_cast<size_t>(h) * p.Smax + t];
-    const uint32_t key = ordered(sum);
-    keys[t - t0] = key;
-    atomicAdd(&sm.hist[0][key >> 21], 1u);
+  constexpr int kAtOnce = 8;                               // keys a thread
+  for (int t = from + tid; t < to; t += kAtOnce * kThreads) {
+    const float* w = p.weights + static_cast<size_t>(b) * p.Hkv * p.Smax + t;
+    float sum[kAtOnce];
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) sum[e] = t + e * kThreads < to ? w[e * kThreads] : 0.f;
+#pragma unroll 4
+    for (int h = 1; h < p.Hkv; ++h) {
+      w += p.Smax;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (t + e * kThreads < to) sum[e] += w[e * kThreads];
+    }
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      if (t + e * kThreads >= to) continue;
+      const uint32_t key = ordered(sum[e]);
+      keys[t + e * kThreads - t0] = key;
+      atomicAdd(&sm.mine[0][key >> 24], 1u);
+    }
   }
   const int choose = n - p.sinks - p.recent;               // how many of them
   uint32_t prefix = 0, left = static_cast<uint32_t>(choose);
   if (choose > 0) {
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int shift = 24 - 8 * pass;
       if (pass > 0) {
-        const int above = pass == 1 ? 21 : 10;
-        for (int t = max(t0, from) + tid; t < min(t1, to); t += kThreads) {
+        for (int t = from + tid; t < to; t += kThreads) {
           const uint32_t key = keys[t - t0];
-          if (key >> above == prefix >> above) atomicAdd(&sm.hist[pass][(key >> shift) & (bins - 1)], 1u);
+          if (key >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&sm.mine[pass][key >> shift & 0xFFu], 1u);
         }
       }
-      if (kBlocks > 1) cluster_sync_all(); else __syncthreads();
-      // Each thread two bins, the highest first.
-      const int high = bins - 1 - 2 * tid;
-      uint32_t c0 = 0, c1 = 0;
-      if (high > 0) {
+      const uint32_t* sums = sm.mine[pass];
+      __syncthreads();
+      if (kBlocks > 1) {
 #pragma unroll
-        for (int r = 0; r < kBlocks; ++r) {
-          c0 += kBlocks > 1 ? remote(&sm.hist[pass][high], r) : sm.hist[pass][high];
-          c1 += kBlocks > 1 ? remote(&sm.hist[pass][high - 1], r) : sm.hist[pass][high - 1];
-        }
+        for (int i = tid; i < kBlocks * kBins; i += kThreads)
+          send(&sm.all[pass & 1][rank][i % kBins], static_cast<uint32_t>(i / kBins), sums[i % kBins]);
+        sync_blocks<kBlocks>();
       }
-      unsigned long long total;
-      const uint32_t before = static_cast<uint32_t>(scan_before(c0 + c1, sm.warp_sum, total));
-      if (high > 0 && before < left && left <= before + c0 + c1) {
-        const bool second = left > before + c0;
-        sm.digit = static_cast<uint32_t>(second ? high - 1 : high);
-        sm.left = left - before - (second ? c0 : 0);
+      // A thread a bin, the highest first.
+      uint32_t c = 0, inc = 0;
+      if (tid < kBins) {
+        const int bin = kBins - 1 - tid;
+        if (kBlocks > 1) {
+#pragma unroll
+          for (int r = 0; r < kBlocks; ++r) c += sm.all[pass & 1][r][bin];
+        } else {
+          c = sums[bin];
+        }
+        inc = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+          if (lane >= d) inc += o;
+        }
+        if (lane == 31) sm.warp_sum[warp] = inc;
+      }
+      __syncthreads();
+      if (tid < kBins) {
+        for (int w = 0; w < warp; ++w) inc += sm.warp_sum[w];
+        if (inc - c < left && left <= inc) {
+          sm.digit = static_cast<uint32_t>(kBins - 1 - tid);
+          sm.left = left - (inc - c);
+        }
       }
       __syncthreads();
       prefix |= sm.digit << shift;
       left = sm.left;
     }
   }
-  // Keys above the threshold stay, and the first `left` that equal it (choose = 0: none).
+  // Keys above the threshold stay, and the first `left` that equal it (choose = 0:
+  // none).  Each warp counts a run of them, then they are put in their places.
   const uint64_t threshold = choose > 0 ? prefix : 1ull << 32;
-  const int per = (t1 - t0 + kThreads - 1) / kThreads;
-  const int i0 = min(t1, t0 + tid * per), i1 = min(t1, i0 + per);
-  unsigned long long mine = 0;
-  for (int t = max(i0, from); t < min(i1, to); ++t) {
-    const uint64_t key = keys[t - t0];
-    mine += key > threshold ? 1ull << 32 : key == threshold ? 1ull : 0ull;
+  const int each = ((to - from + kThreads - 1) / kThreads) * 32;     // keys a warp (none: from > to)
+  const int w0 = from + warp * each, w1 = min(to, w0 + each);
+  uint32_t above = 0, equal = 0;
+  for (int t = w0 + lane; t - lane < w1; t += 32) {
+    const uint64_t key = t < w1 ? keys[t - t0] : 0;
+    above += __popc(__ballot_sync(0xFFFFFFFFu, t < w1 && key > threshold));
+    equal += __popc(__ballot_sync(0xFFFFFFFFu, t < w1 && key == threshold));
   }
-  unsigned long long total;
-  unsigned long long before = scan_before(mine, sm.warp_sum, total);
+  if (lane == 0) sm.warp_counts[warp] = static_cast<uint64_t>(above) << 32 | equal;
+  __syncthreads();
+  uint64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) before = total;
+    total += sm.warp_counts[w];
+  }
   if (kBlocks > 1) {
-    if (tid == 0) sm.counts = total;
-    cluster_sync_all();
-    for (uint32_t r = 0; r < rank; ++r) before += remote(&sm.counts, r);
+    if (tid < kBlocks) send(&sm.counts[rank], static_cast<uint32_t>(tid), total);
+    sync_blocks<kBlocks>();
+    for (uint32_t r = 0; r < rank; ++r) before += sm.counts[r];
   }
-  uint32_t above = static_cast<uint32_t>(before >> 32), equal = static_cast<uint32_t>(before);
-  for (int t = i0; t < i1; ++t) {
-    if (t < from) {
-      kept[t] = t;
-    } else if (t >= to) {
-      kept[n - (S - t)] = t;
-    } else {
-      const uint64_t key = keys[t - t0];
-      const int at = from + static_cast<int>(above + min(equal, left));
-      const bool stays = key > threshold || (key == threshold && equal < left);
-      if (stays) kept[at] = t;
-      above += key > threshold;
-      equal += key == threshold;
-    }
+  above = static_cast<uint32_t>(before >> 32);
+  equal = static_cast<uint32_t>(before);
+  for (int t = w0 + lane; t - lane < w1; t += 32) {
+    const uint64_t key = t < w1 ? keys[t - t0] : 0;
+    const unsigned more = __ballot_sync(0xFFFFFFFFu, t < w1 && key > threshold);
+    const unsigned same = __ballot_sync(0xFFFFFFFFu, t < w1 && key == threshold);
+    const unsigned lower = (1u << lane) - 1u;
+    const uint32_t e = equal + __popc(same & lower);
+    if ((more >> lane & 1u) || ((same >> lane & 1u) && e < left))
+      kept[p.sinks + static_cast<int>(above + __popc(more & lower) + min(e, left))] = t;
+    above += __popc(more);
+    equal += __popc(same);
   }
-  if (kBlocks > 1) cluster_sync_all();                    // (others have read this block's counts)
+  // The first and the last keys, shared out among all.
+  for (int t = me; t < p.sinks; t += threads) kept[t] = t;
+  for (int t = me; t < p.recent; t += threads) kept[n - p.recent + t] = S - p.recent + t;
 }
 
 // ------------------------------------------------------------ compact
@@ -326,28 +344,38 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactPara
 
 // ------------------------------------------------------------ host
 
-// Blocks a stream's cluster has: one where a block gets through its keys soon enough.
-constexpr int kBlocks = 8;
-int select_blocks(int Smax) { return Smax <= 4096 ? 1 : kBlocks; }
-int select_run(int Smax) { return (Smax + select_blocks(Smax) - 1) / select_blocks(Smax); }
+// Blocks of a stream's cluster: as many as the device takes at once (two an SM), none of
+// which a short stream needs: up to 4,096 keys one block is through sooner.
+int select_blocks(int B, int Smax, int sms) {
+  if (Smax <= 4096) return 1;
+  int blocks = kMostBlocks;
+  while (blocks > 1 && static_cast<long long>(B) * blocks > 2 * sms && (Smax + blocks / 2 - 1) / (blocks / 2) <= kMostKeys)
+    blocks /= 2;
+  return blocks;
+}
+bool select_spills(int Smax) { return (Smax + kMostBlocks - 1) / kMostBlocks > kMostKeys; }
 
 bool select_shape_ok(long long B, long long Smax) {
   return B >= 0 && B < (1 << 20) && Smax >= 1 && Smax < (1 << 24);
 }
 
+using SelectFn = void (*)(SelectParams);
+constexpr int kForms = 4;                  // 1, 2, 4 and 8 blocks
 std::mutex g_mutex;
 bool g_ready[kMaxDevices];
 
-int select_ready() {
+int pick_select(int blocks, SelectFn* fn) {
+  static const SelectFn all[kForms] = {select_kernel<1>, select_kernel<2>, select_kernel<4>, select_kernel<8>};
+  *fn = all[blocks == 8 ? 3 : blocks == 4 ? 2 : blocks == 2 ? 1 : 0];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED_DEVICE;
   std::lock_guard<std::mutex> lock(g_mutex);
   if (!g_ready[dev]) {
-    if (cudaFuncSetAttribute(select_kernel<kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostKeys) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return MLA_ERR_LAUNCH;
-    }
+    for (SelectFn f : all)
+      if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostKeys) != cudaSuccess) {
+        cudaGetLastError();
+        return MLA_ERR_LAUNCH;
+      }
     g_ready[dev] = true;
   }
   return MLA_OK;
@@ -360,7 +388,7 @@ extern "C" {
 
 size_t mla_evict_workspace_size(int B, int Smax) {
   using namespace mla::evict;
-  if (!select_shape_ok(B, Smax) || select_run(Smax) <= kMostKeys) return 0;
+  if (!select_shape_ok(B, Smax) || !select_spills(Smax)) return 0;
   return 4 * static_cast<size_t>(B) * Smax;
 }
 
@@ -382,13 +410,14 @@ int mla_evict_select(const float* weights, const int32_t* seq_lens, int B, int H
   if (st != MLA_OK) return st;
   const size_t need = mla_evict_workspace_size(B, Smax);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MLA_ERR_WORKSPACE;
-  st = select_ready();
+  const int blocks = select_blocks(B, Smax, d.sms);
+  SelectFn fn;
+  st = pick_select(blocks, &fn);
   if (st != MLA_OK) return st;
-  const int blocks = select_blocks(Smax);
   const SelectParams p = {weights, seq_lens, kept, keep_lens, need > 0 ? static_cast<uint32_t*>(workspace) : nullptr,
                           d.status_word, Hkv, Smax, budget, sinks, recent};
-  return launch_dependent(blocks > 1 ? select_kernel<kBlocks> : select_kernel<1>, p, dim3(static_cast<unsigned>(B) * blocks), kThreads,
-                          need > 0 ? 0 : 4 * static_cast<size_t>(select_run(Smax)), stream, blocks);
+  return launch_dependent(fn, p, dim3(static_cast<unsigned>(B) * blocks), kThreads,
+                          need > 0 ? 0 : 4 * static_cast<size_t>((Smax + blocks - 1) / blocks), stream, blocks);
 }
 
 int mla_cache_compact(void* pool_a, long long pool_a_stride, int a_bytes, void* pool_b, long long pool_b_stride,
