@@ -241,8 +241,8 @@ struct CompactParams {
   Divisor page;
 };
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveLoads = 8;
+constexpr int kMoveThreads = 512;
+constexpr int kMoveLoads = 4;
 
 // Pool row of a stream's row; -1 (and the page reported) where there is none.
 __device__ __forceinline__ int pool_row(const CompactParams& p, int b, int t) {
@@ -462,10 +462,10 @@ int mla_cache_compact(void* pool_a, long long pool_a_stride, int a_bytes, void* 
   p.Hkv = weights ? Hkv : 0;
   p.B = B;
   p.page = Divisor(page_size);
-  // Slices of 64 bytes, or of less where those would leave the device half empty.
+  // Slices of 128 bytes, or of less where those would leave SMs empty.
   const long long units = static_cast<long long>(p.units[0]) + p.units[1];
-  p.slice_shift = 2;
-  while (p.slice_shift > 0 && ((units + (1 << p.slice_shift) - 1) >> p.slice_shift) * B < 2 * d.sms) --p.slice_shift;
+  p.slice_shift = 3;
+  while (p.slice_shift > 0 && ((units + (1 << p.slice_shift) - 1) >> p.slice_shift) * B < d.sms) --p.slice_shift;
   p.slices = static_cast<int>((units + (1 << p.slice_shift) - 1) >> p.slice_shift);
   return launch_dependent(compact_kernel, p, dim3(p.slices + p.Hkv, B < 65535 ? B : 65535), kMoveThreads, 0, stream);
 }
