@@ -66,6 +66,7 @@ using CombineFn = void (*)(Params, int);
 
 struct Variant {
   AttnFn attn;
+  Fp4Fn fp4;                  // instead, kFp4
   CombineFn combine_parts, combine_few_chunks, combine_many_chunks;
   size_t smem;
   int threads;
@@ -74,7 +75,7 @@ template <int D, bool kBf16>
 Variant variant() {
   constexpr size_t smem = sizeof(Smem<D, kWhole>);
   static_assert(smem <= 232448, "one CTA's shared memory");
-  return {attn_kernel<D, kBf16, kWhole>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
+  return {attn_kernel<D, kBf16, kWhole>, nullptr, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
           combine_many_units<D, kBf16, 3, 2>, smem, kThreads};
 }
 
@@ -88,12 +89,14 @@ int pick(int D, int dtype, Mode mode, Variant* out) {
   const int n = (D == 128 ? 2 : 0) + (dtype == MLA_FP16 ? 1 : 0);
   *out = all[n];
   if (mode == kWindow) out->attn = window_kernel(D, dtype == MLA_BF16);
-  if (mode == kFp4) out->attn = fp4_kernel(D, dtype == MLA_BF16, &out->smem, &out->threads);
+  if (mode == kFp4) out->fp4 = fp4_kernel(D, dtype == MLA_BF16, &out->smem, &out->threads);
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED_DEVICE;
   std::lock_guard<std::mutex> lock(g_ready_mutex);
   if (!g_ready[dev][mode][n]) {
-    if (cudaFuncSetAttribute(out->attn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(out->smem)) !=
+    const cudaFuncAttribute attribute = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const int bytes = static_cast<int>(out->smem);
+    if ((mode == kFp4 ? cudaFuncSetAttribute(out->fp4, attribute, bytes) : cudaFuncSetAttribute(out->attn, attribute, bytes)) !=
         cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_LAUNCH;
@@ -155,6 +158,26 @@ int encode(const DeviceCommon& d, CUtensorMap* map, const void* base, const Call
   return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_LAUNCH;
 }
 
+// The maps of pools held in 4 bits: rows of bytes, a box this many rows of a head's
+// codes (in the swizzle that suits their width), or of 16 bytes that hold its steps.
+int encode_fp4(const DeviceCommon& d, const Call& c, int rows, Fp4Maps* maps) {
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(fp4::row_bytes(c.Hkv, c.D)), static_cast<cuuint64_t>(c.pool_rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.pool_stride[i])};
+    const cuuint32_t codes[2] = {static_cast<cuuint32_t>(c.D / 2), static_cast<cuuint32_t>(rows)};
+    const cuuint32_t steps[2] = {16, static_cast<cuuint32_t>(rows)}, elem[2] = {1, 1};
+    void* const pool = const_cast<void*>(i ? c.v : c.k);
+    if (d.encode(&maps->codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool, dims, strides, codes, elem,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        d.encode(&maps->steps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool, dims, strides, steps, elem,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return MLA_ERR_LAUNCH;
+  }
+  return MLA_OK;
+}
+
 int run(const Call& c) {
   if (!shape_ok(c.B, c.q_len, c.H, c.Hkv, c.D) || c.Smax < 1 || c.Smax >= (1 << 24)) return MLA_ERR_SHAPE;
   if (c.mode == kWindow && (c.window < 1 || c.sinks < 0)) return MLA_ERR_SHAPE;
@@ -198,7 +221,7 @@ int run(const Call& c) {
   if (!few) st = pick(c.D, c.dtype, c.mode, &var);
   if (st != MLA_OK) return st;
 
-  const int box = c.mode == kFp4 ? 0 : box_rows(c);
+  const int box = box_rows(c);
   p.group_sets = (pl.groups + kMaxMembers - 1) / kMaxMembers;
   p.group_members = (pl.groups + p.group_sets - 1) / p.group_sets;
   const int heads = heads_side_by_side(p.k_stride, c.Hkv, p.group_members, grid);
@@ -216,7 +239,12 @@ int run(const Call& c) {
   const CUtensorMapL2promotion promotion =
       fetch_256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   CUtensorMap map_k = {}, map_v = {};
-  if (box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box, box == kKeys ? c.D / 64 : 1, promotion) != MLA_OK ||
+  Fp4Maps fp4_maps = {};
+  if (c.mode == kFp4 && !few && box != 0) {
+    st = encode_fp4(d, c, box, &fp4_maps);
+    if (st != MLA_OK) return st;
+  }
+  if (c.mode != kFp4 && box != 0 && (encode(d, &map_k, c.k, c, p.k_stride, rows, batches, box, box == kKeys ? c.D / 64 : 1, promotion) != MLA_OK ||
                    encode(d, &map_v, c.v, c, p.v_stride, rows, batches, box, box == kKeys ? c.D / 64 : 1, promotion) != MLA_OK))
     return MLA_ERR_LAUNCH;
 
@@ -272,7 +300,8 @@ int run(const Call& c) {
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, var.attn, map_k, map_v, p) != cudaSuccess) {
+  if ((c.mode == kFp4 ? cudaLaunchKernelEx(&cfg, var.fp4, fp4_maps, p)
+                      : cudaLaunchKernelEx(&cfg, var.attn, map_k, map_v, p)) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_LAUNCH;
   }

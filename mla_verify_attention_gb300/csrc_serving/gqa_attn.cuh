@@ -109,8 +109,8 @@ struct Shape {
   // 160 KB of K and V tiles, or 96 KB in 16 bits and 54 or 72 KB in 4.
   static constexpr int kStages = (kMode == kFp4 ? 3 : 5) * (D == 128 ? 1 : 2);
   static constexpr int kRing = 2 * kStages * kTile;
-  static constexpr int kCodes = kKeys * D / 2, kSteps = kKeys * D / 16;      // bytes of a tile in 4 bits
-  static constexpr int kPacked = D == 128 ? 6 : 16;    // stages of them
+  static constexpr int kCodes = kKeys * D / 2, kSteps = kKeys * 16;          // bytes of a tile in 4 bits
+  static constexpr int kPacked = D == 128 ? 6 : 14;    // stages of them
 };
 
 // What only some forms have.
@@ -119,8 +119,8 @@ struct Extra {};
 template <int D>
 struct Extra<D, kFp4> {
   using C = Shape<D, kFp4>;
-  __align__(16) uint8_t codes[2][C::kPacked][C::kCodes];   // [K, V]
-  __align__(16) uint8_t steps[2][C::kPacked][C::kSteps];
+  __align__(1024) uint8_t codes[2][C::kPacked][C::kCodes];   // [K, V]
+  uint8_t steps[2][C::kPacked][C::kSteps];             // 16 bytes a row, this head's among them
   float q_unit[2][kRows];                              // what a row of Q was divided by
   uint64_t packed_full[2][C::kPacked], packed_empty[2][C::kPacked];
 };
@@ -619,10 +619,28 @@ out:
 
 // ------------------------------------------------------------ loads of a cache in 4 bits
 //
-// Warps 0 (K) and 2 (V) copy a tile's codes and steps, row by row, into a ring in 4
-// bits; two more warps each (12 and 13, 14 and 15) turn them into the 16-bit tiles of the
-// products.  (A code times its step is exact in fp16, whatever the type of Q; the
-// pools' factors go to the scale and to the result.)
+// Warps 0 (K) and 2 (V) bring a tile's codes and steps into a ring in 4 bits, by TMA or,
+// where pages are not a multiple of eight rows, row by row; two more warps each (12 and
+// 13, 14 and 15) turn them into the 16-bit tiles of the products, a tile each in turn.
+// (A code times its step is exact in fp16, whatever the type of Q; the pools' factors go
+// to the scale and to the result.)  The 16-byte units of a row's codes are swizzled, as
+// TMA does, so that eight lanes that read a unit of eight rows, and then write eight rows of
+// a tile, meet no bank twice.  The row copies took a warp 1,500 cycles a tile, which was
+// what a tile took (one stream of 64k keys, 9 drafts 53 us).
+struct Fp4Maps {
+  CUtensorMap codes[2], steps[2];              // K, V: boxes of D / 2 and of 16 bytes
+};
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(bar)
+               : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ int code_unit(int row, int u) {
+  return row * (D / 32) + (u ^ (D == 128 ? row >> 1 & 3 : row >> 2 & 1));
+}
 
 // 4, 8 or 16 bytes to shared memory, or as many zero bytes when !full.
 template <int kBytes>
@@ -632,112 +650,154 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bo
                : "memory");
 }
 
+// A box a lane, looked up together and a tile ahead.
 template <int D>
-__device__ __forceinline__ void load_packed(Smem<D, kFp4>& sm, const Params& p, Walk<kFp4> w, bool is_v) {
+__device__ __forceinline__ void load_packed_boxes(Smem<D, kFp4>& sm, const Params& p, const Fp4Maps& maps, Walk<kFp4> w,
+                                                  bool is_v) {
   using C = Shape<D, kFp4>;
-  constexpr int kUnits = D / 32, kPer = 32 / kUnits;     // 16-byte units of a row's codes, rows a warp copies at once
-  constexpr int kAhead = C::kPacked - 1 < 8 ? C::kPacked - 1 : 8;
-  const int lane = threadIdx.x & 31;
-  uint64_t* const full = sm.extra.packed_full[is_v];
-  uint64_t* const empty = sm.extra.packed_empty[is_v];
-  const uint8_t* const pool = is_v ? p.v : p.k;
-  const long long row_stride = is_v ? p.v_stride[1] : p.k_stride[1];
-  const bool withheld = p.test_stall && is_v && blockIdx.x == 0;
-  Ring<C::kPacked> at, landed;
-  int started = 0;
-  auto publish = [&]() {                       // the oldest tile's copies of this lane have landed
-    if (!withheld) mbar_arrive(smem_u32(&full[landed.stage]));
-    landed.advance();
-  };
+  const int lane = threadIdx.x & 31, R = p.box_rows, shift = __ffs(R) - 1;
+  const CUtensorMap* const codes = &maps.codes[is_v];
+  const CUtensorMap* const steps = &maps.steps[is_v];
+  const uint32_t dst = smem_u32(sm.extra.codes[is_v]) + lane * R * (D / 2);
+  const uint32_t dst_steps = smem_u32(sm.extra.steps[is_v]) + lane * R * 16;
+  Ring<C::kPacked> at;
+  int issued = 0;
   Segment s;
   while (w.next(p, s)) {
-    auto key_of = [&](int j, int half) { return s.template key<kFp4>(j) + half * 32 + lane; };
-    auto entry_of = [&](int j, int half) {
-      return j < s.n && key_of(j, half) < s.S ? table_entry(p, s.b, key_of(j, half)) : 0;
-    };
-    auto row_of = [&](int j, int half, int entry) {        // -1 past the stream
-      return key_of(j, half) < s.S ? pool_row(p, entry, key_of(j, half)) : -1;
-    };
+    const int end = min(s.S, (s.tile0 + s.n) * kKeys), step_x = (p.steps_at + s.head * (D / 16)) & ~15;
+    auto entry_of = [&](int key) { return lane * R < kKeys && key < end ? table_entry(p, s.b, key) : 0; };
+    int key = s.tile0 * kKeys + lane * R;
+    int next = entry_of(key);
+    for (int k0 = s.tile0 * kKeys; k0 < end; k0 += kKeys, key += kKeys, at.advance()) {
+      const int n = min(kKeys, end - k0) + R - 1 >> shift;   // boxes
+      const int row = lane < n ? pool_row(p, next, key) : 0;
+      next = entry_of(key + kKeys);
+      if (!wait(sm, sm.extra.packed_empty[is_v][at.stage], at.phase ^ 1, p)) goto out;
+      const uint32_t bar = smem_u32(&sm.extra.packed_full[is_v][at.stage]);
+      if (p.test_stall && is_v && issued == 0 && blockIdx.x == 0) goto out;         // this load never comes
+      arrive_expect_elect(bar, n * R * (D / 2 + 16));
+      __syncwarp();
+      if (lane < n) {
+        tma_rows(dst + at.stage * C::kCodes, codes, s.head * (D / 2), row, bar);
+        tma_rows(dst_steps + at.stage * C::kSteps, steps, step_x, row, bar);
+      }
+      ++issued;
+    }
+  }
+out:
+  for (int n = issued - 1; n >= 0 && n >= issued - C::kPacked; --n)
+    mbar_wait(smem_u32(&sm.extra.packed_full[is_v][n % C::kPacked]), (n / C::kPacked) & 1, kWaitNs / 2);
+}
+
+template <int D>
+__device__ __forceinline__ void load_packed_rows(Smem<D, kFp4>& sm, const Params& p, Walk<kFp4> w, bool is_v) {
+  using C = Shape<D, kFp4>;
+  constexpr int kUnits = D / 32, kPer = 32 / kUnits;     // 16-byte units of a row's codes, rows a warp copies at once
+  const int lane = threadIdx.x & 31;
+  const uint8_t* const pool = is_v ? p.v : p.k;
+  const long long row_stride = is_v ? p.v_stride[1] : p.k_stride[1];
+  const uint32_t full = smem_u32(sm.extra.packed_full[is_v]);
+  // (The swizzle of a row is that of row + kPer.)
+  const uint32_t dst = smem_u32(sm.extra.codes[is_v]) + code_unit<D>(lane / kUnits, lane % kUnits) * 16;
+  const uint32_t dst_steps = smem_u32(sm.extra.steps[is_v]) + lane * 16;
+  const bool withheld = p.test_stall && is_v && blockIdx.x == 0;
+  constexpr int kEntries = 3;                            // tiles whose table entries are under way
+  Ring<C::kPacked> at;
+  Segment s;
+  while (w.next(p, s)) {
+    const int end = min(s.S, (s.tile0 + s.n) * kKeys);
+    auto entry_of = [&](int key) { return key < end ? table_entry(p, s.b, key) : 0; };
     const uint8_t* const codes = pool + s.head * (D / 2) + (lane % kUnits) * 16;
     const uint8_t* const steps = pool + p.steps_at + s.head * (D / 16);
-    // Entries two tiles ahead, rows one.
-    int entry[2] = {entry_of(0, 0), entry_of(0, 1)}, next[2] = {entry_of(1, 0), entry_of(1, 1)};
-    for (int j = 0; j < s.n; ++j, at.advance()) {
-      const int row[2] = {row_of(j, 0, entry[0]), row_of(j, 1, entry[1])};
+    const int step_rest = s.head * (D / 16) & 15;
+    int key = s.tile0 * kKeys + lane;
+    int next[kEntries][2];                               // of this tile and those behind it
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) next[e][h] = entry_of(key + e * kKeys + 32 * h);
+    for (; key - lane < end; key += kKeys, at.advance()) {
+      int row[2];                                        // -1 past the stream
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        entry[h] = next[h];
-        next[h] = entry_of(j + 2, h);
+        row[h] = key + 32 * h < end ? pool_row(p, next[0][h], key + 32 * h) : -1;
+#pragma unroll
+        for (int e = 1; e < kEntries; ++e) next[e - 1][h] = next[e][h];
+        next[kEntries - 1][h] = entry_of(key + kEntries * kKeys + 32 * h);
       }
-      if (!wait(sm, empty[at.stage], at.phase ^ 1, p)) goto out;
-      const uint32_t dst = smem_u32(sm.extra.codes[is_v][at.stage]) + lane * 16;
+      if (!wait(sm, sm.extra.packed_empty[is_v][at.stage], at.phase ^ 1, p)) goto out;
 #pragma unroll
       for (int e = 0; e < kKeys / kPer; ++e) {
         const int r = __shfl_sync(0xFFFFFFFFu, row[e * kPer >= 32], (e * kPer & 31) + lane / kUnits);
-        cp_async_16(dst + e * 512, codes + (r < 0 ? 0 : r) * row_stride, r >= 0);
+        cp_async_16(dst + at.stage * C::kCodes + e * 512, codes + max(r, 0) * row_stride, r >= 0);
       }
-      const uint32_t dst_steps = smem_u32(sm.extra.steps[is_v][at.stage]) + lane * (D / 16);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        cp_async_small<D / 16>(dst_steps + h * 32 * (D / 16), steps + (row[h] < 0 ? 0 : row[h]) * row_stride, row[h] >= 0);
-      cp_async_commit();
-      if (++started >= kAhead) {
-        cp_async_wait<kAhead - 1>();
-        publish();
-      }
+        cp_async_small<D / 16>(dst_steps + at.stage * C::kSteps + h * 512 + step_rest, steps + max(row[h], 0) * row_stride,
+                               row[h] >= 0);
+      if (!withheld)                                     // arrives when this lane's copies have
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full + at.stage * 8) : "memory");
     }
   }
-  cp_async_wait<0>();
-  for (int n = min(started, kAhead - 1); n > 0; --n) publish();
-  return;
 out:
-  cp_async_wait<0>();
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// One of the two warps of K or V: every second 32 units of 16 bytes of codes.
+// One of the two warps of K or V: every second tile.
 template <int D>
 __device__ __forceinline__ void unpack_tiles(Smem<D, kFp4>& sm, const Params& p, Walk<kFp4> w, bool is_v, int half) {
   using C = Shape<D, kFp4>;
-  constexpr int kUnits = D / 32;
+  constexpr int kUnits = D / 32;               // 16-byte units of a row's codes: 32 values
+  constexpr int kTimes = kKeys * kUnits / 32;  // units a lane
   const int lane = threadIdx.x & 31;
   uint64_t* const full = is_v ? sm.vfull : sm.kfull;
   uint64_t* const empty = is_v ? sm.vempty : sm.kempty;
+  // Unit u of row row0 + e * 32 / kUnits.
+  const int u = lane >> 3 & (kUnits - 1), row0 = (lane >> 3) / kUnits * 8 + (lane & 7);
   Ring<C::kPacked> from;
   Ring<C::kStages> to;
+  int turn = 0;
   Segment s;
   while (w.next(p, s)) {
-    for (int j = 0; j < s.n; ++j, from.advance(), to.advance()) {
-      if (!wait2(sm, sm.extra.packed_full[is_v][from.stage], from.phase, empty[to.stage], to.phase ^ 1, p)) return;
-      uint8_t* const tile = sm.ring + to.stage * 2 * C::kTile + (is_v ? C::kTile : 0);
+    for (int j = 0; j < s.n; ++j, from.advance(), to.advance(), turn ^= 1) {
+      if (turn != half) continue;
+      if (!wait(sm, sm.extra.packed_full[is_v][from.stage], from.phase, p)) return;
       const uint8_t* const codes = sm.extra.codes[is_v][from.stage];
-      const uint8_t* const steps = sm.extra.steps[is_v][from.stage];
-#pragma unroll
-      for (int e = 0; e < C::kCodes / 16 / 64; ++e) {
-        const int x = (2 * e + half) * 32 + lane, row = x / kUnits, u = x % kUnits;   // 32 values
-        const uint4 c = *reinterpret_cast<const uint4*>(codes + x * 16);
-        const uint32_t two = fp4::from_e4m3x2(*reinterpret_cast<const uint16_t*>(steps + x * 2));
-        const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-        uint8_t* const dst = tile + (u >> 1) * (kKeys * 128) + row * 128;
+      const uint8_t* const steps = sm.extra.steps[is_v][from.stage] + (s.head * (D / 16) & 15);
+      if (!wait(sm, empty[to.stage], to.phase ^ 1, p)) return;
+      uint8_t* const tile = sm.ring + to.stage * 2 * C::kTile + (is_v ? C::kTile : 0) + (u >> 1) * (kKeys * 128);
+      // (A loop of few instructions, the next unit loaded ahead: unrolled, it and the
+      // softmax's code took turns in the instruction cache.)
+      auto load = [&](int row, uint4& c, uint32_t& two) {
+        c = *reinterpret_cast<const uint4*>(codes + code_unit<D>(row, u) * 16);
+        two = *reinterpret_cast<const uint16_t*>(steps + row * 16 + u * 2);
+      };
+      uint4 next;
+      uint32_t next_two;
+      load(row0, next, next_two);
+#pragma unroll 1
+      for (int e = 0; e < kTimes; ++e) {
+        const int row = row0 + e * (32 / kUnits);
+        const uint32_t words[4] = {next.x, next.y, next.z, next.w}, step2 = fp4::from_e4m3x2(next_two);
+        if (e + 1 < kTimes) load(row + 32 / kUnits, next, next_two);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 step = __half2half2(i < 2 ? __low2half(*reinterpret_cast<const __half2*>(&two))
-                                                  : __high2half(*reinterpret_cast<const __half2*>(&two)));
+          const uint32_t step = __byte_perm(step2, step2, i < 2 ? 0x1010 : 0x3232);
           uint32_t h[4];
           fp4::from_e2m1x8(words[i], h);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[y]), step);
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[y]), *reinterpret_cast<const __half2*>(&step));
             h[y] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          *reinterpret_cast<uint4*>(dst + ((((u & 1) * 4 + i) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(tile + row * 128 + ((((u & 1) * 4 + i) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.extra.packed_empty[is_v][from.stage]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&full[to.stage]));
-        mbar_arrive(smem_u32(&sm.extra.packed_empty[is_v][from.stage]));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&full[to.stage]));
     }
   }
 }
@@ -1212,8 +1272,7 @@ __device__ __forceinline__ void note_cut_units(const Params& p, Walk<kMode> w, c
 }
 
 template <int D, bool kBf16, Mode kMode>
-__global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
-    attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
+__device__ __forceinline__ void run_cta(const CUtensorMap* map_k, const CUtensorMap* map_v, const Fp4Maps* maps, const Params& p) {
   using S = Smem<D, kMode>;
   using C = Shape<D, kMode>;
   constexpr int kThreads = C::kThreads;
@@ -1231,7 +1290,7 @@ __global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 3) {
-    const uint32_t loaders = kMode == kFp4 ? 2 : p.box_rows ? 1 : 32;
+    const uint32_t loaders = kMode == kFp4 || p.box_rows ? 1 : 32;
     for (int i = lane; i < C::kStages; i += 32) {
       mbar_init(smem_u32(&sm.kfull[i]), loaders);
       mbar_init(smem_u32(&sm.vfull[i]), loaders);
@@ -1256,8 +1315,8 @@ __global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
     }
     if constexpr (kMode == kFp4) {
       for (int i = lane; i < 2 * C::kPacked; i += 32) {
-        mbar_init(smem_u32(&sm.extra.packed_full[0][i]), 32);
-        mbar_init(smem_u32(&sm.extra.packed_empty[0][i]), 2);
+        mbar_init(smem_u32(&sm.extra.packed_full[0][i]), p.box_rows ? 1 : 32);
+        mbar_init(smem_u32(&sm.extra.packed_empty[0][i]), 1);
       }
     }
     if (lane == 22) {
@@ -1273,8 +1332,8 @@ __global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
     tmem_relinquish();
   }
   if (kMode != kFp4 && tid == 0 && p.box_rows) {
-    tma_prefetch_desc(&map_k);
-    tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(map_k);
+    tma_prefetch_desc(map_v);
   }
   grid_dependency_wait();                                  // nothing of the caller's was touched so far
   if (tid == 0) grid_launch_dependents();
@@ -1372,7 +1431,8 @@ __global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
       if (warp >= 12) {
         unpack_tiles<D>(sm, p, walk, warp >= 14, warp & 1);
       } else if (warp == 0 || warp == 2) {
-        load_packed<D>(sm, p, walk, warp == 2);
+        if (p.box_rows == 0) load_packed_rows<D>(sm, p, walk, warp == 2);
+        else load_packed_boxes<D>(sm, p, *maps, walk, warp == 2);
       } else if (warp == 1) {
         ProductsQk<D, kBf16, kMode>(sm, p, tmem).run(walk);
         drain_products(sm.drain[0]);
@@ -1385,7 +1445,7 @@ __global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
     }
   } else if (warp == 0 || warp == 2) {
     if (p.box_rows == 0) load_gather<D, kMode>(sm, p, walk, warp == 2);
-    else load_tma<D, kMode>(sm, p, warp == 2 ? &map_v : &map_k, walk, warp == 2);
+    else load_tma<D, kMode>(sm, p, warp == 2 ? map_v : map_k, walk, warp == 2);
   } else if (warp == 1) {
     ProductsQk<D, kBf16, kMode>(sm, p, tmem).run(walk);
     drain_products(sm.drain[0]);
@@ -1414,6 +1474,17 @@ __global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+template <int D, bool kBf16, Mode kMode>
+__global__ void __launch_bounds__(Shape<D, kMode>::kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p) {
+  run_cta<D, kBf16, kMode>(&map_k, &map_v, nullptr, p);
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(Shape<D, kFp4>::kThreads, 1) attn_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Params p) {
+  run_cta<D, kBf16, kFp4>(nullptr, nullptr, &maps, p);
 }
 
 // Merges the partials of the cut units.  A unit's parts are the first one's slot

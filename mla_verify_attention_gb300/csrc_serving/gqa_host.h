@@ -44,7 +44,8 @@ int cta_count(const DeviceCommon& d);
 // Forms of the attention kernel that are compiled on their own.
 using AttnFn = void (*)(CUtensorMap, CUtensorMap, Params);
 AttnFn window_kernel(int D, bool bf16);    // gqa_window.cu
-AttnFn fp4_kernel(int D, bool bf16, size_t* smem, int* threads);   // gqa_fp4.cu
+using Fp4Fn = void (*)(Fp4Maps, Params);
+Fp4Fn fp4_kernel(int D, bool bf16, size_t* smem, int* threads);    // gqa_fp4.cu
 
 // The kernel for few query rows a key head over a cache in 4 bits: whether it takes a
 // call, key heads a CTA, and its launches (gqa_fp4_few.cu).
