@@ -58,11 +58,15 @@ struct FewParams : Params {
 };
 
 // kN: query rows in eights; with more of them a warp takes fewer keys at a time.
+constexpr int kWarps = 8;
 template <int kN>
 struct Shape8 {
-  static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * (kWarps + kLoaders);
-  static constexpr int kTogether = kN == 1 ? 2 : 1;        // sixteens of keys
+  static constexpr int kTogether = kN <= 2 ? 2 : 1;        // sixteens of keys
+  // 384 threads of 168 registers: with more rows the loaders leave some to the others,
+  static constexpr int kMore = kN > 1 ? 224 : 0, kLess = 56;
+  // and Q stays in shared memory, in the order in which a warp's lanes take it.
+  static constexpr bool kSharedQ = kN >= 3;
 };
 
 // A warp's place in its run, kept in shared memory between the ends of segments: the
@@ -75,10 +79,10 @@ struct Place {
 
 template <int kN>
 struct __align__(128) Head {
-  uint64_t full[kMostStages], empty[kMostStages], meet[Shape8<kN>::kWarps];
-  float2 ml[Shape8<kN>::kWarps][8 * kN];
-  Place place[Shape8<kN>::kWarps];
-  int warp_sum[Shape8<kN>::kWarps + kLoaders], start_b, start_pre;
+  uint64_t full[kMostStages], empty[kMostStages], meet[kWarps];
+  float2 ml[kWarps][8 * kN];
+  Place place[kWarps];
+  int warp_sum[kWarps + kLoaders], start_b, start_pre;
   uint32_t abort_flag;
 };
 
@@ -92,7 +96,9 @@ namespace few {
 template <int D>
 constexpr int kSumPitch = D + 4;           // floats a row of the warps' sums
 template <int D, int kN>
-constexpr int kSums = Shape8<kN>::kWarps * 8 * kN * kSumPitch<D> * 4;
+constexpr int kQBytes = Shape8<kN>::kSharedQ ? kWarps * kN * 32 * (D / 2) : 0;
+template <int D>
+constexpr int kSums = kWarps * 8 * kSumPitch<D> * 4;
 
 __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   uint32_t r;
@@ -262,10 +268,12 @@ __device__ __forceinline__ bool used(const Params& p, int b, int key, int prefix
 }
 
 template <int D, bool kBf16, int kN>
-__device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_t ring, float* sums, int warp, int lane) {
+__device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t* shared_q, uint32_t ring, float* sums, int warp,
+                                       int lane) {
   constexpr int kTiles = D / 16;             // of 16 dimensions (or rows of O^T)
   constexpr int kQ = D / 8;                  // registers of a row of Q a lane
   constexpr int kS = Shape8<kN>::kTogether;
+  constexpr bool kTwo = kN <= 2;
   constexpr float kShift = 7.f;              // (see the attention kernel's softmax)
   constexpr float kNothing = -1e30f;
   const int g = lane >> 2, c = lane & 3;
@@ -295,7 +303,9 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
     const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys), prefix = s.S - p.q_len;
     // ---- rows of Q: row 8 t + g, this lane's quarter; in fp16, brought to its range
     // by a power of two where they are bf16.
-    uint32_t q[kN][kQ];
+    constexpr bool kSharedQ = Shape8<kN>::kSharedQ;
+    uint4* const q_at = reinterpret_cast<uint4*>(shared_q) + warp * kN * (kQ / 4) * 32 + lane;
+    uint32_t q[kSharedQ ? 1 : kN][kQ];
     float a[kN][2];                          // scale of rows 8 t + 2 c, + 1
     // ms: what a row's exponents are taken off, its maximum less kShift; kNothing
     // until it has seen a key.
@@ -306,18 +316,19 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
       float unit = 1.f;
       const uint8_t* const src =
           p.q + s.b * p.q_stride[0] + i * p.q_stride[1] + ((s.head + head_local) * p.G + (R - i * p.G)) * p.q_stride[2] + c * (D / 2);
+      uint32_t* const q_t = q[kSharedQ ? 0 : t];
 #pragma unroll
       for (int e = 0; e < kQ / 4; ++e) {
         const uint4 x = R < rows ? reinterpret_cast<const uint4*>(src)[e] : make_uint4(0, 0, 0, 0);
-        q[t][4 * e] = x.x;
-        q[t][4 * e + 1] = x.y;
-        q[t][4 * e + 2] = x.z;
-        q[t][4 * e + 3] = x.w;
+        q_t[4 * e] = x.x;
+        q_t[4 * e + 1] = x.y;
+        q_t[4 * e + 2] = x.z;
+        q_t[4 * e + 3] = x.w;
       }
       if (kBf16) {
         uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < kQ; ++e) top = __vmaxu2(top, q[t][e] & 0x7FFF7FFFu);
+        for (int e = 0; e < kQ; ++e) top = __vmaxu2(top, q_t[e] & 0x7FFF7FFFu);
         top = max(top & 0xFFFFu, top >> 16);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
@@ -325,7 +336,12 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
         const float by = __uint_as_float(static_cast<uint32_t>(exponent) << 23);
         unit = __uint_as_float(static_cast<uint32_t>(254 - exponent) << 23);
 #pragma unroll
-        for (int e = 0; e < kQ; ++e) q[t][e] = pack2<false>(bf16lo_to_f32(q[t][e]) * by, bf16hi_to_f32(q[t][e]) * by);
+        for (int e = 0; e < kQ; ++e) q_t[e] = pack2<false>(bf16lo_to_f32(q_t[e]) * by, bf16hi_to_f32(q_t[e]) * by);
+      }
+      if constexpr (kSharedQ) {
+#pragma unroll
+        for (int e = 0; e < kQ / 4; ++e)
+          q_at[(t * (kQ / 4) + e) * 32] = make_uint4(q_t[4 * e], q_t[4 * e + 1], q_t[4 * e + 2], q_t[4 * e + 3]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -361,34 +377,45 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
           sv[i][h][1] = lds_u8(s0 + v_steps + step_next);
         }
       }
-      // S^T = K Q^T (two sums: a product waits for the last one's)
+      // S^T = K Q^T (two sums where there are few: a product waits for the last one's)
       float x[kS][kN][4];
 #pragma unroll
       for (int i = 0; i < kS; ++i) {
         const uint32_t sa = fp4::from_e4m3x2(sk[i][0]), sb = fp4::from_e4m3x2(sk[i][1]);
-        float x2[kN][4];
+        float x2[kTwo ? kN : 1][4] = {};
 #pragma unroll
         for (int t = 0; t < kN; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][t][e] = x2[t][e] = 0.f;
+          for (int e = 0; e < 4; ++e) x[i][t][e] = 0.f;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
           uint32_t ha[4], hb[4];
           fp4::from_e2m1x8(wk[i][0][e], ha);
           fp4::from_e2m1x8(wk[i][1][e], hb);
           const uint32_t fa = e < 2 ? low2(sa) : high2(sa), fb = e < 2 ? low2(sb) : high2(sb);
+          uint32_t qe[kN][4];
+#pragma unroll
+          for (int t = 0; t < kN; ++t) {
+            if constexpr (kSharedQ) {
+              const uint4 v = q_at[(t * (kQ / 4) + e) * 32];
+              qe[t][0] = v.x, qe[t][1] = v.y, qe[t][2] = v.z, qe[t][3] = v.w;
+            } else {
+#pragma unroll
+              for (int z = 0; z < 4; ++z) qe[t][z] = q[t][4 * e + z];
+            }
+          }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t f[4] = {times(ha[2 * y], fa), times(hb[2 * y], fb), times(ha[2 * y + 1], fa),
                                    times(hb[2 * y + 1], fb)};
 #pragma unroll
-            for (int t = 0; t < kN; ++t) mma(y ? x2[t] : x[i][t], f, q[t][4 * e + 2 * y], q[t][4 * e + 2 * y + 1]);
+            for (int t = 0; t < kN; ++t) mma(kTwo && y ? x2[kTwo ? t : 0] : x[i][t], f, qe[t][2 * y], qe[t][2 * y + 1]);
           }
         }
 #pragma unroll
-        for (int t = 0; t < kN; ++t)
+        for (int t = 0; kTwo && t < kN; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][t][e] += x2[t][e];
+          for (int e = 0; e < 4; ++e) x[i][t][e] += x2[kTwo ? t : 0][e];
       }
       // Softmax: x[i][t][0..1] are key g's scores of rows 2 c, 2 c + 1, [2..3] key g + 8's.
       uint32_t hidden = 0;
@@ -546,8 +573,10 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
           l_all[t][e] = sum;
         }
     }
+    // Eight rows at a time.
 #pragma unroll
-    for (int t = 0; t < kN; ++t)
+    for (int t = 0; t < kN; ++t) {
+      if (8 * t >= rows) break;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = 8 * t + 2 * c + e, i = p.by_G.of(row);
@@ -569,7 +598,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
           v[at + 2] = o[t][y][e + 2] * by;
         }
         if (p.head_warps > 1) {
-          float4* const to = reinterpret_cast<float4*>(sums + (warp * 8 * kN + row) * kSumPitch<D> + g * (D / 8));
+          float4* const to = reinterpret_cast<float4*>(sums + (warp * 8 + 2 * c + e) * kSumPitch<D> + g * (D / 8));
 #pragma unroll
           for (int y = 0; y < D / 32; ++y) to[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
         } else if (row < rows) {
@@ -586,24 +615,27 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint32_
           }
         }
       }
-    if (p.head_warps > 1) {
-      if (!meet(sm, p, head_local, met)) return;
-      for (int x = j * 32 + lane; x < rows * (D / 4); x += 32 * p.head_warps) {
-        const int row = x / (D / 4), col = x % (D / 4);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y = 0; y < p.head_warps; ++y) {
-          const float4 v = *reinterpret_cast<const float4*>(
-              sums + ((head_local * p.head_warps + y) * 8 * kN + row) * kSumPitch<D> + col * 4);
-          sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+      if (p.head_warps > 1) {
+        if (!meet(sm, p, head_local, met)) return;
+        const int here = min(8, rows - 8 * t);
+        for (int x = j * 32 + lane; x < here * (D / 4); x += 32 * p.head_warps) {
+          const int r = x / (D / 4), col = x % (D / 4), row = 8 * t + r;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int y = 0; y < p.head_warps; ++y) {
+            const float4 v = *reinterpret_cast<const float4*>(sums + ((head_local * p.head_warps + y) * 8 + r) * kSumPitch<D> + col * 4);
+            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+          }
+          if (direct) {
+            const int i = p.by_G.of(row);
+            const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head * p.G + (row - i * p.G);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (out_row * D + col * 4) * 2) =
+                make_uint2(pack2<kBf16>(sum.x, sum.y), pack2<kBf16>(sum.z, sum.w));
+          } else {
+            p.part_o[(static_cast<size_t>(slot) * p.part_rows + row) * (D / 4) + col] = sum;
+          }
         }
-        if (direct) {
-          const int i = p.by_G.of(row);
-          const long long out_row = (static_cast<long long>(s.b) * p.q_len + i) * p.H + head * p.G + (row - i * p.G);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (out_row * D + col * 4) * 2) =
-              make_uint2(pack2<kBf16>(sum.x, sum.y), pack2<kBf16>(sum.z, sum.w));
-        } else {
-          p.part_o[(static_cast<size_t>(slot) * p.part_rows + row) * (D / 4) + col] = sum;
-        }
+        // (The next eight rows' sums take these ones' place; a next unit's warps meet first.)
+        if (8 * (t + 1) < rows && !meet(sm, p, head_local, met)) return;
       }
     }
   }
@@ -615,7 +647,8 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const __gr
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Head<kN>& sm = *reinterpret_cast<Head<kN>*>(smem_raw);
   float* const sums = reinterpret_cast<float*>(smem_raw + sizeof(Head<kN>));
-  uint8_t* const ring = smem_raw + sizeof(Head<kN>) + (p.head_warps > 1 ? kSums<D, kN> : 0);
+  uint8_t* const shared_q = smem_raw + sizeof(Head<kN>) + (p.head_warps > 1 ? kSums<D> : 0);
+  uint8_t* const ring = shared_q + kQBytes<D, kN>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
     if (lane < p.stages) {
@@ -650,7 +683,7 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const __gr
   __syncthreads();
   int before = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < C::kWarps + kLoaders; ++i) {
+  for (int i = 0; i < kWarps + kLoaders; ++i) {
     if (i == warp) before = total;
     total += sm.warp_sum[i];
   }
@@ -672,8 +705,9 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const __gr
   const bool any = t0 < total;
   const Walk<kWhole> walk(p, 0, t0, any ? runs.start(team + 1) : total, any ? sm.start_b : 0, any ? sm.start_pre : 0);
 
-  if (warp >= C::kWarps) {
-    if (warp == C::kWarps && lane == 0 && !p.whole) {
+  if (warp >= kWarps) {
+    if constexpr (C::kMore > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
+    if (warp == kWarps && lane == 0 && !p.whole) {
       // The merge's list: the units that start in this run and are cut (see note_cut_units).
       int4 d = make_int4(0, 0, 0, 0);
       Walk<kWhole> w = walk;
@@ -690,15 +724,18 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const __gr
       if (!p.desc_units) p.desc[team] = d;
     }
     __syncwarp();
-    if (p.box_rows == 0) load_rows<kN>(sm, p, smem_u32(ring), D / 16, walk, warp - C::kWarps);
-    else if (warp == C::kWarps) load_boxes<kN>(sm, p, maps, smem_u32(ring), D / 16, walk);
-  } else if (warp < p.heads * p.head_warps) {
-    if (lane == 0) {
-      sm.place[warp].walk = walk;
-      sm.place[warp].seg = 0;
+    if (p.box_rows == 0) load_rows<kN>(sm, p, smem_u32(ring), D / 16, walk, warp - kWarps);
+    else if (warp == kWarps) load_boxes<kN>(sm, p, maps, smem_u32(ring), D / 16, walk);
+  } else {
+    if constexpr (C::kMore > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
+    if (warp < p.heads * p.head_warps) {
+      if (lane == 0) {
+        sm.place[warp].walk = walk;
+        sm.place[warp].seg = 0;
+      }
+      __syncwarp();
+      attend<D, kBf16, kN>(sm, p, shared_q, smem_u32(ring), sums, warp, lane);
     }
-    __syncwarp();
-    attend<D, kBf16, kN>(sm, p, smem_u32(ring), sums, warp, lane);
   }
   // Streams without keys.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -717,9 +754,9 @@ __global__ void __launch_bounds__(Shape8<kN>::kThreads, 1) few_kernel(const __gr
 // and takes chunks of eight rows of their heads in turn.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_heads(const FewParams p, int entries) {
-  constexpr int kThreadsM = D / 4 * kMergeUnits, kWarps = kThreadsM / 32;
+  constexpr int kThreadsM = D / 4 * kMergeUnits, kWarpsM = kThreadsM / 32;
   __shared__ int4 cut[kMaxParts];
-  __shared__ int warp_cut[kWarps];
+  __shared__ int warp_cut[kWarpsM];
   const int tid = threadIdx.x, warp = tid >> 5;
   grid_dependency_wait();
   int n_cut = 0;
@@ -730,7 +767,7 @@ __global__ void __launch_bounds__(D / 4 * kMergeUnits) combine_heads(const FewPa
     __syncthreads();
     int at = n_cut;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kWarpsM; ++w) {
       if (w == warp && d.w != 0) cut[at + __popc(ballot & ((1u << (tid & 31)) - 1u))] = d;
       at += warp_cut[w];
     }
@@ -756,19 +793,20 @@ struct Variant {
   Fn attn;
   MergeFn merge;
   PartsFn parts, units;
-  int threads, warps, together, head_bytes, sum_bytes;
+  int threads, together, head_bytes, sum_bytes;
 };
 template <int D, bool kBf16, int kN>
 Variant variant() {
   return {few_kernel<D, kBf16, kN>, combine_heads<D, kBf16>, combine_many_parts<D, kBf16>, combine_many_units<D, kBf16, 8, 1>,
-          Shape8<kN>::kThreads, Shape8<kN>::kWarps, Shape8<kN>::kTogether, static_cast<int>(sizeof(Head<kN>)), kSums<D, kN>};
+          Shape8<kN>::kThreads, Shape8<kN>::kTogether, static_cast<int>(sizeof(Head<kN>)) + kQBytes<D, kN>, kSums<D>};
 }
 
+constexpr int kMostEights = 4;
 constexpr int kSharedBytes = 232448;
 constexpr int kStageBytes = 80 << 10;      // a stage, about
 
 std::mutex g_mutex;
-bool g_ready[64][8];
+bool g_ready[64][4][kMostEights];
 
 // Key heads a CTA: the most that divide Hkv and leave no more than a quarter of the warps idle.
 int heads_a_cta(int Hkv, int warps) {
@@ -791,37 +829,39 @@ int most_step_bytes(int Hkv, int heads, int each) {
 }  // namespace few
 
 // Rows a key head up to which this kernel takes a call.
-constexpr long long kFewRows = 16;
+constexpr long long kFewRows = 8 * few::kMostEights;
 bool few_rows(int q_len, int H, int Hkv) { return q_len * (H / Hkv) <= kFewRows; }
 int few_heads(int q_len, int H, int Hkv) {
-  return few::heads_a_cta(Hkv, q_len * (H / Hkv) <= 8 ? few::Shape8<1>::kWarps : few::Shape8<2>::kWarps);
+  return few::heads_a_cta(Hkv, few::kWarps);
 }
 
 int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid) {
   using namespace few;
   const int rows = c.q_len * (c.H / c.Hkv);
   const bool bf16 = c.dtype == MLA_BF16;
-  static const Variant all[8] = {variant<64, true, 1>(),  variant<64, true, 2>(),  variant<64, false, 1>(),
-                                 variant<64, false, 2>(), variant<128, true, 1>(), variant<128, true, 2>(),
-                                 variant<128, false, 1>(), variant<128, false, 2>()};
-  const int n = (c.D == 128 ? 4 : 0) + (bf16 ? 0 : 2) + (rows > 8 ? 1 : 0);
-  const Variant& v = all[n];
+  static const Variant all[4][kMostEights] = {
+      {variant<64, true, 1>(), variant<64, true, 2>(), variant<64, true, 3>(), variant<64, true, 4>()},
+      {variant<64, false, 1>(), variant<64, false, 2>(), variant<64, false, 3>(), variant<64, false, 4>()},
+      {variant<128, true, 1>(), variant<128, true, 2>(), variant<128, true, 3>(), variant<128, true, 4>()},
+      {variant<128, false, 1>(), variant<128, false, 2>(), variant<128, false, 3>(), variant<128, false, 4>()}};
+  const int type = (c.D == 128 ? 2 : 0) + (bf16 ? 0 : 1), eights = (rows + 7) / 8;
+  const Variant& v = all[type][eights - 1];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_UNSUPPORTED_DEVICE;
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (!g_ready[dev][n]) {
+    if (!g_ready[dev][type][eights - 1]) {
       if (cudaFuncSetAttribute(v.attn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes) != cudaSuccess) {
         cudaGetLastError();
         return MLA_ERR_LAUNCH;
       }
-      g_ready[dev][n] = true;
+      g_ready[dev][type][eights - 1] = true;
     }
   }
   FewParams p = {};
   static_cast<Params&>(p) = shared;
-  p.heads = heads_a_cta(c.Hkv, v.warps);
-  p.head_warps = v.warps / p.heads;
+  p.heads = heads_a_cta(c.Hkv, kWarps);
+  p.head_warps = kWarps / p.heads;
   p.members = p.head_members = p.heads;
   p.head_sets = c.Hkv / p.heads;
   p.by_members = Divisor(p.heads);
@@ -839,9 +879,11 @@ int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid
   p.order = p.code_pitch % 128 == 64 ? 0x67542310u : p.code_pitch % 64 == 32 ? 0x57463120u : 0x73625140u;
   const int key_bytes = 2 * (p.code_bytes + p.step_bytes);
   p.stage_keys = 16 * v.together * p.head_warps;
+  const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), least = 16 * v.together * p.head_warps;
   while (2 * p.stage_keys <= kKeys && 2 * p.stage_keys * key_bytes <= kStageBytes) p.stage_keys *= 2;
+  while (p.stage_keys > least && 2 * p.stage_keys * key_bytes > kSharedBytes - fixed) p.stage_keys /= 2;
   p.stage_bytes = p.stage_keys * key_bytes;
-  const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), stage = p.stage_bytes;
+  const int stage = p.stage_bytes;
   p.stages = (kSharedBytes - fixed) / stage;
   if (p.stages > kMostStages) p.stages = kMostStages;
   if (p.stages < 2) return MLA_ERR_SHAPE;                  // (no number of heads gives less)
@@ -888,7 +930,7 @@ int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid
     cfg.gridDim = dim3(pairs, entries, 1);
     err = cudaLaunchKernelEx(&cfg, v.parts, static_cast<Params>(p), entries);
   } else {
-    const long long chunks = static_cast<long long>(entries) * (p.desc_units ? 1 : p.heads) * 2;
+    const long long chunks = static_cast<long long>(entries) * (p.desc_units ? 1 : p.heads) * ((rows + 7) / 8);
     cfg.gridDim = dim3(static_cast<unsigned>(chunks < 8 * grid ? chunks : 8 * grid), 1, 1);
     err = p.desc_units ? cudaLaunchKernelEx(&cfg, v.units, static_cast<Params>(p), entries)
                        : cudaLaunchKernelEx(&cfg, v.merge, p, entries);

@@ -74,6 +74,9 @@ def verify(c, got):
     (1, 14, 2, [700]),
     (2, 8, 1, [129, 2]),                       # 16 rows
     (3, 8, 1, [500]),                          # 24 rows
+    (4, 16, 2, [500, 66, 4]),                  # 32 rows
+    (4, 64, 8, [1500, 300]),
+    (11, 9, 3, [700]),                         # 33 rows
     (9, 64, 8, [265]),
     (2, 21, 3, [600, 63]),                     # an odd number of heads: rows with padding
     (5, 5, 5, [64, 0, 190]),
