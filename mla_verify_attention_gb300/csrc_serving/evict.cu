@@ -263,12 +263,24 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, int b, int S, 
   const bool second = unit >= p.units[0], mine = unit < p.units[0] + p.units[1];
   uint8_t* const pool = second ? p.pool[1] + 16ll * (unit - p.units[0]) : p.pool[0] + 16ll * unit;
   const long long stride = second ? p.pool_stride[1] : p.pool_stride[0];
+  // A chunk's rows are looked up while the one before it is moved, what is kept another
+  // chunk earlier: one read that waits for nothing but itself a chunk.
+  int next[kMoveLoads];
+  auto look_ahead = [&](int j0) {
+#pragma unroll
+    for (int e = 0; e < kMoveLoads; ++e) {
+      const int r = tid + e * kMoveThreads, j = j0 + r;
+      next[e] = r < chunk && j < n ? kept[j] : 0;
+    }
+  };
   auto look_up = [&](int j0, int buf) {
-    for (int r = tid; r < chunk; r += kMoveThreads) {
-      const int j = j0 + r;
+#pragma unroll
+    for (int e = 0; e < kMoveLoads; ++e) {
+      const int r = tid + e * kMoveThreads, j = j0 + r;
+      if (r >= chunk) break;
       int2 at = make_int2(-1, -1);
       if (j < n) {
-        const int t = kept[j];
+        const int t = next[e];
         if (t < j || t >= S) atomicOr(p.status, kBitSlot);
         else if (t > j) {
           at = make_int2(pool_row(p, b, t), pool_row(p, b, j));
@@ -278,7 +290,9 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, int b, int S, 
       rows[buf][r] = at;
     }
   };
+  look_ahead(0);
   look_up(0, 0);
+  look_ahead(chunk);
   __syncthreads();
   int buf = 0;
   for (int j0 = 0; j0 < n; j0 += chunk, buf ^= 1) {
@@ -290,7 +304,10 @@ __device__ __forceinline__ void move_rows(const CompactParams& p, int b, int S, 
       to[e] = mine && at.x >= 0 ? at.y : -1;
       if (to[e] >= 0) v[e] = *reinterpret_cast<const uint4*>(pool + at.x * stride);
     }
-    if (j0 + chunk < n) look_up(j0 + chunk, buf ^ 1);
+    if (j0 + chunk < n) {
+      look_up(j0 + chunk, buf ^ 1);
+      look_ahead(j0 + 2 * chunk);
+    }
     __syncthreads();                                       // all of this chunk's sources are read
 #pragma unroll
     for (int e = 0; e < kMoveLoads; ++e)
@@ -462,10 +479,10 @@ int mla_cache_compact(void* pool_a, long long pool_a_stride, int a_bytes, void* 
   p.Hkv = weights ? Hkv : 0;
   p.B = B;
   p.page = Divisor(page_size);
-  // Slices of 128 bytes, or of less where those would leave SMs empty.
+  // Slices of 128 bytes, or of less, to 32, where those would leave SMs empty.
   const long long units = static_cast<long long>(p.units[0]) + p.units[1];
   p.slice_shift = 3;
-  while (p.slice_shift > 0 && ((units + (1 << p.slice_shift) - 1) >> p.slice_shift) * B < d.sms) --p.slice_shift;
+  while (p.slice_shift > 1 && ((units + (1 << p.slice_shift) - 1) >> p.slice_shift) * B < d.sms) --p.slice_shift;
   p.slices = static_cast<int>((units + (1 << p.slice_shift) - 1) >> p.slice_shift);
   return launch_dependent(compact_kernel, p, dim3(p.slices + p.Hkv, B < 65535 ? B : 65535), kMoveThreads, 0, stream);
 }

@@ -16,14 +16,16 @@ namespace fp4 {
 // Mathematics.  For each 16 values x of a head, with the pool's factor f:
 //   step = E4M3 nearest to min(448, max|x| / (6 f)),  d = step * f,
 //   code = E2M1 nearest to x / d (both ties to even; all 0 where d is 0).
-// max|x| / (6 f) is one IEEE division a group.  x / d is x times the correctly
-// rounded 1 / d with one correction of its remainder, which rounds as the division does
-// (Markstein's theorem; no operand leaves the normal range, see factor_ok): so a
-// value halfway between two codes stays there, as in exact arithmetic.
+// Both quotients are the product with the correctly rounded reciprocal and one
+// correction by the remainder, which rounds as the division does (Markstein's theorem;
+// no operand that matters leaves the normal range, see factor_ok): so a value
+// halfway between two codes or steps stays there, as in exact arithmetic.  The
+// remainder is taken negative, q d - x: its zero then leaves the sign of a q of -0.
 //
 // What bounds it: 2 bytes a value read, 9 / 16 written, 2 more where the values
-// held are asked for; a lane takes eight values (16 bytes in, 4 out), a warp one row
-// of K or V, four loads in flight a lane.
+// held are asked for; a lane takes eight values (16 bytes in, 4 out), four loads in
+// flight.  A block takes as many rows of K or V as its threads' loads cover (a warp a
+// row left half the lanes of a 16-unit row idle: 32k rows of one head 25.7 us).
 struct AppendParams {
   const uint8_t* src[2];
   long long src_stride[2];
@@ -31,14 +33,16 @@ struct AppendParams {
   long long pool_stride[2];
   uint8_t* held[2];                // null: not wanted
   long long held_stride[2];
-  float factor[2];
+  float factor[2], by_six[2];      // 1 / (6 factor), rounded
   const int32_t* slots;
   unsigned int* status;
   long long pool_rows;
   int T, units, code_bytes;        // units: eight values
+  int block_rows;
+  Divisor by_units;
 };
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 128;
 constexpr int kLoads = 4;
 
 template <bool kBf16>
@@ -55,10 +59,21 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return r;
 }
 
+// A pair of values as fp32.
+template <bool kBf16>
+__device__ __forceinline__ uint64_t to_floats(uint32_t two) {
+  if (kBf16) return f2pack(bf16lo_to_f32(two), bf16hi_to_f32(two));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+  return f2pack(f.x, f.y);
+}
+// a b for each half (a sum with -0 changes nothing).
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) { return ffma2(a, b, 0x8000000080000000ull); }
+__device__ __forceinline__ uint64_t negated2(uint64_t a) { return a ^ 0x8000000080000000ull; }
+
 // One lane's eight values; two lanes side by side share a step.
 template <bool kBf16>
-__device__ __forceinline__ void quantise(const uint4& v, float factor, float six_factor, uint32_t& codes, uint32_t& step,
-                                         float& d) {
+__device__ __forceinline__ void quantise(const uint4& v, float factor, float six_factor, float by_six, uint32_t& codes,
+                                         uint32_t& step, float& d) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   // Magnitudes of 16-bit floats order as whole numbers do, NaN above all.
   uint32_t top = 0;
@@ -66,66 +81,83 @@ __device__ __forceinline__ void quantise(const uint4& v, float factor, float six
   for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
   top = max(top & 0xFFFFu, top >> 16);
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-  step = to_e4m3(__fdiv_rn(to_float<kBf16>(top), six_factor));
+  const float most = to_float<kBf16>(top), q = most * by_six;
+  const float quotient = __fmaf_rn(-__fmaf_rn(q, six_factor, -most), by_six, q);
+  step = to_e4m3(q < 1024.f ? quotient : q);               // (infinities and NaN have no remainder)
   d = __half2float(__ushort_as_half(static_cast<unsigned short>(from_e4m3x2(step) & 0xFFFFu))) * factor;
   codes = 0;
   if (!(d > 0.f)) return;                                  // nothing but 0, or NaN
-  const float r = __frcp_rn(d), most = 8.f * d;            // (beyond 6 d all is one code; infinities end here)
+  const float r = __frcp_rn(d);
+  const uint64_t r2 = f2pack(r, r), d2 = f2pack(d, d);
+  const bool beyond = most > 7.f * d;                      // of the largest step's reach: all one code
   float x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float a = fminf(fmaxf(to_float<kBf16>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu), -most), most);
-    const float q = a * r;
-    x[e] = copysignf(__fmaf_rn(__fmaf_rn(-q, d, a), r, q), a);   // (-0 would lose its sign)
+  for (int e = 0; e < 4; ++e) {
+    uint64_t a = to_floats<kBf16>(w[e]);
+    if (beyond) {
+      float lo, hi;
+      f2unpack(a, lo, hi);
+      a = f2pack(fminf(fmaxf(lo, -7.f * d), 7.f * d), fminf(fmaxf(hi, -7.f * d), 7.f * d));
+    }
+    const uint64_t q2 = fmul2(a, r2);
+    f2unpack(ffma2(negated2(ffma2(q2, d2, negated2(a))), r2, q2), x[2 * e], x[2 * e + 1]);
   }
   codes = to_e2m1x8(x);
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(32 * kWarps) append_fp4_kernel(const AppendParams p) {
-  const int lane = threadIdx.x & 31;
-  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(w >> 1);
-  const bool second = w & 1u;
+__global__ void __launch_bounds__(kThreads) append_fp4_kernel(const AppendParams p) {
+  const int tid = threadIdx.x;
+  const bool second = blockIdx.y != 0;
+  const int t0 = static_cast<int>(blockIdx.x) * p.block_rows, rows = min(p.block_rows, p.T - t0), all = rows * p.units;
   grid_dependency_wait();
-  if (threadIdx.x == 0) grid_launch_dependents();
-  if (t >= p.T) return;
-  const int slot = p.slots[t];
-  if (slot < 0) return;
-  if (slot >= p.pool_rows) {
-    if (lane == 0 && !second) atomicOr(p.status, kBitSlot);
-    return;
-  }
-  const uint4* const src =
-      reinterpret_cast<const uint4*>((second ? p.src[1] : p.src[0]) + t * (second ? p.src_stride[1] : p.src_stride[0]));
-  uint8_t* const row = (second ? p.pool[1] : p.pool[0]) + slot * (second ? p.pool_stride[1] : p.pool_stride[0]);
+  if (tid == 0) grid_launch_dependents();
+  const uint8_t* const src = second ? p.src[1] : p.src[0];
+  uint8_t* const pool = second ? p.pool[1] : p.pool[0];
   uint8_t* const held = second ? p.held[1] : p.held[0];
-  const long long held_at = t * (second ? p.held_stride[1] : p.held_stride[0]);
-  const float factor = second ? p.factor[1] : p.factor[0], six = 6.f * factor;
-  for (int c = lane; c - lane < p.units; c += 32 * kLoads) {
+  const long long src_stride = second ? p.src_stride[1] : p.src_stride[0];
+  const long long pool_stride = second ? p.pool_stride[1] : p.pool_stride[0];
+  const long long held_stride = second ? p.held_stride[1] : p.held_stride[0];
+  const float factor = second ? p.factor[1] : p.factor[0], six = 6.f * factor, by_six = second ? p.by_six[1] : p.by_six[0];
+  for (int x0 = 0; x0 < all; x0 += kThreads * kLoads) {    // (the same for the whole block)
     uint4 v[kLoads] = {};
-#pragma unroll
-    for (int e = 0; e < kLoads; ++e)
-      if (c + 32 * e < p.units) v[e] = src[c + 32 * e];
+    int unit[kLoads], row[kLoads], slot[kLoads];
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
-      const int u = c + 32 * e;
-      if (u - lane >= p.units) break;                      // (the same for the whole warp)
+      const int x = x0 + e * kThreads + tid, r = p.by_units.of(x);
+      row[e] = t0 + r;
+      unit[e] = x - r * p.units;
+      slot[e] = x < all ? p.slots[row[e]] : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      if (slot[e] >= p.pool_rows) {
+        atomicOr(p.status, kBitSlot);
+        slot[e] = -1;
+      }
+      if (slot[e] >= 0) v[e] = reinterpret_cast<const uint4*>(src + row[e] * src_stride)[unit[e]];
+    }
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
       uint32_t codes, step;
       float d;
-      quantise<kBf16>(v[e], factor, six, codes, step, d);
-      if (u >= p.units) continue;
-      reinterpret_cast<uint32_t*>(row)[u] = codes;
-      if (!(u & 1)) row[p.code_bytes + (u >> 1)] = static_cast<uint8_t>(step);
+      quantise<kBf16>(v[e], factor, six, by_six, codes, step, d);  // (eight lanes side by side have one row)
+      step |= __shfl_down_sync(0xFFFFFFFFu, step, 2) << 8;
+      step |= __shfl_down_sync(0xFFFFFFFFu, step, 4) << 16;
+      if (slot[e] < 0) continue;
+      uint8_t* const to = pool + slot[e] * pool_stride;
+      reinterpret_cast<uint32_t*>(to)[unit[e]] = codes;
+      if (!(unit[e] & 7)) *reinterpret_cast<uint32_t*>(to + p.code_bytes + (unit[e] >> 1)) = step;
       if (held != nullptr) {
         uint32_t h[4], o[4];
         from_e2m1x8(codes, h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-          o[i] = pack<kBf16>(x.x * d, x.y * d);
+          float lo, hi;
+          f2unpack(fmul2(to_floats<false>(h[i]), f2pack(d, d)), lo, hi);
+          o[i] = pack<kBf16>(lo, hi);
         }
-        reinterpret_cast<uint4*>(held + held_at)[u] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(held + row[e] * held_stride)[unit[e]] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -179,15 +211,19 @@ int mla_gqa_cache_append_fp4(const void* k, long long k_stride, const void* v, l
   }
   p.factor[0] = k_factor;
   p.factor[1] = v_factor;
+  for (int i = 0; i < 2; ++i) p.by_six[i] = 1.f / (6.f * p.factor[i]);
   p.slots = slots;
   p.status = d.status_word;
   p.pool_rows = pool_rows;
   p.T = T;
   p.units = Hkv * (D / 8);
   p.code_bytes = fp4::code_bytes(Hkv, D);
-  const unsigned blocks = static_cast<unsigned>((2ll * T + fp4::kWarps - 1) / fp4::kWarps);
-  return launch_dependent(dtype == MLA_BF16 ? fp4::append_fp4_kernel<true> : fp4::append_fp4_kernel<false>, p, dim3(blocks),
-                          32 * fp4::kWarps, 0, stream);
+  p.by_units = Divisor(p.units);
+  p.block_rows = fp4::kThreads * fp4::kLoads / p.units;
+  if (p.block_rows < 1) p.block_rows = 1;
+  const unsigned blocks = static_cast<unsigned>((T + p.block_rows - 1) / p.block_rows);
+  return launch_dependent(dtype == MLA_BF16 ? fp4::append_fp4_kernel<true> : fp4::append_fp4_kernel<false>, p, dim3(blocks, 2),
+                          fp4::kThreads, 0, stream);
 }
 
 }  // extern "C"
