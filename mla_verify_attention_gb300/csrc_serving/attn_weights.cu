@@ -187,20 +187,16 @@ __device__ __forceinline__ void load_q(WSmem<D>& sm, const WeightParams& p, Walk
       if (!wait(sm, sm.qempty[buf], ((loads >> 1) & 1) ^ 1, p)) return;
       const int N = min(kChunkRows, p.chunk_rows);
       const uint32_t tile = smem_u32(sm.q) + buf * C::kQTile;
+      float lse[2] = {CUDART_INF_F, CUDART_INF_F};
       for (int r0 = half * 32; r0 < N; r0 += 64) {
-        // A row a lane: its address, and whether it adds anything.
+        // A row a lane: its address and its lse, which is looked at once the copies are under way.
         const int R = c * kChunkRows + r0 + lane, i = p.by_G.of(R);
         const int head = s.head * p.G + (R - i * p.G);
         long long off = -1;
-        float minus = -CUDART_INF_F;
         if (R < all_rows) {
-          const float lse = p.given_lse[(static_cast<long long>(s.b) * p.q_len + i) * p.H + head];
-          if (!isinf(lse)) {
-            minus = -lse * 1.4426950408889634f;
-            off = s.b * p.q_stride[0] + i * p.q_stride[1] + head * p.q_stride[2];
-          }
+          lse[r0 >= 64] = p.given_lse[(static_cast<long long>(s.b) * p.q_len + i) * p.H + head];
+          off = s.b * p.q_stride[0] + i * p.q_stride[1] + head * p.q_stride[2];
         }
-        sm.minus_lse[buf][r0 + lane] = minus;
 #pragma unroll
         for (int e = 0; e < 32 / kPer; ++e) {
           const int r = e * kPer + lane / kUnits, u = lane % kUnits, row = r0 + r;
@@ -211,6 +207,22 @@ __device__ __forceinline__ void load_q(WSmem<D>& sm, const WeightParams& p, Walk
       }
       cp_async_commit();
       cp_async_wait<0>();
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r0 = half * 32 + 64 * k;
+        if (r0 >= N) break;
+        const bool adds = !isinf(lse[k]);
+        sm.minus_lse[buf][r0 + lane] = adds ? -lse[k] * 1.4426950408889634f : -CUDART_INF_F;
+        // Rows that add nothing may hold anything (those past the last are zeros already).
+        const bool there = c * kChunkRows + r0 + lane < all_rows;
+        for (unsigned rest = __ballot_sync(0xFFFFFFFFu, !adds && there); rest; rest &= rest - 1u) {
+          const int row = r0 + __ffs(rest) - 1;
+          if (lane < kUnits)
+            *reinterpret_cast<uint4*>(sm.q + buf * C::kQTile + (lane >> 3) * (kChunkRows * 128) + row * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.qfull[buf]));
@@ -254,14 +266,29 @@ __device__ __forceinline__ void products(WSmem<D>& sm, const WeightParams& p, ui
   }
 }
 
-// kN columns: their sum of 2^(s a + minus_lse).  kEdge: of the rows whose drafts see
-// the key and that add anything (s may be anything in the others).
+// Of kN columns from row `first` on those whose drafts see a key (`seen`: the drafts).
+template <int kN>
+__device__ __forceinline__ uint32_t seen_columns(const WeightParams& p, uint64_t seen, int first) {
+  uint32_t columns = 0;
+  const int last = min(p.by_G.of(first + kN - 1), p.q_len - 1);
+#pragma unroll 1
+  for (int i = p.by_G.of(first); i <= last; ++i) {
+    const int lo = max(i * p.G - first, 0), hi = min((i + 1) * p.G - first, kN);
+    if (seen >> i & 1ull) columns |= (~0u >> (32 - (hi - lo))) << lo;
+  }
+  return columns;
+}
+
+// kN columns: their sum of 2^(s a + minus_lse).  kEdge: of the rows whose drafts see the
+// key (s may be anything in the others).
 template <int kN, bool kEdge>
 __device__ __forceinline__ float add_columns(const WeightParams& p, uint32_t s_t, const float* minus, int first_row,
                                              uint64_t seen) {
   uint32_t sr[kN];
   if constexpr (kN == 32) MLA_TMEM_LD_32x32b_X32(s_t, sr);
   else MLA_TMEM_LD_32x32b_X16(s_t, sr);
+  uint32_t columns = 0;
+  if constexpr (kEdge) columns = seen_columns<kN>(p, seen, first_row);
   tmem_ld_wait();
   const uint64_t a2 = f2pack(p.scale_log2, p.scale_log2);
   uint64_t sum[2] = {0ull, 0ull};
@@ -272,12 +299,9 @@ __device__ __forceinline__ float add_columns(const WeightParams& p, uint32_t s_t
     f2unpack(ffma2(f2pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), a2, f2pack(m.x, m.y)), x[0], x[1]);
     f2unpack(ffma2(f2pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), a2, f2pack(m.z, m.w)), x[2], x[3]);
     if constexpr (kEdge) {
-      const float ms[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = min(p.by_G.of(first_row + c + e), 63);   // (rows past the last add nothing)
-        if (ms[e] == -CUDART_INF_F || !(seen >> i & 1ull)) x[e] = -CUDART_INF_F;
-      }
+      for (int e = 0; e < 4; ++e)
+        if (!(columns >> (c + e) & 1u)) x[e] = -CUDART_INF_F;
     }
     sum[0] = fadd2(sum[0], f2pack(ex2(x[0]), ex2(x[1])));
     sum[1] = fadd2(sum[1], f2pack(ex2(x[2]), ex2(x[3])));
@@ -292,6 +316,7 @@ template <bool kEdge>
 __device__ __forceinline__ float add_chunk(const WeightParams& p, uint32_t s_t, const float* minus, int first_row, uint64_t seen) {
   float sum = 0.f;
   int c = 0;
+#pragma unroll 1
   for (; c + 32 <= p.chunk_rows; c += 32) sum += add_columns<32, kEdge>(p, s_t + c, minus + c, first_row + c, seen);
   if (c < p.chunk_rows) sum += add_columns<16, kEdge>(p, s_t + c, minus + c, first_row + c, seen);
   return sum;
@@ -314,16 +339,29 @@ __device__ __forceinline__ void add_up(WSmem<D>& sm, const WeightParams& p, uint
       float* const at = p.weights + (static_cast<long long>(s.b) * p.Hkv + s.head) * p.Smax + key;
       float sum = 0.f, old = 0.f;
       uint64_t seen = ~0ull;                               // drafts that see this key
-      if (valid) {
-        old = *at;
-        if (key >= prefix) {
-          const int d = key - prefix;
-          seen = 0;
-          const uint32_t* word = p.mask + static_cast<size_t>(s.b) * p.q_len * words + (d >> 5);
-          for (int i = 0; i < p.q_len; ++i) seen |= static_cast<uint64_t>(word[i * words] >> (d & 31) & 1u) << i;
+      if (valid) old = *at;
+      const bool edge = __any_sync(0xFFFFFFFFu, valid && key >= prefix);
+      if (edge) {
+        // A lane loads the masks of two drafts (one read after the other took 0.4 us each).
+        const uint32_t* const rows = p.mask + static_cast<size_t>(s.b) * p.q_len * words;
+        uint32_t word[2][2] = {};                          // [draft lane or 32 + lane][keys 0 .. 31 or 32 ..]
+        if (lane < p.q_len) {
+          word[0][0] = rows[lane * words];
+          if (words > 1) word[0][1] = rows[lane * words + 1];
         }
+        if (words > 1 && 32 + lane < p.q_len) {
+          word[1][0] = rows[(32 + lane) * words];
+          word[1][1] = rows[(32 + lane) * words + 1];
+        }
+        const int draft = key - prefix;                    // (may be any number)
+        uint64_t mine = 0;
+        for (int i = 0; i < p.q_len; ++i) {
+          const uint32_t lo = __shfl_sync(0xFFFFFFFFu, i < 32 ? word[0][0] : word[1][0], i & 31);
+          const uint32_t hi = __shfl_sync(0xFFFFFFFFu, i < 32 ? word[0][1] : word[1][1], i & 31);
+          mine |= static_cast<uint64_t>((draft & 32 ? hi : lo) >> (draft & 31) & 1u) << i;
+        }
+        if (valid && key >= prefix) seen = mine;
       }
-      const bool edge = __any_sync(0xFFFFFFFFu, seen != ~0ull);
       for (int c = 0; c < p.chunks; ++c) {
         const int buf = loads & 1;
         const bool first_use = p.chunks > 1 || j == 0, last_use = p.chunks > 1 || j + 2 >= s.n;
@@ -391,52 +429,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   if (tid == 0) grid_launch_dependents();
 
-  // This CTA's run: each thread sums a run of streams, then a scan over threads;
-  // the thread whose streams hold the first tile says which.
+  // This CTA's run (as in the attention kernel).
   const int all = p.by_members.of(gridDim.x), team = p.by_members.of(blockIdx.x);
   const int member = static_cast<int>(blockIdx.x) - team * p.members;
-  const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int sum = 0, len;
-  bool off = false;
-  for (int b = b0; b < b1; ++b) {
-    sum += stream_tiles<kWhole>(p, b, len) * p.head_sets;
-    off |= len != 0 && (len < p.q_len || len > p.Smax);
-  }
-  if (off && blockIdx.x == 0) atomicOr(p.status, kBitSeqLen);
-  int inc = sum;
+  int len, total, start_b = 0, start_pre = 0;
+  if (p.B <= 32) {
+    // Every warp by itself, a stream a lane.
+    int work = 0;
+    if (lane < p.B) {
+      work = stream_tiles<kWhole>(p, lane, len) * p.head_sets;
+      if (blockIdx.x == 0 && warp == 0 && len != 0 && (len < p.q_len || len > p.Smax)) atomicOr(p.status, kBitSeqLen);
+    }
+    int inc = work;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
-  }
-  if (lane == 31) sm.warp_sum[warp] = inc;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int before = 0, total = 0;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    const Runs runs(p, total, all);
+    if (team < runs.teams && total > 0) {
+      start_b = __ffs(__ballot_sync(0xFFFFFFFFu, inc > runs.start(team))) - 1;
+      start_pre = __shfl_sync(0xFFFFFFFFu, inc - work, start_b);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    // Each thread sums a run of streams, then a scan over threads; the thread whose
+    // streams hold the first tile says which.
+    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int sum = 0;
+    bool off = false;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
+      sum += stream_tiles<kWhole>(p, b, len) * p.head_sets;
+      off |= len != 0 && (len < p.q_len || len > p.Smax);
+    }
+    if (off && blockIdx.x == 0) atomicOr(p.status, kBitSeqLen);
+    int inc = sum;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i == warp) before = total;
-    total += sm.warp_sum[i];
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 31) sm.warp_sum[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i == warp) before = total;
+      total += sm.warp_sum[i];
+    }
+    const Runs runs(p, total, all);
+    const int t0 = team < runs.teams ? runs.start(team) : total;
+    before += inc - sum;
+    if (t0 >= before && t0 < before + sum) {
+      int b = b0;
+      while (true) {
+        const int n = stream_tiles<kWhole>(p, b, len) * p.head_sets;
+        if (t0 < before + n) break;
+        before += n;
+        ++b;
+      }
+      sm.start_b = b;
+      sm.start_pre = before;
+    }
+    __syncthreads();
+    if (t0 < total) {
+      start_b = sm.start_b;
+      start_pre = sm.start_pre;
+    }
   }
+  const uint32_t tmem = sm.tmem_base;
   const Runs runs(p, total, all);
   const int t0 = team < runs.teams ? runs.start(team) : total;
-  before += inc - sum;
-  if (t0 >= before && t0 < before + sum) {
-    int b = b0;
-    while (true) {
-      const int n = stream_tiles<kWhole>(p, b, len) * p.head_sets;
-      if (t0 < before + n) break;
-      before += n;
-      ++b;
-    }
-    sm.start_b = b;
-    sm.start_pre = before;
-  }
-  __syncthreads();
-  const uint32_t tmem = sm.tmem_base;
-  const bool any = t0 < total;
-  const Walk<kWhole> walk(p, member, t0, any ? runs.start(team + 1) : total, any ? sm.start_b : 0, any ? sm.start_pre : 0);
+  const Walk<kWhole> walk(p, member, t0, team < runs.teams ? runs.start(team + 1) : total, start_b, start_pre);
 
   if (warp == 0) {
     if (p.box_rows == 0) load_k_gather<D>(sm, p, walk);

@@ -82,6 +82,7 @@ struct __align__(128) Head {
   uint64_t full[kMostStages], empty[kMostStages], meet[kWarps];
   float2 ml[kWarps][8 * kN];
   Place place[kWarps];
+  uint64_t mask[kWarps][8 * kN + 1];       // what each row's draft sees of the drafts; all of them
   int warp_sum[kWarps + kLoaders], start_b, start_pre;
   uint32_t abort_flag;
 };
@@ -255,16 +256,17 @@ __device__ __forceinline__ bool meet(Head<kN>& sm, const FewParams& p, int head,
   return wait(sm, sm.meet[head], times++ & 1u, p);
 }
 
-// Whether draft i of stream b sees draft d; whether some draft sees a key of the run.
-__device__ __forceinline__ bool sees(const Params& p, int b, int i, int d) {
+// The drafts that draft i of stream b sees.
+__device__ __forceinline__ uint64_t mask_of(const Params& p, int b, int i) {
   const int words = (p.q_len + 31) >> 5;
-  return p.mask[(static_cast<size_t>(b) * p.q_len + i) * words + (d >> 5)] >> (d & 31) & 1u;
+  const uint32_t* const row = p.mask + (static_cast<size_t>(b) * p.q_len + i) * words;
+  uint64_t m = row[0];
+  if (words > 1) m |= static_cast<uint64_t>(row[1]) << 32;
+  return m;
 }
-__device__ __forceinline__ bool used(const Params& p, int b, int key, int prefix, int end) {
-  if (key >= end || key < prefix) return key < end;
-  bool any = false;
-  for (int i = 0; i < p.q_len; ++i) any |= sees(p, b, i, key - prefix);
-  return any;
+// Whether a key of the run is one that drafts with this mask see.
+__device__ __forceinline__ bool among(uint64_t mask, int key, int prefix, int end) {
+  return key < end && (key < prefix || (mask >> (key - prefix) & 1ull));
 }
 
 template <int D, bool kBf16, int kN>
@@ -301,6 +303,13 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
       }
     }
     const int begin = s.tile0 * kKeys, end = min(s.S, (s.tile0 + s.n) * kKeys), prefix = s.S - p.q_len;
+    if (end > prefix) {
+      const uint64_t used =
+          seen_drafts(p, s.b, p.q_len <= 32 && lane < p.q_len ? p.mask[static_cast<size_t>(s.b) * p.q_len + lane] : 0u, lane);
+      if (lane == 0) sm.mask[warp][8 * kN] = used;
+      if (lane < 8 * kN) sm.mask[warp][lane] = mask_of(p, s.b, p.by_G.of(min(lane, rows - 1)));   // (rows past the last: its)
+      __syncwarp();
+    }
     // ---- rows of Q: row 8 t + g, this lane's quarter; in fp16, brought to its range
     // by a power of two where they are bf16.
     constexpr bool kSharedQ = Shape8<kN>::kSharedQ;
@@ -421,15 +430,16 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
       uint32_t hidden = 0;
       if constexpr (kEdge) {
 #pragma unroll
-        for (int i = 0; i < kS; ++i)
+        for (int t = 0; t < kN; ++t)
 #pragma unroll
-          for (int t = 0; t < kN; ++t)
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t mask = sm.mask[warp][8 * t + 2 * c + e];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = k0 + 16 * i + key_g + (e >> 1) * 8, row = 8 * t + 2 * c + (e & 1);
-              if (key >= end || (key >= prefix && !(row < rows && sees(p, s.b, p.by_G.of(row), key - prefix))))
-                hidden |= 1u << ((i * kN + t) * 4 + e);
-            }
+            for (int i = 0; i < kS; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!among(mask, k0 + 16 * i + key_g + 8 * h, prefix, end)) hidden |= 1u << ((i * kN + t) * 4 + 2 * h + e);
+          }
       }
       float y[kS][kN][4];
       auto shifted = [&]() {
@@ -492,8 +502,8 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
         for (int h = 0; h < 2; ++h) {
           if constexpr (kEdge) {
             // Rows past the run, and drafts that none sees, may hold anything.
-            if (!used(p, s.b, k0 + 16 * i + 8 * h + key_c, prefix, end)) sv[i][h][0] = 0;
-            if (!used(p, s.b, k0 + 16 * i + 8 * h + key_c1, prefix, end)) sv[i][h][1] = 0;
+            if (!among(sm.mask[warp][8 * kN], k0 + 16 * i + 8 * h + key_c, prefix, end)) sv[i][h][0] = 0;
+            if (!among(sm.mask[warp][8 * kN], k0 + 16 * i + 8 * h + key_c1, prefix, end)) sv[i][h][1] = 0;
           }
           scale[h] = fp4::from_e4m3x2(sv[i][h][0] | sv[i][h][1] << 8);
         }

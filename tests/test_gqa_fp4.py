@@ -77,6 +77,8 @@ def verify(c, got):
     (4, 16, 2, [500, 66, 4]),                  # 32 rows
     (4, 64, 8, [1500, 300]),
     (11, 9, 3, [700]),                         # 33 rows
+    (32, 2, 2, [700, 32, 33, 60]),             # 32 drafts of a head: one mask word, all of it
+    (32, 8, 8, [100]),
     (9, 64, 8, [265]),
     (2, 21, 3, [600, 63]),                     # an odd number of heads: rows with padding
     (5, 5, 5, [64, 0, 190]),
