@@ -472,7 +472,7 @@ int mla_gqa_verify_attn_window_paged(const void* q, const void* k_pool, const vo
  *   Hkv * D / 2 bytes of codes (E2M1; heads in order, dimension 2 i in the low
  *     half of a head's byte i),
  *   Hkv * D / 16 bytes of steps (E4M3), one for every 16 values of a head,
- *   padding up to a multiple of 16 bytes, never read or written,
+ *   padding up to a multiple of 16 bytes, without a meaning and never written,
  * mla_gqa_fp4_row_bytes in all (0 for sizes that are not supported: D is 64 or
  * 128, Hkv <= MLA_FP4_MAX_HEADS), and stands for the values
  *   E2M1(code) * E4M3(step) * factor
@@ -564,7 +564,7 @@ int mla_gqa_attn_weights_paged(const void* q, const void* k_pool, const int64_t*
  *   workspace  mla_evict_workspace_size(B, Smax) bytes, 4-byte aligned (NULL where that
  *              is 0, as up to 393,216 keys); contents do not matter.
  *   0 <= B < 2^20, 1 <= Smax < 2^24, 1 <= Hkv <= 65536, sinks, recent >= 0 and
- *   sinks + recent <= budget (MLA_ERR_SHAPE).
+ *   sinks + recent <= budget <= 2^30 (MLA_ERR_SHAPE).
  * A seq_lens[b] outside [0, Smax] records MLA_ERR_SEQLEN and keeps nothing.
  */
 size_t mla_evict_workspace_size(int B, int Smax);
@@ -577,7 +577,8 @@ int mla_evict_select(const float* weights, const int32_t* seq_lens, int B, int H
  * The rows that stay move together, in place: row j of stream b takes the value
  * that row kept[b][j] had before the call, for every j < keep_lens[b]; what is left
  * behind them keeps no particular value.  seq_lens stays as it is: mla_blocks_trim to keep_lens follows.
- *   pool_a, pool_b, block_table, max_blocks, page_size  as for mla_cache_keep.
+ *   pool_a, pool_b, block_table, max_blocks, page_size  as for mla_cache_keep;
+ *              max_blocks * page_size <= 2^30 and budget <= 2^30 (MLA_ERR_SHAPE).
  *   weights    NULL, or [B, Hkv, max_blocks * page_size] fp32 that move along; entries
  *              from keep_lens[b] up to seq_lens[b] become 0.
  *   kept       [B, budget] int32, increasing in each stream, as mla_evict_select leaves it.

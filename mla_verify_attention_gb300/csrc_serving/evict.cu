@@ -35,6 +35,8 @@ constexpr int kPasses = 4;
 constexpr int kMostBlocks = 8;
 constexpr int kMaxDevices = 64;
 constexpr int kMostKeys = 49152;           // a block holds in shared memory
+// Rows and budgets at most: positions are counted on past them in 32 bits.
+constexpr long long kMostBudget = 1ll << 30;
 
 struct SelectParams {
   const float* weights;                    // [B][Hkv][Smax]
@@ -414,7 +416,7 @@ int mla_evict_select(const float* weights, const int32_t* seq_lens, int B, int H
                      cudaStream_t stream) {
   using namespace mla;
   using namespace mla::evict;
-  if (!select_shape_ok(B, Smax) || Hkv < 1 || Hkv > (1 << 16) || budget < 1 || sinks < 0 || recent < 0 ||
+  if (!select_shape_ok(B, Smax) || Hkv < 1 || Hkv > (1 << 16) || budget < 1 || budget > kMostBudget || sinks < 0 || recent < 0 ||
       static_cast<long long>(sinks) + recent > budget)
     return MLA_ERR_SHAPE;
   if (B == 0) return MLA_OK;
@@ -443,8 +445,8 @@ int mla_cache_compact(void* pool_a, long long pool_a_stride, int a_bytes, void* 
                       const int32_t* keep_lens, int B, cudaStream_t stream) {
   using namespace mla;
   using namespace mla::evict;
-  if (B < 0 || B >= (1 << 20) || budget < 1 || max_blocks < 1 || page_size < 1 ||
-      static_cast<long long>(max_blocks) * page_size >= (1ll << 31) || a_bytes < 16 || b_bytes < 0 || pool_rows < page_size ||
+  if (B < 0 || B >= (1 << 20) || budget < 1 || budget > kMostBudget || max_blocks < 1 || page_size < 1 ||
+      static_cast<long long>(max_blocks) * page_size > kMostBudget || a_bytes < 16 || b_bytes < 0 || pool_rows < page_size ||
       pool_rows >= (1ll << 31) || (weights && (Hkv < 1 || Hkv > (1 << 16))))
     return MLA_ERR_SHAPE;
   const long long limit = 1ll << 32;

@@ -2,7 +2,7 @@
 //   Hkv * D / 2 bytes of codes (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
 //     negatives), heads in order, dimension 2 i in the low half of byte i;
 //   Hkv * D / 16 bytes of steps (E4M3), one for every 16 values of a head;
-//   padding up to a multiple of 16 bytes, neither read nor written;
+//   padding up to a multiple of 16 bytes, without a meaning and never written;
 // value = (E2M1 of the code) * step * the pool's own factor.  A step and a code
 // have 4 and 2 significant bits, so their product is exact in fp16 (2^-10 .. 2,688).
 #pragma once

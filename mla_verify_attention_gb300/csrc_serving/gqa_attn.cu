@@ -214,8 +214,8 @@ int run(const Call& c) {
   st = device_common(&d);
   if (st != MLA_OK) return st;
   const int grid = cta_count(d);
-  const bool few = c.mode == kFp4 && few_rows(c.q_len, c.H, c.Hkv);
-  const Layout lay = layout(pl, few ? grid * few_heads(c.q_len, c.H, c.Hkv) : grid, c.D);
+  const bool few = c.mode == kFp4 && few_rows(c.B, c.q_len, c.H, c.Hkv, c.Smax);
+  const Layout lay = layout(pl, few ? grid * few_heads(c.Hkv) : grid, c.D);
   if (!c.workspace || c.workspace_bytes < lay.bytes) return MLA_ERR_WORKSPACE;
   Variant var = {};
   if (!few) st = pick(c.D, c.dtype, c.mode, &var);
@@ -407,8 +407,9 @@ size_t mla_gqa_fp4_workspace_size(int B, int q_len, int H, int Hkv, int D) {
   if (!gqa::shape_ok(B, q_len, H, Hkv, D) || Hkv > MLA_FP4_MAX_HEADS) return 0;
   DeviceCommon d;
   if (device_common(&d) != MLA_OK) return 0;
-  const int parts = gqa::cta_count(d) * (gqa::few_rows(q_len, H, Hkv) ? gqa::few_heads(q_len, H, Hkv) : 1);
-  return gqa::layout(gqa::plan(q_len, H, Hkv), parts, D).bytes;
+  // (Whichever kernel takes the call: that is for the table's size to say.)
+  const bool few = gqa::few_rows(1, q_len, H, Hkv, 1 << 24);
+  return gqa::layout(gqa::plan(q_len, H, Hkv), gqa::cta_count(d) * (few ? gqa::few_heads(Hkv) : 1), D).bytes;
 }
 
 int mla_gqa_verify_attn_fp4_paged(const void* q, const int64_t* q_strides, const void* k_pool, long long k_pool_stride,

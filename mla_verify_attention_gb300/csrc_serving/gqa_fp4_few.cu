@@ -813,7 +813,8 @@ Variant variant() {
 
 constexpr int kMostEights = 4;
 constexpr int kSharedBytes = 232448;
-constexpr int kStageBytes = 80 << 10;      // a stage, about
+constexpr int kStageBytes = 80 << 10;      // a stage, at most (40 KB: 150 us where 80 take 138)
+constexpr int kStageKeys = 256;            // 32 boxes of eight rows, which is what a loader's lanes see to
 
 std::mutex g_mutex;
 bool g_ready[64][4][kMostEights];
@@ -838,12 +839,20 @@ int most_step_bytes(int Hkv, int heads, int each) {
 
 }  // namespace few
 
-// Rows a key head up to which this kernel takes a call.
-constexpr long long kFewRows = 8 * few::kMostEights;
-bool few_rows(int q_len, int H, int Hkv) { return q_len * (H / Hkv) <= kFewRows; }
-int few_heads(int q_len, int H, int Hkv) {
-  return few::heads_a_cta(Hkv, few::kWarps);
+// Whether this kernel takes a call, by its rows a key head and the keys that its tables
+// have room for.  GPU time here / with the tcgen05 kernel, us, D = 128, 8 heads a key head
+// unless said:
+//   64 streams of 1k to 32k keys, 16-row pages, 8 key heads: one token 134 / 425, 2 tokens
+//     175 / 423, 3 232 / 430, 4 292 / 430; 2 key heads: 59 / 116, 4 tokens 155 / 113 (the
+//     warps of a head have much to put together); of 200 to 400 keys 18 / 44, 4 tokens 37 / 46;
+//   one stream of 64k keys: 2 tokens 37 / 47, 4 51 / 47; of 2,048 keys: one token 13.7 / 13.6,
+//     2 tokens 17 / 13.7; of 256 keys 13.7 / 9.6 (one CTA has all heads of a key).
+bool few_rows(int B, int q_len, int H, int Hkv, int Smax) {
+  const long long rows = static_cast<long long>(q_len) * (H / Hkv), keys = static_cast<long long>(B) * Smax;
+  if (rows <= 8) return keys >= 2048;
+  return rows <= 8 * few::kMostEights && few_heads(Hkv) == few::kWarps && keys >= 16384;
 }
+int few_heads(int Hkv) { return few::heads_a_cta(Hkv, few::kWarps); }
 
 int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid) {
   using namespace few;
@@ -890,7 +899,7 @@ int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid
   const int key_bytes = 2 * (p.code_bytes + p.step_bytes);
   p.stage_keys = 16 * v.together * p.head_warps;
   const int fixed = v.head_bytes + (p.head_warps > 1 ? v.sum_bytes : 0), least = 16 * v.together * p.head_warps;
-  while (2 * p.stage_keys <= kKeys && 2 * p.stage_keys * key_bytes <= kStageBytes) p.stage_keys *= 2;
+  while (2 * p.stage_keys <= kStageKeys && 2 * p.stage_keys * key_bytes <= kStageBytes) p.stage_keys *= 2;
   while (p.stage_keys > least && 2 * p.stage_keys * key_bytes > kSharedBytes - fixed) p.stage_keys /= 2;
   p.stage_bytes = p.stage_keys * key_bytes;
   const int stage = p.stage_bytes;

@@ -49,8 +49,8 @@ Fp4Fn fp4_kernel(int D, bool bf16, size_t* smem, int* threads);    // gqa_fp4.cu
 
 // The kernel for few query rows a key head over a cache in 4 bits: whether it takes a
 // call, key heads a CTA, and its launches (gqa_fp4_few.cu).
-bool few_rows(int q_len, int H, int Hkv);
-int few_heads(int q_len, int H, int Hkv);
+bool few_rows(int B, int q_len, int H, int Hkv, int Smax);
+int few_heads(int Hkv);
 int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid);
 
 // Parts a unit from which four part groups share the merge of a row.

@@ -18,11 +18,14 @@ from test_gqa_attn import trees
 BF16, FP16 = torch.bfloat16, torch.float16
 
 
-def case(q, H, Hkv, D, lens, page, dt=BF16, tree="random", seed=0, spread=0.0, k_scale=0.125, v_scale=0.5, scale=None):
-    """Pools of random codes and steps, so that every value is exact; rows that no stream has hold NaN."""
+def case(q, H, Hkv, D, lens, page, dt=BF16, tree="random", seed=0, spread=0.0, k_scale=0.125, v_scale=0.5, scale=None, room=0):
+    """Pools of random codes and steps, so that every value is exact; rows that no stream has hold NaN.
+    room: keys that the table has room for, at least (by which the kernel for few rows is chosen)."""
     gen = torch.Generator().manual_seed(seed + 19 * q + D + page)
     B = len(lens)
     table, total = plain.pages(gen, lens, page)
+    if table.shape[1] * page < room:
+        table = torch.cat([table, torch.full((B, -(-room // page) - table.shape[1]), -1, dtype=torch.int32)], 1)
     n = mva.gqa_fp4_row_bytes(Hkv, D)
     codes = Hkv * D // 2
     pools = []
@@ -64,6 +67,7 @@ def verify(c, got):
         plain.check(got[0][b], got[1][b], plain.attend(c["q"][b], k, v, see, c["scale"], weight_u=2.0 ** -11), "stream %d" % b)
 
 
+@pytest.mark.parametrize("room", [0, 20000])
 @pytest.mark.parametrize("dt", [BF16, FP16])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("q,H,Hkv,lens", [
@@ -86,62 +90,63 @@ def verify(c, got):
     (33, 16, 4, [2000]),
     (64, 14, 2, [100, 1000]),                  # 448 rows
 ])
-def test_matches_plain(q, H, Hkv, lens, D, dt):
-    c = case(q, H, Hkv, D, lens, 64, dt)
+def test_matches_plain(q, H, Hkv, lens, D, dt, room):
+    c = case(q, H, Hkv, D, lens, 64, dt, room=room)
     verify(c, run(c))
 
 
 @pytest.mark.parametrize("page", [1, 5, 8, 16, 24, 64, 100, 128, 4096])
-@pytest.mark.parametrize("q,H", [(1, 16), (5, 16)])
-def test_pages(q, H, page):
+@pytest.mark.parametrize("q,H,Hkv", [(1, 16, 2), (5, 16, 2), (5, 24, 8)])
+def test_pages(q, H, Hkv, page):
     for D, dt in ((64, FP16), (128, BF16)):
-        c = case(q, H, 2, D, [1500, 5, 700, 64, 0, 4000], page, dt)
+        c = case(q, H, Hkv, D, [1500, 5, 700, 64, 0, 4000], page, dt, room=4000)
         verify(c, run(c))
 
 
 @pytest.mark.parametrize("q,H,Hkv", [(1, 8, 1), (1, 8, 8), (1, 6, 3), (1, 16, 16), (1, 40, 40), (1, 12, 12), (4, 4, 2), (1, 72, 24), (9, 36, 36)])
 def test_head_layouts(q, H, Hkv):
     for D in (64, 128):
-        c = case(q, H, Hkv, D, [3, 200, 1111], 16) if q <= 3 else case(q, H, Hkv, D, [q, 200, 1111], 16)
+        c = case(q, H, Hkv, D, [max(q, 3), 200, 1111], 16, room=6000)
         verify(c, run(c))
 
 
 @pytest.mark.parametrize("tree", ["chain", "any"])
 @pytest.mark.parametrize("q,G,lens", [(1, 8, [1, 64, 65]), (2, 4, [2, 66]), (9, 8, [9, 70]), (40, 2, [41, 130]), (64, 4, [64, 129])])
 def test_masks(q, G, lens, tree):
-    c = case(q, 2 * G, 2, 64, lens, 16, tree=tree)
-    verify(c, run(c))
+    for Hkv, room in ((2, 0), (2, 1100), (8, 9000)):
+        c = case(q, Hkv * G, Hkv, 64, lens, 16, tree=tree, room=room)
+        verify(c, run(c))
 
 
 def test_lengths_around_tile_edges():
-    for q, H in ((1, 4), (4, 16)):
-        c = case(q, H, 1, 128, [n for k in (16, 32, 64, 128, 192, 256, 512, 1024) for n in (k - 1, k, k + 1)], 64)
+    for q, H, Hkv in ((1, 4, 1), (4, 16, 1), (4, 16, 8)):
+        c = case(q, H, Hkv, 128, [n for k in (16, 32, 64, 128, 192, 256, 512, 1024) for n in (k - 1, k, k + 1)], 64)
         verify(c, run(c))
-        c = case(q, H, 1, 64, list(range(q, 100)), 16)
+        c = case(q, H, Hkv, 64, list(range(q, 100)), 16)
         verify(c, run(c))
 
 
 @pytest.mark.parametrize("q", [1, 9])
 def test_steps_and_queries_of_every_size(q):
     for D, dt in ((64, BF16), (128, FP16), (128, BF16)):
-        c = case(q, 8, 2, D, [900, 77], 16, dt, spread=1.5)
+        c = case(q, 8, 2, D, [900, 77], 16, dt, spread=1.5, room=1024)
         verify(c, run(c))
     for size in (1e-30, 1e-6, 1e4, 1e30):                  # bf16 has fp32's range
-        c = case(q, 8, 2, 64, [900, 77], 16, BF16)
+        c = case(q, 8, 2, 64, [900, 77], 16, BF16, room=1024)
         c["q"] = (c["q"].float() * size).to(BF16)
         c["scale"] /= size
         verify(c, run(c))
     for scale in (0.0, -0.7, 3.0):
-        c = case(q, 8, 2, 128, [900, 77], 16, scale=scale)
+        c = case(q, 8, 2, 128, [900, 77], 16, scale=scale, room=1024)
         verify(c, run(c))
-    c = case(q, 8, 2, 128, [900, 77], 16, k_scale=2.0 ** -40, v_scale=2.0 ** 30)
+    c = case(q, 8, 2, 128, [900, 77], 16, k_scale=2.0 ** -40, v_scale=2.0 ** 30, room=1024)
     verify(c, run(c))
 
 
 @pytest.mark.parametrize("q", [1, 2, 9])
 def test_drafts_that_none_sees_hold_anything(q):
     # Padding drafts' rows: codes with steps of NaN.
-    c = case(q, 16, 2, 128, [300, 64 + q], 16)
+    c = case(q, 16, 8 if q == 2 else 2, 128, [300, 64 + q], 16, room=9000)
     c["seen"][0, :, q - 1] = False
     c["mask"] = gqa_plain.mask_words(c["seen"]).cuda()
     for p, x in zip(c["pools"], c["cpu"]):
@@ -162,17 +167,17 @@ def test_nan_of_a_row_stays_in_it():
             assert torch.equal(torch.isnan(out[0]).all(-1), bad) and torch.equal(torch.isnan(out[0]).any(-1), bad)
 
 
-@pytest.mark.parametrize("q,H", [(1, 8), (3, 16), (5, 16)])
-def test_many_streams_and_long_ones(q, H):
+@pytest.mark.parametrize("q,H,Hkv", [(1, 8, 2), (3, 16, 2), (5, 16, 2), (3, 24, 8), (4, 32, 8)])
+def test_many_streams_and_long_ones(q, H, Hkv):
     gen = torch.Generator().manual_seed(3)
     lens = [int(x) for x in torch.randint(q, 900, (300,), generator=gen)] + [0]
-    c = case(q, H, 2, 64, lens, 16)
+    c = case(q, H, Hkv, 64, lens, 16)
     a = run(c)
     verify(c, a)
     for _ in range(10):
         b = run(c)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
-    c = case(q, H, 2, 128, [40000, q, 20000], 64)
+    c = case(q, H, Hkv, 128, [40000, q, 20000], 64)
     verify(c, run(c))
 
 
@@ -260,18 +265,18 @@ def test_a_loop_of_steps_and_its_graph(q, H):
     assert mva.last_device_error() == 0
 
 
-@pytest.mark.parametrize("q", [1, 9])
-def test_a_wait_that_runs_out_is_reported(q):
-    c = case(q, 64, 2, 128, [3000], 16)
+@pytest.mark.parametrize("q,page", [(1, 16), (1, 5), (9, 16), (9, 5)])
+def test_a_wait_that_runs_out_is_reported(q, page):
+    c = case(q, 16, 2, 128, [3000], page)
     with mva.forced(stall=True):
-        mva.gqa_verify_attn_fp4_paged(c["q"], *c["pools"], 2, c["table_t"], 16, c["lens_t"], c["mask"], 0.1)
+        mva.gqa_verify_attn_fp4_paged(c["q"], *c["pools"], 2, c["table_t"], page, c["lens_t"], c["mask"], 0.1)
         assert mva.last_device_error() == -7
     verify(c, run(c))
 
 
-@pytest.mark.parametrize("q,H", [(1, 8), (9, 8)])
-def test_pages_and_lengths_out_of_range_are_reported(q, H):
-    c = case(q, H, 2, 64, [500, 40], 16)
+@pytest.mark.parametrize("q,H,room", [(1, 8, 0), (1, 8, 4096), (9, 8, 0)])
+def test_pages_and_lengths_out_of_range_are_reported(q, H, room):
+    c = case(q, H, 2, 64, [500, 40], 16, room=room)
     call = lambda table, lens: mva.gqa_verify_attn_fp4_paged(c["q"], *c["pools"], 2, table, 16, lens, c["mask"], 0.1)
     for at in (0, 31):
         for bad in (-1, 1 << 20):
@@ -279,7 +284,7 @@ def test_pages_and_lengths_out_of_range_are_reported(q, H):
             t[0, at] = bad
             call(t, c["lens_t"])
             assert mva.last_device_error() == -10
-    out, lse = call(c["table_t"], torch.tensor([513, 40], dtype=torch.int32).cuda())
+    out, lse = call(c["table_t"], torch.tensor([max(513, room + 1), 40], dtype=torch.int32).cuda())
     assert mva.last_device_error() == -8
     assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
 

@@ -111,7 +111,8 @@ def test_weights_paged_arguments(lib, kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), SHAPE), (dict(B=1 << 20), SHAPE), (dict(Smax=0), SHAPE), (dict(Smax=1 << 24), SHAPE), (dict(Hkv=0), SHAPE),
     (dict(Hkv=65537), SHAPE), (dict(budget=0), SHAPE), (dict(sinks=-1), SHAPE), (dict(recent=-1), SHAPE),
-    (dict(sinks=41), SHAPE), (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), SHAPE), (dict(w=0), NULL), (dict(lens=0), NULL),
+    (dict(sinks=41), SHAPE), (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), SHAPE),
+    (dict(budget=(1 << 30) + 1), SHAPE), (dict(w=0), NULL), (dict(lens=0), NULL),
     (dict(kept=0), NULL), (dict(keep=0), NULL), (dict(w=2), ALIGN), (dict(kept=6), ALIGN), (dict(B=0, w=0), OK)])
 def test_select_arguments(lib, kw, want):
     assert call(lib.mla_evict_select, SELECT, **kw) == want
@@ -124,7 +125,7 @@ def test_select_workspace():
 
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), SHAPE), (dict(budget=0), SHAPE), (dict(max_blocks=0), SHAPE), (dict(page=0), SHAPE), (dict(max_blocks=1 << 28), SHAPE),
-    (dict(na=0), SHAPE), (dict(nb=-16), SHAPE), (dict(rows=10), SHAPE), (dict(pas=512), SHAPE), (dict(pbs=512), SHAPE),
+    (dict(max_blocks=(1 << 24) + 1, rows=1 << 30), SHAPE), (dict(budget=(1 << 30) + 1), SHAPE), (dict(na=0), SHAPE), (dict(nb=-16), SHAPE), (dict(rows=10), SHAPE), (dict(pas=512), SHAPE), (dict(pbs=512), SHAPE),
     (dict(Hkv=0), SHAPE), (dict(pa=0), NULL), (dict(pb=0), NULL), (dict(table=0), NULL), (dict(lens=0), NULL), (dict(kept=0), NULL),
     (dict(keep=0), NULL), (dict(pa=8), ALIGN), (dict(na=1000), ALIGN), (dict(pbs=1032), ALIGN), (dict(w=2), ALIGN),
     (dict(kept=2), ALIGN), (dict(B=0, pa=0), OK)])
