@@ -476,39 +476,52 @@ def gqa_cache_append_fp4(k_pool, v_pool, k, v, slots, k_scale=1.0, v_scale=1.0, 
     """
     if _call is None:
         _bind()
-    if k.dim() != 3 or v.shape != k.shape:
+    shape, pool = k.shape, k_pool.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("expected k and v [T,Hkv,D]")
-    T, heads, width = k.shape
+    T, heads, width = shape
     dt = k.dtype
     if dt is not _bf16 and dt is not _fp16:
         raise ValueError("k and v must be bfloat16 or float16")
-    rows, n_bytes, kp_stride, vp_stride = _byte_pools(k_pool, v_pool)
-    if n_bytes != gqa_fp4_row_bytes(heads, width):
-        raise ValueError("k_pool and v_pool must be uint8 [rows,%d]" % gqa_fp4_row_bytes(heads, width))
-    a_stride, b_stride = _head_rows("k", k, dt, heads, width), _head_rows("v", v, dt, heads, width)
-    _ints("slots", slots, T)
-    kh = vh = kh_stride = vh_stride = 0
+    n = _row_bytes.get((heads, width)) or gqa_fp4_row_bytes(heads, width)
+    ks, vs, kps, vps = k.stride(), v.stride(), k_pool.stride(), v_pool.stride()
+    i32 = _int32
+    # (Everything at once, and one by one where something is wrong.)
+    if not (T > 1 and heads > 1 and ks[2] == 1 == vs[2] and ks[1] == width == vs[1] and v.dtype is dt and len(pool) == 2
+            and pool == v_pool.shape and pool[1] == n and pool[0] > 1 and kps[1] == 1 == vps[1] and k_pool.dtype is _uint8
+            and v_pool.dtype is _uint8 and slots.dtype is i32 and slots.shape == (T,) and slots.is_contiguous()):
+        rows, n_bytes, k_pool_stride, v_pool_stride = _byte_pools(k_pool, v_pool)
+        if n_bytes != n or n == 0:
+            raise ValueError("k_pool and v_pool must be uint8 [rows,%d]" % n)
+        k_stride, v_stride = _head_rows("k", k, dt, heads, width), _head_rows("v", v, dt, heads, width)
+        _ints("slots", slots, T)
+    else:
+        rows, k_pool_stride, v_pool_stride, k_stride, v_stride = pool[0], kps[0], vps[0], 2 * ks[0], 2 * vs[0]
     dev = k_pool.get_device()
-    for name, t in (("k_held", k_held), ("v_held", v_held)):
-        if t is None:
-            continue
-        if t.shape != k.shape:
-            raise ValueError("%s must have k's shape" % name)
-        st = _head_rows(name, t, dt, heads, width)
-        if t.get_device() != dev:
-            _wrong_device(k_pool, t)
-        if t is k_held:
-            kh, kh_stride = t.data_ptr(), st
-        if t is v_held:
-            vh, vh_stride = t.data_ptr(), st
     if not (_on_current(dev) and dev == v_pool.get_device() == k.get_device() == v.get_device() == slots.get_device()):
         _wrong_device(k_pool, v_pool, k, v, slots)
+    kh = vh = kh_stride = vh_stride = 0
+    if k_held is not None:
+        kh, kh_stride = _held("k_held", k_held, k, dev)
+    if v_held is not None:
+        vh, vh_stride = _held("v_held", v_held, k, dev)
     st = _call(_APPEND_FP4, _pack_append_fp4(
-        k.data_ptr(), a_stride, v.data_ptr(), b_stride, heads, width, 0 if dt is _bf16 else 1, k_scale, v_scale,
-        k_pool.data_ptr(), kp_stride, v_pool.data_ptr(), vp_stride, rows, slots.data_ptr(), T, kh, kh_stride, vh,
+        k.data_ptr(), k_stride, v.data_ptr(), v_stride, heads, width, 0 if dt is _bf16 else 1, k_scale, v_scale,
+        k_pool.data_ptr(), k_pool_stride, v_pool.data_ptr(), v_pool_stride, rows, slots.data_ptr(), T, kh, kh_stride, vh,
         vh_stride, _handle(stream, dev)))
     if st != MLA_OK:
         raise MLAError(st, "mla_gqa_cache_append_fp4")
+
+
+def _held(name, t, like, dev):
+    """Address and byte stride of rows of `like`'s shape and type that take held values."""
+    if t.shape != like.shape:
+        raise ValueError("%s must have k's shape" % name)
+    if t.get_device() != dev:
+        _wrong_device(like, t)
+    if t.dtype is like.dtype and t.is_contiguous():
+        return t.data_ptr(), 2 * t.shape[1] * t.shape[2]
+    return t.data_ptr(), _head_rows(name, t, like.dtype, t.shape[1], t.shape[2])
 
 
 def gqa_fp4_workspace_size(B: int, q_len: int, H: int, Hkv: int, D: int) -> int:
