@@ -5,7 +5,10 @@ The computation runs in hand-written CUDA kernels behind the C ABI declared in
 binds it with ctypes.  Next to the verify call on a latent cache there are the
 same for separate keys and values with grouped query heads (``gqa_verify_attn``)
 and the cache operators around a verify step: ``blocks_extend``, ``cache_append``,
-``cache_keep`` and ``blocks_trim``.  ``inputs`` makes seeded synthetic workloads.
+``cache_keep`` and ``blocks_trim``.  Long caches are kept small by a sliding window
+(``gqa_verify_attn_window``), rows held in 4 bits (``gqa_cache_append_fp4``,
+``gqa_verify_attn_fp4_paged``) and eviction (``gqa_attn_weights``, ``evict_select``,
+``gqa_cache_compact``).  ``inputs`` makes seeded synthetic workloads.
 """
 from ._lib import (TWO_TERM_MAX_KEYS_DEFAULT, MLAError, forced, last_device_error, load_library,
                    paged_workspace_size, plan, set_timing_events, set_two_term_max_keys, strerror,

@@ -8,7 +8,10 @@
 // registers, and no sum crosses threads, tiles or blocks.
 //
 // What bounds it: K is read once (2 D bytes a key and head; the weights add 8), up to
-// ~100 rows; beyond, a thread's exponentials: 16 a cycle and SM.
+// ~100 rows; beyond, a thread's exponentials: 16 a cycle and SM.  Measured (GPU time, D =
+// 128, loads first): 64 streams of 1k to 32k keys, one token, 16-row pages, 8 heads a key
+// head 207 us, 6.0 TB/s (88 % of the measured copy rate); one stream of 64k keys, 9 drafts
+// 31 us, of 262k 89 us (91 %); 64 drafts (512 rows a key head) over 8k keys 49 us.
 //
 // Split.  As in the attention kernel: equal runs of 64-key tiles, teams of CTAs
 // with the key heads of a cache row side by side.  A run's tiles are taken two at a

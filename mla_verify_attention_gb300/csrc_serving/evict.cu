@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams 
 // have later sources (behind every row written so far), so that nothing is
 // overwritten that is still to be read, whatever is ahead of whom within the block,
 // and slices have nothing to do with each other.  The weights of a key head are
-// one more slice, of 4 bytes a key.
+// one more slice, of 4 bytes a key.  Bound by HBM: 8 streams of 16k to 32k keys to 8k,
+// 4 KB a row 100 us, 5.4 TB/s (80 % of the measured copy rate) in slices of 128 bytes
+// (of 32, 64, 256: 147, 124, 163 us with 256 threads).
 struct CompactParams {
   uint8_t* pool[2];
   long long pool_stride[2];

@@ -23,12 +23,13 @@ namespace fp4 {
 // or more away (x has 11 bits, a step 4, a border 3).  The values are taken negative and
 // their remainder as q d - x: its zero then leaves the sign of a q of -0.
 //
-// What bounds it: 2 bytes a value read, 9 / 16 written, 2 more where the values
-// held are asked for, and as much the conversions and quotients: 32,251 tokens of 8 heads
-// of 128 with the values held 54.7 us, 5.5 TB/s (81 % of the measured copy rate), at 3.1
-// instructions a cycle and SM.  A lane takes eight values (16 bytes in, 4 out), four loads
-// in flight (2 or 8: 65, 62 us; values read before the slot is known: no change).  A block takes as many rows of K or V as its threads' loads cover (a warp a
-// row left half the lanes of a 16-unit row idle: 32k rows of one head 25.7 us).
+// What bounds it: 2 bytes a value read, 9 / 16 written, 2 more where the values held are
+// asked for, and as much the conversions and quotients: 32,251 tokens of 8 heads of 128
+// with the values held 54.7 us, 5.5 TB/s (81 % of the measured copy rate), at 3.1
+// instructions a cycle and SM.  A lane takes eight values (16 bytes in, 4 out), four
+// loads in flight (2 or 8: 65, 62 us; values read before the slot is known: no change).
+// A block takes as many rows of K or V as its threads' loads cover (a warp a row left
+// half the lanes of a 16-unit row idle: 32k rows of one head 25.7 us).
 struct AppendParams {
   const uint8_t* src[2];
   uint8_t* pool[2];

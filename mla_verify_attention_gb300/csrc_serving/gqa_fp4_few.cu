@@ -13,18 +13,24 @@
 //      2 c + 8, 2 c + 9; the halves of two keys' bytes are interleaved before they
 //      are converted, so that a pair of keys lies in a register as the product wants.
 // S^T's layout is P's but for a transpose of 8 x 8 (movmatrix).  The keys' order in
-// shared memory is permuted (kOrder) so that neither K's nor V's reads collide.
+// shared memory is permuted (`order`) so that K's and V's reads collide as little as the
+// rows' pitch allows.
 //
-// What bounds it: 1,152 bytes a key of 8 heads at D = 128, 23 bytes a cycle and SM; the
-// conversions (78 values a cycle and SM measured) take about half of that time.
+// What bounds it: 1,152 bytes a key of 8 heads at D = 128, 23 bytes a cycle and SM, and as
+// much the instructions: 268 a warp for 16 keys of a head and eight rows (70 conversions,
+// 64 fp16 products, 16 mma.sync), 1.6 a cycle and SM with two warps a scheduler.
+// Measured (GPU time, bf16, D = 128, 64 streams of 1k to 32k keys, 8 key heads, 16-row
+// pages): one token of 8 heads a key head 134 us, 5.0 TB/s (74 % of the measured copy
+// rate); 2, 3, 4 tokens 175, 232, 292 us.
 //
 // Split.  Equal runs of 64-key tiles as in the attention kernel, but a CTA takes all (up
-// to 16) key heads of a run: whole rows of the cache come in by TMA boxes of eight rows
+// to eight) key heads of a run: whole rows of the cache come in by TMA boxes of eight rows
 // or more (a bulk copy a row took 64 cycles each, 2.6 TB/s in all; boxes of eight 7.1),
 // or, where pages are not a multiple of eight rows, by four warps' 16-byte copies.
-// The other warps are shared out among the heads; those of one head take 16 keys in
-// turn and are put together at a unit's end.  The heads of a CTA count as a team's
-// members for the merge.
+// Eight other warps are shared out among the heads; those of one head take 16 or 32 keys
+// in turn and are put together at a unit's end.  (16 warps of 16 keys: 173 us against
+// 150, for registers and instructions; 12 warps on four heads 181.)  The heads of a CTA
+// count as a team's members for the merge.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
