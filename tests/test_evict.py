@@ -261,3 +261,36 @@ def test_refusals():
             mva.gqa_cache_compact(*args)
     with pytest.raises(ValueError):
         mva.gqa_cache_compact(*good, weights=w)
+
+
+def test_compact_in_pools_beyond_2_to_the_32_bytes():
+    page, rows = 64, 2_300_000
+    pools = [torch.zeros((rows // page * page, 8, 128), dtype=BF16, device="cuda") for _ in range(2)]
+    lens, budget = [3000], 700
+    table = torch.tensor([[rows // page - 1 - j if j % 2 else j for j in range(47)]], dtype=torch.int32)
+    at = plain.rows_of(table[0], page, 3000).cuda()
+    for p in pools:
+        p[at] = torch.randn((3000, 8, 128), device="cuda").to(BF16)
+    kept = torch.randperm(3000, generator=torch.Generator().manual_seed(0))[:budget].sort().values
+    want = [p[at[kept.cuda()]].clone() for p in pools]
+    mva.gqa_cache_compact(*pools, table.cuda(), page, i32(lens), kept.int()[None].cuda(), i32([budget]))
+    assert mva.last_device_error() == 0
+    assert all(torch.equal(p[at[:budget]], w) for p, w in zip(pools, want))
+
+
+def test_compact_and_select_of_more_streams_than_a_grid_is_high():
+    B, page = 66000, 2
+    table = torch.arange(2 * B, dtype=torch.int32, device="cuda").view(B, 2)
+    pool = torch.arange(4 * B, dtype=torch.int64, device="cuda")[:, None].repeat(1, 2).view(torch.uint8)
+    lens = torch.full((B,), 4, dtype=torch.int32, device="cuda")
+    w = torch.rand((B, 1, 4), device="cuda")
+    kept, keep = torch.empty((B, 3), dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    mva.evict_select(w, lens, 0, 0, kept, keep)
+    want = w[:, 0].argsort(dim=1, descending=True)[:, :3].sort(dim=1).values
+    assert torch.equal(kept.long(), want) and (keep == 3).all()
+    second = pool.clone()
+    mva.gqa_cache_compact(pool, second, table, page, lens, kept, keep)
+    assert mva.last_device_error() == 0
+    rows = (torch.arange(B, device="cuda")[:, None] * 4 + want)
+    for p in (pool, second):
+        assert torch.equal(p.view(torch.int64)[:, 0].view(B, 4)[:, :3], rows)

@@ -312,3 +312,33 @@ def test_refusals():
     with pytest.raises(mva.MLAError) as e:
         mva.gqa_verify_attn_fp4_paged(*good, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -4
+
+
+@pytest.mark.parametrize("q,Hkv", [(1, 8), (3, 8), (9, 8)])
+@pytest.mark.parametrize("page", [64, 100])
+def test_pools_beyond_2_to_the_32_bytes(q, Hkv, page):
+    # Rows appended to, and read from, both ends of pools of 5 GB.
+    D, H, n = 128, 8 * Hkv, 9_000_000
+    width = mva.gqa_fp4_row_bytes(Hkv, D)
+    pages = n // page
+    pools = [torch.zeros((pages * page, width), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    lens = [300, 2000]
+    table = torch.zeros((2, -(-9000 // page)), dtype=torch.int32)
+    for b, length in enumerate(lens):
+        for j in range(-(-length // page)):
+            table[b, j] = pages - 1 - (2 * j + b) if j % 3 else 2 * j + b
+    gen = torch.Generator().manual_seed(q)
+    x = [torch.randn((sum(lens), Hkv, D), generator=gen).to(BF16).cuda() for _ in range(2)]
+    slots = torch.cat([plain.rows_of(table[b], page, m) for b, m in enumerate(lens)]).int().cuda()
+    held = [torch.empty_like(y) for y in x]
+    mva.gqa_cache_append_fp4(*pools, *x, slots, 0.25, 0.25, *held)
+    seen = trees(gen, 2, q, "random")
+    qs = torch.randn((2, q, H, D), generator=gen).to(BF16).cuda()
+    out, lse = mva.gqa_verify_attn_fp4_paged(qs, *pools, Hkv, table.cuda(), page, torch.tensor(lens, dtype=torch.int32).cuda(),
+                                             gqa_plain.mask_words(seen).cuda(), 0.1, 0.25, 0.25)
+    assert mva.last_device_error() == 0
+    at = 0
+    for b, m in enumerate(lens):
+        k, v = (y[at:at + m].double() for y in held)
+        plain.check(out[b], lse[b], plain.attend(qs[b], k, v, plain.seen_keys(seen[b], m), 0.1, weight_u=2.0 ** -11), "stream %d" % b)
+        at += m
