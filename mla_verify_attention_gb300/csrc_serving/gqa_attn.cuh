@@ -261,6 +261,7 @@ __device__ __forceinline__ bool wait_loop(S& sm, uint32_t bar, uint32_t parity, 
     }
   }
 }
+constexpr long long kWaitCycles = 4000000000ll;    // two seconds at 2 GHz
 // Out of line, except where warps have register counts of their own (a call's
 // registers cannot be allocated there).
 template <class S>
@@ -277,8 +278,21 @@ struct InlineWaits<Smem<D, kFp4>> {
 };
 template <class S>
 __device__ __forceinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
-  if constexpr (InlineWaits<S>::value) return wait_loop(sm, bar, parity, p);
-  else return wait_call(sm, bar, parity, p);
+  if constexpr (InlineWaits<S>::value) {
+    // Little code, for it stands at every wait: with the loop above here instead, one stream
+    // of 64k keys in 4 bits, 9 drafts took 52 us, not 46.
+    const long long t0 = clock64();
+    while (!*reinterpret_cast<volatile uint32_t*>(&sm.abort_flag)) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (clock64() - t0 > kWaitCycles) {
+        atomicOr(p.status, kBitTimeout);
+        *reinterpret_cast<volatile uint32_t*>(&sm.abort_flag) = 1u;
+      }
+    }
+    return false;
+  } else {
+    return wait_call(sm, bar, parity, p);
+  }
 }
 // By a whole converged warp; the result is warp-uniform.
 template <class S>
