@@ -280,7 +280,7 @@ template <class S>
 __device__ __forceinline__ bool wait_slow(S& sm, uint32_t bar, uint32_t parity, const Params& p) {
   if constexpr (InlineWaits<S>::value) {
     // Little code, for it stands at every wait: with the loop above here instead, one stream
-    // of 64k keys in 4 bits, 9 drafts took 52 us, not 46.
+    // of 64k keys in 4 bits, 9 drafts took 52 us, not 41.
     const long long t0 = clock64();
     while (!*reinterpret_cast<volatile uint32_t*>(&sm.abort_flag)) {
       if (mbar_try_wait(bar, parity)) return true;
@@ -639,8 +639,11 @@ out:
 // (A code times its step is exact in fp16, whatever the type of Q; the pools' factors go
 // to the scale and to the result.)  The 16-byte units of a row's codes are swizzled, as
 // TMA does, so that eight lanes that read a unit of eight rows, and then write eight rows of
-// a tile, meet no bank twice.  The row copies took a warp 1,500 cycles a tile, which was
-// what a tile took (one stream of 64k keys, 9 drafts 53 us).
+// a tile, meet no bank twice.
+// Measured (GPU time, bf16, D = 128): one stream of 64k keys, 9 drafts of 8 heads a key
+// head 39.7 us, 64 streams of 1k to 32k keys, 5 tokens 352 us: ~1,000 cycles a tile of
+// 64 keys, most of them the softmax's, whose warps, the unpacking and the products' share
+// the instruction cache (16-bit caches: 860 cycles).
 struct Fp4Maps {
   CUtensorMap codes[2], steps[2];              // K, V: boxes of D / 2 and of 16 bytes
 };
@@ -780,8 +783,9 @@ __device__ __forceinline__ void unpack_tiles(Smem<D, kFp4>& sm, const Params& p,
       const uint8_t* const steps = sm.extra.steps[is_v][from.stage] + (s.head * (D / 16) & 15);
       if (!wait(sm, empty[to.stage], to.phase ^ 1, p)) return;
       uint8_t* const tile = sm.ring + to.stage * 2 * C::kTile + (is_v ? C::kTile : 0) + (u >> 1) * (kKeys * 128);
-      // (A loop of few instructions, the next unit loaded ahead: unrolled, it and the
-      // softmax's code took turns in the instruction cache.)
+      // (A loop of few instructions, the next unit loaded ahead: unrolled further, it and the
+      // softmax's code take turns in the instruction cache.  One stream of 64k keys, 9
+      // drafts: 41.1, 39.7, 39.6 and 48.3 us with 1, 2, 4 and 8 units of its 8.)
       auto load = [&](int row, uint4& c, uint32_t& two) {
         c = *reinterpret_cast<const uint4*>(codes + code_unit<D>(row, u) * 16);
         two = *reinterpret_cast<const uint16_t*>(steps + row * 16 + u * 2);
@@ -789,7 +793,7 @@ __device__ __forceinline__ void unpack_tiles(Smem<D, kFp4>& sm, const Params& p,
       uint4 next;
       uint32_t next_two;
       load(row0, next, next_two);
-#pragma unroll 1
+#pragma unroll 2
       for (int e = 0; e < kTimes; ++e) {
         const int row = row0 + e * (32 / kUnits);
         const uint32_t words[4] = {next.x, next.y, next.z, next.w}, step2 = fp4::from_e4m3x2(next_two);

@@ -287,6 +287,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
   const int g = lane >> 2, c = lane & 3;
   const int head_local = warp / p.head_warps, j = warp - head_local * p.head_warps;
   const int rows = p.q_len * p.G;
+  const bool several = kN == 1 && p.head_warps > 1;        // warps of a head (more rows: always one, see few_rows)
   const int key_g = p.order >> (4 * g) & 7, key_c = p.order >> (8 * c) & 7, key_c1 = p.order >> (8 * c + 4) & 7;
   // Where this lane reads, from a stage's start and of the first 16 keys: K's codes (and
   // their steps, from where the head's steps are), the same of V, and from there to
@@ -570,9 +571,9 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
         m_all[t][e] = ms[t][e];
         l_all[t][e] = l[t][e];
         w_mine[t][e] = 1.f;
-        if (p.head_warps > 1 && g == 0) sm.ml[warp][8 * t + 2 * c + e] = make_float2(ms[t][e], l[t][e]);
+        if (several && g == 0) sm.ml[warp][8 * t + 2 * c + e] = make_float2(ms[t][e], l[t][e]);
       }
-    if (p.head_warps > 1) {
+    if (several) {
       if (!meet(sm, p, head_local, met)) return;
 #pragma unroll
       for (int t = 0; t < kN; ++t)
@@ -613,7 +614,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
           v[at] = o[t][y][e] * by;
           v[at + 2] = o[t][y][e + 2] * by;
         }
-        if (p.head_warps > 1) {
+        if (several) {
           float4* const to = reinterpret_cast<float4*>(sums + (warp * 8 + 2 * c + e) * kSumPitch<D> + g * (D / 8));
 #pragma unroll
           for (int y = 0; y < D / 32; ++y) to[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
@@ -631,7 +632,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
           }
         }
       }
-      if (p.head_warps > 1) {
+      if (several) {
         if (!meet(sm, p, head_local, met)) return;
         const int here = min(8, rows - 8 * t);
         for (int x = j * 32 + lane; x < here * (D / 4); x += 32 * p.head_warps) {
@@ -650,8 +651,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
             p.part_o[(static_cast<size_t>(slot) * p.part_rows + row) * (D / 4) + col] = sum;
           }
         }
-        // (The next eight rows' sums take these ones' place; a next unit's warps meet first.)
-        if (8 * (t + 1) < rows && !meet(sm, p, head_local, met)) return;
+        // (A next unit's warps meet before its sums take these ones' place.)
       }
     }
   }
@@ -848,15 +848,17 @@ int most_step_bytes(int Hkv, int heads, int each) {
 // Whether this kernel takes a call, by its rows a key head and the keys that its tables
 // have room for.  GPU time here / with the tcgen05 kernel, us, D = 128, 8 heads a key head
 // unless said:
-//   64 streams of 1k to 32k keys, 16-row pages, 8 key heads: one token 134 / 425, 2 tokens
-//     175 / 423, 3 232 / 430, 4 292 / 430; 2 key heads: 59 / 116, 4 tokens 155 / 113 (the
-//     warps of a head have much to put together); of 200 to 400 keys 18 / 44, 4 tokens 37 / 46;
-//   one stream of 64k keys: 2 tokens 37 / 47, 4 51 / 47; of 2,048 keys: one token 13.7 / 13.6,
-//     2 tokens 17 / 13.7; of 256 keys 13.7 / 9.6 (one CTA has all heads of a key).
+//   64 streams of 1k to 32k keys, 16-row pages, 8 key heads: one token 134 / 345, 2 tokens
+//     175 / 350, 3 225 / 352, 4 287 / 354; 2 key heads: one token 60 / 100, 4 tokens 155 / 101
+//     (the warps of a head have much to put together);
+//   64 streams of 200 to 400 keys: one token 18 / 39, 4 tokens 38 / 41;
+//   one stream, 64-row pages, of 64k keys: one token 32 / 38, 2 tokens 36 / 38, 4 51 / 38; of
+//     128k 2 tokens 52 / 64, 4 78 / 64; one token of 8,192 keys 15.7 / 15.0, of 2,048 13.7 /
+//     13.0, of 256 13.7 / 9.6 (one CTA has all heads of a key).
 bool few_rows(int B, int q_len, int H, int Hkv, int Smax) {
   const long long rows = static_cast<long long>(q_len) * (H / Hkv), keys = static_cast<long long>(B) * Smax;
   if (rows <= 8) return keys >= 2048;
-  return rows <= 8 * few::kMostEights && few_heads(Hkv) == few::kWarps && keys >= 16384;
+  return rows <= 8 * few::kMostEights && few_heads(Hkv) == few::kWarps && keys >= (rows <= 16 ? 1 << 15 : 1 << 18);
 }
 int few_heads(int Hkv) { return few::heads_a_cta(Hkv, few::kWarps); }
 

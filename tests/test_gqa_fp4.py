@@ -67,7 +67,7 @@ def verify(c, got):
         plain.check(got[0][b], got[1][b], plain.attend(c["q"][b], k, v, see, c["scale"], weight_u=2.0 ** -11), "stream %d" % b)
 
 
-@pytest.mark.parametrize("room", [0, 20000])
+@pytest.mark.parametrize("room", [0, 270000])
 @pytest.mark.parametrize("dt", [BF16, FP16])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("q,H,Hkv,lens", [
@@ -80,6 +80,9 @@ def verify(c, got):
     (3, 8, 1, [500]),                          # 24 rows
     (4, 16, 2, [500, 66, 4]),                  # 32 rows
     (4, 64, 8, [1500, 300]),
+    (2, 64, 8, [700, 2, 65]),                  # 16 and 24 rows of eight key heads
+    (3, 64, 8, [1500, 300]),
+    (3, 48, 16, [700, 3]),                     # two sets of eight heads
     (11, 9, 3, [700]),                         # 33 rows
     (32, 2, 2, [700, 32, 33, 60]),             # 32 drafts of a head: one mask word, all of it
     (32, 8, 8, [100]),
@@ -99,21 +102,22 @@ def test_matches_plain(q, H, Hkv, lens, D, dt, room):
 @pytest.mark.parametrize("q,H,Hkv", [(1, 16, 2), (5, 16, 2), (5, 24, 8)])
 def test_pages(q, H, Hkv, page):
     for D, dt in ((64, FP16), (128, BF16)):
-        c = case(q, H, Hkv, D, [1500, 5, 700, 64, 0, 4000], page, dt, room=4000)
+        c = case(q, H, Hkv, D, [1500, 5, 700, 64, 0, 4000], page, dt, room=50000)
         verify(c, run(c))
 
 
 @pytest.mark.parametrize("q,H,Hkv", [(1, 8, 1), (1, 8, 8), (1, 6, 3), (1, 16, 16), (1, 40, 40), (1, 12, 12), (4, 4, 2), (1, 72, 24), (9, 36, 36)])
 def test_head_layouts(q, H, Hkv):
     for D in (64, 128):
-        c = case(q, H, Hkv, D, [max(q, 3), 200, 1111], 16, room=6000)
+        c = case(q, H, Hkv, D, [max(q, 3), 200, 1111], 16, room=90000)
         verify(c, run(c))
 
 
 @pytest.mark.parametrize("tree", ["chain", "any"])
-@pytest.mark.parametrize("q,G,lens", [(1, 8, [1, 64, 65]), (2, 4, [2, 66]), (9, 8, [9, 70]), (40, 2, [41, 130]), (64, 4, [64, 129])])
+@pytest.mark.parametrize("q,G,lens", [(1, 8, [1, 64, 65]), (2, 4, [2, 66]), (4, 4, [4, 70]), (6, 4, [6, 65]), (8, 4, [9, 70]),
+                                      (9, 8, [9, 70]), (40, 2, [41, 130]), (64, 4, [64, 129])])
 def test_masks(q, G, lens, tree):
-    for Hkv, room in ((2, 0), (2, 1100), (8, 9000)):
+    for Hkv, room in ((2, 0), (2, 1100), (8, 140000)):
         c = case(q, Hkv * G, Hkv, 64, lens, 16, tree=tree, room=room)
         verify(c, run(c))
 
@@ -146,7 +150,7 @@ def test_steps_and_queries_of_every_size(q):
 @pytest.mark.parametrize("q", [1, 2, 9])
 def test_drafts_that_none_sees_hold_anything(q):
     # Padding drafts' rows: codes with steps of NaN.
-    c = case(q, 16, 8 if q == 2 else 2, 128, [300, 64 + q], 16, room=9000)
+    c = case(q, 16, 8 if q == 2 else 2, 128, [300, 64 + q], 16, room=140000)
     c["seen"][0, :, q - 1] = False
     c["mask"] = gqa_plain.mask_words(c["seen"]).cuda()
     for p, x in zip(c["pools"], c["cpu"]):
