@@ -27,7 +27,7 @@ namespace evict {
 // What bounds it beside that read: chains of barriers and reads.  Blocks send their
 // histograms and counts to all others' shared memory and meet once a pass: read from
 // there after the barrier instead, 2,048 bins took 8,000 cycles a pass, more than
-// two passes of 256 take in all (one stream of 64k keys, 8 heads 30.6 -> 15.7 us).
+// two passes of 256 take in all (one stream of 64k keys, 8 heads 30.6 -> 15.8 us).
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 256;
@@ -77,6 +77,13 @@ __device__ __forceinline__ void sync_blocks() {
   else __syncthreads();
 }
 
+// All blocks of the cluster have started (the other half of the kernel's first arrival).
+template <int kBlocks>
+__device__ __forceinline__ void await_blocks() {
+  __syncwarp();
+  if (kBlocks > 1) cluster_wait();
+}
+
 // kBlocks: of a stream's cluster.
 template <int kBlocks>
 __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams p) {
@@ -85,6 +92,9 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = kBlocks > 1 ? cluster_ctarank() : 0u;
   const int b = static_cast<int>(blockIdx.x / kBlocks);
+  // Another block's shared memory may be written once that block has started: all arrive
+  // here, and wait (await_blocks) before the first of them sends or returns.
+  if (kBlocks > 1) cluster_arrive_relaxed();
   for (int i = tid; i < kPasses * kBins; i += kThreads) sm.mine[0][i] = 0;
   grid_dependency_wait();
   if (tid == 0) grid_launch_dependents();
@@ -99,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams 
   const int threads = kBlocks * kThreads, me = static_cast<int>(rank) * kThreads + tid;
   for (int j = n + me; j < p.budget; j += threads) kept[j] = -1;
   if (S <= p.budget) {                                     // (the whole cluster)
+    await_blocks<kBlocks>();
     for (int j = me; j < n; j += threads) kept[j] = j;
     return;
   }
@@ -127,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams 
       atomicAdd(&sm.mine[0][key >> 24], 1u);
     }
   }
+  await_blocks<kBlocks>();
   const int choose = n - p.sinks - p.recent;               // how many of them
   uint32_t prefix = 0, left = static_cast<uint32_t>(choose);
   if (choose > 0) {

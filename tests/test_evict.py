@@ -294,3 +294,75 @@ def test_compact_and_select_of_more_streams_than_a_grid_is_high():
     rows = (torch.arange(B, device="cuda")[:, None] * 4 + want)
     for p in (pool, second):
         assert torch.equal(p.view(torch.int64)[:, 0].view(B, 4)[:, :3], rows)
+
+
+def streams_for(blocks):
+    """How many streams of more than 4,096 keys make select take this many blocks a stream (as many as the device
+    holds at once, two an SM, up to eight)."""
+    most = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    return {8: 3, 4: most // 8 + 1, 2: most // 4 + 1, 1: most // 2 + 1}[blocks]
+
+
+@pytest.mark.parametrize("blocks", [8, 4, 2, 1])
+@pytest.mark.parametrize("sinks,recent,budget", [
+    (0, 0, 700),
+    (4, 512, 3000),
+    (1200, 800, 2000),                            # nothing to choose: all of it first and last keys
+    (0, 2000, 2000),
+    (2500, 3100, 5700),                           # whole blocks hold first or last keys only
+    (5900, 0, 5901),
+    (0, 5900, 5999),
+])
+def test_select_with_every_number_of_blocks(blocks, sinks, recent, budget):
+    gen = torch.Generator().manual_seed(blocks + budget)
+    B, S = streams_for(blocks), 6000
+    lens = [S, S - 1, budget, budget + 1, 0, 4097] + [37] * B
+    lens = lens[:B] if B > 6 else lens[:2] + [budget + 1]
+    check_select(mass(gen, B, 2, S), lens, sinks, recent, budget)
+    check_select(torch.randint(0, 3, (B, 1, S), generator=gen).float(), lens, sinks, recent, budget)
+    check_select(torch.ones((B, 1, S)), lens, sinks, recent, budget)
+
+
+@pytest.mark.parametrize("blocks", [4, 2, 1])
+def test_select_with_long_runs_of_a_block(blocks):
+    gen = torch.Generator().manual_seed(blocks)
+    B, S = streams_for(blocks), 49000
+    check_select(mass(gen, B, 1, S), [S, 5, 30001, 0] + [100] * (B - 4), 4, 1000, 9000)
+
+
+def test_select_and_compact_on_another_stream_and_in_a_graph_of_it():
+    gen = torch.Generator().manual_seed(8)
+    page, budget, lens = 16, 2500, [6000, 100, 5000]
+    table, pools = streams(gen, lens, page, (2, 64))
+    table, smax = table.clamp_min(0).cuda(), table.shape[1] * page
+    w, lens_t = mass(gen, 3, 2, smax).cuda(), i32(lens)
+    state = [x.clone() for x in (*pools, w)]
+    kept, keep = torch.empty((3, budget), dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def both(stream):
+        mva.evict_select(w, lens_t, 4, 64, kept, keep, stream=stream)
+        mva.gqa_cache_compact(*pools, table, page, lens_t, kept, keep, weights=w, stream=stream)
+
+    def check():
+        torch.cuda.synchronize()
+        assert mva.last_device_error() == 0
+        for b, n in enumerate(lens):
+            want = plain.select(state[2][b].cpu(), n, 4, 64, budget)
+            assert int(keep[b]) == len(want) and kept[b, :len(want)].tolist() == want and (kept[b, len(want):] == -1).all()
+            rows = plain.rows_of(table[b], page, n)
+            for p, old in zip(pools, state):
+                assert torch.equal(p.cpu()[rows[:len(want)]], old.cpu()[rows[want]])
+            assert torch.equal(w[b, :, :len(want)].cpu(), state[2][b].cpu()[:, want]) and not w[b, :, len(want):n].any()
+
+    torch.cuda.synchronize()
+    both(side)
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        both(side)
+    for x, y in zip((*pools, w), state):
+        x.copy_(y)
+    kept.fill_(-9)
+    graph.replay()
+    check()
