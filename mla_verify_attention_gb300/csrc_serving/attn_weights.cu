@@ -11,7 +11,7 @@
 // ~100 rows; beyond, a thread's exponentials: 16 a cycle and SM.  Measured (GPU time, D =
 // 128, loads first): 64 streams of 1k to 32k keys, one token, 16-row pages, 8 heads a key
 // head 207 us, 6.0 TB/s (88 % of the measured copy rate); one stream of 64k keys, 9 drafts
-// 31 us, of 262k 89 us (91 %); 64 drafts (512 rows a key head) over 8k keys 49 us.
+// 30 us, of 262k 89 us (91 %); 64 drafts (512 rows a key head) over 8k keys 24 us.
 //
 // Split.  As in the attention kernel: equal runs of 64-key tiles, teams of CTAs
 // with the key heads of a cache row side by side.  A run's tiles are taken two at a
@@ -54,6 +54,7 @@ struct __align__(1024) WSmem {
   uint8_t ring[WShape<D>::kStages * WShape<D>::kTile];
   uint8_t q[2 * WShape<D>::kQTile];
   float minus_lse[2][kChunkRows];          // in log2 units; -inf: the row adds nothing
+  uint32_t adds[2][kChunkRows / 32];       // rows that add something, a bit each
   uint64_t kfull[WShape<D>::kStages], kempty[WShape<D>::kStages];
   uint64_t qfull[2], qempty[2], sfull[2][2], sempty[2][2], drain;   // s: [group][buffer]
   int warp_sum[kThreads / 32], start_b, start_pre;
@@ -217,9 +218,11 @@ __device__ __forceinline__ void load_q(WSmem<D>& sm, const WeightParams& p, Walk
         if (r0 >= N) break;
         const bool adds = !isinf(lse[k]);
         sm.minus_lse[buf][r0 + lane] = adds ? -lse[k] * 1.4426950408889634f : -CUDART_INF_F;
+        const uint32_t adding = __ballot_sync(0xFFFFFFFFu, adds);
+        if (lane == 0) sm.adds[buf][r0 / 32] = adding;
         // Rows that add nothing may hold anything (those past the last are zeros already).
         const bool there = c * kChunkRows + r0 + lane < all_rows;
-        for (unsigned rest = __ballot_sync(0xFFFFFFFFu, !adds && there); rest; rest &= rest - 1u) {
+        for (unsigned rest = ~adding & __ballot_sync(0xFFFFFFFFu, there); rest; rest &= rest - 1u) {
           const int row = r0 + __ffs(rest) - 1;
           if (lane < kUnits)
             *reinterpret_cast<uint4*>(sm.q + buf * C::kQTile + (lane >> 3) * (kChunkRows * 128) + row * 128 + (lane & 7) * 16) =
@@ -283,15 +286,15 @@ __device__ __forceinline__ uint32_t seen_columns(const WeightParams& p, uint64_t
 }
 
 // kN columns: their sum of 2^(s a + minus_lse).  kEdge: of the rows whose drafts see the
-// key (s may be anything in the others).
+// key and that add something (s may be anything in the others).
 template <int kN, bool kEdge>
-__device__ __forceinline__ float add_columns(const WeightParams& p, uint32_t s_t, const float* minus, int first_row,
-                                             uint64_t seen) {
+__device__ __forceinline__ float add_columns(const WeightParams& p, uint32_t s_t, const float* minus, uint32_t adds,
+                                             int first_row, uint64_t seen) {
   uint32_t sr[kN];
   if constexpr (kN == 32) MLA_TMEM_LD_32x32b_X32(s_t, sr);
   else MLA_TMEM_LD_32x32b_X16(s_t, sr);
   uint32_t columns = 0;
-  if constexpr (kEdge) columns = seen_columns<kN>(p, seen, first_row);
+  if constexpr (kEdge) columns = adds & seen_columns<kN>(p, seen, first_row);
   tmem_ld_wait();
   const uint64_t a2 = f2pack(p.scale_log2, p.scale_log2);
   uint64_t sum[2] = {0ull, 0ull};
@@ -316,12 +319,14 @@ __device__ __forceinline__ float add_columns(const WeightParams& p, uint32_t s_t
 }
 
 template <bool kEdge>
-__device__ __forceinline__ float add_chunk(const WeightParams& p, uint32_t s_t, const float* minus, int first_row, uint64_t seen) {
+__device__ __forceinline__ float add_chunk(const WeightParams& p, uint32_t s_t, const float* minus, const uint32_t* adds,
+                                           int first_row, uint64_t seen) {
   float sum = 0.f;
   int c = 0;
 #pragma unroll 1
-  for (; c + 32 <= p.chunk_rows; c += 32) sum += add_columns<32, kEdge>(p, s_t + c, minus + c, first_row + c, seen);
-  if (c < p.chunk_rows) sum += add_columns<16, kEdge>(p, s_t + c, minus + c, first_row + c, seen);
+  for (; c + 32 <= p.chunk_rows; c += 32)
+    sum += add_columns<32, kEdge>(p, s_t + c, minus + c, adds[c / 32], first_row + c, seen);
+  if (c < p.chunk_rows) sum += add_columns<16, kEdge>(p, s_t + c, minus + c, adds[c / 32], first_row + c, seen);
   return sum;
 }
 
@@ -357,13 +362,13 @@ __device__ __forceinline__ void add_up(WSmem<D>& sm, const WeightParams& p, uint
           word[1][1] = rows[(32 + lane) * words + 1];
         }
         const int draft = key - prefix;                    // (may be any number)
-        uint64_t mine = 0;
+        uint64_t drafts = 0;
         for (int i = 0; i < p.q_len; ++i) {
           const uint32_t lo = __shfl_sync(0xFFFFFFFFu, i < 32 ? word[0][0] : word[1][0], i & 31);
           const uint32_t hi = __shfl_sync(0xFFFFFFFFu, i < 32 ? word[0][1] : word[1][1], i & 31);
-          mine |= static_cast<uint64_t>((draft & 32 ? hi : lo) >> (draft & 31) & 1u) << i;
+          drafts |= static_cast<uint64_t>((draft & 32 ? hi : lo) >> (draft & 31) & 1u) << i;
         }
-        if (valid && key >= prefix) seen = mine;
+        if (valid && key >= prefix) seen = drafts;
       }
       for (int c = 0; c < p.chunks; ++c) {
         const int buf = loads & 1;
@@ -374,8 +379,16 @@ __device__ __forceinline__ void add_up(WSmem<D>& sm, const WeightParams& p, uint
           if (!wait(sm, sm.sfull[g][b], (done >> 1) & 1, p)) return;
           tc_fence_after();
           const uint32_t s_t = tmem + lanes + (2 * g + b) * kChunkRows;
-          sum += edge ? add_chunk<true>(p, s_t, sm.minus_lse[buf], c * kChunkRows, seen)
-                      : add_chunk<false>(p, s_t, sm.minus_lse[buf], c * kChunkRows, seen);
+          float x = 0.f;
+          bool careful = edge;
+          if (!edge) {
+            x = add_chunk<false>(p, s_t, sm.minus_lse[buf], sm.adds[buf], c * kChunkRows, seen);
+            // A key that is not finite gives NaN in the rows that add nothing, too (0 times it):
+            // once more, without them.
+            careful = __any_sync(0xFFFFFFFFu, valid && x != x);
+          }
+          if (careful) x = add_chunk<true>(p, s_t, sm.minus_lse[buf], sm.adds[buf], c * kChunkRows, seen);
+          sum += x;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.sempty[g][b]));

@@ -235,3 +235,40 @@ def test_refusals():
     pool, table = c["k"].view(100, 2, 64), torch.tensor([[7]], dtype=torch.int32).cuda()
     mva.gqa_attn_weights_paged(c["q"], pool, table, 100, c["lens_t"], c["mask"], c["lse"], c["scale"], c["w"])
     assert mva.last_device_error() == -10
+
+
+@pytest.mark.parametrize("out", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("q,H,Hkv,D,dt", [(9, 16, 2, 128, BF16), (2, 2, 1, 64, FP16), (17, 8, 1, 128, FP16), (64, 8, 2, 64, BF16)])
+def test_rows_left_out_see_keys_that_are_not_finite(q, H, Hkv, D, dt, out):
+    # A batch padded to one q_len: the padding's drafts see themselves and their ancestors, their rows of k hold
+    # anything, and their lse leaves them out.  The sums are those over finite rows, bit by bit.
+    accepted = max(q // 3, 1)
+    c = case(q, H, Hkv, D, [300, q, 64 + q, 1000], dt)
+    c["lse"][:, accepted:] = out
+    want = run(c)
+    for b, n in enumerate(c["lens"]):
+        at = n - q + accepted
+        assert torch.equal(want[b, :, at:], c["w"][b, :, at:])
+        c["k"][b, at:n] = float("nan")
+        c["k"][b, n - 1] = float("inf")
+    assert torch.equal(run(c), want)
+
+
+@pytest.mark.parametrize("q,G", [(1, 1), (3, 8), (9, 8), (17, 8)])
+def test_keys_of_minus_infinity(q, G):
+    # A key whose score is -inf for every row gets nothing, with rows that fill no sixteen and rows left out beside them.
+    c = case(q, 2 * G, 2, 64, [300, 65 + q])
+    c["q"][..., 0] = c["q"][..., 0].abs() + 0.1
+    keys = [0, 17, 64]
+    for b, n in enumerate(c["lens"]):
+        c["k"][b, keys, :, 0] = -float("inf")
+        see = plain.seen_keys(c["seen"][b], n)
+        c["lse"][b] = plain.attend(c["q"][b], c["k"][b, :n], c["k"][b, :n], see, c["scale"])[1].float()
+    c["lse"][0, q // 2] = float("inf")
+    got = run(c)
+    assert torch.equal(got[:, :, keys], c["w"][:, :, keys])
+    for b, n in enumerate(c["lens"]):                  # the others as without those keys
+        c["k"][b, keys] = 0.0
+    rest = run(c)
+    at = [t for t in range(c["k"].shape[1]) if t not in keys]
+    assert torch.isfinite(got[0, :, :300]).all() and torch.equal(got[:, :, at], rest[:, :, at])
