@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -283,7 +284,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
   constexpr int kS = Shape8<kN>::kTogether;
   constexpr bool kTwo = kN <= 2;
   constexpr float kShift = 7.f;              // (see the attention kernel's softmax)
-  constexpr float kNothing = -1e30f;
+  constexpr float kNothing = -FLT_MAX;       // no score is smaller
   const int g = lane >> 2, c = lane & 3;
   const int head_local = warp / p.head_warps, j = warp - head_local * p.head_warps;
   const int rows = p.q_len * p.G;
@@ -567,7 +568,7 @@ __device__ __forceinline__ void attend(Head<kN>& sm, const FewParams& p, uint8_t
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], d);
-        if (ms[t][e] == kNothing) ms[t][e] = -CUDART_INF_F;
+        if (l[t][e] == 0.f) ms[t][e] = -CUDART_INF_F;
         m_all[t][e] = ms[t][e];
         l_all[t][e] = l[t][e];
         w_mine[t][e] = 1.f;

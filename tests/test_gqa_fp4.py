@@ -346,3 +346,33 @@ def test_pools_beyond_2_to_the_32_bytes(q, Hkv, page):
         k, v = (y[at:at + m].double() for y in held)
         plain.check(out[b], lse[b], plain.attend(qs[b], k, v, plain.seen_keys(seen[b], m), 0.1, weight_u=2.0 ** -11), "stream %d" % b)
         at += m
+
+
+@pytest.mark.parametrize("q,H,Hkv,room", [(1, 8, 2, 4096), (1, 8, 2, 0), (1, 8, 8, 4096), (2, 64, 8, 140000), (3, 64, 8, 270000),
+                                          (4, 64, 8, 270000), (3, 64, 8, 0), (9, 8, 2, 0)])
+def test_scores_far_below_zero(q, H, Hkv, room):
+    # Every score is -2^106 or -2^105 (exact in fp32, as are the quotients): the larger ones share the weight.
+    for lens, larger in (([max(q, 1), 70, 900], 0), ([70, 130, 900], 40)):
+        c = case(q, H, Hkv, 64, lens, 16, BF16, tree="chain", room=room)
+        c["scale"], c["k_scale"] = 2.0 ** -4, 0.25
+        head, codes = 32, Hkv * 32
+        for h in range(Hkv):
+            c["cpu"][0][:, h * head] = 0x22                    # 1.0 and 1.0
+            c["cpu"][0][:, codes + h * 4] = 0x38               # a step of 1
+        for b, n in enumerate(lens):
+            if larger:
+                c["cpu"][0][plain.rows_of(c["table"][b], 16, n)[larger - 1], [h * head for h in range(Hkv)]] = 0x21   # 0.5
+        c["pools"][0].copy_(c["cpu"][0])
+        c["q"].zero_()
+        c["q"][..., 0] = -2.0 ** 112
+        out, lse = run(c)
+        for b, n in enumerate(lens):
+            rows = plain.rows_of(c["table"][b], 16, n)
+            v = plain.unpack_fp4(c["cpu"][1][rows], Hkv, 64, c["v_scale"]).cuda()
+            see = plain.seen_keys(c["seen"][b], n)
+            if larger:
+                see &= (torch.arange(n) == larger - 1)[None]
+            even = plain.attend(torch.zeros_like(c["q"][b]), v, v, see, 1.0, weight_u=2.0 ** -11)
+            plain.check(out[b], even[1].float(), even, "stream %d" % b)
+            want = torch.full_like(lse[b], -2.0 ** (105 if larger else 106)).double()
+            assert ((lse[b].double() - want).abs() <= 2.0 ** -22 * want.abs()).all()
