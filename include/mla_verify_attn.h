@@ -488,7 +488,9 @@ size_t mla_gqa_fp4_row_bytes(int Hkv, int D);
  * k_pool and v_pool takes k[t] and v[t], of type `dtype`.  For each 16 values x
  *   step = the E4M3 nearest to min(448, max|x| / (6 factor)),
  *   code = the E2M1 nearest to x / (step factor)   (both ties to even; 0 where the step is 0);
- * a group with a NaN gets a NaN step.
+ * a group with a NaN gets a NaN step.  Exact for factors that are powers of two; with
+ * others 6 factor, step factor and the quotients are rounded to fp32, so that a quotient
+ * within 2^-22 (relative) of halfway between two numbers may become either.
  *   k, v            T rows [Hkv, D] at k_stride / v_stride bytes; 16-byte aligned, as all
  *                   rows and strides here; apart from the pools.
  *   k_held, v_held  NULL, or T rows [Hkv, D] of type `dtype` that take the values that

@@ -18,9 +18,11 @@ namespace fp4 {
 //   code = E2M1 nearest to x / d (both ties to even; all 0 where d is 0).
 // A quotient x / d is q = x r for an approximate reciprocal r (relative error e < 2^-22)
 // and one correction by the remainder, q + (x - q d) r, both fused: off by e^2 before
-// its one rounding.  So a quotient that is a number halfway between two codes or
-// steps comes out as that number, as in exact arithmetic, and one that is not lies 2^-19
-// or more away (x has 11 bits, a step 4, a border 3).  The values are taken negative and
+// its one rounding.  Where f is a power of two, a quotient that is a number halfway
+// between two codes or steps so comes out as that number, as in exact arithmetic, and one
+// that is not lies 2^-19 or more away (x has 11 bits, a step 4, a border 3).  For another
+// f, 6 f and step f are rounded to fp32 (2^-24) before the division and its quotient
+// once more: one within 2^-22 of halfway may come out on either side.  The values are taken negative and
 // their remainder as q d - x: its zero then leaves the sign of a q of -0.
 //
 // What bounds it: 2 bytes a value read, 9 / 16 written, 2 more where the values held are

@@ -164,3 +164,60 @@ def test_refusals():
             with pytest.raises(mva.MLAError) as e:
                 call(p[0], p[1], x, x, slots, **kw)
             assert e.value.status == -9
+
+
+def allowed(x, factor, step_codes, codes):
+    """Whether steps and codes are what the definition says of groups x [n,16]: the nearest to quotients in 64 bits,
+    either of two neighbours where a quotient is within 2^-22 of the middle between them."""
+    f, t = torch.tensor(factor, dtype=torch.float32).double(), 2.0 ** -22
+    steps, levels = plain.e4m3_values(), torch.tensor(plain.LEVELS, dtype=torch.float64)
+    z = x.double().abs().amax(-1) / (6 * f)
+    ok = torch.zeros_like(z, dtype=torch.bool)
+    for e in (1 - t, 1.0, 1 + t):
+        ok |= plain.nearest_even(z * e, steps) == step_codes
+    d = (steps[step_codes] * f)[:, None]
+    z = torch.where(d > 0, x.double().abs() / d, 0.0)
+    right = torch.zeros_like(z, dtype=torch.bool)
+    for e in (1 - t, 1.0, 1 + t):
+        right |= plain.nearest_even(z * e, levels) == (codes & 7)
+    sign = (codes >> 3 == torch.signbit(x)) | (d == 0) | (x == 0)
+    return ok, right & sign
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("factor", [0.1, 3.7, 1 - 2.0 ** -24, 1 + 2.0 ** -23, 1.5 - 2.0 ** -23, 1.0 / 3, 1.0 / 2688, 0.7853981852531433, 2.0 ** -7])
+def test_borders_with_any_factor(dt, factor):
+    # The values of the type nearest to every border of two steps, and of two codes at every step, and their neighbours.
+    f = torch.tensor(factor, dtype=torch.float32).double()
+    steps = plain.e4m3_values()[1:]
+    least = torch.finfo(dt).tiny
+    one = torch.tensor(1, dtype=torch.int16)
+    near = lambda y: (y.to(dt).view(torch.int16) + torch.arange(-2, 3, dtype=torch.int16)[:, None] * one).view(dt)
+    borders = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    groups = []
+    tops = torch.cat([6 * f * steps, 6 * f * (steps[1:] + steps[:-1]) / 2, 3 * f * steps[:1]])
+    for i, top in enumerate(near(tops[tops >= 4 * least]).flatten()):
+        g = torch.zeros(16, dtype=dt)
+        g[0] = top
+        groups.append(g)
+    for s in steps:
+        d = s * f
+        for y in near((borders * d)).view(5, 7):
+            g = torch.zeros(16, dtype=dt)
+            g[0] = (6 * d).to(dt)
+            g[1:8], g[8:15] = y, -y
+            groups.append(g)
+    x = torch.stack(groups)
+    x = x[(x.abs().double() >= least).any(-1) & torch.isfinite(x).all(-1)]
+    x = torch.cat([x, x[:(-len(x)) % 8]])
+    rows = x.view(-1, 2, 64)
+    p = pools(len(rows), 2, 64)
+    mva.gqa_cache_append_fp4(*p, rows.cuda(), (-rows).cuda(), torch.arange(len(rows)).int().cuda(), factor, factor)
+    assert mva.last_device_error() == 0
+    for pool, y in zip(p, (x, -x)):
+        got = pool.cpu().long()
+        codes = torch.stack([got[:, :64] & 15, got[:, :64] >> 4], -1).view(-1, 16)
+        ok, right = allowed(y, factor, got[:, 64:72].reshape(-1), codes)
+        assert ok.all(), "step of %s" % y[~ok][0].tolist()
+        assert right.all(), "codes of %s" % y[~right.all(-1)][0].tolist()
+    check(rows.cuda(), (-rows).cuda(), torch.arange(len(rows)).int(), None, factor, factor)
