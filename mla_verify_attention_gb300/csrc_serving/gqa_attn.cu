@@ -214,7 +214,7 @@ int run(const Call& c) {
   st = device_common(&d);
   if (st != MLA_OK) return st;
   const int grid = cta_count(d);
-  const bool few = c.mode == kFp4 && few_rows(c.B, c.q_len, c.H, c.Hkv, c.Smax);
+  const bool few = c.mode == kFp4 && few_rows(c);
   const Layout lay = layout(pl, few ? grid * few_heads(c.Hkv) : grid, c.D);
   if (!c.workspace || c.workspace_bytes < lay.bytes) return MLA_ERR_WORKSPACE;
   Variant var = {};
@@ -408,7 +408,7 @@ size_t mla_gqa_fp4_workspace_size(int B, int q_len, int H, int Hkv, int D) {
   DeviceCommon d;
   if (device_common(&d) != MLA_OK) return 0;
   // (Whichever kernel takes the call: that is for the table's size to say.)
-  const bool few = gqa::few_rows(1, q_len, H, Hkv, 1 << 24);
+  const bool few = gqa::few_can(q_len, H, Hkv);
   return gqa::layout(gqa::plan(q_len, H, Hkv), gqa::cta_count(d) * (few ? gqa::few_heads(Hkv) : 1), D).bytes;
 }
 

@@ -21,7 +21,7 @@
 // 64 fp16 products, 16 mma.sync), 1.6 a cycle and SM with two warps a scheduler.
 // Measured (GPU time, bf16, D = 128, 64 streams of 1k to 32k keys, 8 key heads, 16-row
 // pages): one token of 8 heads a key head 134 us, 5.0 TB/s (74 % of the measured copy
-// rate); 2, 3, 4 tokens 175, 232, 292 us.
+// rate); 2, 3, 4 tokens 174, 227, 285 us.
 //
 // Split.  Equal runs of 64-key tiles as in the attention kernel, but a CTA takes all (up
 // to eight) key heads of a run: whole rows of the cache come in by TMA boxes of eight rows
@@ -846,20 +846,38 @@ int most_step_bytes(int Hkv, int heads, int each) {
 
 }  // namespace few
 
-// Whether this kernel takes a call, by its rows a key head and the keys that its tables
-// have room for.  GPU time here / with the tcgen05 kernel, us, D = 128, 8 heads a key head
-// unless said:
-//   64 streams of 1k to 32k keys, 16-row pages, 8 key heads: one token 134 / 345, 2 tokens
-//     175 / 350, 3 225 / 352, 4 287 / 354; 2 key heads: one token 60 / 100, 4 tokens 155 / 101
-//     (the warps of a head have much to put together);
-//   64 streams of 200 to 400 keys: one token 18 / 39, 4 tokens 38 / 41;
-//   one stream, 64-row pages, of 64k keys: one token 32 / 38, 2 tokens 36 / 38, 4 51 / 38; of
-//     128k 2 tokens 52 / 64, 4 78 / 64; one token of 8,192 keys 15.7 / 15.0, of 2,048 13.7 /
-//     13.0, of 256 13.7 / 9.6 (one CTA has all heads of a key).
-bool few_rows(int B, int q_len, int H, int Hkv, int Smax) {
-  const long long rows = static_cast<long long>(q_len) * (H / Hkv), keys = static_cast<long long>(B) * Smax;
-  if (rows <= 8) return keys >= 2048;
-  return rows <= 8 * few::kMostEights && few_heads(Hkv) == few::kWarps && keys >= (rows <= 16 ? 1 << 15 : 1 << 18);
+// Whether this kernel can take a call, and whether it does: by its rows a key head, the
+// sets of key heads that CTAs take apart (streams times Hkv / few_heads) and the keys that
+// the table has room for.  GPU time here / with the tcgen05 kernel, us, D = 128, 8 heads
+// a key head, 8 key heads, tables without spare room, pages of 64 rows unless said:
+//   one stream of 1k, 4k, 16k, 64k, 256k keys (one CTA has all heads of a key):
+//     one token  13.7 / 12.3, 14.3 / 13.4, 18.5 / 18.2, 30 / 38, 69 / 118
+//     2 tokens   17 / 12, 17 / 14, 22 / 18, 35 / 38, 83 / 118
+//     3          20 / 13, 21 / 14, 25 / 18, 42 / 38, 106 / 118 (of 128k 64 / 65; 16-row pages 64 / 84)
+//     4          25 / 13, 25 / 14, 30 / 18, 50 / 38, 129 / 118 (of 128k 77 / 65; 16-row pages 77 / 84; D 64 48 / 63)
+//   4 streams of 256, 1k, 4k, 16k, 64k keys:
+//     one token  14.0 / 10.1, 14 / 19, 16 / 24, 29 / 42, 66 / 121
+//     2 tokens   18 / 10, 18 / 19, 20 / 24, 36 / 43, 83 / 122
+//     3          22 / 10, 21 / 19, 23 / 24, 43 / 43, 106 / 122
+//     4          28 / 10, 29 / 19, 33 / 24, 58 / 43, 136 / 122 (16-row pages 58 / 49, 136 / 158 the last two)
+//   32 streams of 64, 512, 4k, 16k: 2 tokens 11 / 16, 22 / 31, 54 / 76, 151 / 233; 3 13 / 16, 26 / 31, 67 / 78,
+//     196 / 235; 4 16 / 16, 34 / 31, 85 / 79, 244 / 236 (16-row pages 84 / 93, 245 / 309 the last two)
+//   64 streams of 64, 512, 4k, 16k: 4 tokens 16 / 29, 47 / 53, 144 / 148, 463 / 459; of 1k to 32k 287 / 356;
+//   one token, one stream of 1k and 4k keys: 4 key heads 12 / 12, 12 / 14; one 9 / 11, 10 / 12.
+// (A table with more room than its streams have keys is judged by its room: that costs up to
+// the difference above, as 8 streams of 1k to 32k keys, 3 tokens, 58 / 50.)
+bool few_can(int q_len, int H, int Hkv) {
+  const long long rows = static_cast<long long>(q_len) * (H / Hkv);
+  return rows <= 8 || (rows <= 8 * few::kMostEights && few_heads(Hkv) == few::kWarps);
+}
+bool few_rows(const Call& c) {
+  if (!few_can(c.q_len, c.H, c.Hkv)) return false;
+  const int rows = c.q_len * (c.H / c.Hkv), heads = few_heads(c.Hkv);
+  const long long sets = static_cast<long long>(c.B) * (c.Hkv / heads), keys = sets * c.Smax;
+  if (rows <= 8) return keys >= (sets == 1 && heads > 4 ? 1 << 14 : 1 << 11);
+  if (sets >= (rows <= 24 ? 32 : 64)) return true;
+  if (rows <= 16) return keys >= (sets == 1 ? 1 << 16 : 1 << 13);
+  return (rows <= 24 || c.D == 64 || box_rows(c) < kKeys) && keys >= 1 << 17;
 }
 int few_heads(int Hkv) { return few::heads_a_cta(Hkv, few::kWarps); }
 

@@ -47,9 +47,10 @@ AttnFn window_kernel(int D, bool bf16);    // gqa_window.cu
 using Fp4Fn = void (*)(Fp4Maps, Params);
 Fp4Fn fp4_kernel(int D, bool bf16, size_t* smem, int* threads);    // gqa_fp4.cu
 
-// The kernel for few query rows a key head over a cache in 4 bits: whether it takes a
-// call, key heads a CTA, and its launches (gqa_fp4_few.cu).
-bool few_rows(int B, int q_len, int H, int Hkv, int Smax);
+// The kernel for few query rows a key head over a cache in 4 bits: whether it can take a
+// call and whether it does, key heads a CTA, and its launches (gqa_fp4_few.cu).
+bool few_can(int q_len, int H, int Hkv);
+bool few_rows(const Call& c);
 int few_heads(int Hkv);
 int run_few(const Call& c, const Params& shared, const DeviceCommon& d, int grid);
 

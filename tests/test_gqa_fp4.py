@@ -376,3 +376,29 @@ def test_scores_far_below_zero(q, H, Hkv, room):
             plain.check(out[b], even[1].float(), even, "stream %d" % b)
             want = torch.full_like(lse[b], -2.0 ** (105 if larger else 106)).double()
             assert ((lse[b].double() - want).abs() <= 2.0 ** -22 * want.abs()).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 100])
+@pytest.mark.parametrize("q", [1, 2, 3, 4])
+def test_up_to_32_rows_whatever_the_table_has_room_for(q, page, D, dt):
+    # 7 or 8 heads a key head, 8 key heads: the kernel for few rows and the other one, by streams and room.
+    for H, lens, room in ((64, [700], 0), (64, [700], 140000), (56, [300, 64, 1200], 3000), (56, [300, 64, 1200], 50000)):
+        c = case(q, H, 8, D, lens, page, dt, room=room)
+        verify(c, run(c))
+    gen = torch.Generator().manual_seed(q)
+    for B in (33, 70):
+        c = case(q, 64, 8, D, [int(x) for x in torch.randint(q, 200, (B,), generator=gen)], page, dt)
+        verify(c, run(c))
+
+
+def test_the_workspace_does_for_every_room():
+    # Its size is asked for without a table's room.
+    for q, H, Hkv in ((1, 64, 8), (2, 64, 8), (3, 64, 8), (4, 64, 8), (5, 64, 8), (1, 40, 5), (1, 24, 3)):
+        ws = torch.full((mva.gqa_fp4_workspace_size(3, q, H, Hkv, 128) + 4096,), 7, dtype=torch.uint8, device="cuda")
+        for room in (0, 3000, 70000, 270000):
+            c = case(q, H, Hkv, 128, [700, 30, 2500], 16, room=room)
+            got = run(c, workspace=ws[:-4096])
+            verify(c, got)
+            assert (ws[-4096:] == 7).all()
