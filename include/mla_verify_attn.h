@@ -543,6 +543,12 @@ int mla_gqa_verify_attn_fp4_paged(const void* q, const int64_t* q_strides, const
  *   weights    [B, Hkv, Smax] fp32 (Smax = max_blocks * page_size), in and out; entries
  *              from seq_lens[b] on are neither read nor written.
  * Scores, exponentials and sums are fp32; deterministic.  No workspace.
+ * Sums belong to places of the cache, and no other call than mla_cache_compact touches
+ * them: mla_cache_keep moves the accepted drafts' rows without their sums, and a place
+ * that mla_blocks_trim gives up keeps its sum, from which its next key would go on.  So
+ * after a step that does not keep all its drafts either move those sums as the rows are
+ * moved and clear the places behind them, or use mla_cache_compact in place of
+ * mla_cache_keep (kept: the whole prefix, then the accepted drafts' places).
  */
 int mla_gqa_attn_weights(const void* q, const void* k, const int64_t* strides, const int32_t* seq_lens,
                          const uint32_t* tree_mask, const float* lse, int B, int q_len, int H, int Hkv, int D, int Smax,

@@ -641,6 +641,11 @@ def gqa_attn_weights(q, k, seq_lens, tree_mask, lse, scale, weights, stream=None
     q, k, seq_lens and tree_mask as for ``gqa_verify_attn``, lse [B,q,H] as it
     returns it (rows with lse +inf or -inf add nothing: +inf leaves out drafts
     that were not accepted), weights [B,Hkv,Smax] fp32.
+
+    Sums belong to places of the cache: ``gqa_cache_keep`` moves the accepted
+    drafts' rows without their sums, ``blocks_trim`` leaves those of the places that
+    it gives up.  Move them along and clear what is behind them, or use
+    ``gqa_cache_compact`` with weights in place of ``gqa_cache_keep``.
     """
     if _call is None:
         _bind()
