@@ -11,7 +11,7 @@
 // ~100 rows; beyond, a thread's exponentials: 16 a cycle and SM.  Measured (GPU time, D =
 // 128, loads first): 64 streams of 1k to 32k keys, one token, 16-row pages, 8 heads a key
 // head 207 us, 6.0 TB/s (88 % of the measured copy rate); one stream of 64k keys, 9 drafts
-// 30 us, of 262k 89 us (91 %); 64 drafts (512 rows a key head) over 8k keys 24 us.
+// 30 us, of 262k 93 us (87 %); 64 drafts (512 rows a key head) over 8k keys 24 us.
 //
 // Split.  As in the attention kernel: equal runs of 64-key tiles, teams of CTAs
 // with the key heads of a cache row side by side.  A run's tiles are taken two at a

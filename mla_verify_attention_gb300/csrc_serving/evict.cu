@@ -377,8 +377,10 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactPara
 
 // ------------------------------------------------------------ host
 
-// Blocks of a stream's cluster: as many as the device takes at once (two an SM), none of
-// which a short stream needs: up to 4,096 keys one block is through sooner.
+// Blocks of a stream's cluster: as many as the device takes at once, none of which a
+// short stream needs: up to 4,096 keys one block is through sooner.  (Two an SM: that is
+// so while a block has room for no more than some 22k keys; longer runs fill an SM each,
+// and the last clusters wait for the first.)
 int select_blocks(int B, int Smax, int sms) {
   if (Smax <= 4096) return 1;
   int blocks = kMostBlocks;

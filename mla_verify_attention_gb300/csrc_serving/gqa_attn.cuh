@@ -68,7 +68,7 @@ constexpr float kLazy = 8.0f;              // log2 units a row's max may grow be
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // What the kernel attends over: a stream's whole cache, its first keys and a
-// sliding window (see Window below), or a whole cache held in 4 bits (gqa_fp4.cuh).
+// sliding window (see Window below), or a whole cache held in 4 bits (gqa_fp4.cu).
 enum Mode { kWhole, kWindow, kFp4 };
 
 struct Params {
@@ -641,9 +641,10 @@ out:
 // TMA does, so that eight lanes that read a unit of eight rows, and then write eight rows of
 // a tile, meet no bank twice.
 // Measured (GPU time, bf16, D = 128): one stream of 64k keys, 9 drafts of 8 heads a key
-// head 39.7 us, 64 streams of 1k to 32k keys, 5 tokens 352 us: ~1,000 cycles a tile of
+// head 39.9 us, 64 streams of 1k to 32k keys, 5 tokens 353 us: ~1,000 cycles a tile of
 // 64 keys, most of them the softmax's, whose warps, the unpacking and the products' share
-// the instruction cache (16-bit caches: 860 cycles).
+// the instruction cache (16-bit caches: 860 cycles).  The kernel spills: 72 bytes stored, 360
+// loaded, in a thread's 128 registers at launch (168 and 88 by role).
 struct Fp4Maps {
   CUtensorMap codes[2], steps[2];              // K, V: boxes of D / 2 and of 16 bytes
 };
