@@ -402,3 +402,12 @@ def test_the_workspace_does_for_every_room():
             got = run(c, workspace=ws[:-4096])
             verify(c, got)
             assert (ws[-4096:] == 7).all()
+
+
+@pytest.mark.parametrize("page", [1, 5, 100])
+@pytest.mark.parametrize("q,H,Hkv", [(1, 16, 16), (1, 24, 12), (1, 40, 40), (1, 20, 5), (1, 72, 24), (4, 64, 16), (3, 64, 16)])
+def test_sets_of_heads_in_pages_that_are_copied_row_by_row(q, H, Hkv, page):
+    # More key heads than a CTA takes at once: their steps begin anywhere in 16 bytes of a row.
+    for D, dt in ((64, BF16), (128, FP16)):
+        c = case(q, H, Hkv, D, [700, max(q, 3), 0, 1111], page, dt, room=90000)
+        verify(c, run(c))
